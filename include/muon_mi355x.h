@@ -321,6 +321,140 @@ int muon_step_groups_workspace_bytes(const muon_group* groups, int64_t ngroups,
 int muon_step_groups(const muon_group* groups, int64_t ngroups, const muon_hparams* hp,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- the linear product and its gradients -------------------------------- */
+
+/* Activations of the linear product. */
+#define MUON_ACT_NONE 0
+#define MUON_ACT_RELU 1       /* max(z, 0) */
+#define MUON_ACT_RELU2 2      /* max(z, 0)^2 */
+#define MUON_ACT_SILU 3       /* z / (1 + exp(-z)) */
+#define MUON_ACT_GELU 4       /* z/2 (1 + erf(z / sqrt 2)) */
+#define MUON_ACT_GELU_TANH 5  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+
+/* y = act(x w^T + bias) + residual, what the matrix weights of the step do in
+ * a layer: x [m][k], w [n][k] (a parameter [out][in] as the step holds it),
+ * y and residual [m][n], bias [n].  All products are summed in fp32 (bf16
+ * operands on bf16 MFMA, fp32 ones on fp32 MFMA), the epilogue is fp32 and y
+ * and preact are rounded once, on store.
+ * Rows have unit column stride; row strides are in elements, and only
+ * alignment to the element size is required (16-byte aligned rows are
+ * fastest).  k == 0 gives act(bias) + residual.
+ * preact (dtype `dtype`, may be NULL) receives x w^T + bias, which
+ * muon_linear_backward reads when there is an activation.
+ * y may be the residual itself (same pointer, type and stride); any other
+ * overlap of an output with an input or the other output is refused.  Tensors
+ * that are columns of one buffer with a common row stride do not overlap. */
+typedef struct muon_linear_problem {
+  int64_t m, n, k;
+  int32_t dtype;         /* of x, w and preact: MUON_BF16 or MUON_F32 */
+  int32_t activation;    /* MUON_ACT_* */
+  const void* x; int64_t x_row_stride;
+  const void* w; int64_t w_row_stride;
+  const void* bias;      /* or NULL */
+  const void* residual; int64_t residual_row_stride;  /* or NULL */
+  void* y; int64_t y_row_stride;
+  void* preact; int64_t preact_row_stride;            /* or NULL */
+  int32_t bias_dtype, residual_dtype, y_dtype;
+  int32_t reserved;      /* must be 0 */
+} muon_linear_problem;
+
+/* Workspace bytes muon_linear needs for this problem (its pointers are looked
+ * at for their alignment only). */
+int muon_linear_workspace_bytes(const muon_linear_problem* p, size_t* bytes);
+/* Errors: MUON_ERR_INVALID_ARG (null pointers, negative or too large sizes,
+ * strides below the columns or of 2^23 bytes and more, misaligned or
+ * overlapping tensors), MUON_ERR_UNSUPPORTED (types, activation),
+ * MUON_ERR_WORKSPACE, MUON_ERR_HIP. */
+int muon_linear(const muon_linear_problem* p, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of muon_linear.  With g = dy act'(preact):
+ *   dx = g w,  dw = g^T x,  dbias = sum over rows of g
+ * (the residual's gradient is dy).  Outputs that are NULL are not computed;
+ * x is read for dw only, w for dx only, preact only with an activation.
+ * g is rounded to `dtype` where an activation (or dy of another type) makes
+ * it differ from dy, since it is an operand of both products; dbias sums the
+ * unrounded g in fp32.  dw and dbias are what a step takes as gradients: dw
+ * contiguous in bf16 or fp32.  With accumulate they are added to what the
+ * outputs hold (in fp32, one rounding on store).  m == 0 gives zero dw and
+ * dbias.  Results do not depend on anything but the arguments: sums are added
+ * in a fixed order. */
+typedef struct muon_linear_grad {
+  int64_t m, n, k;
+  int32_t dtype;         /* of x, w and preact */
+  int32_t activation;
+  const void* dy; int64_t dy_row_stride;
+  const void* x; int64_t x_row_stride;
+  const void* w; int64_t w_row_stride;
+  const void* preact; int64_t preact_row_stride;
+  void* dx; int64_t dx_row_stride;
+  void* dw; int64_t dw_row_stride;
+  void* dbias;
+  int32_t dy_dtype, dx_dtype, dw_dtype, dbias_dtype;
+  int32_t accumulate;    /* 0 or 1 */
+  int32_t reserved;      /* must be 0 */
+} muon_linear_grad;
+
+int muon_linear_backward_workspace_bytes(const muon_linear_grad* p, size_t* bytes);
+int muon_linear_backward(const muon_linear_grad* p, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- per-head norms of queries and keys with the position rotation --------- */
+
+/* One strided [batch][tokens][heads][dim] tensor with unit stride in dim, e.g.
+ * a view of the packed rows that a fused q/k/v product writes; strides are in
+ * elements and not negative. */
+typedef struct muon_heads {
+  void* p;
+  int64_t batch_stride, token_stride, head_stride;
+} muon_heads;
+
+/* For every head row x of q and of k (index 0 and 1):
+ *   u = x / sqrt(mean(x^2) + eps) * weight        (weight [dim], NULL: ones)
+ *   y = R u, which turns pair p of the first rotary_dim values by
+ *       theta = positions[axis[p]][batch][token] * inv_freq[p]:
+ *       (a, b) -> scale (a cos theta - b sin theta, b cos theta + a sin theta)
+ * and leaves the values past rotary_dim as they are.  Pair p holds values p
+ * and p + rotary_dim / 2, or 2 p and 2 p + 1 when interleaved.  Several axes
+ * (time, height, width) are position tensors of one shape and the axis every
+ * pair turns by.  Angles are formed in fp64, the rest is fp32 with one rounding
+ * on store.
+ * heads[i] == 0 leaves tensor i out.  An output may be its own input (the same
+ * view); any other overlap of an output is refused. */
+#define MUON_QK_MAX_DIM 1024
+#define MUON_QK_MAX_PAIRS 256
+#define MUON_QK_MAX_AXES 4
+typedef struct muon_qk_problem {
+  int64_t batch, tokens;
+  int32_t heads[2];
+  int32_t dim;                 /* 1..MUON_QK_MAX_DIM */
+  int32_t rotary_dim;          /* even, <= dim and <= 2 MUON_QK_MAX_PAIRS; 0: no rotation */
+  int32_t dtype;               /* of every head tensor */
+  int32_t weight_dtype;        /* of weight and dweight */
+  muon_heads x[2];             /* q and k before the call */
+  muon_heads g[2];             /* backward: gradients of the outputs */
+  muon_heads y[2];             /* outputs; backward: dq and dk */
+  const void* weight[2];
+  void* dweight[2];            /* backward: [dim], or NULL */
+  const void* positions;
+  int64_t pos_axis_stride, pos_batch_stride, pos_token_stride;
+  const void* inv_freq;        /* [rotary_dim / 2] */
+  int32_t positions_i64;       /* 1: int64, 0: int32 */
+  int32_t inv_freq_f64;        /* 1: double, 0: float */
+  int32_t interleaved;
+  int32_t axes;                /* 1..MUON_QK_MAX_AXES */
+  float scale;                 /* of cos and sin (1) */
+  float eps;
+  uint8_t axis[MUON_QK_MAX_PAIRS];
+} muon_qk_problem;
+
+int muon_qk_norm_rope(const muon_qk_problem* p, void* stream);
+/* Gradients dq, dk (y) and dweight from the gradients of the outputs (g), the
+ * inputs (x) and the weights.  dq and dk may be their own g. */
+int muon_qk_norm_rope_backward_workspace_bytes(const muon_qk_problem* p, size_t* bytes);
+int muon_qk_norm_rope_backward(const muon_qk_problem* p, void* workspace, size_t workspace_bytes, void* stream);
+/* The rotation alone, and its gradient: y = scale R^T g (x is not read). */
+int muon_rope(const muon_qk_problem* p, void* stream);
+int muon_rope_backward(const muon_qk_problem* p, void* stream);
+
 /* ---- launch timing ------------------------------------------------------ */
 
 /* Kernel classes the library launches. */

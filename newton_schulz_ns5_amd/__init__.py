@@ -20,7 +20,13 @@ Entry points (same names as the C ABI):
 * ``normuon_normalize(o, v, beta2, eps)`` -- NorMuon on [n, rows, cols];
 * ``step_group(...)`` -- one Muon / NorMuon step of same-shape parameters;
 * ``MuonNS5`` -- a small optimizer that groups parameters by flattened shape
-  and calls ``step_group`` per group.
+  and calls ``step_group`` per group;
+* ``linear``, ``linear_backward`` -- the product of a layer's rows with a matrix
+  weight, with bias, activation and residual, and its gradients (``dw`` in the
+  form a step takes);
+* ``qk_norm_rope``, ``rope`` and their ``_backward`` -- per-head norms of queries
+  and keys with the position rotation (one or several axes) in the same pass,
+  and the rotation alone.
 """
 import ctypes
 import math
@@ -32,7 +38,8 @@ from ._lib import MUON_BF16, MUON_F32, MuonError, NSConfig, NSProblem, Group, HP
 __all__ = ["ns_batched", "ns_batched_noalloc", "NOALLOC_WORKSPACE_BYTES", "ns_groups", "ns_groups_workspace_bytes", "normuon_normalize", "step_group", "step_groups", "step_groups_workspace_bytes", "MuonNS5", "per_head_view", "ns_config",
            "hparams", "ns_workspace_bytes", "step_workspace_bytes", "normuon_workspace_bytes",
            "profile_enable", "profile_classes", "profile_reset", "profile_query", "MuonError", "QUINTIC", "abi_version",
-           "state_layout_version", "lib"]
+           "state_layout_version", "lib", "linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope",
+           "rope_backward", "ACTIVATIONS"]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 lib = _lib.lib
@@ -529,3 +536,18 @@ def profile_query(kernel_class):
     _lib.check(lib().muon_profile_query(int(kernel_class), ctypes.byref(n), ctypes.byref(ms), ctypes.byref(fl),
                                         ctypes.byref(by)))
     return {"launches": n.value, "ms": ms.value, "flop": fl.value, "bytes": by.value}
+
+
+# ---- layer operators ---------------------------------------------------------------
+_LAYER_OPS = ("linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward", "ACTIVATIONS")
+
+
+def __getattr__(name):
+    # The layer operators are defined with torch (autograd functions), which
+    # this module itself imports on first use only.
+    if name in _LAYER_OPS:
+        from . import layer_ops
+        for n in _LAYER_OPS:
+            globals()[n] = getattr(layer_ops, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -56,6 +56,39 @@ class HParams(ctypes.Structure):
                 ("fan_out", c_i64), ("fan_in", c_i64), ("ns", NSConfig)]
 
 
+class LinearProblem(ctypes.Structure):
+    _fields_ = [("m", c_i64), ("n", c_i64), ("k", c_i64), ("dtype", c_i32), ("activation", c_i32),
+                ("x", c_vp), ("x_row_stride", c_i64), ("w", c_vp), ("w_row_stride", c_i64), ("bias", c_vp),
+                ("residual", c_vp), ("residual_row_stride", c_i64), ("y", c_vp), ("y_row_stride", c_i64),
+                ("preact", c_vp), ("preact_row_stride", c_i64),
+                ("bias_dtype", c_i32), ("residual_dtype", c_i32), ("y_dtype", c_i32), ("reserved", c_i32)]
+
+
+class LinearGrad(ctypes.Structure):
+    _fields_ = [("m", c_i64), ("n", c_i64), ("k", c_i64), ("dtype", c_i32), ("activation", c_i32),
+                ("dy", c_vp), ("dy_row_stride", c_i64), ("x", c_vp), ("x_row_stride", c_i64),
+                ("w", c_vp), ("w_row_stride", c_i64), ("preact", c_vp), ("preact_row_stride", c_i64),
+                ("dx", c_vp), ("dx_row_stride", c_i64), ("dw", c_vp), ("dw_row_stride", c_i64), ("dbias", c_vp),
+                ("dy_dtype", c_i32), ("dx_dtype", c_i32), ("dw_dtype", c_i32), ("dbias_dtype", c_i32),
+                ("accumulate", c_i32), ("reserved", c_i32)]
+
+
+QK_MAX_PAIRS = 256
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("p", c_vp), ("batch_stride", c_i64), ("token_stride", c_i64), ("head_stride", c_i64)]
+
+
+class QkProblem(ctypes.Structure):
+    _fields_ = [("batch", c_i64), ("tokens", c_i64), ("heads", c_i32 * 2), ("dim", c_i32), ("rotary_dim", c_i32),
+                ("dtype", c_i32), ("weight_dtype", c_i32), ("x", Heads * 2), ("g", Heads * 2), ("y", Heads * 2),
+                ("weight", c_vp * 2), ("dweight", c_vp * 2), ("positions", c_vp), ("pos_axis_stride", c_i64),
+                ("pos_batch_stride", c_i64), ("pos_token_stride", c_i64), ("inv_freq", c_vp),
+                ("positions_i64", c_i32), ("inv_freq_f64", c_i32), ("interleaved", c_i32), ("axes", c_i32),
+                ("scale", c_f32), ("eps", c_f32), ("axis", ctypes.c_uint8 * QK_MAX_PAIRS)]
+
+
 SIGNATURES = {
     "muon_ns_default_config": (None, [ctypes.POINTER(NSConfig)]),
     "muon_default_hparams": (None, [ctypes.POINTER(HParams)]),
@@ -79,6 +112,15 @@ SIGNATURES = {
     "muon_step_groups_workspace_bytes": (c_i32, [ctypes.POINTER(Group), c_i64, ctypes.POINTER(HParams),
                                                  ctypes.POINTER(c_sz)]),
     "muon_step_groups": (c_i32, [ctypes.POINTER(Group), c_i64, ctypes.POINTER(HParams), c_vp, c_sz, c_vp]),
+    "muon_linear_workspace_bytes": (c_i32, [ctypes.POINTER(LinearProblem), ctypes.POINTER(c_sz)]),
+    "muon_linear": (c_i32, [ctypes.POINTER(LinearProblem), c_vp, c_sz, c_vp]),
+    "muon_linear_backward_workspace_bytes": (c_i32, [ctypes.POINTER(LinearGrad), ctypes.POINTER(c_sz)]),
+    "muon_linear_backward": (c_i32, [ctypes.POINTER(LinearGrad), c_vp, c_sz, c_vp]),
+    "muon_qk_norm_rope": (c_i32, [ctypes.POINTER(QkProblem), c_vp]),
+    "muon_qk_norm_rope_backward_workspace_bytes": (c_i32, [ctypes.POINTER(QkProblem), ctypes.POINTER(c_sz)]),
+    "muon_qk_norm_rope_backward": (c_i32, [ctypes.POINTER(QkProblem), c_vp, c_sz, c_vp]),
+    "muon_rope": (c_i32, [ctypes.POINTER(QkProblem), c_vp]),
+    "muon_rope_backward": (c_i32, [ctypes.POINTER(QkProblem), c_vp]),
     "muon_profile_enable": (c_i32, [c_i32]),
     "muon_profile_classes": (c_i32, [ctypes.c_uint32]),
     "muon_profile_reset": (c_i32, []),

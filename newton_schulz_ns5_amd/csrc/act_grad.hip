@@ -1,0 +1,140 @@
+// Gradient at the pre-activation, G = dy act'(z), with the bias gradient's
+// column sums in the same pass, and the sum of their partials.
+//
+// Bound by HBM: dy and z are read once and G written once.  A workgroup owns
+// 256 columns of a chunk of rows; a thread owns 8 consecutive columns of every
+// eighth row of it, keeps their sums in registers, and the eight row groups
+// are added in order through LDS, so a column's sum is added in an order that
+// depends on the sizes only.
+#include "layer_internal.h"
+#include "layer_math.h"
+
+namespace muon {
+namespace {
+
+constexpr int CW = 256;  // columns per workgroup
+
+// 8 consecutive elements as fp32, the first `valid` of them when not `vec`.
+__device__ __forceinline__ void get8(const void* base, int64_t idx, bool bf, bool vec, int valid, float (&v)[8]) {
+  if (vec && valid >= 8) {
+    if (bf) {
+      const u32x4 a = *(const u32x4*)((const uint16_t*)base + idx);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        v[2 * w] = __uint_as_float(a[w] << 16);
+        v[2 * w + 1] = __uint_as_float(a[w] & 0xffff0000u);
+      }
+    } else {
+      const f32x4 a = *(const f32x4*)((const float*)base + idx), b = *(const f32x4*)((const float*)base + idx + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < valid ? load_elem(base, idx + e, bf) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void put8(void* base, int64_t idx, bool bf, bool vec, int valid, const float (&v)[8]) {
+  if (vec && valid >= 8) {
+    if (bf) {
+      u32x4 a;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) a[w] = pack_bf2(v[2 * w], v[2 * w + 1]);
+      *(u32x4*)((uint16_t*)base + idx) = a;
+    } else {
+      *(f32x4*)((float*)base + idx) = f32x4{v[0], v[1], v[2], v[3]};
+      *(f32x4*)((float*)base + idx + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < valid) store_elem(base, idx + e, v[e], bf);
+  }
+}
+
+template <bool BF>
+__global__ __launch_bounds__(256) void act_grad_kernel(const ActGrad p) {
+  __shared__ float red[8][CW + 8];
+  const int tid = threadIdx.x, rg = tid >> 5, cg = (tid & 31) * 8;
+  const int64_t j = (int64_t)blockIdx.x * CW + cg;
+  const int valid = j >= p.N ? 0 : (p.N - j < 8 ? (int)(p.N - j) : 8);
+  const int64_t r0 = (int64_t)blockIdx.y * p.rows_per;
+  const int64_t r1 = r0 + p.rows_per < p.M ? r0 + p.rows_per : p.M;
+  const bool vec = p.vec != 0;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  if (valid > 0) {
+    with_act(p.act, [&](auto act_c) {
+      constexpr int ACT = decltype(act_c)::value;
+#pragma unroll 2
+      for (int64_t i = r0 + rg; i < r1; i += 8) {
+        float g[8];
+        get8(p.dy, i * p.lddy + j, p.dy_dtype == MUON_BF16, vec, valid, g);
+        if constexpr (ACT != MUON_ACT_NONE) {
+          float z[8];
+          get8(p.z, i * p.ldz + j, BF, vec, valid, z);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(z[e]);
+        }
+        if (p.G) put8(p.G, i * p.ldg + j, BF, vec, valid, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += g[e];
+      }
+    });
+  }
+  if (!p.partial) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) red[rg][cg + e] = sum[e];
+  __syncthreads();
+  const int64_t c = (int64_t)blockIdx.x * CW + tid;
+  if (c >= p.N) return;
+  float t = red[0][tid];
+#pragma unroll
+  for (int g = 1; g < 8; ++g) t += red[g][tid];
+  p.partial[(int64_t)blockIdx.y * p.N + c] = t;
+}
+
+struct ColSum {
+  const float* partial; int32_t chunks; int64_t n;
+  void* out; int32_t out_dtype; int32_t accumulate;
+};
+
+// Four threads per column add every fourth chunk, then the four sums in order.
+__global__ __launch_bounds__(256) void col_sum_kernel(const ColSum p) {
+  __shared__ float red[4][64];
+  const int col = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t j = (int64_t)blockIdx.x * 64 + col;
+  float t = 0.f;
+  if (j < p.n)
+    for (int c = q; c < p.chunks; c += 4) t += p.partial[(int64_t)c * p.n + j];
+  red[q][col] = t;
+  __syncthreads();
+  if (q || j >= p.n) return;
+  t = ((red[0][col] + red[1][col]) + red[2][col]) + red[3][col];
+  const bool bf = p.out_dtype == MUON_BF16;
+  if (p.accumulate) t += load_elem(p.out, j, bf);
+  store_elem(p.out, j, t, bf);
+}
+
+}  // namespace
+
+hipError_t launch_act_grad(const ActGrad& g, bool bf16, hipStream_t s) {
+  const int64_t cols = (g.N + CW - 1) / CW;
+  if (cols <= 0 || g.M <= 0) return hipSuccess;
+  if (cols > INT32_MAX || g.chunks > 65535 || g.chunks * g.rows_per < g.M) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)cols, (unsigned)g.chunks);
+  return bf16 ? launch_kernel(act_grad_kernel<true>, grid, g, s) : launch_kernel(act_grad_kernel<false>, grid, g, s);
+}
+
+hipError_t launch_col_sum(const float* partial, int chunks, int64_t n, void* out, int32_t out_dtype, bool accumulate,
+                          hipStream_t s) {
+  const int64_t blocks = (n + 63) / 64;
+  if (blocks <= 0) return hipSuccess;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const ColSum p{partial, chunks, n, out, out_dtype, accumulate ? 1 : 0};
+  return launch_kernel(col_sum_kernel, dim3((unsigned)blocks), p, s);
+}
+
+}  // namespace muon

@@ -1,0 +1,513 @@
+// Host side of the layer operators: validation, workspace carve-up and launch
+// sequences of the linear product, its gradients and the per-head norms with
+// rotation.  Every argument is checked before anything is enqueued.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <algorithm>
+
+#include "layer_internal.h"
+#include "muon_mi355x.h"
+
+using namespace muon;
+
+namespace {
+
+int fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return report(code, buf);
+}
+int ok() { return report(MUON_OK, ""); }
+int hip_fail(hipError_t e, const char* what) { return fail(MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e)); }
+
+bool dtype_ok(int32_t d) { return d == MUON_F32 || d == MUON_BF16; }
+int64_t esize(int32_t d) { return d == MUON_BF16 ? 2 : 4; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (!need) return MUON_OK;
+  if (!ws) return fail(MUON_ERR_INVALID_ARG, "workspace is NULL");
+  if ((uintptr_t)ws & 255) return fail(MUON_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (have < need) return fail(MUON_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, have);
+  return MUON_OK;
+}
+
+// Bytes a strided set of rows reaches: rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  const char* name;
+  uintptr_t at;
+  int64_t rows, width, stride;
+};
+Rows rows_of(const char* name, const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld) {
+  return {name, (uintptr_t)p, rows, cols * esize(dt), rows > 1 ? ld * esize(dt) : cols * esize(dt)};
+}
+// Whether two sets may share a byte.  Sets with one common stride are told
+// apart by their place within it (columns of one packed buffer), others by
+// their whole extent.
+bool meet(const Rows& a, const Rows& b) {
+  if (!a.at || !b.at || !a.rows || !b.rows || !a.width || !b.width) return false;
+  const uintptr_t ae = a.at + (uintptr_t)((a.rows - 1) * a.stride + a.width);
+  const uintptr_t be = b.at + (uintptr_t)((b.rows - 1) * b.stride + b.width);
+  if (a.at >= be || b.at >= ae) return false;
+  const int64_t S = a.rows > 1 ? a.stride : b.stride;
+  if ((a.rows > 1 && b.rows > 1 && a.stride != b.stride) || a.width > S || b.width > S) return true;
+  const int64_t d = (int64_t)((a.at >= b.at ? a.at - b.at : S - (int64_t)((b.at - a.at) % (uintptr_t)S)) % (uintptr_t)S);
+  return !(d >= b.width && d + a.width <= S);
+}
+
+// ---- the linear product -------------------------------------------------------------
+// Dimensions stay below 2^30 and a row stride below 2^23 bytes, so that a
+// tile's panel of rows is addressed with 32-bit offsets.
+constexpr int64_t kMaxSize = (int64_t)1 << 30, kMaxRowBytes = ((int64_t)1 << 23) - 1;
+
+int check_sizes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 0 || k < 0) return fail(MUON_ERR_INVALID_ARG, "negative size (m=%lld n=%lld k=%lld)", (long long)m, (long long)n, (long long)k);
+  if (m > kMaxSize || n > kMaxSize || k > kMaxSize) return fail(MUON_ERR_INVALID_ARG, "m, n and k must be at most 2^30");
+  // one workgroup per 64 x 64 tile of an output, and a grid holds fewer than 2^31
+  if (std::max({cdiv(m, 64) * cdiv(n, 64), cdiv(m, 64) * cdiv(k, 64), cdiv(n, 64) * cdiv(k, 64)}) > INT32_MAX)
+    return fail(MUON_ERR_INVALID_ARG, "an output has too many tiles");
+  return MUON_OK;
+}
+
+int check_matrix(const char* name, const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld) {
+  if (!dtype_ok(dt)) return fail(MUON_ERR_UNSUPPORTED, "%s dtype %d is not MUON_F32 or MUON_BF16", name, dt);
+  if (rows == 0 || cols == 0) return MUON_OK;
+  if (!p) return fail(MUON_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < cols && rows > 1) return fail(MUON_ERR_INVALID_ARG, "%s row stride %lld is smaller than its %lld columns", name, (long long)ld, (long long)cols);
+  if (cols * esize(dt) > kMaxRowBytes || (rows > 1 && ld * esize(dt) > kMaxRowBytes))
+    return fail(MUON_ERR_INVALID_ARG, "%s rows must be less than 2^23 bytes apart", name);
+  if ((uintptr_t)p % esize(dt)) return fail(MUON_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
+  return MUON_OK;
+}
+
+int check_act(int32_t act) {
+  if (act < MUON_ACT_NONE || act > MUON_ACT_GELU_TANH) return fail(MUON_ERR_UNSUPPORTED, "activation %d is not one of MUON_ACT_*", act);
+  return MUON_OK;
+}
+
+int check_linear(const muon_linear_problem* q) {
+  if (!q) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
+  if (q->reserved) return fail(MUON_ERR_INVALID_ARG, "reserved must be 0");
+  int rc;
+  if ((rc = check_sizes(q->m, q->n, q->k)) || (rc = check_act(q->activation))) return rc;
+  if ((rc = check_matrix("x", q->x, q->dtype, q->m, q->k, q->x_row_stride))) return rc;
+  if ((rc = check_matrix("w", q->w, q->dtype, q->n, q->k, q->w_row_stride))) return rc;
+  if ((rc = check_matrix("y", q->y, q->y_dtype, q->m, q->n, q->y_row_stride))) return rc;
+  if (q->bias && (rc = check_matrix("bias", q->bias, q->bias_dtype, 1, q->n, q->n))) return rc;
+  if (q->residual && (rc = check_matrix("residual", q->residual, q->residual_dtype, q->m, q->n, q->residual_row_stride))) return rc;
+  if (q->preact && (rc = check_matrix("preact", q->preact, q->dtype, q->m, q->n, q->preact_row_stride))) return rc;
+  const Rows y = rows_of("y", q->y, q->y_dtype, q->m, q->n, q->y_row_stride);
+  const Rows z = rows_of("preact", q->preact, q->dtype, q->m, q->n, q->preact_row_stride);
+  const Rows in[] = {rows_of("x", q->x, q->dtype, q->m, q->k, q->x_row_stride),
+                     rows_of("w", q->w, q->dtype, q->n, q->k, q->w_row_stride),
+                     rows_of("bias", q->bias, q->bias_dtype, 1, q->n, q->n),
+                     rows_of("residual", q->residual, q->residual_dtype, q->m, q->n, q->residual_row_stride)};
+  for (const Rows& r : in) {
+    const bool same = r.at == y.at && r.name == in[3].name && q->residual_dtype == q->y_dtype &&
+                      (q->m <= 1 || q->residual_row_stride == q->y_row_stride);
+    if (!same && meet(y, r)) return fail(MUON_ERR_INVALID_ARG, "y overlaps %s (only y == residual is allowed)", r.name);
+    if (meet(z, r)) return fail(MUON_ERR_INVALID_ARG, "preact overlaps %s", r.name);
+  }
+  if (meet(y, z)) return fail(MUON_ERR_INVALID_ARG, "preact overlaps y");
+  return MUON_OK;
+}
+
+int check_linear_grad(const muon_linear_grad* q) {
+  if (!q) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
+  if (q->reserved) return fail(MUON_ERR_INVALID_ARG, "reserved must be 0");
+  int rc;
+  if ((rc = check_sizes(q->m, q->n, q->k)) || (rc = check_act(q->activation))) return rc;
+  if (!dtype_ok(q->dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype %d is not MUON_F32 or MUON_BF16", q->dtype);
+  if ((rc = check_matrix("dy", q->dy, q->dy_dtype, q->m, q->n, q->dy_row_stride))) return rc;
+  const bool act = q->activation != MUON_ACT_NONE;
+  if (act && (rc = check_matrix("preact", q->preact, q->dtype, q->m, q->n, q->preact_row_stride))) return rc;
+  if (q->dw && (rc = check_matrix("x", q->x, q->dtype, q->m, q->k, q->x_row_stride))) return rc;
+  if (q->dx && (rc = check_matrix("w", q->w, q->dtype, q->n, q->k, q->w_row_stride))) return rc;
+  if (q->dx && (rc = check_matrix("dx", q->dx, q->dx_dtype, q->m, q->k, q->dx_row_stride))) return rc;
+  if (q->dw && (rc = check_matrix("dw", q->dw, q->dw_dtype, q->n, q->k, q->dw_row_stride))) return rc;
+  if (q->dbias && (rc = check_matrix("dbias", q->dbias, q->dbias_dtype, 1, q->n, q->n))) return rc;
+  if (q->accumulate != 0 && q->accumulate != 1) return fail(MUON_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  const Rows in[] = {rows_of("dy", q->dy, q->dy_dtype, q->m, q->n, q->dy_row_stride),
+                     rows_of("preact", act ? q->preact : nullptr, q->dtype, q->m, q->n, q->preact_row_stride),
+                     rows_of("x", q->dw ? q->x : nullptr, q->dtype, q->m, q->k, q->x_row_stride),
+                     rows_of("w", q->dx ? q->w : nullptr, q->dtype, q->n, q->k, q->w_row_stride)};
+  const Rows out[] = {rows_of("dx", q->dx, q->dx_dtype, q->m, q->k, q->dx_row_stride),
+                      rows_of("dw", q->dw, q->dw_dtype, q->n, q->k, q->dw_row_stride),
+                      rows_of("dbias", q->dbias, q->dbias_dtype, 1, q->n, q->n)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Rows& r : in)
+      if (meet(out[i], r)) return fail(MUON_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, r.name);
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return fail(MUON_ERR_INVALID_ARG, "%s overlaps %s", out[i].name, out[j].name);
+  }
+  return MUON_OK;
+}
+
+// Work of a gradient call: the elementwise pass runs when the gradient at the
+// pre-activation differs from dy (an activation, or dy of another type than
+// the operands) or the bias gradient is wanted.
+struct GradPlan {
+  bool store_g, colsum;
+  int64_t ldg;
+  int chunks;
+  int64_t rows_per;
+  size_t g_off, partial_off, total;
+};
+
+GradPlan plan_grad(const muon_linear_grad* q) {
+  GradPlan P{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t at = off; off = align256(off + bytes); return at; };
+  if (q->m == 0 || q->n == 0) return P;
+  P.store_g = (q->dx || q->dw) && (q->activation != MUON_ACT_NONE || q->dy_dtype != q->dtype);
+  P.colsum = q->dbias != nullptr;
+  // Rows per workgroup of the elementwise pass: enough workgroups to fill the
+  // chip (256 columns each), at least 32 rows so that partial sums stay few.
+  const int64_t cols = cdiv(q->n, 256);
+  const int64_t want = std::max<int64_t>(1, 2048 / cols);
+  P.rows_per = std::max<int64_t>(32, cdiv(q->m, want));
+  P.rows_per = std::max<int64_t>(P.rows_per, cdiv(q->m, 4096));
+  P.chunks = (int)cdiv(q->m, P.rows_per);
+  P.ldg = cdiv(q->n, 8) * 8;
+  if (P.store_g) P.g_off = take((size_t)(q->m * P.ldg * esize(q->dtype)));
+  if (P.colsum) P.partial_off = take((size_t)P.chunks * (size_t)q->n * 4);
+  P.total = off;
+  return P;
+}
+
+bool rows16(const void* p, int64_t ld, int32_t dt) {
+  return ((uintptr_t)p & 15) == 0 && (ld * esize(dt)) % 16 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_linear_workspace_bytes(const muon_linear_problem* q, size_t* bytes) {
+  if (!q || !bytes) return fail(MUON_ERR_INVALID_ARG, "problem or bytes is NULL");
+  int rc = check_sizes(q->m, q->n, q->k);
+  if (rc) return rc;
+  *bytes = 0;
+  return ok();
+}
+
+int muon_linear(const muon_linear_problem* q, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_linear(q);
+  if (rc) return rc;
+  if (q->m == 0 || q->n == 0) return ok();
+  (void)workspace; (void)workspace_bytes;
+  LinGemm g{};
+  g.A = q->x; g.lda = q->x_row_stride;
+  g.B = q->w; g.ldb = q->w_row_stride;
+  g.M = q->m; g.N = q->n; g.K = q->k;
+  g.bias = q->bias; g.bias_dtype = q->bias_dtype;
+  g.add = q->residual; g.add_dtype = q->residual_dtype; g.ldadd = q->residual_row_stride;
+  g.Y = q->y; g.y_dtype = q->y_dtype; g.ldy = q->y_row_stride;
+  g.Z = q->preact; g.ldz = q->preact_row_stride;
+  g.act = q->activation;
+  const hipError_t e = launch_linear_simple(g, q->dtype == MUON_BF16, kRowRow, (hipStream_t)stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "linear kernels");
+}
+
+int muon_linear_backward_workspace_bytes(const muon_linear_grad* q, size_t* bytes) {
+  if (!q || !bytes) return fail(MUON_ERR_INVALID_ARG, "problem or bytes is NULL");
+  int rc = check_sizes(q->m, q->n, q->k);
+  if (rc) return rc;
+  if (!dtype_ok(q->dtype) || !dtype_ok(q->dy_dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype and dy_dtype must be MUON_F32 or MUON_BF16");
+  *bytes = plan_grad(q).total;
+  return ok();
+}
+
+int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_linear_grad(q);
+  if (rc) return rc;
+  const GradPlan P = plan_grad(q);
+  if ((rc = check_workspace(workspace, workspace_bytes, P.total))) return rc;
+  const bool bf = q->dtype == MUON_BF16;
+  hipStream_t s = (hipStream_t)stream;
+  char* ws = (char*)workspace;
+  const void* G = q->dy;
+  int64_t ldg = q->dy_row_stride;
+  hipError_t e;
+  if (P.store_g || P.colsum) {
+    ActGrad a{};
+    a.dy = q->dy; a.dy_dtype = q->dy_dtype; a.lddy = q->dy_row_stride;
+    a.act = q->activation;
+    if (a.act != MUON_ACT_NONE) { a.z = q->preact; a.ldz = q->preact_row_stride; }
+    if (P.store_g) {
+      a.G = ws + P.g_off; a.ldg = P.ldg;
+      G = a.G; ldg = P.ldg;
+    }
+    if (P.colsum) a.partial = (float*)(ws + P.partial_off);
+    a.chunks = P.chunks; a.rows_per = P.rows_per;
+    a.M = q->m; a.N = q->n;
+    a.vec = rows16(a.dy, a.lddy, a.dy_dtype) && (!a.z || rows16(a.z, a.ldz, q->dtype)) ? 1 : 0;
+    if ((e = launch_act_grad(a, bf, s)) != hipSuccess) return hip_fail(e, "gradient at the pre-activation");
+  }
+  if (q->dbias && q->n > 0) {
+    e = launch_col_sum((const float*)(ws + P.partial_off), P.chunks, q->n, q->dbias, q->dbias_dtype, q->accumulate != 0, s);
+    if (e != hipSuccess) return hip_fail(e, "bias gradient");
+  }
+  if (q->dx && q->m > 0 && q->k > 0) {
+    LinGemm g{};
+    g.A = G; g.lda = ldg;
+    g.B = q->w; g.ldb = q->w_row_stride;
+    g.M = q->m; g.N = q->k; g.K = q->n;
+    g.Y = q->dx; g.y_dtype = q->dx_dtype; g.ldy = q->dx_row_stride;
+    if ((e = launch_linear_simple(g, bf, kRowCol, s)) != hipSuccess) return hip_fail(e, "input gradient");
+  }
+  if (q->dw && q->n > 0 && q->k > 0) {
+    LinGemm g{};
+    g.A = G; g.lda = ldg;
+    g.B = q->x; g.ldb = q->x_row_stride;
+    g.M = q->n; g.N = q->k; g.K = q->m;
+    g.Y = q->dw; g.y_dtype = q->dw_dtype; g.ldy = q->dw_row_stride;
+    if (q->accumulate) { g.add = q->dw; g.add_dtype = q->dw_dtype; g.ldadd = q->dw_row_stride; }
+    if ((e = launch_linear_simple(g, bf, kColCol, s)) != hipSuccess) return hip_fail(e, "weight gradient");
+  }
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- per-head norms and rotation -------------------------------------------------------
+
+const char* kQ[2] = {"q", "k"};
+
+// Extent of one strided [batch][token][head][dim] tensor in bytes; strides are
+// not negative.
+struct Span { uintptr_t lo, hi; };
+
+int check_heads(const char* what, int i, const muon_heads* t, int32_t dt, const muon_qk_problem* q) {
+  if (!t->p) return fail(MUON_ERR_INVALID_ARG, "%s of %s is NULL", what, kQ[i]);
+  if (t->batch_stride < 0 || t->token_stride < 0 || t->head_stride < 0)
+    return fail(MUON_ERR_INVALID_ARG, "%s of %s has a negative stride", what, kQ[i]);
+  if ((uintptr_t)t->p % esize(dt)) return fail(MUON_ERR_INVALID_ARG, "%s of %s is not aligned to its element size", what, kQ[i]);
+  return MUON_OK;
+}
+
+Span span_of(const muon_heads& t, int64_t heads, int32_t dt, const muon_qk_problem* q) {
+  const int64_t last = (q->batch - 1) * t.batch_stride + (q->tokens - 1) * t.token_stride + (heads - 1) * t.head_stride + q->dim;
+  return {(uintptr_t)t.p, (uintptr_t)t.p + (uintptr_t)(last * esize(dt))};
+}
+
+// No element of a strided tensor is another one's: sorted by stride, each
+// stride reaches past everything the smaller ones cover.
+bool self_disjoint(const muon_heads& t, int64_t heads, const muon_qk_problem* q) {
+  struct D { int64_t stride, n; } d[3] = {{t.batch_stride, q->batch}, {t.token_stride, q->tokens}, {t.head_stride, heads}};
+  std::sort(d, d + 3, [](const D& a, const D& b) { return a.stride < b.stride; });
+  int64_t reach = q->dim;
+  for (const D& x : d) {
+    if (x.n <= 1) continue;
+    if (x.stride < reach) return false;
+    reach += (x.n - 1) * x.stride;
+  }
+  return true;
+}
+
+bool same_view(const muon_heads& a, const muon_heads& b, const muon_qk_problem* q, int64_t heads) {
+  return a.p == b.p && (q->batch <= 1 || a.batch_stride == b.batch_stride) &&
+         (q->tokens <= 1 || a.token_stride == b.token_stride) && (heads <= 1 || a.head_stride == b.head_stride);
+}
+
+// Whether two tensors may share a byte.  Views of one packed buffer with the
+// same token stride, each token's heads within it, are told apart by their
+// place within that stride; others by their whole extent.
+bool may_meet(const muon_heads& a, int64_t ha, const muon_heads& b, int64_t hb, int32_t dt, const muon_qk_problem* q) {
+  const Span x = span_of(a, ha, dt, q), y = span_of(b, hb, dt, q);
+  if (x.lo >= y.hi || y.lo >= x.hi) return false;
+  const int64_t S = a.token_stride;
+  const int64_t wa = (ha - 1) * a.head_stride + q->dim, wb = (hb - 1) * b.head_stride + q->dim;
+  const bool batched = q->batch > 1;
+  if (S != b.token_stride || S <= 0 || wa > S || wb > S) return true;
+  if (batched && (a.batch_stride % S || b.batch_stride % S)) return true;
+  const int64_t bytes = S * esize(dt);
+  const int64_t d = (int64_t)((x.lo >= y.lo ? x.lo - y.lo : (uintptr_t)bytes - (y.lo - x.lo) % (uintptr_t)bytes) % (uintptr_t)bytes);
+  return !(d >= wb * esize(dt) && d + wa * esize(dt) <= bytes);
+}
+
+int check_qk(const muon_qk_problem* q, bool backward, bool norm) {
+  if (!q) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
+  if (q->batch < 0 || q->tokens < 0) return fail(MUON_ERR_INVALID_ARG, "negative batch or tokens");
+  if (q->batch > kMaxSize || q->tokens > kMaxSize || q->batch * q->tokens > kMaxSize) return fail(MUON_ERR_INVALID_ARG, "more than 2^30 tokens");
+  if (q->dim < 1 || q->dim > MUON_QK_MAX_DIM) return fail(MUON_ERR_INVALID_ARG, "dim %d is not in 1..%d", q->dim, MUON_QK_MAX_DIM);
+  if (q->rotary_dim < 0 || q->rotary_dim % 2 || q->rotary_dim > q->dim || q->rotary_dim > 2 * kMaxPairs)
+    return fail(MUON_ERR_INVALID_ARG, "rotary_dim %d must be even, at most dim %d and at most %d", q->rotary_dim, q->dim, 2 * kMaxPairs);
+  if (q->axes < 1 || q->axes > kMaxAxes) return fail(MUON_ERR_INVALID_ARG, "axes must be in 1..%d", kMaxAxes);
+  for (int i = 0; i < q->rotary_dim / 2; ++i)
+    if (q->axis[i] >= q->axes) return fail(MUON_ERR_INVALID_ARG, "pair %d turns by axis %d of %d", i, q->axis[i], q->axes);
+  if (!dtype_ok(q->dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype %d is not MUON_F32 or MUON_BF16", q->dtype);
+  if (norm && !dtype_ok(q->weight_dtype)) return fail(MUON_ERR_UNSUPPORTED, "weight_dtype %d is not MUON_F32 or MUON_BF16", q->weight_dtype);
+  if (!std::isfinite(q->scale)) return fail(MUON_ERR_INVALID_ARG, "scale must be finite");
+  if (norm && !(std::isfinite(q->eps) && q->eps >= 0)) return fail(MUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  for (int i = 0; i < 2; ++i)
+    if (q->heads[i] < 0 || q->heads[i] > 65536) return fail(MUON_ERR_INVALID_ARG, "heads must be in 0..65536");
+  if (q->batch == 0 || q->tokens == 0 || (q->heads[0] == 0 && q->heads[1] == 0)) return MUON_OK;
+  if (q->rotary_dim) {
+    if (!q->positions) return fail(MUON_ERR_INVALID_ARG, "positions is NULL");
+    if (!q->inv_freq) return fail(MUON_ERR_INVALID_ARG, "inv_freq is NULL");
+    if ((uintptr_t)q->positions % (q->positions_i64 ? 8 : 4) || (uintptr_t)q->inv_freq % (q->inv_freq_f64 ? 8 : 4))
+      return fail(MUON_ERR_INVALID_ARG, "positions or inv_freq is not aligned to its element size");
+    if (q->pos_axis_stride < 0 || q->pos_batch_stride < 0 || q->pos_token_stride < 0) return fail(MUON_ERR_INVALID_ARG, "positions has a negative stride");
+  }
+  int rc;
+  for (int i = 0; i < 2; ++i) {
+    if (!q->heads[i]) continue;
+    if (!(backward && !norm) && (rc = check_heads("input", i, &q->x[i], q->dtype, q))) return rc;
+    if (backward && (rc = check_heads("gradient", i, &q->g[i], q->dtype, q))) return rc;
+    if ((rc = check_heads("output", i, &q->y[i], q->dtype, q))) return rc;
+    if (!self_disjoint(q->y[i], q->heads[i], q)) return fail(MUON_ERR_INVALID_ARG, "output of %s overlaps itself", kQ[i]);
+    if (norm && q->weight[i] && (uintptr_t)q->weight[i] % esize(q->weight_dtype)) return fail(MUON_ERR_INVALID_ARG, "weight of %s is not aligned to its element size", kQ[i]);
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (!q->heads[i]) continue;
+    for (int k = 0; k < 2; ++k) {
+      if (!q->heads[k]) continue;
+      const bool same = i == k;
+      if (!(backward && !norm) && !(same && same_view(q->y[i], q->x[k], q, q->heads[i])) &&
+          may_meet(q->y[i], q->heads[i], q->x[k], q->heads[k], q->dtype, q))
+        return fail(MUON_ERR_INVALID_ARG, "output of %s overlaps the input of %s (only the same view is allowed)", kQ[i], kQ[k]);
+      if (backward && !(same && same_view(q->y[i], q->g[k], q, q->heads[i])) &&
+          may_meet(q->y[i], q->heads[i], q->g[k], q->heads[k], q->dtype, q))
+        return fail(MUON_ERR_INVALID_ARG, "output of %s overlaps the gradient of %s (only the same view is allowed)", kQ[i], kQ[k]);
+    }
+  }
+  if (q->heads[0] && q->heads[1] && may_meet(q->y[0], q->heads[0], q->y[1], q->heads[1], q->dtype, q))
+    return fail(MUON_ERR_INVALID_ARG, "outputs of q and k overlap");
+  return MUON_OK;
+}
+
+// Launch geometry of one call: chunk size, tokens per wave item, row parts,
+// workgroups.  It depends on the problem only, so results do too.
+struct QkPlan { int vec, tw, parts, blocks; };
+
+QkPlan plan_qk(const muon_qk_problem* q, bool backward, bool norm) {
+  QkPlan P{1, 1, 1, 1};
+  const int64_t tokens = q->batch * q->tokens;
+  // Largest chunk that divides the head and its rotated part in pairs and
+  // whose every access is aligned (16 bytes at most per access).
+  for (int vec : {8, 4, 2}) {
+    if (q->dim % (2 * vec) || q->rotary_dim % (2 * vec) || q->dim / (2 * vec) > 32) continue;
+    const int64_t al = std::min<int64_t>(16, vec * esize(q->dtype));
+    bool good = true;
+    auto look = [&](const muon_heads& t, int64_t heads) {
+      if (!heads) return;
+      const int64_t e = esize(q->dtype);
+      good &= (uintptr_t)t.p % al == 0 && (q->batch <= 1 || t.batch_stride * e % al == 0) &&
+              (q->tokens <= 1 || t.token_stride * e % al == 0) && (heads <= 1 || t.head_stride * e % al == 0);
+    };
+    for (int i = 0; i < 2; ++i) {
+      if (!(backward && !norm)) look(q->x[i], q->heads[i]);
+      if (backward) look(q->g[i], q->heads[i]);
+      look(q->y[i], q->heads[i]);
+    }
+    if (good) { P.vec = vec; break; }
+  }
+  const bool sums = backward && norm;
+  if (P.vec == 1) {
+    P.blocks = (int)std::min<int64_t>(tokens, sums ? 1024 : 65536);
+    return P;
+  }
+  const int nch = q->dim / (2 * P.vec);
+  int lpr = 4;
+  while (lpr < nch) lpr *= 2;
+  const int rpw = 64 / lpr;
+  int hmin = 65537, hmax = 0;
+  for (int i = 0; i < 2; ++i)
+    if (q->heads[i]) { hmin = std::min(hmin, q->heads[i]); hmax = std::max(hmax, q->heads[i]); }
+  P.tw = std::max(1, std::min(8, rpw / hmin));
+  if (q->rotary_dim) P.tw = std::min(P.tw, 512 / (q->rotary_dim / 2));
+  const int64_t groups = cdiv(tokens, P.tw);
+  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv((int64_t)P.tw * hmax, rpw), 2048 / groups));
+  P.blocks = (int)std::min<int64_t>(cdiv(groups * P.parts, 4), sums ? 1024 : 8192);
+  return P;
+}
+
+size_t qk_partial_bytes(const muon_qk_problem* q, const QkPlan& P) {
+  return align256((size_t)P.blocks * 2 * q->dim * 4);
+}
+
+int run_qk(const muon_qk_problem* q, int mode, float sign, void* workspace, hipStream_t s) {
+  const bool backward = sign < 0 || mode == 2;
+  const QkPlan P = plan_qk(q, backward, mode != 0);
+  QkParams p{};
+  for (int i = 0; i < 2; ++i) {
+    auto conv = [](const muon_heads& t) { return QkTensor{t.p, t.batch_stride, t.token_stride, t.head_stride}; };
+    p.x[i] = conv(mode == 0 && backward ? q->g[i] : q->x[i]);
+    p.g[i] = conv(q->g[i]);
+    p.y[i] = conv(q->y[i]);
+    p.heads[i] = q->heads[i];
+    p.w[i] = mode ? q->weight[i] : nullptr;
+  }
+  p.w_dtype = q->weight_dtype;
+  p.seq = q->tokens; p.tokens = q->batch * q->tokens;
+  p.dim = q->dim; p.rot = q->rotary_dim;
+  p.pos = q->positions; p.pos_i64 = q->positions_i64;
+  p.pos_sa = q->pos_axis_stride; p.pos_sb = q->pos_batch_stride; p.pos_st = q->pos_token_stride;
+  p.inv_freq = q->inv_freq; p.inv_freq_f64 = q->inv_freq_f64;
+  p.scale = q->scale; p.sign = sign; p.eps = q->eps;
+  p.partial = (float*)workspace;
+  p.tw = P.tw; p.parts = P.parts; p.blocks = P.blocks;
+  for (int i = 0; i < q->rotary_dim / 2; ++i) p.axis[i] = q->axis[i];
+  hipError_t e = launch_qk(p, mode, q->dtype == MUON_BF16, q->interleaved != 0, P.vec, s);
+  if (e != hipSuccess) return hip_fail(e, "norm and rotation kernel");
+  if (mode == 2 && (q->dweight[0] || q->dweight[1])) {
+    e = launch_qk_weight_sum(p, q->dweight, q->weight_dtype, s);
+    if (e != hipSuccess) return hip_fail(e, "norm weight gradients");
+  }
+  return ok();
+}
+
+bool qk_empty(const muon_qk_problem* q) {
+  return q->batch == 0 || q->tokens == 0 || (q->heads[0] == 0 && q->heads[1] == 0);
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_qk_norm_rope(const muon_qk_problem* q, void* stream) {
+  int rc = check_qk(q, false, true);
+  if (rc) return rc;
+  return qk_empty(q) ? ok() : run_qk(q, 1, 1.f, nullptr, (hipStream_t)stream);
+}
+
+int muon_rope(const muon_qk_problem* q, void* stream) {
+  int rc = check_qk(q, false, false);
+  if (rc) return rc;
+  return qk_empty(q) ? ok() : run_qk(q, 0, 1.f, nullptr, (hipStream_t)stream);
+}
+
+int muon_rope_backward(const muon_qk_problem* q, void* stream) {
+  int rc = check_qk(q, true, false);
+  if (rc) return rc;
+  return qk_empty(q) ? ok() : run_qk(q, 0, -1.f, nullptr, (hipStream_t)stream);
+}
+
+int muon_qk_norm_rope_backward_workspace_bytes(const muon_qk_problem* q, size_t* bytes) {
+  if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+  int rc = check_qk(q, true, true);
+  if (rc) return rc;
+  *bytes = qk_empty(q) ? 0 : qk_partial_bytes(q, plan_qk(q, true, true));
+  return ok();
+}
+
+int muon_qk_norm_rope_backward(const muon_qk_problem* q, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_qk(q, true, true);
+  if (rc) return rc;
+  for (int i = 0; i < 2; ++i)
+    if (q->dweight[i] && (uintptr_t)q->dweight[i] % esize(q->weight_dtype))
+      return fail(MUON_ERR_INVALID_ARG, "dweight of %s is not aligned to its element size", kQ[i]);
+  if (qk_empty(q)) return ok();
+  if ((rc = check_workspace(workspace, workspace_bytes, qk_partial_bytes(q, plan_qk(q, true, true))))) return rc;
+  return run_qk(q, 2, -1.f, workspace, (hipStream_t)stream);
+}
+
+}  // extern "C"

@@ -16,6 +16,7 @@
 #include <string>
 #include <vector>
 
+#include "layer_internal.h"
 #include "muon_internal.h"
 #include "muon_mi355x.h"
 
@@ -24,6 +25,18 @@ using namespace muon;
 namespace {
 
 thread_local std::string g_err;
+
+}  // namespace
+
+int muon::report(int code, const char* msg) noexcept {
+  try {
+    g_err = msg;
+  } catch (...) {  // out of memory: the code alone
+  }
+  return code;
+}
+
+namespace {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];

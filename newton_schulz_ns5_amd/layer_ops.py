@@ -1,0 +1,465 @@
+"""Layer operators: the linear product with bias, activation and residual, the
+per-head norms of queries and keys with the position rotation, the rotation
+alone, and the gradients of each.
+
+Thin marshalling like the rest of the binding: shapes and strides in, raw
+pointers to the library, work enqueued on the current stream.  ``linear``,
+``qk_norm_rope`` and ``rope`` record themselves for autograd when an input
+requires a gradient; the ``*_backward`` entry points are the same gradients
+called directly.
+"""
+import ctypes
+
+import torch
+
+from . import MuonError, _dt, _lib
+from ._lib import LinearGrad, LinearProblem, QkProblem
+
+__all__ = ["linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward",
+           "ACTIVATIONS"]
+
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+
+
+def _bad(text):
+    raise MuonError(_lib.MUON_ERR_INVALID_ARG, text)
+
+
+def _act(name):
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"activation {name!r} is not one of {sorted(filter(None, ACTIVATIONS))}")
+
+
+def _same_device(first, *others):
+    dev = first.device
+    if dev.type != "cuda":
+        _bad(f"tensors must be on a GPU, got {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            _bad(f"tensors are on {t.device} and {dev}")
+    return dev
+
+
+def _call(dev, fn, problem, need):
+    """Run fn(problem[, workspace]) on the device's current stream.  The device
+    is made current for the launch when another one is."""
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call_here(dev, fn, problem, need)
+    return _call_here(dev, fn, problem, need)
+
+
+def _call_here(dev, fn, problem, need):
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    p = ctypes.byref(problem)
+    if need is None:
+        return _lib.check(fn(p, stream))
+    size = ctypes.c_size_t(0)
+    _lib.check(need(p, ctypes.byref(size)))
+    if not size.value:
+        return _lib.check(fn(p, None, 0, stream))
+    # Taken from torch's allocator for this call: it goes back to the stream that
+    # runs the call, and one taken under capture belongs to that graph alone.
+    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    return _lib.check(fn(p, ws.data_ptr(), size.value, stream))
+
+
+# ---- the linear product ---------------------------------------------------------------
+def _rows(t, name, cols=None):
+    """(pointer, rows, columns, row stride) of a [..., columns] tensor seen as rows."""
+    if t.dim() < 1:
+        _bad(f"{name} needs at least one dimension")
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1]) if t.shape[-1] else \
+                t.new_empty((t.shape[:-1].numel(), 0))
+        except RuntimeError:
+            _bad(f"the leading dimensions of {name} cannot be seen as one")
+    r, c = t.shape
+    if cols is not None and c != cols:
+        _bad(f"{name} has {c} columns, not {cols}")
+    if r and c > 1 and t.stride(1) != 1:
+        _bad(f"{name} needs unit column stride")
+    return t.data_ptr(), r, c, (t.stride(0) if r > 1 and c else c)
+
+
+def _vector(t, name, n):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        _bad(f"{name} must be a contiguous [{n}] tensor")
+    return t.data_ptr()
+
+
+def _check_matrix(t, name, rows, cols):
+    p, r, c, ld = _rows(t, name)
+    if (r, c) != (rows, cols):
+        _bad(f"{name} is [{r}, {c}], not [{rows}, {cols}]")
+    return p, ld
+
+
+def _refuse_capture():
+    if torch.cuda.is_current_stream_capturing():
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED,
+                        "autograd is not recorded under stream capture: call the *_backward entry point there")
+
+
+def _wants_grad(*ts):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+
+
+def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=False, out=None, preact=None):
+    """``activation(x @ w.T + bias) + residual`` for x [..., k] and w [n, k] (see muon_linear).
+
+    ``activation`` is None, "relu", "relu2", "silu", "gelu" or "gelu_tanh".
+    The result has the residual's type, or x's without one, unless ``out`` is
+    given (``out`` may be the residual).  ``return_preact=True`` returns
+    (y, x @ w.T + bias), the second in x's type, which
+    :func:`linear_backward` takes when there is an activation.
+    """
+    if _wants_grad(x, w, bias, residual):
+        if out is not None or preact is not None:
+            _bad("out and preact cannot be given when an input requires a gradient")
+        _refuse_capture()
+        y, z = _Linear.apply(x, w, bias, residual, activation, return_preact)
+        return (y, z) if return_preact else y
+    return _linear(x, w, bias, residual, activation, return_preact, out, preact)
+
+
+def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=None):
+    act = _act(activation)
+    dev = _same_device(x, w, bias, residual, out, preact)
+    code = _dt(x)
+    if w.dtype != x.dtype:
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"x is {x.dtype} and w {w.dtype}: one type is needed")
+    if w.dim() != 2:
+        _bad("w must be [n, k]")
+    wp, n, k, ldw = _rows(w, "w")
+    xp, m, _, ldx = _rows(x, "x", k)
+    shape = x.shape[:-1] + (n,)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype if residual is None else residual.dtype, device=dev)
+    if (return_preact or preact is not None):
+        if preact is None:
+            preact = torch.empty(shape, dtype=x.dtype, device=dev)
+        elif preact.dtype != x.dtype:
+            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"preact must be {x.dtype} like x")
+    yp, ldy = _check_matrix(out, "out", m, n)
+    zp, ldz = _check_matrix(preact, "preact", m, n) if preact is not None else (None, 0)
+    rp, ldr = _check_matrix(residual, "residual", m, n) if residual is not None else (None, 0)
+    bp = _vector(bias, "bias", n) if bias is not None else None
+    prob = LinearProblem(m, n, k, code, act, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz,
+                         _dt(bias) if bias is not None else 0, _dt(residual) if residual is not None else 0, _dt(out), 0)
+    L = _lib.lib()
+    _call(dev, L.muon_linear, prob, L.muon_linear_workspace_bytes)
+    return (out, preact) if return_preact else out
+
+
+def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, need_dw=True, need_dbias=False,
+                    dw_dtype=None, dbias_dtype=None, dx=None, dw=None, dbias=None, accumulate=False):
+    """(dx, dw, dbias) of :func:`linear` for the gradient ``dy`` of its result (see
+    muon_linear_backward); None for those not asked for.  The residual's
+    gradient is dy itself.
+
+    ``preact`` is the pre-activation that linear returned (needed with an
+    activation).  ``dw_dtype`` and ``dbias_dtype`` default to w's type;
+    bf16 and fp32 are both what a step takes as a gradient.  Given outputs are
+    written in place, and with ``accumulate`` dw and dbias are added to.
+    """
+    act = _act(activation)
+    dev = _same_device(dy, x, w, preact, dx, dw, dbias)
+    code = _dt(x)
+    if w.dtype != x.dtype:
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"x is {x.dtype} and w {w.dtype}: one type is needed")
+    if w.dim() != 2:
+        _bad("w must be [n, k]")
+    wp, n, k, ldw = _rows(w, "w")
+    xp, m, _, ldx = _rows(x, "x", k)
+    gp, ldg = _check_matrix(dy, "dy", m, n)
+    zp, ldz = None, 0
+    if act:
+        if preact is None:
+            _bad("an activation's gradient needs preact")
+        if preact.dtype != x.dtype:
+            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"preact must be {x.dtype} like x")
+        zp, ldz = _check_matrix(preact, "preact", m, n)
+    if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
+        _bad("accumulate needs the tensors to add to")
+    if dx is None and need_dx:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if dw is None and need_dw:
+        dw = torch.empty((n, k), dtype=dw_dtype or w.dtype, device=dev)
+    if dbias is None and need_dbias:
+        dbias = torch.empty((n,), dtype=dbias_dtype or w.dtype, device=dev)
+    dxp, lddx = _check_matrix(dx, "dx", m, k) if dx is not None else (None, 0)
+    dwp, lddw = _check_matrix(dw, "dw", n, k) if dw is not None else (None, 0)
+    dbp = _vector(dbias, "dbias", n) if dbias is not None else None
+    prob = LinearGrad(m, n, k, code, act, gp, ldg, xp, ldx, wp, ldw, zp, ldz, dxp, lddx, dwp, lddw, dbp,
+                      _dt(dy), _dt(dx) if dx is not None else 0, _dt(dw) if dw is not None else 0,
+                      _dt(dbias) if dbias is not None else 0, int(bool(accumulate)), 0)
+    L = _lib.lib()
+    _call(dev, L.muon_linear_backward, prob, L.muon_linear_backward_workspace_bytes)
+    return dx, dw, dbias
+
+
+def _rowable(t):
+    """t as rows of unit column stride (autograd may hand over expanded or transposed gradients)."""
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+        return t
+    return t.contiguous()
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, activation, return_preact):
+        keep = _act(activation) != 0
+        r = _linear(x, w, bias, residual, activation, keep or return_preact)
+        y, z = r if keep or return_preact else (r, None)
+        ctx.save_for_backward(x, w, z if keep else None)
+        ctx.activation = activation
+        ctx.bias_dtype = bias.dtype if bias is not None else None
+        ctx.set_materialize_grads(False)
+        if z is not None:
+            ctx.mark_non_differentiable(z)
+        return y, z
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, _):
+        if dy is None:
+            return (None,) * 6
+        _refuse_capture()
+        x, w, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if need[0] or need[1] or need[2]:
+            dx, dw, db = linear_backward(_rowable(dy), x, w, activation=ctx.activation, preact=z, need_dx=need[0],
+                                         need_dw=need[1], need_dbias=need[2], dbias_dtype=ctx.bias_dtype)
+        return dx, dw, db, (dy if need[3] else None), None, None
+
+
+# ---- per-head norms and rotation ----------------------------------------------------------
+_NO_HEADS = (None, 0, 0, 0)
+
+
+def _heads_of(t, name, like=None):
+    """(pointer, batch, token, head stride) of a [tokens, heads, dim] or [batch, tokens, heads, dim] tensor."""
+    if t is None:
+        return _NO_HEADS
+    if like is not None and t.shape != like.shape:
+        _bad(f"{name} is {tuple(t.shape)}, not {tuple(like.shape)}")
+    if t.dim() not in (3, 4):
+        _bad(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    st = t.stride()
+    if t.shape[-1] > 1 and t.numel() and st[-1] != 1:
+        _bad(f"{name} needs unit stride in its last dimension")
+    return t.data_ptr(), (st[0] if t.dim() == 4 else 0), st[-3], st[-2]
+
+
+def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x, g, y, weight, dweight, eps):
+    """The problem of one call; q and k (either may be None) give the shapes, x,
+    g and y are pairs of tensors or None."""
+    first = q if q is not None else k
+    if first is None:
+        _bad("q and k are both None")
+    if q is not None and k is not None:
+        if q.dim() != k.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+            _bad(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
+        if q.dtype != k.dtype:
+            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"q is {q.dtype} and k {k.dtype}: one type is needed")
+    if first.dim() not in (3, 4):
+        _bad("q and k must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    every = [t for pair in (x, g, y) if pair is not None for t in pair if t is not None]
+    wts = [t for pair in (weight, dweight) for t in pair if t is not None]
+    dev = _same_device(first, positions, inv_freq, *every, *wts)
+    for t in every:
+        if t.dtype != first.dtype:
+            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"head tensors are {t.dtype} and {first.dtype}: one type is needed")
+    batch, tokens = (first.shape[0], first.shape[1]) if first.dim() == 4 else (1, first.shape[0])
+    dim = first.shape[-1]
+    p = QkProblem()
+    p.batch, p.tokens, p.dim = batch, tokens, dim
+    p.heads[0] = q.shape[-2] if q is not None else 0
+    p.heads[1] = k.shape[-2] if k is not None else 0
+    p.dtype = _dt(first)
+    for field, pair in ((p.x, x), (p.g, g), (p.y, y)):
+        if pair is not None:
+            for i, like in ((0, q), (1, k)):
+                if (pair[i] is None) != (like is None):
+                    _bad("q and k must both be given, or both be left out, in every pair of tensors")
+                field[i] = _heads_of(pair[i], "qk"[i], like)
+    for i in range(2):
+        if weight[i] is not None:
+            p.weight[i] = _vector(weight[i], f"the norm weight of {'qk'[i]}", dim)
+        if dweight[i] is not None:
+            p.dweight[i] = _vector(dweight[i], f"the weight gradient of {'qk'[i]}", dim)
+    if wts:
+        if any(t.dtype != wts[0].dtype for t in wts):
+            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "the norm weights and their gradients need one type")
+        p.weight_dtype = _dt(wts[0])
+    if inv_freq.dim() != 1 or inv_freq.dtype not in (torch.float32, torch.float64) or not inv_freq.is_contiguous():
+        _bad("inv_freq must be a contiguous fp32 or fp64 vector of one frequency per pair")
+    pairs = inv_freq.shape[0]
+    if 2 * pairs > dim or pairs > _lib.QK_MAX_PAIRS:
+        _bad(f"{pairs} pairs do not fit heads of {dim} (at most {_lib.QK_MAX_PAIRS})")
+    p.rotary_dim = 2 * pairs
+    p.inv_freq, p.inv_freq_f64 = inv_freq.data_ptr(), int(inv_freq.dtype == torch.float64)
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"positions are {positions.dtype}, not int32 or int64")
+    lead, shape, st = tuple(first.shape[:-2]), tuple(positions.shape), positions.stride()
+    p.axes = 1
+    if shape == lead:
+        p.pos_token_stride = st[-1]
+        p.pos_batch_stride = st[0] if len(lead) == 2 else 0
+    elif len(shape) == len(lead) + 1 and shape[1:] == lead:
+        p.axes, p.pos_axis_stride, p.pos_token_stride = shape[0], st[0], st[-1]
+        p.pos_batch_stride = st[1] if len(lead) == 2 else 0
+    elif len(lead) == 2 and shape == lead[1:]:
+        p.pos_token_stride = st[0]
+    else:
+        _bad(f"positions {shape} do not go with tokens {lead}")
+    p.positions, p.positions_i64 = positions.data_ptr(), int(positions.dtype == torch.int64)
+    if axes is not None and sections is not None:
+        _bad("give sections or axes, not both")
+    if sections is not None:
+        if len(sections) != p.axes or sum(sections) != pairs or min(sections) < 0:
+            _bad(f"sections {list(sections)} do not split {pairs} pairs over {p.axes} axes")
+        turns = b"".join(bytes((i,)) * n for i, n in enumerate(sections))
+    elif axes is not None:
+        turns = bytes(axes)
+        if len(turns) != pairs or (turns and max(turns) >= p.axes):
+            _bad(f"axes must name one of {p.axes} axes for each of {pairs} pairs")
+    elif p.axes > 1:
+        _bad("positions with several axes need sections or axes")
+    else:
+        turns = b""
+    if turns and p.axes > 1:
+        ctypes.memmove(p.axis, turns, len(turns))
+    p.interleaved, p.scale, p.eps = int(bool(interleaved)), float(scale), float(eps)
+    return dev, p
+
+
+def _like(t, out):
+    if out is not None:
+        return out
+    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6, sections=None, axes=None,
+                 interleaved=False, scale=1.0, q_out=None, k_out=None):
+    """RMS norm of every head of q and k, times its weight, then the position rotation (see muon_qk_norm_rope).
+
+    q and k are [tokens, heads, dim] or [batch, tokens, heads, dim] of any
+    strides with a contiguous head (views of packed q/k/v rows, heads-first
+    layouts); either may be None.  ``positions`` is [tokens] / [batch, tokens]
+    (int32 or int64), or has a leading dimension of up to four axes, and then
+    ``sections`` (pairs per axis, in order) or ``axes`` (one axis per pair)
+    says which pair turns by which.  ``inv_freq`` [rotary pairs] is fp32 or
+    fp64.  Returns (q_out, k_out); an output may be its own input.
+    """
+    if _wants_grad(q, k, q_weight, k_weight):
+        if q_out is not None or k_out is not None:
+            _bad("q_out and k_out cannot be given when an input requires a gradient")
+        _refuse_capture()
+        how = dict(eps=eps, sections=sections, axes=axes, interleaved=interleaved, scale=scale)
+        return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, how)
+    y = (_like(q, q_out), _like(k, k_out))
+    dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
+                         (q_weight, k_weight), (None, None), eps)
+    _call(dev, _lib.lib().muon_qk_norm_rope, p, None)
+    return y
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6,
+                          sections=None, axes=None, interleaved=False, scale=1.0, dq=None, dk=None):
+    """(dq, dk, dq_weight, dk_weight) of :func:`qk_norm_rope` for the gradients of its outputs; None for what
+    was not given.  dq may be dq_out, and dk dk_out."""
+    y = (_like(q, dq), _like(k, dk))
+    dwt = (_like(q_weight, None), _like(k_weight, None))
+    dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), (dq_out, dk_out), y,
+                         (q_weight, k_weight), dwt, eps)
+    if p.batch * p.tokens == 0:
+        for t in dwt:
+            if t is not None:
+                t.zero_()
+    L = _lib.lib()
+    _call(dev, L.muon_qk_norm_rope_backward, p, L.muon_qk_norm_rope_backward_workspace_bytes)
+    return y + dwt
+
+
+def rope(q, k, positions, inv_freq, *, sections=None, axes=None, interleaved=False, scale=1.0, q_out=None, k_out=None):
+    """The position rotation of :func:`qk_norm_rope` without its norm (see muon_rope)."""
+    if _wants_grad(q, k):
+        if q_out is not None or k_out is not None:
+            _bad("q_out and k_out cannot be given when an input requires a gradient")
+        _refuse_capture()
+        how = dict(sections=sections, axes=axes, interleaved=interleaved, scale=scale)
+        return _Rope.apply(q, k, positions, inv_freq, how)
+    y = (_like(q, q_out), _like(k, k_out))
+    dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
+                         (None, None), (None, None), 0.0)
+    _call(dev, _lib.lib().muon_rope, p, None)
+    return y
+
+
+def rope_backward(dq_out, dk_out, positions, inv_freq, *, sections=None, axes=None, interleaved=False, scale=1.0,
+                  dq=None, dk=None):
+    """(dq, dk) of :func:`rope`: the rotation by the opposite angles.  dq may be dq_out, and dk dk_out."""
+    y = (_like(dq_out, dq), _like(dk_out, dk))
+    dev, p = _qk_problem(dq_out, dk_out, positions, inv_freq, sections, axes, interleaved, scale, None,
+                         (dq_out, dk_out), y, (None, None), (None, None), 0.0)
+    _call(dev, _lib.lib().muon_rope_backward, p, None)
+    return y
+
+
+def _head_grad(g, like):
+    """A gradient of a head tensor, zeros where autograd has none."""
+    if like is None:
+        return None
+    if g is None:
+        return torch.zeros(like.shape, dtype=like.dtype, device=like.device)
+    return g if g.shape[-1] <= 1 or g.stride(-1) == 1 else g.contiguous()
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, how):
+        y = qk_norm_rope(q, k, positions, inv_freq, q_weight=q_weight, k_weight=k_weight, **how)
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.how = how
+        ctx.set_materialize_grads(False)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk):
+        if gq is None and gk is None:
+            return (None,) * 7
+        _refuse_capture()
+        q, k, wq, wk, positions, inv_freq = ctx.saved_tensors
+        grads = qk_norm_rope_backward(_head_grad(gq, q), _head_grad(gk, k), q, k, positions, inv_freq, q_weight=wq,
+                                      k_weight=wk, **ctx.how)
+        return tuple(t if n else None for t, n in zip(grads, ctx.needs_input_grad)) + (None, None, None)
+
+
+class _Rope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, how):
+        y = rope(q, k, positions, inv_freq, **how)
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.like = [None if t is None else (t.shape, t.dtype, t.device) for t in (q, k)]
+        ctx.how = how
+        ctx.set_materialize_grads(False)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk):
+        _refuse_capture()
+        positions, inv_freq = ctx.saved_tensors
+        # a gradient that autograd does not have is left out of the call
+        gs = [None if g is None else (g if g.shape[-1] <= 1 or g.stride(-1) == 1 else g.contiguous()) for g in (gq, gk)]
+        if gs[0] is None and gs[1] is None:
+            return (None,) * 5
+        dq, dk = rope_backward(gs[0], gs[1], positions, inv_freq, **ctx.how)
+        return dq, dk, None, None, None

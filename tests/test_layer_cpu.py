@@ -1,0 +1,197 @@
+"""Layer operators without a GPU: the C structures, and every refusal reported
+before anything is enqueued."""
+import ctypes
+import os
+import subprocess
+import tempfile
+
+import pytest
+import torch
+
+import newton_schulz_ns5_amd as ns
+from newton_schulz_ns5_amd import _lib
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 30  # a non-null, aligned address that is never dereferenced
+MIB = 1 << 20
+
+STRUCTS = [("muon_linear_problem", _lib.LinearProblem), ("muon_linear_grad", _lib.LinearGrad),
+           ("muon_heads", _lib.Heads), ("muon_qk_problem", _lib.QkProblem)]
+
+
+def test_ctypes_structs_match_c_layout():
+    lines = []
+    for c, py in STRUCTS:
+        lines.append(f'printf("{c} %zu\\n", sizeof({c}));')
+        lines += [f'printf("{c}.{f} %zu\\n", offsetof({c}, {f}));' for f, _ in py._fields_]
+    src = '#include <stdio.h>\n#include <stddef.h>\n#include "muon_mi355x.h"\nint main(void) {' + "\n".join(lines) + "return 0; }"
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "l.c"), os.path.join(d, "l")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), c, "-o", exe], check=True)
+        lay = dict(x.split() for x in subprocess.run([exe], check=True, capture_output=True, text=True).stdout.splitlines())
+    for c, py in STRUCTS:
+        assert ctypes.sizeof(py) == int(lay[c]), c
+        for f, _ in py._fields_:
+            assert getattr(py, f).offset == int(lay[f"{c}.{f}"]), (c, f)
+
+
+def linear_problem(**over):
+    a = dict(m=8, n=16, k=32, dtype=1, activation=0, x=FAKE, x_row_stride=32, w=FAKE + MIB, w_row_stride=32, bias=None,
+             residual=None, residual_row_stride=16, y=FAKE + 2 * MIB, y_row_stride=16, preact=None, preact_row_stride=16,
+             bias_dtype=1, residual_dtype=1, y_dtype=1, reserved=0)
+    a.update(over)
+    p = _lib.LinearProblem()
+    for k, v in a.items():
+        setattr(p, k, v)
+    return p
+
+
+Y = FAKE + 2 * MIB
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(m=-1), -1), (dict(n=-1), -1), (dict(k=-1), -1), (dict(x=None), -1), (dict(w=None), -1), (dict(y=None), -1),
+    (dict(x_row_stride=31), -1), (dict(w_row_stride=31), -1), (dict(y_row_stride=15), -1),
+    (dict(dtype=2), -2), (dict(y_dtype=7), -2), (dict(bias=FAKE + 3 * MIB, bias_dtype=5), -2),
+    (dict(residual=FAKE + 3 * MIB, residual_dtype=-1), -2), (dict(activation=6), -2), (dict(activation=-1), -2),
+    (dict(x=FAKE + 1), -1), (dict(y=FAKE + 2 * MIB + 2, y_dtype=0), -1), (dict(m=(1 << 30) + 1), -1),
+    (dict(x_row_stride=1 << 22), -1), (dict(reserved=1), -1),
+    (dict(y=FAKE), -1), (dict(y=FAKE + MIB), -1), (dict(preact=Y), -1), (dict(preact=FAKE), -1),
+    (dict(residual=Y + 2), -1), (dict(residual=Y, residual_dtype=0), -1), (dict(residual=Y, residual_row_stride=32), -1),
+    (dict(preact=FAKE + 3 * MIB, residual=FAKE + 3 * MIB), -1),
+])
+def test_linear_refusals(over, code):
+    L = _lib.lib()
+    p = linear_problem(**over)
+    assert L.muon_linear(ctypes.byref(p), FAKE, 1 << 40, None) == code
+    assert L.muon_last_error()
+
+
+def test_linear_null_problem_and_empty_calls():
+    L = _lib.lib()
+    assert L.muon_linear(None, FAKE, 0, None) == -1
+    assert L.muon_linear_workspace_bytes(None, None) == -1
+    for over in (dict(m=0, x=None, y=None), dict(n=0, w=None, y=None)):
+        p = linear_problem(**over)
+        assert L.muon_linear(ctypes.byref(p), None, 0, None) == 0  # nothing to enqueue
+
+
+def grad_problem(**over):
+    a = dict(m=8, n=16, k=32, dtype=1, activation=3, dy=FAKE, dy_row_stride=16, x=FAKE + MIB, x_row_stride=32,
+             w=FAKE + 2 * MIB, w_row_stride=32, preact=FAKE + 3 * MIB, preact_row_stride=16, dx=FAKE + 4 * MIB,
+             dx_row_stride=32, dw=FAKE + 5 * MIB, dw_row_stride=32, dbias=FAKE + 6 * MIB, dy_dtype=1, dx_dtype=1,
+             dw_dtype=0, dbias_dtype=0, accumulate=0, reserved=0)
+    a.update(over)
+    p = _lib.LinearGrad()
+    for k, v in a.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(m=-1), -1), (dict(dy=None), -1), (dict(x=None), -1), (dict(w=None), -1), (dict(preact=None), -1),
+    (dict(dy_row_stride=3), -1), (dict(dw_row_stride=31), -1), (dict(dtype=4), -2), (dict(dw_dtype=9), -2),
+    (dict(dy_dtype=3), -2), (dict(activation=17), -2), (dict(accumulate=2), -1), (dict(reserved=3), -1),
+    (dict(dx=FAKE), -1), (dict(dw=FAKE + MIB), -1), (dict(dbias=FAKE + 5 * MIB), -1), (dict(dx=FAKE + 3 * MIB), -1),
+    (dict(dx=FAKE + 2 * MIB), -1),
+])
+def test_linear_backward_refusals(over, code):
+    L = _lib.lib()
+    p = grad_problem(**over)
+    assert L.muon_linear_backward(ctypes.byref(p), FAKE, 1 << 40, None) == code
+    assert L.muon_last_error()
+
+
+def test_linear_backward_workspace():
+    L = _lib.lib()
+    p = grad_problem()
+    need = ctypes.c_size_t()
+    assert L.muon_linear_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0 and need.value > 0
+    assert L.muon_linear_backward(ctypes.byref(p), FAKE, need.value - 1, None) == -3
+    assert L.muon_linear_backward(ctypes.byref(p), FAKE + 16, need.value, None) == -1
+    assert L.muon_linear_backward(ctypes.byref(p), None, need.value, None) == -1
+
+
+def qk_problem(**over):
+    p = _lib.QkProblem()
+    a = dict(batch=1, tokens=5, dim=64, rotary_dim=64, dtype=1, weight_dtype=1, positions=FAKE, pos_token_stride=1,
+             inv_freq=FAKE + MIB, positions_i64=1, inv_freq_f64=1, axes=1, scale=1.0, eps=1e-6)
+    hq, hk = over.pop("heads", (4, 2))
+    p.heads[0], p.heads[1] = hq, hk
+    # packed rows of q, k and v heads
+    row = (hq + 2 * hk) * 64
+    x = over.pop("x", (FAKE + 2 * MIB, FAKE + 2 * MIB + hq * 128))
+    y = over.pop("y", x)
+    for i in range(2):
+        p.x[i] = p.g[i] = _lib.Heads(x[i], 0, row, 64)
+        p.y[i] = _lib.Heads(y[i], 0, row, 64)
+    a.update(over)
+    for k, v in a.items():
+        setattr(p, k, v)
+    return p
+
+
+QKV = FAKE + 2 * MIB
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(batch=-1), -1), (dict(tokens=-2), -1), (dict(dim=0), -1), (dict(dim=1025), -1), (dict(rotary_dim=63), -1),
+    (dict(rotary_dim=66), -1), (dict(axes=0), -1), (dict(axes=5), -1), (dict(dtype=2), -2), (dict(weight_dtype=3), -2),
+    (dict(scale=float("inf")), -1), (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(heads=(-1, 2)), -1),
+    (dict(positions=None), -1), (dict(inv_freq=None), -1), (dict(inv_freq=FAKE + 4), -1), (dict(pos_token_stride=-1), -1),
+    (dict(x=(None, QKV)), -1), (dict(x=(QKV + 1, QKV + 512)), -1),
+    (dict(y=(QKV, QKV)), -1),              # k's output over q's input
+    (dict(y=(QKV + 2, QKV + 512)), -1),    # shifted in place
+    (dict(y=(QKV + MIB, QKV + MIB)), -1),  # both outputs in one place
+    (dict(tokens=(1 << 30) + 1), -1),
+])
+def test_qk_refusals(over, code):
+    L = _lib.lib()
+    p = qk_problem(**over)
+    assert L.muon_qk_norm_rope(ctypes.byref(p), None) == code
+    assert L.muon_last_error()
+    assert L.muon_qk_norm_rope_backward(ctypes.byref(p), FAKE, 1 << 40, None) == code
+
+
+def test_qk_axis_out_of_range_and_null():
+    L = _lib.lib()
+    p = qk_problem(axes=2)
+    p.axis[31] = 2
+    assert L.muon_rope(ctypes.byref(p), None) == -1 and b"pair 31" in L.muon_last_error()
+    assert L.muon_qk_norm_rope(None, None) == -1 and L.muon_rope_backward(None, None) == -1
+
+
+def test_qk_empty_calls_and_workspace():
+    L = _lib.lib()
+    for over in (dict(tokens=0), dict(batch=0), dict(heads=(0, 0))):
+        p = qk_problem(**over)
+        assert L.muon_qk_norm_rope(ctypes.byref(p), None) == 0
+        assert L.muon_rope(ctypes.byref(p), None) == 0
+    p = qk_problem()
+    need = ctypes.c_size_t()
+    assert L.muon_qk_norm_rope_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0 and need.value
+    assert L.muon_qk_norm_rope_backward(ctypes.byref(p), FAKE, need.value - 1, None) == -3
+
+
+def test_qk_output_that_overlaps_itself():
+    L = _lib.lib()
+    p = qk_problem()
+    p.y[0] = _lib.Heads(FAKE + 8 * MIB, 0, 64, 64)  # every token's heads run into the next token's
+    assert L.muon_qk_norm_rope(ctypes.byref(p), None) == -1 and b"itself" in L.muon_last_error()
+
+
+def code_of(f):
+    with pytest.raises(ns.MuonError) as e:
+        f()
+    return e.value.status
+
+
+def test_python_refusals():
+    x, w = torch.zeros(4, 8), torch.zeros(16, 8)
+    assert code_of(lambda: ns.linear(x, w)) == -1                          # not on a GPU
+    assert code_of(lambda: ns.linear(x, w, activation="swish")) == -2
+    q = torch.zeros(4, 2, 8)
+    pos, f = torch.zeros(4, dtype=torch.int64), torch.ones(4)
+    assert code_of(lambda: ns.qk_norm_rope(q, q, pos, f)) == -1
+    assert code_of(lambda: ns.rope(None, None, pos, f)) == -1
