@@ -362,7 +362,7 @@ typedef struct muon_linear_problem {
  * at for their alignment only). */
 int muon_linear_workspace_bytes(const muon_linear_problem* p, size_t* bytes);
 /* Errors: MUON_ERR_INVALID_ARG (null pointers, negative or too large sizes,
- * strides below the columns or of 2^23 bytes and more, misaligned or
+ * strides below the columns or above 2^23 - 32 bytes, misaligned or
  * overlapping tensors), MUON_ERR_UNSUPPORTED (types, activation),
  * MUON_ERR_WORKSPACE, MUON_ERR_HIP. */
 int muon_linear(const muon_linear_problem* p, void* workspace, size_t workspace_bytes, void* stream);

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuon_mi355x.so")
 SOURCES = ["gemm_bf16.hip", "gemm_f32.hip", "elementwise.hip", "poly_small.hip", "update_gram128.hip",
-           "muon_host.hip", "linear_simple.hip", "act_grad.hip", "qk_norm_rope.hip", "layer_host.hip"]
+           "muon_host.hip", "linear_tiles.hip", "linear_small.hip", "act_grad.hip", "qk_norm_rope.hip", "layer_host.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-mcode-object-version=5", "-O3", "-std=c++17", "-fPIC",

@@ -7,51 +7,12 @@
 // are added in order through LDS, so a column's sum is added in an order that
 // depends on the sizes only.
 #include "layer_internal.h"
-#include "layer_math.h"
+#include "linear_epilogue.h"
 
 namespace muon {
 namespace {
 
 constexpr int CW = 256;  // columns per workgroup
-
-// 8 consecutive elements as fp32, the first `valid` of them when not `vec`.
-__device__ __forceinline__ void get8(const void* base, int64_t idx, bool bf, bool vec, int valid, float (&v)[8]) {
-  if (vec && valid >= 8) {
-    if (bf) {
-      const u32x4 a = *(const u32x4*)((const uint16_t*)base + idx);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        v[2 * w] = __uint_as_float(a[w] << 16);
-        v[2 * w + 1] = __uint_as_float(a[w] & 0xffff0000u);
-      }
-    } else {
-      const f32x4 a = *(const f32x4*)((const float*)base + idx), b = *(const f32x4*)((const float*)base + idx + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[4 + e] = b[e]; }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < valid ? load_elem(base, idx + e, bf) : 0.f;
-  }
-}
-
-__device__ __forceinline__ void put8(void* base, int64_t idx, bool bf, bool vec, int valid, const float (&v)[8]) {
-  if (vec && valid >= 8) {
-    if (bf) {
-      u32x4 a;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) a[w] = pack_bf2(v[2 * w], v[2 * w + 1]);
-      *(u32x4*)((uint16_t*)base + idx) = a;
-    } else {
-      *(f32x4*)((float*)base + idx) = f32x4{v[0], v[1], v[2], v[3]};
-      *(f32x4*)((float*)base + idx + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < valid) store_elem(base, idx + e, v[e], bf);
-  }
-}
 
 template <bool BF>
 __global__ __launch_bounds__(256) void act_grad_kernel(const ActGrad p) {
@@ -78,7 +39,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGrad p) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(z[e]);
         }
-        if (p.G) put8(p.G, i * p.ldg + j, BF, vec, valid, g);
+        if (p.G) put8(p.G, i * p.ldg + j, BF, true, 8, g);  // values past N are zero
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += g[e];
       }

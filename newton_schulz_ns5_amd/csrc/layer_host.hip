@@ -61,9 +61,10 @@ bool meet(const Rows& a, const Rows& b) {
 }
 
 // ---- the linear product -------------------------------------------------------------
-// Dimensions stay below 2^30 and a row stride below 2^23 bytes, so that a
-// tile's panel of rows is addressed with 32-bit offsets.
-constexpr int64_t kMaxSize = (int64_t)1 << 30, kMaxRowBytes = ((int64_t)1 << 23) - 1;
+// Dimensions stay below 2^30 and a row stride (rounded up to 32 bytes, as
+// copies are) below 2^23 bytes, so that a tile's panel of rows is addressed
+// with 32-bit offsets.
+constexpr int64_t kMaxSize = (int64_t)1 << 30, kMaxRowBytes = ((int64_t)1 << 23) - 32;
 
 int check_sizes(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n < 0 || k < 0) return fail(MUON_ERR_INVALID_ARG, "negative size (m=%lld n=%lld k=%lld)", (long long)m, (long long)n, (long long)k);
@@ -80,7 +81,7 @@ int check_matrix(const char* name, const void* p, int32_t dt, int64_t rows, int6
   if (!p) return fail(MUON_ERR_INVALID_ARG, "%s is NULL", name);
   if (ld < cols && rows > 1) return fail(MUON_ERR_INVALID_ARG, "%s row stride %lld is smaller than its %lld columns", name, (long long)ld, (long long)cols);
   if (cols * esize(dt) > kMaxRowBytes || (rows > 1 && ld * esize(dt) > kMaxRowBytes))
-    return fail(MUON_ERR_INVALID_ARG, "%s rows must be less than 2^23 bytes apart", name);
+    return fail(MUON_ERR_INVALID_ARG, "%s rows must be at most 2^23 - 32 bytes apart", name);
   if ((uintptr_t)p % esize(dt)) return fail(MUON_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
   return MUON_OK;
 }
@@ -148,40 +149,192 @@ int check_linear_grad(const muon_linear_grad* q) {
   return MUON_OK;
 }
 
-// Work of a gradient call: the elementwise pass runs when the gradient at the
+bool rows16(const void* p, int64_t ld, int32_t dt) {
+  return ((uintptr_t)p & 15) == 0 && (ld * esize(dt)) % 16 == 0;
+}
+
+// Elements per 16 bytes.
+int64_t per16(int32_t dt) { return 16 / esize(dt); }
+
+// An operand of a product: a [rows][cols] matrix, used in place where the
+// tiled kernels can load it (16-byte aligned rows, whole 16-byte chunks of K
+// in a row operand), else copied into the workspace with zeros behind its
+// rows (one read and one write of it, against the product's many).
+struct Operand {
+  const void* p;
+  int64_t rows, cols, ld;
+  bool pack;
+  size_t off;  // of the copy in the workspace
+};
+
+Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dt, bool row_kind) {
+  Operand o{p, rows, cols, ld, false, 0};
+  if (rows <= 1) o.ld = cdiv(cols, per16(dt)) * per16(dt);  // a single row's stride means nothing
+  o.pack = ((uintptr_t)p & 15) || (o.ld % per16(dt)) || (row_kind && cols % per16(dt));
+  return o;
+}
+
+// How a product M x N over K runs: tile edge and chunks of the sum.
+//
+// Each workgroup of a tile edge costs its slices of K times that edge's time
+// per slice, and the chip holds so many of them at once; a split sum shortens
+// the slices per workgroup where there are too few tiles to fill the chip, and
+// pays for storing and adding the chunks' fp32 products.  The estimate below
+// compares the candidates in microseconds.
+struct Tiling { int tile, split; };
+
+Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
+  // Edge, workgroups on the chip at once (256 CUs), microseconds per slice with
+  // the chip full.
+  struct Edge { int bt, slots; double us; };
+  static const Edge bf_edges[] = {{256, 256, 1.45}, {128, 512, 0.85}, {64, 1024, 0.55}};
+  static const Edge f32_edges[] = {{128, 512, 6.0}, {64, 1024, 3.2}};
+  const Edge* edges = bf ? bf_edges : f32_edges;
+  const int n = bf ? 3 : 2;
+  const int64_t slices = std::max<int64_t>(1, cdiv(K, bf ? 64 : 32));
+  Tiling best{64, 1};
+  double least = 1e30;
+  for (int i = 0; i < n; ++i) {
+    const int64_t tiles = cdiv(M, edges[i].bt) * cdiv(N, edges[i].bt);
+    for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (split > 1 && (split > slices / 4 || tiles * split > 4 * edges[i].slots)) break;
+      const double rounds = (double)cdiv(tiles * split, edges[i].slots);
+      // fixed cost of a workgroup: pipeline start and epilogue, about 4 slices
+      double t = rounds * (double)(cdiv(slices, split) + 4) * edges[i].us;
+      if (split > 1) t += 3.0 + (double)(M * N) * 4.0 * (split + 1) / 4e6;  // a launch, and the products at 4 TB/s
+      if (t < least) {
+        least = t;
+        best = {edges[i].bt, split};
+      }
+    }
+  }
+  return best;
+}
+
+int64_t part_ld(int64_t N) { return cdiv(N, 8) * 8; }
+size_t part_bytes(int64_t M, int64_t N, int split) {
+  return split > 1 ? align256((size_t)split * (size_t)M * (size_t)part_ld(N) * 4) : 0;
+}
+
+// Pack launches of the operands that need one, two per launch.
+hipError_t pack_all(Operand* const* ops, int n, int32_t dt, char* ws, hipStream_t s) {
+  PackJobs jobs{};
+  for (int i = 0; i < n; ++i) {
+    Operand& o = *ops[i];
+    if (o.pack) {
+      const int64_t ld = cdiv(o.cols, per16(dt)) * per16(dt);
+      jobs.job[jobs.n++] = PackJob{o.p, o.ld, ws + o.off, ld, o.rows, o.cols};
+      o.p = ws + o.off;
+      o.ld = ld;
+    }
+    if (jobs.n == 2 || (i == n - 1 && jobs.n)) {
+      const hipError_t e = launch_pack(jobs, dt == MUON_BF16, s);
+      if (e != hipSuccess) return e;
+      jobs.n = 0;
+    }
+  }
+  return hipSuccess;
+}
+
+size_t pack_bytes(const Operand& o, int32_t dt) {
+  return o.pack ? align256((size_t)(o.rows * cdiv(o.cols, per16(dt)) * 16)) : 0;
+}
+
+hipError_t run_product(LinGemm g, int32_t dt, LinKind kind, const Tiling& t, char* part, hipStream_t s) {
+  const bool bf = dt == MUON_BF16;
+  g.Kcol = g.K;
+  // a row operand whose K is not whole chunks is a copy with zeros behind K
+  if (kind != kColCol) g.K = cdiv(g.K, per16(dt)) * per16(dt);
+  g.split = t.split;
+  g.part = t.split > 1 ? (float*)part : nullptr;
+  g.ldpart = part_ld(g.N);
+  hipError_t e = launch_linear_tiles(g, bf, kind, t.tile, s);
+  if (e == hipSuccess && t.split > 1) e = launch_split_finish(g, bf, s);
+  return e;
+}
+
+int vec_flags(const LinGemm& g, int32_t dt) {
+  int v = 0;
+  if (g.bias && ((uintptr_t)g.bias & 15) == 0) v |= kVecBias;
+  if (g.add && rows16(g.add, g.ldadd, g.add_dtype)) v |= kVecAdd;
+  if (rows16(g.Y, g.ldy, g.y_dtype)) v |= kVecY;
+  if (g.Z && rows16(g.Z, g.ldz, dt)) v |= kVecZ;
+  return v;
+}
+
+// Work of a forward call: the small kernel for few rows, else tiles.
+struct LinearPlan {
+  bool small;
+  Operand x, w;
+  Tiling t;
+  size_t part_off, total;
+};
+
+LinearPlan plan_linear(const muon_linear_problem* q) {
+  LinearPlan P{};
+  P.small = q->m <= kSmallRows;
+  if (P.small || q->m == 0 || q->n == 0) return P;
+  P.x = operand(q->x, q->m, q->k, q->x_row_stride, q->dtype, true);
+  P.w = operand(q->w, q->n, q->k, q->w_row_stride, q->dtype, true);
+  P.t = choose_tiling(q->m, q->n, q->k, q->dtype == MUON_BF16);
+  size_t off = 0;
+  P.x.off = off; off += pack_bytes(P.x, q->dtype);
+  P.w.off = off; off += pack_bytes(P.w, q->dtype);
+  P.part_off = off; off += part_bytes(q->m, q->n, P.t.split);
+  P.total = off;
+  return P;
+}
+
+// Work of a gradient call.  The elementwise pass runs when the gradient at the
 // pre-activation differs from dy (an activation, or dy of another type than
-// the operands) or the bias gradient is wanted.
+// the operands), when dy's rows cannot be loaded in place, or when the bias
+// gradient is wanted.  The split sums of dx and dw use one region in turn.
 struct GradPlan {
   bool store_g, colsum;
   int64_t ldg;
   int chunks;
   int64_t rows_per;
-  size_t g_off, partial_off, total;
+  Operand x, w;
+  Tiling tx, tw;
+  size_t g_off, partial_off, part_off, total;
 };
 
 GradPlan plan_grad(const muon_linear_grad* q) {
   GradPlan P{};
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t at = off; off = align256(off + bytes); return at; };
-  if (q->m == 0 || q->n == 0) return P;
-  P.store_g = (q->dx || q->dw) && (q->activation != MUON_ACT_NONE || q->dy_dtype != q->dtype);
-  P.colsum = q->dbias != nullptr;
+  const bool dx = q->dx && q->m > 0 && q->k > 0, dw = q->dw && q->n > 0 && q->k > 0;
+  const Operand dy = operand(q->dy, q->m, q->n, q->dy_row_stride, q->dtype, dx);
+  P.store_g = q->m > 0 && q->n > 0 && (dx || dw) && (q->activation != MUON_ACT_NONE || q->dy_dtype != q->dtype || dy.pack);
+  P.colsum = q->dbias && q->n > 0;
   // Rows per workgroup of the elementwise pass: enough workgroups to fill the
   // chip (256 columns each), at least 32 rows so that partial sums stay few.
-  const int64_t cols = cdiv(q->n, 256);
+  const int64_t cols = std::max<int64_t>(1, cdiv(q->n, 256));
   const int64_t want = std::max<int64_t>(1, 2048 / cols);
   P.rows_per = std::max<int64_t>(32, cdiv(q->m, want));
-  P.rows_per = std::max<int64_t>(P.rows_per, cdiv(q->m, 4096));
   P.chunks = (int)cdiv(q->m, P.rows_per);
   P.ldg = cdiv(q->n, 8) * 8;
   if (P.store_g) P.g_off = take((size_t)(q->m * P.ldg * esize(q->dtype)));
   if (P.colsum) P.partial_off = take((size_t)P.chunks * (size_t)q->n * 4);
+  const bool bf = q->dtype == MUON_BF16;
+  size_t part = 0;
+  if (dx) {
+    P.w = operand(q->w, q->n, q->k, q->w_row_stride, q->dtype, false);
+    if (q->n == 0) { P.w.pack = false; P.w.p = nullptr; }  // an empty sum reads nothing
+    P.w.off = take(pack_bytes(P.w, q->dtype));
+    P.tx = choose_tiling(q->m, q->k, q->n, bf);
+    part = std::max(part, part_bytes(q->m, q->k, P.tx.split));
+  }
+  if (dw) {
+    P.x = operand(q->x, q->m, q->k, q->x_row_stride, q->dtype, false);
+    if (q->m == 0) { P.x.pack = false; P.x.p = nullptr; }
+    P.x.off = take(pack_bytes(P.x, q->dtype));
+    P.tw = choose_tiling(q->n, q->k, q->m, bf);
+    part = std::max(part, part_bytes(q->n, q->k, P.tw.split));
+  }
+  P.part_off = take(part);
   P.total = off;
   return P;
-}
-
-bool rows16(const void* p, int64_t ld, int32_t dt) {
-  return ((uintptr_t)p & 15) == 0 && (ld * esize(dt)) % 16 == 0;
 }
 
 }  // namespace
@@ -190,9 +343,9 @@ extern "C" {
 
 int muon_linear_workspace_bytes(const muon_linear_problem* q, size_t* bytes) {
   if (!q || !bytes) return fail(MUON_ERR_INVALID_ARG, "problem or bytes is NULL");
-  int rc = check_sizes(q->m, q->n, q->k);
+  int rc = check_linear(q);
   if (rc) return rc;
-  *bytes = 0;
+  *bytes = plan_linear(q).total;
   return ok();
 }
 
@@ -200,7 +353,10 @@ int muon_linear(const muon_linear_problem* q, void* workspace, size_t workspace_
   int rc = check_linear(q);
   if (rc) return rc;
   if (q->m == 0 || q->n == 0) return ok();
-  (void)workspace; (void)workspace_bytes;
+  LinearPlan P = plan_linear(q);
+  if ((rc = check_workspace(workspace, workspace_bytes, P.total))) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  char* ws = (char*)workspace;
   LinGemm g{};
   g.A = q->x; g.lda = q->x_row_stride;
   g.B = q->w; g.ldb = q->w_row_stride;
@@ -210,15 +366,25 @@ int muon_linear(const muon_linear_problem* q, void* workspace, size_t workspace_
   g.Y = q->y; g.y_dtype = q->y_dtype; g.ldy = q->y_row_stride;
   g.Z = q->preact; g.ldz = q->preact_row_stride;
   g.act = q->activation;
-  const hipError_t e = launch_linear_simple(g, q->dtype == MUON_BF16, kRowRow, (hipStream_t)stream);
+  g.vec = vec_flags(g, q->dtype);
+  g.split = 1;
+  hipError_t e;
+  if (P.small) {
+    e = launch_linear_small(g, q->dtype == MUON_BF16, s);
+  } else {
+    Operand* ops[] = {&P.x, &P.w};
+    if ((e = pack_all(ops, 2, q->dtype, ws, s)) != hipSuccess) return hip_fail(e, "operand copies");
+    g.A = P.x.p; g.lda = P.x.ld;
+    g.B = P.w.p; g.ldb = P.w.ld;
+    e = run_product(g, q->dtype, kRowRow, P.t, ws + P.part_off, s);
+  }
   return e == hipSuccess ? ok() : hip_fail(e, "linear kernels");
 }
 
 int muon_linear_backward_workspace_bytes(const muon_linear_grad* q, size_t* bytes) {
   if (!q || !bytes) return fail(MUON_ERR_INVALID_ARG, "problem or bytes is NULL");
-  int rc = check_sizes(q->m, q->n, q->k);
+  int rc = check_linear_grad(q);
   if (rc) return rc;
-  if (!dtype_ok(q->dtype) || !dtype_ok(q->dy_dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype and dy_dtype must be MUON_F32 or MUON_BF16");
   *bytes = plan_grad(q).total;
   return ok();
 }
@@ -226,15 +392,16 @@ int muon_linear_backward_workspace_bytes(const muon_linear_grad* q, size_t* byte
 int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_linear_grad(q);
   if (rc) return rc;
-  const GradPlan P = plan_grad(q);
+  GradPlan P = plan_grad(q);
   if ((rc = check_workspace(workspace, workspace_bytes, P.total))) return rc;
   const bool bf = q->dtype == MUON_BF16;
   hipStream_t s = (hipStream_t)stream;
   char* ws = (char*)workspace;
-  const void* G = q->dy;
-  int64_t ldg = q->dy_row_stride;
   hipError_t e;
-  if (P.store_g || P.colsum) {
+  // the gradient at the pre-activation; dy itself where they are the same
+  const void* G = q->m && q->n ? q->dy : nullptr;
+  int64_t ldg = q->m > 1 ? q->dy_row_stride : P.ldg;
+  if (P.store_g || (P.colsum && P.chunks > 0)) {
     ActGrad a{};
     a.dy = q->dy; a.dy_dtype = q->dy_dtype; a.lddy = q->dy_row_stride;
     a.act = q->activation;
@@ -249,26 +416,31 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
     a.vec = rows16(a.dy, a.lddy, a.dy_dtype) && (!a.z || rows16(a.z, a.ldz, q->dtype)) ? 1 : 0;
     if ((e = launch_act_grad(a, bf, s)) != hipSuccess) return hip_fail(e, "gradient at the pre-activation");
   }
-  if (q->dbias && q->n > 0) {
+  if (P.colsum) {
     e = launch_col_sum((const float*)(ws + P.partial_off), P.chunks, q->n, q->dbias, q->dbias_dtype, q->accumulate != 0, s);
     if (e != hipSuccess) return hip_fail(e, "bias gradient");
   }
-  if (q->dx && q->m > 0 && q->k > 0) {
+  const bool dx = q->dx && q->m > 0 && q->k > 0, dw = q->dw && q->n > 0 && q->k > 0;
+  Operand* ops[] = {&P.w, &P.x};
+  if ((e = pack_all(ops, 2, q->dtype, ws, s)) != hipSuccess) return hip_fail(e, "operand copies");
+  if (dx) {
     LinGemm g{};
     g.A = G; g.lda = ldg;
-    g.B = q->w; g.ldb = q->w_row_stride;
+    g.B = P.w.p; g.ldb = P.w.ld;
     g.M = q->m; g.N = q->k; g.K = q->n;
     g.Y = q->dx; g.y_dtype = q->dx_dtype; g.ldy = q->dx_row_stride;
-    if ((e = launch_linear_simple(g, bf, kRowCol, s)) != hipSuccess) return hip_fail(e, "input gradient");
+    g.vec = vec_flags(g, q->dtype);
+    if ((e = run_product(g, q->dtype, kRowCol, P.tx, ws + P.part_off, s)) != hipSuccess) return hip_fail(e, "input gradient");
   }
-  if (q->dw && q->n > 0 && q->k > 0) {
+  if (dw) {
     LinGemm g{};
     g.A = G; g.lda = ldg;
-    g.B = q->x; g.ldb = q->x_row_stride;
+    g.B = P.x.p; g.ldb = P.x.ld;
     g.M = q->n; g.N = q->k; g.K = q->m;
     g.Y = q->dw; g.y_dtype = q->dw_dtype; g.ldy = q->dw_row_stride;
     if (q->accumulate) { g.add = q->dw; g.add_dtype = q->dw_dtype; g.ldadd = q->dw_row_stride; }
-    if ((e = launch_linear_simple(g, bf, kColCol, s)) != hipSuccess) return hip_fail(e, "weight gradient");
+    g.vec = vec_flags(g, q->dtype);
+    if ((e = run_product(g, q->dtype, kColCol, P.tw, ws + P.part_off, s)) != hipSuccess) return hip_fail(e, "weight gradient");
   }
   return ok();
 }

@@ -19,22 +19,42 @@ int report(int code, const char* msg) noexcept;
 //   input gradient   g [M][N] row, w [N][K] col  (M x K out, sum over N)
 //   weight gradient  g [M][N] col, x [M][K] col  (N x K out, sum over M)
 // Epilogue: z = C + bias_j; zout = z; y = act(z) + add(i, j).
+// kVec*: every row of that tensor starts 16-byte aligned.
+constexpr int kVecBias = 1, kVecAdd = 2, kVecY = 4, kVecZ = 8;
 struct LinGemm {
   const void* A; int64_t lda;
   const void* B; int64_t ldb;
   int64_t M, N, K;
+  int64_t Kcol;                                        // K values a col operand holds (K, or fewer: zeros from there on)
   const void* bias; int32_t bias_dtype;
   const void* add; int32_t add_dtype; int64_t ldadd;  // residual, or the output itself (accumulation)
   void* Y; int32_t y_dtype; int64_t ldy;
   void* Z; int64_t ldz;                                // pre-activation (operand type), or null
   int32_t act;
+  int32_t vec;                                         // kVec* flags
+  float* part; int64_t ldpart;                         // split sum: [split][M][ldpart] fp32, else null
+  int32_t split;                                       // chunks of the sum, >= 1
 };
 enum LinKind { kRowRow = 0, kRowCol = 1, kColCol = 2 };
 
-hipError_t launch_linear_simple(const LinGemm& g, bool bf16, LinKind kind, hipStream_t s);
+// Tiled kernels (tile edge 256, 128 or 64; fp32: 128 or 64).  Operand rows
+// must start 16-byte aligned, and a row operand's K be a multiple of 16 bytes
+// (launch_pack makes such a copy); with split > 1 the kernel stores the
+// chunks' products and launch_split_finish adds them and runs the epilogue.
+hipError_t launch_linear_tiles(const LinGemm& g, bool bf16, LinKind kind, int tile, hipStream_t s);
+hipError_t launch_split_finish(const LinGemm& g, bool bf16, hipStream_t s);
+// Few rows (M <= kSmallRows), kRowRow: any stride and alignment.
+constexpr int kSmallRows = 64;
+hipError_t launch_linear_small(const LinGemm& g, bool bf16, hipStream_t s);
+// dst [rows][ldd] = src [rows][cols] with zeros in columns cols .. ldd - 1, up
+// to two matrices per launch.
+struct PackJob { const void* src; int64_t lds; void* dst; int64_t ldd; int64_t rows, cols; };
+struct PackJobs { PackJob job[2]; int32_t n; int64_t start[3]; };
+hipError_t launch_pack(PackJobs& p, bool bf16, hipStream_t s);
 
 // ---- gradient at the pre-activation ----------------------------------------------
-// G = round(dy * act'(z)) in the operand type (G null: not stored) and, when
+// G = round(dy * act'(z)) in the operand type (G null: not stored), with zeros
+// in columns N .. ldg - 1 (ldg the next multiple of 8), and, when
 // partial is not null, partial[c][j] = the sum over row chunk c of dy * act'(z)
 // (unrounded), rows c * rows_per .. of M.
 struct ActGrad {
@@ -44,7 +64,7 @@ struct ActGrad {
   float* partial; int32_t chunks; int64_t rows_per;
   int64_t M, N;
   int32_t act;
-  int32_t vec;                         // 1: every row of dy, z and G starts 16-byte aligned
+  int32_t vec;                         // 1: every row of dy and z starts 16-byte aligned (G's always do)
 };
 hipError_t launch_act_grad(const ActGrad& g, bool bf16, hipStream_t s);
 // out[j] (+)= sum over chunks of partial[c][j], c ascending.

@@ -1,0 +1,182 @@
+// The linear product for few rows (decoding: 1 to 64 tokens).
+//
+// Bound by HBM: the weight is read once, 2 bytes per 2 M operations.  A
+// workgroup owns 16 NB weight rows and all tokens; its eight waves take the
+// 128-byte steps of K in turn (so together they read a kilobyte of each row at
+// a time) and stream them straight into registers, 32 bytes per lane of every
+// row, as one operand of 16x16 MFMAs whose other operand is the tokens (16 MB,
+// from the caches).  The order of K within a step differs between the lanes'
+// layout and memory, but in the same way for both operands, so every product
+// is formed once.  The waves' sums are added in order through LDS and finished
+// there: one launch, nothing through HBM but operands and results.
+#include "layer_internal.h"
+#include "linear_epilogue.h"
+
+namespace muon {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// Weight and token rows may start anywhere: unaligned 16-byte loads.
+template <typename T>
+struct Loads;
+template <>
+struct Loads<uint16_t> { typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2))); };
+template <>
+struct Loads<float> { typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(4))); };
+
+constexpr int NWV = 8;
+
+template <typename T, int MB, int NB, int U>
+__global__ __launch_bounds__(NWV * 64) void linear_small_kernel(const LinGemm p) {
+  constexpr bool BF = sizeof(T) == 2;
+  constexpr int E = 32 / sizeof(T);        // values of K per lane and step
+  constexpr int KS = 4 * E;                // values of K per step
+  constexpr int NR = 16 * NB, PITCH = NR + 4;
+  typedef typename Loads<T>::v4 v4u;
+  __shared__ __attribute__((aligned(16))) float red[NWV][16 * MB * PITCH];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * NR;
+  const T* wrow[NB];
+  const T* xrow[MB];
+  bool tok[MB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int64_t n = n0 + 16 * b + r;
+    wrow[b] = (const T*)p.B + (n < p.N ? n : p.N - 1) * p.ldb + g * E;
+  }
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    tok[b] = 16 * b + r < p.M;
+    xrow[b] = (const T*)p.A + (tok[b] ? 16 * b + r : 0) * p.lda + g * E;
+  }
+  f32x4 acc[MB][NB];
+#pragma unroll
+  for (int a = 0; a < MB; ++a)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto products = [&](const u32x4 (&w)[NB][2], const u32x4 (&x)[MB][2]) {
+#pragma unroll
+    for (int a = 0; a < MB; ++a)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if constexpr (BF) {
+            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[b][q]),
+                                                                __builtin_bit_cast(bf16x8, x[a][q]), acc[a][b], 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[b][q][e]), __uint_as_float(x[a][q][e]),
+                                                               acc[a][b], 0, 0, 0);
+          }
+        }
+  };
+  // Up to 8 whole-step chunks of one row: 16 bytes each at k and k + 16 bytes.
+  const int64_t full = p.K / KS, steps = (p.K + KS - 1) / KS;
+  int64_t s = wave;
+  for (; s + (int64_t)(U - 1) * NWV < full; s += (int64_t)U * NWV) {
+    u32x4 w[U][NB][2], x[U][MB][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (s + (int64_t)u * NWV) * KS;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        w[u][b][0] = *(const v4u*)(wrow[b] + k);
+        w[u][b][1] = *(const v4u*)(wrow[b] + k + E / 2);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (s + (int64_t)u * NWV) * KS;
+#pragma unroll
+      for (int a = 0; a < MB; ++a) {
+        x[u][a][0] = x[u][a][1] = u32x4{0, 0, 0, 0};
+        if (tok[a]) {
+          x[u][a][0] = *(const v4u*)(xrow[a] + k);
+          x[u][a][1] = *(const v4u*)(xrow[a] + k + E / 2);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) products(w[u], x[u]);
+  }
+  for (; s < steps; s += NWV) {  // the rest, values of K past the end as zeros
+    u32x4 w[NB][2], x[MB][2];
+    const int64_t k = s * KS;
+    auto part = [&](const T* row, int q, bool on) -> u32x4 {
+      const T* at = row + k + q * (E / 2);
+      const int64_t left = p.K - (k + g * E + q * (E / 2));
+      if (on && left >= E / 2) return *(const v4u*)at;
+      T v[E / 2];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) v[e] = on && e < left ? at[e] : T(0);
+      u32x4 o;
+      __builtin_memcpy(&o, v, 16);
+      return o;
+    };
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) w[b][q] = part(wrow[b], q, true);
+#pragma unroll
+      for (int a = 0; a < MB; ++a) x[a][q] = part(xrow[a], q, tok[a]);
+    }
+    products(w, x);
+  }
+  // D of a 16 x 16 block: lane l holds token l % 16, weight rows 4 (l / 16) .. + 3.
+#pragma unroll
+  for (int a = 0; a < MB; ++a)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) *(f32x4*)(&red[wave][(16 * a + r) * PITCH + 16 * b + 4 * g]) = acc[a][b];
+  __syncthreads();
+  with_act(p.act, [&](auto act_c) {
+    constexpr int ACT = decltype(act_c)::value;
+    for (int at = threadIdx.x; at < (int)p.M * (NR / 8); at += NWV * 64) {
+      const int i = at / (NR / 8), c8 = (at % (NR / 8)) * 8;
+      const int64_t j = n0 + c8;
+      const int valid = j >= p.N ? 0 : (p.N - j < 8 ? (int)(p.N - j) : 8);
+      if (valid <= 0) continue;
+      float v[8], b[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = red[0][i * PITCH + c8 + e];
+#pragma unroll
+      for (int w = 1; w < NWV; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += red[w][i * PITCH + c8 + e];
+      bias8(p, j, valid, b);
+      finish8<ACT, BF>(p, i, j, valid, b, v);
+    }
+  });
+}
+
+template <typename T, int MB, int NB, int U>
+hipError_t launch_one(const LinGemm& g, hipStream_t s) {
+  const int64_t grid = (g.N + 16 * NB - 1) / (16 * NB);
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  return launch_kernel(linear_small_kernel<T, MB, NB, U>, dim3((unsigned)grid), g, s, NWV * 64);
+}
+
+template <typename T>
+hipError_t launch_type(const LinGemm& g, hipStream_t s) {
+  if (g.M <= 0 || g.N <= 0) return hipSuccess;
+  // 32 weight rows per workgroup halve the reads of the tokens; 16 where 32
+  // would leave CUs without work.
+  const bool wide = g.N >= 32 * 256;
+  const int mb = (int)((g.M + 15) / 16);
+  if (mb == 1) return wide ? launch_one<T, 1, 2, 4>(g, s) : launch_one<T, 1, 1, 4>(g, s);
+  if (mb == 2) return wide ? launch_one<T, 2, 2, 2>(g, s) : launch_one<T, 2, 1, 4>(g, s);
+  if (mb == 3) return wide ? launch_one<T, 3, 2, 2>(g, s) : launch_one<T, 3, 1, 2>(g, s);
+  if (mb == 4) return wide ? launch_one<T, 4, 2, 1>(g, s) : launch_one<T, 4, 1, 2>(g, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_linear_small(const LinGemm& g, bool bf16, hipStream_t s) {
+  return bf16 ? launch_type<uint16_t>(g, s) : launch_type<float>(g, s);
+}
+
+}  // namespace muon
