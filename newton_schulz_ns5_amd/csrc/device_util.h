@@ -75,8 +75,13 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* base, int64_t bytes) {
 // The LDS address reaches the instruction through M0, passed as an input
 // operand bound to that register: the compiler writes M0 itself and knows
 // it is read here, so nothing the compiler keeps in M0 is overwritten.
+// The compiler does not look inside the assembly for the wait states that the
+// hardware leaves to software: five between a vector instruction that writes
+// a scalar register (v_readfirstlane) and a memory instruction that reads it,
+// one between a write of M0 and an LDS load.  The s_nop covers both, whatever
+// the compiler put in front.
 __device__ __forceinline__ void lds_dma16_asm(i32x4 rsrc, uint32_t lds, int voff, int soff) {
-  asm volatile("buffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc),
                  "s"(__builtin_amdgcn_readfirstlane(soff))

@@ -142,14 +142,25 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_tile_kernel(const LinGemm p
     const int64_t r = rows < BT ? rows : BT;
     return Kc > 0 ? ((r - 1) * ld + (Kc + 16 / ES - 1) / (16 / ES) * (16 / ES)) * ES : 0;
   };
-  const int64_t kcol = (p.Kcol < kend ? p.Kcol : kend) - kbeg;
   const i32x4 ars = rsrc_words(Ab, ACOL ? 0 : span(arows, p.lda));
   const i32x4 brs = rsrc_words(Bb, BCOL ? 0 : span(brows, p.ldb));
-  auto col_rsrc = [&](const char* base, int64_t ld, int64_t rows, int t) {
-    const int64_t k = (int64_t)t * KS, left = kcol - k;
-    const int64_t cols = (rows < BT ? (rows + 16 / ES - 1) / (16 / ES) * (16 / ES) : BT);
-    const int64_t n = left <= 0 ? 0 : ((left < KS ? left : KS) - 1) * ld + cols;
-    return rsrc_words(base + k * ld * ES, n * ES);
+  // Scalar arithmetic only (32-bit compares and products), so that the words
+  // stay in scalar registers.
+  const int kcol = (int)((p.Kcol < kend ? p.Kcol : kend) - kbeg);
+  auto col_bytes = [&](int ld, int64_t rows, int left) {
+    const int cols = rows < BT ? ((int)rows + 16 / ES - 1) / (16 / ES) * (16 / ES) : BT;
+    return left <= 0 ? 0 : (((left < KS ? left : KS) - 1) * ld + cols) * ES;
+  };
+  const int afull = ACOL ? col_bytes(lda, arows, KS) : 0, alast = ACOL ? col_bytes(lda, arows, kcol - (KT - 1) * KS) : 0;
+  const int bfull = BCOL ? col_bytes(ldb, brows, KS) : 0, blast = BCOL ? col_bytes(ldb, brows, kcol - (KT - 1) * KS) : 0;
+  auto col_rsrc = [&](const char* base, int ld, int full, int end, int t) {
+    const uint64_t a = (uint64_t)base + (uint64_t)(uint32_t)t * (uint32_t)(KS * ld * ES);
+    i32x4 r;
+    r[0] = (int)(uint32_t)a;
+    r[1] = (int)((uint32_t)(a >> 32) & 0xffffu);
+    r[2] = t >= KT - 1 ? end : full;
+    r[3] = 0x00020000;
+    return r;
   };
 
   const uint32_t smem_lds =
@@ -161,10 +172,10 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_tile_kernel(const LinGemm p
     const int tc = last ? KT - 1 : t;
     const uint32_t dst = smem_lds + (uint32_t)(((2 * t + op) % NSLOT) * OPB + (wave * DPW + q) * 1024);
     if (op == 0) {
-      if constexpr (ACOL) lds_dma16_asm(col_rsrc(Ab, p.lda, arows, tc), dst, avo[q], 0);
+      if constexpr (ACOL) lds_dma16_asm(col_rsrc(Ab, lda, afull, alast, tc), dst, avo[q], 0);
       else lds_dma16_asm(ars, dst, last ? tail(avo[q], q) : avo[q], tc * ROWB);
     } else {
-      if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bb, p.ldb, brows, tc), dst, bvo[q], 0);
+      if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bb, ldb, bfull, blast, tc), dst, bvo[q], 0);
       else lds_dma16_asm(brs, dst, last ? tail(bvo[q], q) : bvo[q], tc * ROWB);
     }
   };
