@@ -174,38 +174,59 @@ Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t d
   return o;
 }
 
-// How a product M x N over K runs: tile edge and chunks of the sum.
+// How a product M x N over K runs: columns 0 .. n1 - 1 in tiles `first`, the
+// others in tiles `rest`, and the sum in `split` chunks.
 //
-// Each workgroup of a tile edge costs its slices of K times that edge's time
-// per slice, and the chip holds so many of them at once; a split sum shortens
-// the slices per workgroup where there are too few tiles to fill the chip, and
-// pays for storing and adding the chunks' fp32 products.  The estimate below
-// compares the candidates in microseconds.
-struct Tiling { int tile, split; };
+// Workgroups of a tile run in rounds of as many as the chip holds at once; a
+// round takes a fixed time (pipeline start, epilogue) and a time per slice of
+// K, which is bounded by latency (u0) while few workgroups run and by the
+// chip's rate (u1) in a full round.  Measured for every tile with 16 to 1024
+// workgroups; bf16, 4096 x 14336 over 4096: 414 us in 256 x 256 tiles (3.5
+// rounds), 416 in 256 x 128 (7 rounds), HYB with the last half round of the
+// larger ones in the smaller; 2048 x 4096 over 6144: 132 us in 256 x 256 (half
+// a round), 94 in 256 x 128, 118 in 128, 166 in 64.
+struct Tiling { LinTile first, rest; int64_t n1; int split; };
+
+struct TileCost { LinTile tile; int bm, bn, slots; double fixed, u0, u1; };
+constexpr TileCost kCostBf16[] = {{kTile256, 256, 256, 256, 8.0, 1.15, 1.65},
+                                  {kTile256x128, 256, 128, 256, 6.0, 0.58, 0.87},
+                                  {kTile128, 128, 128, 512, 6.0, 0.75, 1.13},
+                                  {kTile64, 64, 64, 1024, 4.5, 0.44, 0.75}};
+constexpr TileCost kCostF32[] = {{kTile128, 128, 128, 512, 9.0, 2.1, 3.95}, {kTile64, 64, 64, 1024, 5.0, 0.6, 2.03}};
+
+// Microseconds of `wgs` workgroups of `slices` slices each.
+double tile_time(const TileCost& c, int64_t wgs, int64_t slices) {
+  const int64_t full = wgs / c.slots, last = wgs % c.slots;
+  double t = (double)full * (c.fixed + (double)slices * c.u1);
+  if (last) t += c.fixed + (double)slices * std::max(c.u0, c.u1 * (double)last / c.slots);
+  return t;
+}
 
 Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
-  // Edge, workgroups on the chip at once (256 CUs), microseconds per slice with
-  // the chip full.
-  struct Edge { int bt, slots; double us; };
-  static const Edge bf_edges[] = {{256, 256, 1.45}, {128, 512, 0.85}, {64, 1024, 0.55}};
-  static const Edge f32_edges[] = {{128, 512, 6.0}, {64, 1024, 3.2}};
-  const Edge* edges = bf ? bf_edges : f32_edges;
-  const int n = bf ? 3 : 2;
+  const TileCost* costs = bf ? kCostBf16 : kCostF32;
+  const int n = bf ? 4 : 2;
   const int64_t slices = std::max<int64_t>(1, cdiv(K, bf ? 64 : 32));
-  Tiling best{64, 1};
+  Tiling best{kTile64, kTile64, N, 1};
   double least = 1e30;
   for (int i = 0; i < n; ++i) {
-    const int64_t tiles = cdiv(M, edges[i].bt) * cdiv(N, edges[i].bt);
+    const TileCost& c = costs[i];
+    const int64_t tiles = cdiv(M, c.bm) * cdiv(N, c.bn);
     for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (split > 1 && (split > slices / 4 || tiles * split > 4 * edges[i].slots)) break;
-      const double rounds = (double)cdiv(tiles * split, edges[i].slots);
-      // fixed cost of a workgroup: pipeline start and epilogue, about 4 slices
-      double t = rounds * (double)(cdiv(slices, split) + 4) * edges[i].us;
-      if (split > 1) t += 3.0 + (double)(M * N) * 4.0 * (split + 1) / 4e6;  // a launch, and the products at 4 TB/s
+      // chunks of at least two slices, and at most two rounds of them
+      if (split > 1 && (split > slices / 2 || tiles * split > 2 * c.slots)) break;
+      double t = tile_time(c, tiles * split, cdiv(slices, split));
+      if (split > 1) t += 4.0 + (double)(M * N) * 4.0 * (split + 1) / 4e6;  // a launch, and the products at 4 TB/s
       if (t < least) {
         least = t;
-        best = {edges[i].bt, split};
+        best = {c.tile, c.tile, N, split};
       }
+    }
+  }
+  if (bf) {  // whole rounds of the largest tile, the rest in the next smaller
+    const int64_t tm = cdiv(M, 256), cols = tm <= 256 ? cdiv(N, 256) * tm / 256 * 256 / tm : 0;
+    if (cols > 0 && cols * 256 < N) {
+      const double t = tile_time(kCostBf16[0], cols * tm, slices) + tile_time(kCostBf16[1], tm * cdiv(N - cols * 256, 128), slices);
+      if (t < least) best = {kTile256, kTile256x128, cols * 256, 1};
     }
   }
   return best;
@@ -248,7 +269,22 @@ hipError_t run_product(LinGemm g, int32_t dt, LinKind kind, const Tiling& t, cha
   g.split = t.split;
   g.part = t.split > 1 ? (float*)part : nullptr;
   g.ldpart = part_ld(g.N);
-  hipError_t e = launch_linear_tiles(g, bf, kind, t.tile, s);
+  hipError_t e;
+  if (t.n1 < g.N) {
+    LinGemm r = g;  // columns n1 .. N - 1
+    const int64_t n1 = t.n1;
+    auto past = [&](const void* p, int64_t elems, int32_t d) { return p ? (const char*)p + elems * esize(d) : nullptr; };
+    r.N = g.N - n1;
+    r.B = past(g.B, kind == kRowRow ? n1 * g.ldb : n1, dt);
+    r.bias = past(g.bias, n1, g.bias_dtype);
+    r.add = past(g.add, n1, g.add_dtype);
+    r.Y = (void*)past(g.Y, n1, g.y_dtype);
+    r.Z = (void*)past(g.Z, n1, dt);
+    g.N = n1;
+    e = launch_linear_tiles(g, bf, kind, t.first, s);
+    return e == hipSuccess ? launch_linear_tiles(r, bf, kind, t.rest, s) : e;
+  }
+  e = launch_linear_tiles(g, bf, kind, t.first, s);
   if (e == hipSuccess && t.split > 1) e = launch_split_finish(g, bf, s);
   return e;
 }

@@ -37,11 +37,12 @@ struct LinGemm {
 };
 enum LinKind { kRowRow = 0, kRowCol = 1, kColCol = 2 };
 
-// Tiled kernels (tile edge 256, 128 or 64; fp32: 128 or 64).  Operand rows
+// Tiled kernels (fp32: the two smaller tiles).  Operand rows
 // must start 16-byte aligned, and a row operand's K be a multiple of 16 bytes
 // (launch_pack makes such a copy); with split > 1 the kernel stores the
 // chunks' products and launch_split_finish adds them and runs the epilogue.
-hipError_t launch_linear_tiles(const LinGemm& g, bool bf16, LinKind kind, int tile, hipStream_t s);
+enum LinTile { kTile256 = 0, kTile256x128 = 1, kTile128 = 2, kTile64 = 3 };
+hipError_t launch_linear_tiles(const LinGemm& g, bool bf16, LinKind kind, LinTile tile, hipStream_t s);
 hipError_t launch_split_finish(const LinGemm& g, bool bf16, hipStream_t s);
 // Few rows (M <= kSmallRows), kRowRow: any stride and alignment.
 constexpr int kSmallRows = 64;

@@ -5,17 +5,25 @@
 // operands that are each re-read once per tile of the other, so it is bound by
 // the matrix units once a tile is large enough; the kernel is built to keep
 // them fed:
-//  - one workgroup per BT x BT output tile; BT = 256: eight waves of 128 x 64,
-//    two per SIMD; BT = 128 and 64: four waves, two and four workgroups per CU
-//    for problems with too few large tiles to fill the chip;
+//  - one workgroup per BM x BN output tile, its waves in WM x WN, each wave a
+//    block of 16 x 16 products (v_mfma_f32_16x16x32_bf16: 3 % faster here than
+//    the 32x32x16 form, which moves more accumulator values per operation;
+//    fp32: 16x16x4).  256 x 256: eight waves of 128 x 64, two per SIMD;
+//    256 x 128: eight of 64 x 64; 128 and 64: four waves, two and four
+//    workgroups per CU, for outputs with too few large tiles to fill the chip;
 //  - K advances by 128 bytes of a row (64 bf16 or 32 fp32 values) per slice,
-//    brought HBM -> LDS directly into a ring of five operand slots, one and a
-//    half slices ahead, with one barrier per slice; loads, fragment reads and
-//    MFMAs are interleaved in fixed slots;
+//    brought HBM -> LDS directly into a ring of operand slots, one and a half
+//    to two slices ahead, with one barrier per slice; loads, fragment reads
+//    and MFMAs are interleaved in fixed slots;
 //  - row operands: a slot row is 128 bytes of K with its 16-byte chunks
 //    XOR-swizzled by (row / 2) mod 8, one ds_read_b128 per fragment; col
-//    operands: a slot row is one K value of all BT indices, read through the
-//    transposing ds_read_b64_tr_b16 (bf16) or single words (fp32).
+//    operands: a slot row is one K value of all the tile's indices, read
+//    through the transposing ds_read_b64_tr_b16 (bf16) or single words (fp32),
+//    with its blocks XOR-swizzled so that no bank is read twice;
+//  - every LDS address of a lane is one register per operand plus constants: a
+//    version that formed them per read spilled six registers in the product
+//    of two col operands, whose reloads waited out the loads in flight
+//    (537 us where this takes LAST us, 14336 x 4096 over 4096).
 // Ragged sizes cost nothing in the loop: rows past the end repeat the last one
 // (their products are not stored), K values past the end are zeros from the
 // buffer descriptor's bounds check (which the loads of the last slice are sent
@@ -27,12 +35,10 @@ namespace muon {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 #define MUON_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
-constexpr int NSLOT = 5;    // LDS ring of operand slots
 constexpr int ROWB = 128;   // bytes of K per slice
 constexpr int kOut = (int)0x80000000;  // a byte offset past every descriptor's end
 
@@ -54,37 +60,92 @@ __device__ __forceinline__ void decode(int tiles_m, int tiles_n, int& sp, int& t
   tn = r / gsz;
 }
 
-template <typename T, int KIND, int BT, int NW>
-__global__ __launch_bounds__(NW * 64, 1) void linear_tile_kernel(const LinGemm p) {
+// LDS reads and addresses of one operand: EXT its tile edge, COL its layout.
+template <typename T, int EXT, bool COL>
+struct Operand {
+  static constexpr bool BF = sizeof(T) == 2;
+  static constexpr int ES = sizeof(T);
+  static constexpr int KS = ROWB / ES;
+  static constexpr int BYTES = EXT * ROWB;    // of one slot
+  static constexpr int CROWB = EXT * ES;      // col: bytes of one K row
+  static constexpr int CCH = CROWB / 16;      // col: 16-byte chunks of it
+  // XOR key of a K row of a col slot.  bf16, on 32-byte blocks: 32 lanes of a
+  // transposing read touch one block of the rows 8 g + 0 .. 3 of two
+  // neighbouring g (and, in a 128-byte row, rows of equal parity share banks).
+  // fp32, on 64-byte blocks: a word read touches one block of rows 4 g of four
+  // g.
+  static __device__ __forceinline__ int key(int row) {
+    if constexpr (!BF) return (row >> 2) & 3;
+    else if constexpr (EXT == 64) return ((row >> 1) & 1) | (((row >> 3) & 1) << 1);
+    else return (row & 3) | (((row >> 3) & 1) << 2);
+  }
+  // Global chunk that the load landing at (slot row, chunk c) fetches.
+  static __device__ __forceinline__ int source_chunk(int row, int c) {
+    if constexpr (!COL) return c ^ ((row >> 1) & 7);
+    else if constexpr (BF) return 2 * ((c >> 1) ^ key(row)) + (c & 1);
+    else return 4 * ((c >> 2) ^ key(row)) + (c & 3);
+  }
+  // A lane's address within a slot for its wave's indices from `at` on (a
+  // multiple of the wave's extent): see read().
+  static __device__ __forceinline__ uint32_t lane_base(int lane, int at) {
+    const int i = lane & 15, g = lane >> 4;
+    if constexpr (!COL) return (uint32_t)((at + i) * ROWB + (g ^ ((i >> 1) & 7)) * 16);
+    else if constexpr (BF) return (uint32_t)((8 * g + (i >> 2)) * CROWB + ((at >> 4) ^ key(8 * g + (i >> 2))) * 32 + (i & 3) * 8);
+    else return (uint32_t)(4 * g * CROWB + ((at >> 4) ^ key(4 * g)) * 64 + i * 4);
+  }
+  // Fragment f of half hf of a slice: for index 16 f + l % 16 of the wave's,
+  // 16 bytes of K: bf16, values 32 hf + 8 g .. + 7 (g = l / 16), one product;
+  // fp32, values 16 hf + 4 g .. + 3, one for each of four products.
+  static __device__ __forceinline__ u32x4 read(uint32_t base, int hf, int f) {
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    typedef __attribute__((address_space(3))) uint32_t lds_u32;
+    if constexpr (!COL) {
+      return *(const lds_u32x4*)(uintptr_t)((base ^ (uint32_t)(hf * 64)) + (uint32_t)(f * 16 * ROWB));
+    } else if constexpr (BF) {
+      const uint32_t at = (base ^ (uint32_t)(f * 32)) + (uint32_t)(hf * 32 * CROWB);
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)at);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(at + 4 * CROWB));
+      return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      const uint32_t at = (base ^ (uint32_t)(f * 64)) + (uint32_t)(hf * 16 * CROWB);
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *(const lds_u32*)(uintptr_t)(at + e * CROWB);
+      return v;
+    }
+  }
+};
+
+template <typename T, int KIND, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinGemm p) {
   constexpr bool BF = sizeof(T) == 2;
   constexpr bool ACOL = KIND == kColCol, BCOL = KIND != kRowRow;
-  constexpr int ES = sizeof(T);
-  constexpr int KS = ROWB / ES;         // K per slice
-  constexpr int NTH = NW * 64;
-  constexpr int WT = BT / 2;            // wave tile rows (two rows of waves)
-  constexpr int WC = BT / (NW / 2);     // wave tile columns
-  constexpr int F = WT / 32, FN = WC / 32;
-  constexpr int OPB = BT * ROWB;        // bytes of one slot
-  constexpr int DPW = BT / NW / 8;      // load instructions per wave, operand and slice
-  constexpr int DQ = DPW / 2;
-  constexpr int NM = F * FN;            // block products per quarter slice
-  constexpr int MPS = NM >= 8 ? 2 : 1;  // block products per slot
-  constexpr int NSL = NM / MPS;
-  constexpr int FPS = (F + FN + NSL - 1) / NSL;  // fragment reads per slot
-  constexpr int RH = BT / 2;
-  constexpr int PITCH = BT + 4;
-  constexpr int EPI = RH * PITCH * 4;
-  constexpr int LDS_BYTES = NSLOT * OPB > EPI ? NSLOT * OPB : EPI;
-  static_assert(DQ >= 1 && DPW % 2 == 0, "a quarter loads half an operand slice");
-  __shared__ __attribute__((aligned(16))) uint8_t smem[LDS_BYTES];
+  typedef Operand<T, BM, ACOL> OA;
+  typedef Operand<T, BN, BCOL> OB;
+  constexpr int ES = sizeof(T), KS = ROWB / ES;
+  constexpr int NW = WM * WN, NTH = NW * 64;
+  constexpr int WT = BM / WM, WC = BN / WN;      // wave tile
+  constexpr int F = WT / 16, FN = WC / 16, FH = F / 2;
+  constexpr int DPA = BM / NW / 8, DPB = BN / NW / 8;  // load instructions per wave, operand and slice
+  // Ring: equal operands share five slots (A of slice t in 2 t mod 5, B in
+  // 2 t + 1 mod 5), else each has three.
+  constexpr bool RING5 = BM == BN;
+  constexpr int RING_A = RING5 ? 5 * OA::BYTES : 3 * OA::BYTES;
+  constexpr int RING = RING5 ? RING_A : RING_A + 3 * OB::BYTES;
+  constexpr int RH = BM / 2, PITCH = BN + 4;
+  constexpr int LDS_BYTES = RING > RH * PITCH * 4 ? RING : RH * PITCH * 4;
+  static_assert(DPA >= 1 && DPB >= 1 && (!RING5 || DPB % 2 == 0) && F % 2 == 0 && FN % 2 == 0, "tile shape");
+  static_assert((WT & (WT - 1)) == 0 && (WC & (WC - 1)) == 0, "fragment indices are XORed into addresses");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / (NW / 2), wn = wave % (NW / 2);
-  const int tiles_m = (int)((p.M + BT - 1) / BT), tiles_n = (int)((p.N + BT - 1) / BT);
+  const int wm = wave / WN, wn = wave % WN;
+  const int tiles_m = (int)((p.M + BM - 1) / BM), tiles_n = (int)((p.N + BN - 1) / BN);
   int sp, tm, tn;
   decode(tiles_m, tiles_n, sp, tm, tn);
-  const int64_t i0 = (int64_t)tm * BT, j0 = (int64_t)tn * BT;
+  const int64_t i0 = (int64_t)tm * BM, j0 = (int64_t)tn * BN;
 
   // This workgroup's slices of K: chunk sp of the split sum.
   const int slices = (int)((p.K + KS - 1) / KS);
@@ -95,64 +156,52 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_tile_kernel(const LinGemm p
   const int64_t kend = (int64_t)t1 * KS < p.K ? (int64_t)t1 * KS : p.K;
   const int Kc = (int)(kend - kbeg);                // K values of this workgroup
 
-  // Per operand: base, and each lane's byte offset for each load instruction.
-  // Row operand: instruction q of a wave fills slot rows wave * 8 DPW + 8 q ..
-  // + 7; lane l lands at row l / 8, chunk l % 8, and fetches the row's chunk
-  // (l % 8) ^ ((row / 2) % 8).  Col operand: slot rows are K values, BT ES
-  // bytes each.
-  constexpr int CROWB = BT * ES, CCH = CROWB / 16, CRPI = 1024 / CROWB;
-  static_assert(KS / NW == DPW * CRPI, "a wave's K rows of a col slice take DPW instructions");
-  // XOR key of a K row in a col slot, on 32-byte blocks, so that the four rows
-  // and two blocks that 32 lanes of a transposing read touch fall on distinct
-  // banks (fp32 is read by single words in order and needs none).
-  auto ckey = [](int row) { return !BF ? 0 : (BT == 64 ? 2 * ((row >> 1) & 1) : 2 * (row & 3)); };
-  int avo[DPW], bvo[DPW];
+  // Each lane's byte offset for each load instruction.  Instruction q of a
+  // wave fills the 1024 bytes of a slot from (wave DP + q) 1024 on, lane l its
+  // 16 bytes there: slot row and chunk follow.
+  int avo[DPA], bvo[DPB];
   const int64_t arows = p.M - i0, brows = p.N - j0;
   const int lda = __builtin_amdgcn_readfirstlane((int)p.lda), ldb = __builtin_amdgcn_readfirstlane((int)p.ldb);
-  auto offsets = [&](int (&vo)[DPW], bool col, int ld, int64_t rows) {
-#pragma unroll
-    for (int q = 0; q < DPW; ++q) {
-      if (col) {
-        const int row = wave * (KS / NW) + q * CRPI + lane / CCH, c = lane % CCH;
-        const int g = ES == 2 ? 2 * ((c >> 1) ^ ckey(row)) + (c & 1) : c;
-        vo[q] = row * ld * ES + g * 16;
-      } else {
-        const int row = wave * 8 * DPW + 8 * q + (lane >> 3);
-        const int g = (lane & 7) ^ ((row >> 1) & 7);
-        const int src = row < rows ? row : (int)rows - 1;
-        vo[q] = src * ld * ES + g * 16;
-      }
+  auto offset = [&](auto op, bool col, int at, int ld, int64_t rows) {
+    typedef decltype(op) O;
+    if (col) {
+      const int row = at / O::CROWB, c = (at % O::CROWB) / 16;
+      return row * ld * ES + O::source_chunk(row, c) * 16;
     }
+    const int row = at / ROWB, c = (at % ROWB) / 16;
+    return (row < rows ? row : (int)rows - 1) * ld * ES + O::source_chunk(row, c) * 16;
   };
-  offsets(avo, ACOL, lda, arows);
-  offsets(bvo, BCOL, ldb, brows);
+#pragma unroll
+  for (int q = 0; q < DPA; ++q) avo[q] = offset(OA{}, ACOL, (wave * DPA + q) * 1024 + lane * 16, lda, arows);
+#pragma unroll
+  for (int q = 0; q < DPB; ++q) bvo[q] = offset(OB{}, BCOL, (wave * DPB + q) * 1024 + lane * 16, ldb, brows);
   // The last slice's loads: row chunks past K go past the descriptor's end.
   const int klast = Kc - (KT - 1) * KS;             // K values of the last slice (0: none)
-  auto tail = [&](int vo, int q) {
-    const int row = wave * 8 * DPW + 8 * q + (lane >> 3);
-    const int g = (lane & 7) ^ ((row >> 1) & 7);
-    return g * (16 / ES) < klast ? vo : kOut;
+  auto tail = [&](int vo, int at) {
+    const int row = at / ROWB, c = (at % ROWB) / 16;
+    return (c ^ ((row >> 1) & 7)) * (16 / ES) < klast ? vo : kOut;
   };
   // A row operand's panel: its descriptor spans the tile's rows from K value
   // kbeg on.  A col operand's: rebased every slice, ending after its last K
   // row's columns (rounded up to whole chunks).
   const char* const Ab = (const char*)p.A + (ACOL ? kbeg * p.lda + i0 : i0 * p.lda + kbeg) * ES;
   const char* const Bb = (const char*)p.B + (BCOL ? kbeg * p.ldb + j0 : j0 * p.ldb + kbeg) * ES;
-  auto span = [&](int64_t rows, int64_t ld) {
-    const int64_t r = rows < BT ? rows : BT;
+  auto span = [&](int64_t rows, int ext, int64_t ld) {
+    const int64_t r = rows < ext ? rows : ext;
     return Kc > 0 ? ((r - 1) * ld + (Kc + 16 / ES - 1) / (16 / ES) * (16 / ES)) * ES : 0;
   };
-  const i32x4 ars = rsrc_words(Ab, ACOL ? 0 : span(arows, p.lda));
-  const i32x4 brs = rsrc_words(Bb, BCOL ? 0 : span(brows, p.ldb));
+  const i32x4 ars = rsrc_words(Ab, ACOL ? 0 : span(arows, BM, p.lda));
+  const i32x4 brs = rsrc_words(Bb, BCOL ? 0 : span(brows, BN, p.ldb));
   // Scalar arithmetic only (32-bit compares and products), so that the words
   // stay in scalar registers.
   const int kcol = (int)((p.Kcol < kend ? p.Kcol : kend) - kbeg);
-  auto col_bytes = [&](int ld, int64_t rows, int left) {
-    const int cols = rows < BT ? ((int)rows + 16 / ES - 1) / (16 / ES) * (16 / ES) : BT;
+  auto col_bytes = [&](int ld, int64_t rows, int ext, int left) {
+    const int cols = rows < ext ? ((int)rows + 16 / ES - 1) / (16 / ES) * (16 / ES) : ext;
     return left <= 0 ? 0 : (((left < KS ? left : KS) - 1) * ld + cols) * ES;
   };
-  const int afull = ACOL ? col_bytes(lda, arows, KS) : 0, alast = ACOL ? col_bytes(lda, arows, kcol - (KT - 1) * KS) : 0;
-  const int bfull = BCOL ? col_bytes(ldb, brows, KS) : 0, blast = BCOL ? col_bytes(ldb, brows, kcol - (KT - 1) * KS) : 0;
+  const int left = kcol - (KT - 1) * KS;
+  const int afull = ACOL ? col_bytes(lda, arows, BM, KS) : 0, alast = ACOL ? col_bytes(lda, arows, BM, left) : 0;
+  const int bfull = BCOL ? col_bytes(ldb, brows, BN, KS) : 0, blast = BCOL ? col_bytes(ldb, brows, BN, left) : 0;
   auto col_rsrc = [&](const char* base, int ld, int full, int end, int t) {
     const uint64_t a = (uint64_t)base + (uint64_t)(uint32_t)t * (uint32_t)(KS * ld * ES);
     i32x4 r;
@@ -165,134 +214,162 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_tile_kernel(const LinGemm p
 
   const uint32_t smem_lds =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem);
-  // Load instruction q of operand op (0: A, 1: B) of slice t.  Slices past the
-  // last (the pipeline runs ahead) repeat it into slots nobody reads.
-  auto dma = [&](int t, int op, int q) {
+  // Load instruction q of an operand of slice t into the slot at `slot`.
+  // Slices past the last (the pipeline runs ahead) repeat it into slots nobody
+  // reads.
+  auto load_a = [&](int t, uint32_t slot, int q) {
     const bool last = t >= KT - 1;
-    const int tc = last ? KT - 1 : t;
-    const uint32_t dst = smem_lds + (uint32_t)(((2 * t + op) % NSLOT) * OPB + (wave * DPW + q) * 1024);
-    if (op == 0) {
-      if constexpr (ACOL) lds_dma16_asm(col_rsrc(Ab, lda, afull, alast, tc), dst, avo[q], 0);
-      else lds_dma16_asm(ars, dst, last ? tail(avo[q], q) : avo[q], tc * ROWB);
-    } else {
-      if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bb, ldb, bfull, blast, tc), dst, bvo[q], 0);
-      else lds_dma16_asm(brs, dst, last ? tail(bvo[q], q) : bvo[q], tc * ROWB);
-    }
+    const int tc = last ? KT - 1 : t, at = (wave * DPA + q) * 1024;
+    if constexpr (ACOL) lds_dma16_asm(col_rsrc(Ab, lda, afull, alast, tc), slot + at, avo[q], 0);
+    else lds_dma16_asm(ars, slot + at, last ? tail(avo[q], at + lane * 16) : avo[q], tc * ROWB);
   };
-  auto slot = [&](int t, int op) { return smem + ((2 * t + op) % NSLOT) * OPB; };
-
-  // A fragment: 16 bytes of K per lane for index l % 32 of a 32-block: bf16,
-  // the K values 16 ks + 8 (l / 32) .. + 7 of one 32x32x16 product; fp32, the K
-  // values 4 (2 ks + l / 32) .. + 3, one for each of four 32x32x2 products.
-  const int h = lane >> 5, r32 = lane & 31;
-  const int trow = (8 * h + ((lane & 15) >> 2)) * CROWB;
-  auto frag = [&](bool col, int t, int op, int ks, int at) -> u32x4 {
-    if (!col) {
-      const int so = ((2 * ks + h) ^ ((r32 >> 1) & 7)) * 16;
-      return *(const u32x4*)(slot(t, op) + (at + r32) * ROWB + so);
-    }
-    if constexpr (BF) {
-      // Lane l of 16-lane group supplies row 8 h + (l % 16) / 4 (+ 4) of the 16
-      // K rows and four columns; the transposing read hands it column l % 32.
-      const int row = (lane & 15) >> 2;
-      const int blk = ((at >> 4) + ((lane >> 4) & 1)) ^ ckey(row);
-      const uint8_t* base = slot(t, op) + 16 * ks * CROWB + trow + blk * 32 + (lane & 3) * 8;
-      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)MUON_LDS(base));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)MUON_LDS(base + 4 * CROWB));
-      return __builtin_bit_cast(u32x4, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    } else {
-      const uint8_t* base = slot(t, op) + 4 * (2 * ks + h) * CROWB + (at + r32) * 4;
-      u32x4 v;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = *(const uint32_t*)(base + e * CROWB);
-      return v;
-    }
+  auto load_b = [&](int t, uint32_t slot, int q) {
+    const bool last = t >= KT - 1;
+    const int tc = last ? KT - 1 : t, at = (wave * DPB + q) * 1024;
+    if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bb, ldb, bfull, blast, tc), slot + at, bvo[q], 0);
+    else lds_dma16_asm(brs, slot + at, last ? tail(bvo[q], at + lane * 16) : bvo[q], tc * ROWB);
   };
-  // Fragment u (0 .. F + FN - 1) of quarter ks, in the order the products need
-  // them: a[0], b[0 .. FN - 1], a[1 .. F - 1].
-  auto read = [&](int t, int ks, int u, u32x4 (&a)[F], u32x4 (&b)[FN]) {
-    if (u == 0) a[0] = frag(ACOL, t, 0, ks, wm * WT);
-    else if (u <= FN) b[u - 1] = frag(BCOL, t, 1, ks, wn * WC + (u - 1) * 32);
-    else a[u - FN] = frag(ACOL, t, 0, ks, wm * WT + (u - FN) * 32);
+  // Slot of the next slice of the same operand.
+  auto next_a = [&](uint32_t s) {
+    const uint32_t step = RING5 ? 2 * OA::BYTES : OA::BYTES, end = smem_lds + RING_A;
+    return s + step >= end ? s + step - RING_A : s + step;
+  };
+  auto next_b = [&](uint32_t s) {
+    const uint32_t step = RING5 ? 2 * OB::BYTES : OB::BYTES, end = smem_lds + RING;
+    return s + step >= end ? s + step - (RING5 ? RING : 3 * OB::BYTES) : s + step;
   };
 
-  f32x16 acc[F][FN];
+  f32x4 acc[F][FN];
 #pragma unroll
   for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto product = [&](const u32x4& a, const u32x4& b, f32x16& c) {
+  // The B fragment comes first, so that a lane's four results are consecutive
+  // columns of one row (l % 16).
+  auto product = [&](const u32x4& a, const u32x4& b, f32x4& c) {
     if constexpr (BF) {
-      c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
-    }
-  };
-  // One quarter of a slice: its products on (ac, bc); the first slots also read
-  // the next quarter's fragments (of slice rt) into (an, bn), and load
-  // instructions q0 .. q0 + DQ - 1 of operand dop of slice dt are spread over
-  // the slots.
-  auto quarter = [&](int rt, int rks, u32x4 (&an)[F], u32x4 (&bn)[FN], const u32x4 (&ac)[F], const u32x4 (&bc)[FN],
-                     int dt, int dop, int q0) {
-#pragma unroll
-    for (int u = 0; u < NSL; ++u) {
-#pragma unroll
-      for (int q = 0; q < DQ; ++q)
-        if (u == (q * NSL) / DQ) dma(dt, dop, q0 + q);
-#pragma unroll
-      for (int f = u * FPS; f < (u + 1) * FPS && f < F + FN; ++f) read(rt, rks, f, an, bn);
-#pragma unroll
-      for (int m = u * MPS; m < (u + 1) * MPS; ++m) product(ac[m / FN], bc[m % FN], acc[m / FN][m % FN]);
-      __builtin_amdgcn_sched_barrier(0);
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(b[e]), __uint_as_float(a[e]), c, 0, 0, 0);
     }
   };
 
-  // Pipeline.  Step t multiplies slice t in four quarters; between the third
-  // and the fourth it waits for its own loads of slice t + 1 and meets the
-  // other waves, which publishes slice t + 1 and frees slice t's slots.
-  //   last quarter of step t - 1, first of step t:  B of slice t + 1
-  //   second and third quarter of step t:           A of slice t + 2
-  u32x4 a0[F], b0[FN], a1[F], b1[FN];
+  // A slice is multiplied in four quarters: half hf of its K (0, 0, 1, 1), the
+  // upper or lower half of the wave's rows.  A fragments alternate between two
+  // buffers by quarter, B fragments by half.  Each quarter reads what the next
+  // needs:
+  //   quarter 0: A half 0 lower, B half 1 (first part)
+  //   quarter 1: A half 1 upper, B half 1 (rest)
+  //   quarter 2: A half 1 lower
+  //   quarter 3: A half 0 upper and B half 0 of the next slice
+  u32x4 a[2][FH], b[2][FN];
+  uint32_t va, vb;  // this lane's addresses in the slice being read
+  const uint32_t la = OA::lane_base(lane, wm * WT), lb = OB::lane_base(lane, wn * WC);
+  auto read = [&](auto q_c, int u) {
+    constexpr int q = decltype(q_c)::value;
+    if constexpr (q == 3) {  // in the order the next products need them
+      if (u == 0) a[0][0] = OA::read(va, 0, 0);
+      else if (u <= FN) b[0][u - 1] = OB::read(vb, 0, u - 1);
+      else a[0][u - FN] = OA::read(va, 0, u - FN);
+    } else if constexpr (q == 0) {
+      if (u < FH) a[1][u] = OA::read(va, 0, FH + u);
+      else b[1][u - FH] = OB::read(vb, 1, u - FH);
+    } else if constexpr (q == 1) {
+      if (u < FH) a[0][u] = OA::read(va, 1, u);
+      else b[1][FN / 2 + u - FH] = OB::read(vb, 1, FN / 2 + u - FH);
+    } else {
+      a[1][u] = OA::read(va, 1, FH + u);
+    }
+  };
+  // Quarter q: its products in NSL slots, with its reads and the loads
+  // load(0) .. load(ND - 1) spread over them.
+  auto quarter = [&](auto q_c, auto nd_c, auto&& load) {
+    constexpr int q = decltype(q_c)::value, ND = decltype(nd_c)::value;
+    constexpr int NM = FH * FN, NSL = NM < 4 ? NM : 4, MPS = NM / NSL;
+    constexpr int NR = q == 3 ? FH + FN : (q == 2 ? FH : FH + FN / 2);
+    constexpr int RPS = (NR + NSL - 1) / NSL;
 #pragma unroll
-  for (int q = 0; q < DPW; ++q) dma(0, 0, q);
+    for (int u = 0; u < NSL; ++u) {
 #pragma unroll
-  for (int q = 0; q < DPW; ++q) dma(0, 1, q);
+      for (int d = 0; d < ND; ++d)
+        if (u == d * NSL / (ND ? ND : 1)) load(d);
 #pragma unroll
-  for (int q = 0; q < DPW; ++q) dma(1, 0, q);
+      for (int r = u * RPS; r < (u + 1) * RPS && r < NR; ++r) read(q_c, r);
 #pragma unroll
-  for (int q = 0; q < DQ; ++q) dma(1, 1, q);
-  wait_vmcnt<DPW + DQ>();
+      for (int m = u * MPS; m < (u + 1) * MPS; ++m)
+        product(a[q & 1][m / FN], b[q >> 1][m % FN], acc[(q & 1) * FH + m / FN][m % FN]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using Q0 = std::integral_constant<int, 0>;
+  using Q1 = std::integral_constant<int, 1>;
+  using Q2 = std::integral_constant<int, 2>;
+  using Q3 = std::integral_constant<int, 3>;
+
+  // Pipeline.  Between the third and the fourth quarter of slice t a wave
+  // waits for its own loads of slice t + 1 and meets the others: that
+  // publishes slice t + 1 and frees slice t's slots (the fourth quarter's
+  // fragments are in registers).  Loads, each into slots freed before:
+  //   five slots:  B of slice t + 1 in the fourth quarter of slice t - 1 and
+  //                the first of slice t, A of slice t + 2 in the second and third;
+  //   three each:  slice t + 2 in the first three quarters of slice t.
+  uint32_t sa = smem_lds, sb = smem_lds + (RING5 ? OA::BYTES : RING_A);   // slots of slice t
+  {
+    const uint32_t sa1 = next_a(sa), sb1 = next_b(sb);
+#pragma unroll
+    for (int q = 0; q < DPA; ++q) load_a(0, sa, q);
+#pragma unroll
+    for (int q = 0; q < DPB; ++q) load_b(0, sb, q);
+#pragma unroll
+    for (int q = 0; q < DPA; ++q) load_a(1, sa1, q);
+#pragma unroll
+    for (int q = 0; q < (RING5 ? DPB / 2 : DPB); ++q) load_b(1, sb1, q);
+  }
+  wait_vmcnt<DPA + (RING5 ? DPB / 2 : DPB)>();
   __builtin_amdgcn_s_barrier();
+  va = la + sa;
+  vb = lb + sb;
 #pragma unroll
-  for (int u = 0; u < F + FN; ++u) read(0, 0, u, a0, b0);
+  for (int u = 0; u < FH + FN; ++u) read(Q3{}, u);
   __builtin_amdgcn_sched_barrier(0);
   for (int t = 0; t < KT; ++t) {
-    quarter(t, 1, a1, b1, a0, b0, t + 1, 1, DQ);
-    quarter(t, 2, a0, b0, a1, b1, t + 2, 0, 0);
-    quarter(t, 3, a1, b1, a0, b0, t + 2, 0, DQ);
-    wait_vmcnt<DPW>();
+    const uint32_t sa1 = next_a(sa), sb1 = next_b(sb), sa2 = next_a(sa1), sb2 = next_b(sb1);
+    if constexpr (RING5) {
+      quarter(Q0{}, std::integral_constant<int, DPB / 2>{}, [&](int d) { load_b(t + 1, sb1, DPB / 2 + d); });
+      quarter(Q1{}, std::integral_constant<int, DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, d); });
+      quarter(Q2{}, std::integral_constant<int, DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, DPA / 2 + d); });
+      wait_vmcnt<DPA>();
+    } else {
+      quarter(Q0{}, std::integral_constant<int, DPB>{}, [&](int d) { load_b(t + 2, sb2, d); });
+      quarter(Q1{}, std::integral_constant<int, DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, d); });
+      quarter(Q2{}, std::integral_constant<int, DPA - DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, DPA / 2 + d); });
+      wait_vmcnt<DPA + DPB>();
+    }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of slice t are done
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    quarter(t + 1, 0, a0, b0, a1, b1, t + 2, 1, 0);
+    sa = sa1;
+    sb = sb1;
+    va = la + sa;
+    vb = lb + sb;
+    if constexpr (RING5)
+      quarter(Q3{}, std::integral_constant<int, DPB / 2>{}, [&](int d) { load_b(t + 2, sb2, d); });
+    else
+      quarter(Q3{}, std::integral_constant<int, 0>{}, [&](int) {});
   }
   // Loads past the last slice have landed and every wave is done with the ring.
   wait_vmcnt<0>();
   __syncthreads();
 
-  // Epilogue.  Register e of a 32 x 32 block holds row 8 (e / 4) + 4 h + e % 4,
-  // column l % 32.  Half the tile's rows at a time (the upper, then the lower
-  // half of every wave's) go through LDS as rows of fp32, then a thread
-  // finishes 8 consecutive columns of a row.
+  // Epilogue.  Half the tile's rows at a time (the upper, then the lower half
+  // of every wave's) go through LDS as rows of fp32, then a thread finishes 8
+  // consecutive columns of a row.
   float* const S = reinterpret_cast<float*>(smem);
   constexpr int HWT = WT / 2;
-  constexpr int CPR = BT / 8, RPI = NTH / CPR, NIT = RH / RPI;
+  constexpr int CPR = BN / 8, RPI = NTH / CPR, NIT = RH / RPI;
   const int c8 = (tid % CPR) * 8, rr0 = tid / CPR;
   const int64_t j = j0 + c8;
   const int valid = j >= p.N ? 0 : (p.N - j < 8 ? (int)(p.N - j) : 8);
@@ -300,18 +377,11 @@ __global__ __launch_bounds__(NW * 64, 1) void linear_tile_kernel(const LinGemm p
   if (!p.part) bias8(p, j, valid, bias);
   auto pass = [&](auto pass_c) {
     constexpr int ps = decltype(pass_c)::value;
-    // F == 1: a wave's 32 rows are split between the passes by register.
 #pragma unroll
-    for (int ii = 0; ii < (F + 1) / 2; ++ii)
+    for (int ii = 0; ii < FH; ++ii)
 #pragma unroll
       for (int jj = 0; jj < FN; ++jj)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (F == 1 && (e >> 3) != ps) continue;
-          const int blk = F == 1 ? 0 : ps * (F / 2) + ii;
-          const int row = 8 * (e >> 2) + 4 * h + (e & 3) - (F == 1 ? 16 * ps : 0);
-          S[(wm * HWT + ii * 32 + row) * PITCH + wn * WC + jj * 32 + r32] = acc[blk][jj][e];
-        }
+        *(f32x4*)(S + (wm * HWT + ii * 16 + (lane & 15)) * PITCH + wn * WC + jj * 16 + (lane >> 4) * 4) = acc[ps * FH + ii][jj];
     __syncthreads();
     with_act(p.act, [&](auto act_c) {
       constexpr int ACT = decltype(act_c)::value;
@@ -384,28 +454,34 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackJobs p) {
   *(u32x4*)((T*)w.dst + r * w.ldd + c) = o;
 }
 
-template <typename T, int KIND, int BT, int NW>
+template <typename T, int KIND, int BM, int BN, int WM, int WN>
 hipError_t launch_tile(const LinGemm& g, hipStream_t s) {
-  const int64_t grid = ((g.M + BT - 1) / BT) * ((g.N + BT - 1) / BT) * g.split;
+  const int64_t grid = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN) * g.split;
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return launch_kernel(linear_tile_kernel<T, KIND, BT, NW>, dim3((unsigned)grid), g, s, NW * 64);
+  return launch_kernel(linear_tile_kernel<T, KIND, BM, BN, WM, WN>, dim3((unsigned)grid), g, s, WM * WN * 64);
 }
 
 template <int KIND>
-hipError_t launch_kind(const LinGemm& g, bool bf16, int tile, hipStream_t s) {
+hipError_t launch_kind(const LinGemm& g, bool bf16, LinTile tile, hipStream_t s) {
   if (bf16) {
-    if (tile == 256) return launch_tile<uint16_t, KIND, 256, 8>(g, s);
-    if (tile == 128) return launch_tile<uint16_t, KIND, 128, 4>(g, s);
-    return launch_tile<uint16_t, KIND, 64, 4>(g, s);
+    switch (tile) {
+      case kTile256: return launch_tile<uint16_t, KIND, 256, 256, 2, 4>(g, s);
+      case kTile256x128: return launch_tile<uint16_t, KIND, 256, 128, 4, 2>(g, s);
+      case kTile128: return launch_tile<uint16_t, KIND, 128, 128, 2, 2>(g, s);
+      default: return launch_tile<uint16_t, KIND, 64, 64, 2, 2>(g, s);
+    }
   }
-  if (tile == 128) return launch_tile<float, KIND, 128, 4>(g, s);
-  return launch_tile<float, KIND, 64, 4>(g, s);
+  switch (tile) {
+    case kTile128: return launch_tile<float, KIND, 128, 128, 2, 2>(g, s);
+    case kTile64: return launch_tile<float, KIND, 64, 64, 2, 2>(g, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
-hipError_t launch_linear_tiles(const LinGemm& g, bool bf16, LinKind kind, int tile, hipStream_t s) {
+hipError_t launch_linear_tiles(const LinGemm& g, bool bf16, LinKind kind, LinTile tile, hipStream_t s) {
   // What the kernel's loads assume: 16-byte aligned operand rows, and panels
   // and slices within a descriptor's 2^31 bytes.
   const int64_t es = bf16 ? 2 : 4, ch = 16 / es;
@@ -414,8 +490,6 @@ hipError_t launch_linear_tiles(const LinGemm& g, bool bf16, LinKind kind, int ti
   if ((!acol || !bcol) && g.K % ch) return hipErrorInvalidValue;
   if (g.lda * es >= ((int64_t)1 << 23) || g.ldb * es >= ((int64_t)1 << 23)) return hipErrorInvalidValue;
   if (g.split < 1 || (g.split > 1 && !g.part) || (g.part && g.ldpart % 8)) return hipErrorInvalidValue;
-  if (tile != 256 && tile != 128 && tile != 64) return hipErrorInvalidValue;
-  if (!bf16 && tile == 256) return hipErrorInvalidValue;
   if (kind == kRowRow) return launch_kind<kRowRow>(g, bf16, tile, s);
   if (kind == kRowCol) return launch_kind<kRowCol>(g, bf16, tile, s);
   return launch_kind<kColCol>(g, bf16, tile, s);
