@@ -112,15 +112,15 @@ SIGNATURES = {
     "muon_step_groups_workspace_bytes": (c_i32, [ctypes.POINTER(Group), c_i64, ctypes.POINTER(HParams),
                                                  ctypes.POINTER(c_sz)]),
     "muon_step_groups": (c_i32, [ctypes.POINTER(Group), c_i64, ctypes.POINTER(HParams), c_vp, c_sz, c_vp]),
-    "muon_linear_workspace_bytes": (c_i32, [ctypes.POINTER(LinearProblem), ctypes.POINTER(c_sz)]),
-    "muon_linear": (c_i32, [ctypes.POINTER(LinearProblem), c_vp, c_sz, c_vp]),
-    "muon_linear_backward_workspace_bytes": (c_i32, [ctypes.POINTER(LinearGrad), ctypes.POINTER(c_sz)]),
-    "muon_linear_backward": (c_i32, [ctypes.POINTER(LinearGrad), c_vp, c_sz, c_vp]),
-    "muon_qk_norm_rope": (c_i32, [ctypes.POINTER(QkProblem), c_vp]),
-    "muon_qk_norm_rope_backward_workspace_bytes": (c_i32, [ctypes.POINTER(QkProblem), ctypes.POINTER(c_sz)]),
-    "muon_qk_norm_rope_backward": (c_i32, [ctypes.POINTER(QkProblem), c_vp, c_sz, c_vp]),
-    "muon_rope": (c_i32, [ctypes.POINTER(QkProblem), c_vp]),
-    "muon_rope_backward": (c_i32, [ctypes.POINTER(QkProblem), c_vp]),
+    "muon_linear_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
+    "muon_linear": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
+    "muon_linear_backward_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
+    "muon_linear_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
+    "muon_qk_norm_rope": (c_i32, [c_vp, c_vp]),
+    "muon_qk_norm_rope_backward_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
+    "muon_qk_norm_rope_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
+    "muon_rope": (c_i32, [c_vp, c_vp]),
+    "muon_rope_backward": (c_i32, [c_vp, c_vp]),
     "muon_profile_enable": (c_i32, [c_i32]),
     "muon_profile_classes": (c_i32, [ctypes.c_uint32]),
     "muon_profile_reset": (c_i32, []),

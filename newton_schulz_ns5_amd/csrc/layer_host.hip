@@ -594,15 +594,15 @@ int check_qk(const muon_qk_problem* q, bool backward, bool norm) {
 
 // Launch geometry of one call: chunk size, tokens per wave item, row parts,
 // workgroups.  It depends on the problem only, so results do too.
-struct QkPlan { int vec, tw, parts, blocks; };
+struct QkPlan { int vec, tw[2], parts[2], blocks[2]; };
 
 QkPlan plan_qk(const muon_qk_problem* q, bool backward, bool norm) {
-  QkPlan P{1, 1, 1, 1};
+  QkPlan P{1, {1, 1}, {1, 1}, {0, 0}};
   const int64_t tokens = q->batch * q->tokens;
   // Largest chunk that divides the head and its rotated part in pairs and
   // whose every access is aligned (16 bytes at most per access).
   for (int vec : {8, 4, 2}) {
-    if (q->dim % (2 * vec) || q->rotary_dim % (2 * vec) || q->dim / (2 * vec) > 32) continue;
+    if (vec * esize(q->dtype) > 16 || q->dim % (2 * vec) || q->rotary_dim % (2 * vec) || q->dim / (2 * vec) > 64) continue;
     const int64_t al = std::min<int64_t>(16, vec * esize(q->dtype));
     bool good = true;
     auto look = [&](const muon_heads& t, int64_t heads) {
@@ -619,27 +619,32 @@ QkPlan plan_qk(const muon_qk_problem* q, bool backward, bool norm) {
     if (good) { P.vec = vec; break; }
   }
   const bool sums = backward && norm;
-  if (P.vec == 1) {
-    P.blocks = (int)std::min<int64_t>(tokens, sums ? 1024 : 65536);
-    return P;
+  // Weight sums keep one partial per workgroup: at most 1024 of them.
+  for (int i = 0; i < 2; ++i) {
+    if (!q->heads[i]) continue;
+    if (P.vec == 1) {
+      P.blocks[i] = (int)std::min<int64_t>(tokens, sums ? 1024 : 65536);
+      continue;
+    }
+    const int nch = q->dim / (2 * P.vec);
+    int lpr = 4;
+    while (lpr < nch) lpr *= 2;
+    const int rpw = 64 / lpr;
+    // Tokens of one wave item: as many as fill four loads of the wave's lanes
+    // (the token's angles are formed once per item), up to eight.
+    P.tw[i] = std::max(1, std::min(8, 4 * rpw / q->heads[i]));
+    if (q->rotary_dim) P.tw[i] = std::min(P.tw[i], 512 / (q->rotary_dim / 2));
+    // few tokens: one each, and its heads over several waves
+    while (P.tw[i] > 1 && cdiv(tokens, P.tw[i]) < 2048) P.tw[i] /= 2;
+    const int64_t groups = cdiv(tokens, P.tw[i]);
+    P.parts[i] = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv((int64_t)P.tw[i] * q->heads[i], rpw), 2048 / groups));
+    P.blocks[i] = (int)std::min<int64_t>(cdiv(groups * P.parts[i], 4), sums ? 1024 : 8192);
   }
-  const int nch = q->dim / (2 * P.vec);
-  int lpr = 4;
-  while (lpr < nch) lpr *= 2;
-  const int rpw = 64 / lpr;
-  int hmin = 65537, hmax = 0;
-  for (int i = 0; i < 2; ++i)
-    if (q->heads[i]) { hmin = std::min(hmin, q->heads[i]); hmax = std::max(hmax, q->heads[i]); }
-  P.tw = std::max(1, std::min(8, rpw / hmin));
-  if (q->rotary_dim) P.tw = std::min(P.tw, 512 / (q->rotary_dim / 2));
-  const int64_t groups = cdiv(tokens, P.tw);
-  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv((int64_t)P.tw * hmax, rpw), 2048 / groups));
-  P.blocks = (int)std::min<int64_t>(cdiv(groups * P.parts, 4), sums ? 1024 : 8192);
   return P;
 }
 
 size_t qk_partial_bytes(const muon_qk_problem* q, const QkPlan& P) {
-  return align256((size_t)P.blocks * 2 * q->dim * 4);
+  return align256((size_t)(P.blocks[0] + P.blocks[1]) * q->dim * 4);
 }
 
 int run_qk(const muon_qk_problem* q, int mode, float sign, void* workspace, hipStream_t s) {
@@ -662,7 +667,7 @@ int run_qk(const muon_qk_problem* q, int mode, float sign, void* workspace, hipS
   p.inv_freq = q->inv_freq; p.inv_freq_f64 = q->inv_freq_f64;
   p.scale = q->scale; p.sign = sign; p.eps = q->eps;
   p.partial = (float*)workspace;
-  p.tw = P.tw; p.parts = P.parts; p.blocks = P.blocks;
+  for (int i = 0; i < 2; ++i) { p.tw[i] = P.tw[i]; p.parts[i] = P.parts[i]; p.blocks[i] = P.blocks[i]; }
   for (int i = 0; i < q->rotary_dim / 2; ++i) p.axis[i] = q->axis[i];
   hipError_t e = launch_qk(p, mode, q->dtype == MUON_BF16, q->interleaved != 0, P.vec, s);
   if (e != hipSuccess) return hip_fail(e, "norm and rotation kernel");

@@ -88,8 +88,8 @@ struct QkParams {
   const void* inv_freq; int32_t inv_freq_f64;
   float scale, sign;                       // cos and sin times scale, sin times sign
   float eps;
-  float* partial;                          // backward: [blocks][2][dim]
-  int32_t tw, parts, blocks;               // tokens per wave item, row parts per item, grid
+  float* partial;                          // backward: [blocks[0] + blocks[1]][dim]
+  int32_t tw[2], parts[2], blocks[2];      // of q and k: tokens per wave item, row parts per item, workgroups
   uint8_t axis[kMaxPairs];
 };
 // mode 0: rotation only; 1: norm and rotation; 2: backward of 1.  vec is the

@@ -27,7 +27,7 @@ struct Loads<float> { typedef uint32_t v4 __attribute__((ext_vector_type(4), ali
 constexpr int NWV = 8;
 
 template <typename T, int MB, int NB, int U>
-__global__ __launch_bounds__(NWV * 64) void linear_small_kernel(const LinGemm p) {
+__global__ __launch_bounds__(NWV * 64, 4) void linear_small_kernel(const LinGemm p) {
   constexpr bool BF = sizeof(T) == 2;
   constexpr int E = 32 / sizeof(T);        // values of K per lane and step
   constexpr int KS = 4 * E;                // values of K per step

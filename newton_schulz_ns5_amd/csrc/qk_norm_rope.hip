@@ -21,6 +21,8 @@
 #include "device_util.h"
 #include "muon_mi355x.h"
 
+#include <algorithm>
+
 namespace muon {
 namespace {
 
@@ -41,39 +43,39 @@ __device__ __forceinline__ f32x2_t cos_sin(const QkParams& p, int64_t tok, int p
   return f32x2_t{c * p.scale, s * p.scale * p.sign};
 }
 
+// VEC consecutive values as they are stored, in registers of 4 bytes.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_chunk(const T* src, float* v) {
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (VEC >= 4) {
+struct Chunk {
+  static constexpr int W = VEC * (int)sizeof(T) / 4;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T* src) {
+    if constexpr (W >= 4) {
 #pragma unroll
-      for (int q = 0; q < VEC / 4; ++q) {
-        const f32x4 t = ((const f32x4*)src)[q];
+      for (int q = 0; q < W / 4; ++q) {
+        const u32x4 t = ((const u32x4*)src)[q];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * q + e] = t[e];
+        for (int e = 0; e < 4; ++e) w[4 * q + e] = t[e];
       }
-    } else {
-      const f32x2_t t = *(const f32x2_t*)src;
-      v[0] = t[0]; v[1] = t[1];
-    }
-  } else {
-    uint32_t w[VEC / 2];
-    if constexpr (VEC == 8) {
-      const u32x4 t = *(const u32x4*)src;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = t[e];
-    } else if constexpr (VEC == 4) {
+    } else if constexpr (W == 2) {
       const u32x2 t = *(const u32x2*)src;
       w[0] = t[0]; w[1] = t[1];
     } else {
       w[0] = *(const uint32_t*)src;
     }
+  }
+  __device__ __forceinline__ void values(float* v) const {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      for (int e = 0; e < W; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
     }
   }
-}
+};
 
 template <typename T, int VEC>
 __device__ __forceinline__ void store_chunk(T* dst, const float* v) {
@@ -101,13 +103,19 @@ __device__ __forceinline__ T* row_ptr(const QkTensor& x, const QkParams& p, int6
   return (T*)x.p + b * x.sb + t * x.st + head * x.sh;
 }
 
-// MODE 0: rotation; 1: norm and rotation; 2: backward of 1.
+// MODE 0: rotation; 1: norm and rotation; 2: backward of 1.  A workgroup works
+// on q (the first blocks[0] workgroups) or on k.
 template <typename T, int MODE, bool INTER, int VEC, int LPR>
-__global__ __launch_bounds__(NT) void qk_kernel(const QkParams p) {
-  constexpr int RPW = 64 / LPR;           // head rows a wave holds at once
+__global__ __launch_bounds__(NT, MODE == 2 ? 4 : 5) void qk_kernel(const QkParams p) {
+  constexpr int RPW = 64 / LPR;           // head rows a wave takes at once
   __shared__ f32x2_t cs_all[NT / 64][kCsPairs];
+  __shared__ __attribute__((aligned(16))) float wts[MODE == 0 ? 4 : 2 * VEC * LPR];
   __shared__ float red[MODE == 2 ? NT / 64 : 1][MODE == 2 ? 2 * VEC * LPR : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int q = (int)blockIdx.x >= p.blocks[0];
+  const int block = (int)blockIdx.x - (q ? p.blocks[0] : 0);
+  const int H = p.heads[q], tw = p.tw[q], parts = p.parts[q];
+  const QkTensor px = p.x[q], pg = p.g[q], py = p.y[q];
   f32x2_t* const cs = cs_all[wave];
   const int pairs = p.rot / 2;
   const int j = lane % LPR, grp = lane / LPR;
@@ -127,131 +135,124 @@ __global__ __launch_bounds__(NT) void qk_kernel(const QkParams p) {
     c0 = rot0 ? j * VEC : p.rot + (j - rch) * 2 * VEC;
     c1 = rot0 ? c0 + p.rot / 2 : c0 + VEC;
   }
-  float w[2][2 * VEC], acc[2][2 * VEC];
+  float acc[MODE == 2 ? 2 * VEC : 1];
+  if constexpr (MODE == 2) {
+#pragma unroll
+    for (int e = 0; e < 2 * VEC; ++e) acc[e] = 0.f;
+  }
   if constexpr (MODE != 0) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const bool has = live && p.w[q] && p.heads[q];
-        w[q][e] = has ? load_elem(p.w[q], c0 + e, p.w_dtype == MUON_BF16) : 1.f;
-        w[q][VEC + e] = has ? load_elem(p.w[q], c1 + e, p.w_dtype == MUON_BF16) : 1.f;
-        acc[q][e] = acc[q][VEC + e] = 0.f;
-      }
+    for (int d = threadIdx.x; d < p.dim; d += NT) wts[d] = p.w[q] ? load_elem(p.w[q], d, p.w_dtype == MUON_BF16) : 1.f;
+    __syncthreads();
   }
   const float inv_d = 1.f / (float)p.dim;
-  const int64_t groups = (p.tokens + p.tw - 1) / p.tw;
-  const int64_t items = groups * p.parts;
-  for (int64_t item = (int64_t)blockIdx.x * (NT / 64) + wave; item < items; item += (int64_t)gridDim.x * (NT / 64)) {
-    const int64_t grp_tok = item / p.parts;
-    const int part = (int)(item - grp_tok * p.parts);
-    const int64_t tok0 = grp_tok * p.tw;
-    const int ntok = (int)(p.tokens - tok0 < p.tw ? p.tokens - tok0 : p.tw);
+  const int64_t groups = (p.tokens + tw - 1) / tw;
+  const int64_t items = groups * parts;
+  for (int64_t item = (int64_t)block * (NT / 64) + wave; item < items; item += (int64_t)p.blocks[q] * (NT / 64)) {
+    const int64_t grp_tok = item / parts;
+    const int part = (int)(item - grp_tok * parts);
+    const int64_t tok0 = grp_tok * tw;
+    const int ntok = (int)(p.tokens - tok0 < tw ? p.tokens - tok0 : tw);
+    const int rows = ntok * H, step = parts * RPW;
+    Chunk<T, VEC> xc[2], gc[2];
+    // Row r of the item: its token and head, and its values in xc (and gc).
+    auto load_row = [&](int r) {
+      if (!live || r >= rows) return;
+      const int t = ntok == 1 ? 0 : r / H;
+      const T* const xr = row_ptr<const T>(px, p, tok0 + t, r - t * H);
+      xc[0].load(xr + c0);
+      xc[1].load(xr + c1);
+      if constexpr (MODE == 2) {
+        const T* const gr = row_ptr<const T>(pg, p, tok0 + t, r - t * H);
+        gc[0].load(gr + c0);
+        gc[1].load(gr + c1);
+      }
+    };
+    const int r0 = part * RPW + grp;
+    load_row(r0);                         // in flight while the angles are formed
     for (int i = lane; i < ntok * pairs; i += 64) {
       const int t = i / pairs;
       cs[i] = cos_sin(p, tok0 + t, i - t * pairs);
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);   // the wave's own LDS writes before its reads
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int H = p.heads[q], rows = ntok * H;
-      for (int r = part * RPW + grp; r < rows; r += p.parts * RPW) {
-        const int t = ntok == 1 ? 0 : r / H;
-        const int head = r - t * H;
-        const int64_t tok = tok0 + t;
-        float c[2 * VEC], s[2 * VEC];     // per value: its pair's cos and sin
-        if (live) {
-          const f32x2_t* const at = cs + t * pairs;
-          if constexpr (INTER) {
-#pragma unroll
-            for (int e = 0; e < VEC / 2; ++e) {
-              const f32x2_t a = rot0 ? at[c0 / 2 + e] : f32x2_t{1.f, 0.f};
-              const f32x2_t b = rot1 ? at[c1 / 2 + e] : f32x2_t{1.f, 0.f};
-              c[2 * e] = a[0]; s[2 * e] = a[1];
-              c[VEC + 2 * e] = b[0]; s[VEC + 2 * e] = b[1];
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const f32x2_t a = rot0 ? at[c0 + e] : f32x2_t{1.f, 0.f};
-              c[e] = a[0]; s[e] = a[1];
-            }
-          }
+    for (int r = r0; r < rows; r += step) {
+      const int t = ntok == 1 ? 0 : r / H;
+      float x[2 * VEC], g[2 * VEC];
+      float ss = 0.f;
+      if (live) {
+        xc[0].values(x);
+        xc[1].values(x + VEC);
+        if constexpr (MODE == 2) {
+          gc[0].values(g);
+          gc[1].values(g + VEC);
         }
-        // v <- R v
-        auto turn = [&](float (&v)[2 * VEC]) {
-          if constexpr (INTER) {
+        if constexpr (MODE != 0) {
 #pragma unroll
-            for (int e = 0; e < 2 * VEC; e += 2) {
-              const float a = v[e], b = v[e + 1];
-              v[e] = a * c[e] - b * s[e];
-              v[e + 1] = b * c[e] + a * s[e];
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float a = v[e], b = v[VEC + e];
-              v[e] = a * c[e] - b * s[e];
-              v[VEC + e] = b * c[e] + a * s[e];
-            }
-          }
-        };
-        auto row_sum = [&](float v) {
-#pragma unroll
-          for (int off = LPR / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-          return v;
-        };
-        float x[2 * VEC], g[2 * VEC];
-        const T* const xr = row_ptr<const T>(p.x[q], p, tok, head);
-        float ss = 0.f;
-        if (live) {
-          load_chunk<T, VEC>(xr + c0, x);
-          load_chunk<T, VEC>(xr + c1, x + VEC);
-          if constexpr (MODE == 2) {
-            const T* const gr = row_ptr<const T>(p.g[q], p, tok, head);
-            load_chunk<T, VEC>(gr + c0, g);
-            load_chunk<T, VEC>(gr + c1, g + VEC);
-          }
-          if constexpr (MODE != 0) {
-#pragma unroll
-            for (int e = 0; e < 2 * VEC; ++e) ss += x[e] * x[e];
-          }
+          for (int e = 0; e < 2 * VEC; ++e) ss += x[e] * x[e];
         }
-        T* const yr = row_ptr<T>(p.y[q], p, tok, head);
-        if constexpr (MODE == 0) {
-          if (live) turn(x);
+      }
+      load_row(r + step);                 // in flight during this row's arithmetic
+      const f32x2_t* const at = cs + t * pairs;
+      // v <- R v
+      auto turn = [&](float (&v)[2 * VEC]) {
+        if constexpr (INTER) {
+#pragma unroll
+          for (int e = 0; e < 2 * VEC; e += 2) {
+            const bool on = e < VEC ? rot0 : rot1;
+            const f32x2_t cv = on ? at[((e < VEC ? c0 + e : c1 + e - VEC)) / 2] : f32x2_t{1.f, 0.f};
+            const float va = v[e], vb = v[e + 1];
+            v[e] = va * cv[0] - vb * cv[1];
+            v[e + 1] = vb * cv[0] + va * cv[1];
+          }
         } else {
-          const float rs = __frsqrt_rn(row_sum(ss) * inv_d + p.eps);
-          if constexpr (MODE == 1) {
-            if (live) {
 #pragma unroll
-              for (int e = 0; e < 2 * VEC; ++e) x[e] = x[e] * rs * w[q][e];
-              turn(x);
-            }
-          } else {
-            float dot = 0.f;
-            if (live) {
-              turn(g);
-#pragma unroll
-              for (int e = 0; e < 2 * VEC; ++e) {
-                x[e] *= rs;
-                acc[q][e] += g[e] * x[e];
-                g[e] *= w[q][e];
-                dot += g[e] * x[e];
-              }
-            }
-            dot = row_sum(dot) * inv_d;
-            if (live) {
-#pragma unroll
-              for (int e = 0; e < 2 * VEC; ++e) x[e] = rs * (g[e] - x[e] * dot);
-            }
+          for (int e = 0; e < VEC; ++e) {
+            const f32x2_t cv = rot0 ? at[c0 + e] : f32x2_t{1.f, 0.f};
+            const float va = v[e], vb = v[VEC + e];
+            v[e] = va * cv[0] - vb * cv[1];
+            v[VEC + e] = vb * cv[0] + va * cv[1];
           }
         }
-        if (live) {
-          store_chunk<T, VEC>(yr + c0, x);
-          store_chunk<T, VEC>(yr + c1, x + VEC);
+      };
+      auto weight = [&](int e) { return wts[e < VEC ? c0 + e : c1 + e - VEC]; };
+      auto row_sum = [&](float v) {
+#pragma unroll
+        for (int off = LPR / 2; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+        return v;
+      };
+      if constexpr (MODE == 0) {
+        if (live) turn(x);
+      } else {
+        const float rs = __frsqrt_rn(row_sum(ss) * inv_d + p.eps);
+        if constexpr (MODE == 1) {
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 2 * VEC; ++e) x[e] = x[e] * rs * weight(e);
+            turn(x);
+          }
+        } else {
+          float dot = 0.f;
+          if (live) {
+            turn(g);
+#pragma unroll
+            for (int e = 0; e < 2 * VEC; ++e) {
+              x[e] *= rs;
+              acc[e] += g[e] * x[e];
+              g[e] *= weight(e);
+              dot += g[e] * x[e];
+            }
+          }
+          dot = row_sum(dot) * inv_d;
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 2 * VEC; ++e) x[e] = rs * (g[e] - x[e] * dot);
+          }
         }
+      }
+      if (live) {
+        T* const yr = row_ptr<T>(py, p, tok0 + t, r - t * H);
+        store_chunk<T, VEC>(yr + c0, x);
+        store_chunk<T, VEC>(yr + c1, x + VEC);
       }
     }
     // the next token's cos and sin go where this one's were read from
@@ -261,19 +262,15 @@ __global__ __launch_bounds__(NT) void qk_kernel(const QkParams p) {
   if constexpr (MODE == 2) {
     // Weight gradients: the row groups of a wave, then the waves, in order.
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int e = 0; e < 2 * VEC; ++e) {
+      float v = acc[e];
 #pragma unroll
-      for (int e = 0; e < 2 * VEC; ++e) {
-        float v = acc[q][e];
-#pragma unroll
-        for (int off = 32; off >= LPR; off >>= 1) v += __shfl_xor(v, off, 64);
-        if (grp == 0 && live) red[wave][(e < VEC ? c0 + e : c1 + e - VEC)] = v;
-      }
-      __syncthreads();
-      for (int d = threadIdx.x; d < p.dim; d += NT)
-        p.partial[((int64_t)blockIdx.x * 2 + q) * p.dim + d] = ((red[0][d] + red[1][d]) + red[2][d]) + red[3][d];
-      __syncthreads();
+      for (int off = 32; off >= LPR; off >>= 1) v += __shfl_xor(v, off, 64);
+      if (grp == 0 && live) red[wave][(e < VEC ? c0 + e : c1 + e - VEC)] = v;
     }
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.dim; d += NT)
+      p.partial[(int64_t)blockIdx.x * p.dim + d] = ((red[0][d] + red[1][d]) + red[2][d]) + red[3][d];
   }
 }
 
@@ -286,10 +283,12 @@ template <typename T, int MODE, bool INTER>
 __global__ __launch_bounds__(64) void qk_plain_kernel(const QkParams p) {
   constexpr bool BF = sizeof(T) == 2;
   __shared__ f32x2_t cs[kMaxPairs];
-  __shared__ float xs[kMaxDim], gs[kMaxDim], dws[MODE == 2 ? 2 : 1][MODE == 2 ? kMaxDim : 1];
+  __shared__ float xs[kMaxDim], gs[kMaxDim], dws[MODE == 2 ? kMaxDim : 1];
   const int lane = threadIdx.x, pairs = p.rot / 2;
+  const int q = (int)blockIdx.x >= p.blocks[0];
+  const int block = (int)blockIdx.x - (q ? p.blocks[0] : 0);
   if constexpr (MODE == 2) {
-    for (int d = lane; d < p.dim; d += 64) dws[0][d] = dws[1][d] = 0.f;
+    for (int d = lane; d < p.dim; d += 64) dws[d] = 0.f;
   }
   // partner of value d, its pair and the sign of the sine term
   auto turned = [&](const float* v, int d) {
@@ -301,10 +300,9 @@ __global__ __launch_bounds__(64) void qk_plain_kernel(const QkParams p) {
     const f32x2_t a = cs[pair];
     return v[d] * a[0] + (first ? -v[other] : v[other]) * a[1];
   };
-  for (int64_t tok = blockIdx.x; tok < p.tokens; tok += gridDim.x) {
+  for (int64_t tok = block; tok < p.tokens; tok += p.blocks[q]) {
     __syncthreads();
     for (int i = lane; i < pairs; i += 64) cs[i] = cos_sin(p, tok, i);
-    for (int q = 0; q < 2; ++q)
       for (int head = 0; head < p.heads[q]; ++head) {
         const T* const xr = row_ptr<const T>(p.x[q], p, tok, head);
         T* const yr = row_ptr<T>(p.y[q], p, tok, head);
@@ -327,7 +325,7 @@ __global__ __launch_bounds__(64) void qk_plain_kernel(const QkParams p) {
           float dot = 0.f;
           for (int d = lane; d < p.dim; d += 64) {
             const float g = turned(gs, d), n = xs[d] * rs;
-            dws[q][d] += g * n;
+            dws[d] += g * n;
             dot += g * wt(d) * n;
           }
           dot = wave_sum(dot) / (float)p.dim;
@@ -338,32 +336,32 @@ __global__ __launch_bounds__(64) void qk_plain_kernel(const QkParams p) {
   }
   if constexpr (MODE == 2) {
     __syncthreads();
-    for (int d = lane; d < p.dim; d += 64) {
-      p.partial[((int64_t)blockIdx.x * 2) * p.dim + d] = dws[0][d];
-      p.partial[((int64_t)blockIdx.x * 2 + 1) * p.dim + d] = dws[1][d];
-    }
+    for (int d = lane; d < p.dim; d += 64) p.partial[(int64_t)blockIdx.x * p.dim + d] = dws[d];
   }
 }
 
 template <typename T, int MODE, bool INTER, int VEC>
 hipError_t launch_vec(const QkParams& p, hipStream_t s) {
   const int nch = p.dim / (2 * VEC);
-  const dim3 g((unsigned)p.blocks);
+  const dim3 g((unsigned)(p.blocks[0] + p.blocks[1]));
   if (nch <= 4) return launch_kernel(qk_kernel<T, MODE, INTER, VEC, 4>, g, p, s, NT);
   if (nch <= 8) return launch_kernel(qk_kernel<T, MODE, INTER, VEC, 8>, g, p, s, NT);
   if (nch <= 16) return launch_kernel(qk_kernel<T, MODE, INTER, VEC, 16>, g, p, s, NT);
   if (nch <= 32) return launch_kernel(qk_kernel<T, MODE, INTER, VEC, 32>, g, p, s, NT);
+  if (nch <= 64) return launch_kernel(qk_kernel<T, MODE, INTER, VEC, 64>, g, p, s, NT);
   return hipErrorInvalidValue;
 }
 
 template <typename T, int MODE, bool INTER>
 hipError_t launch_mode(const QkParams& p, int vec, hipStream_t s) {
-  if (vec > 1 && (p.dim % (2 * vec) || p.rot % (2 * vec) || p.tw * (p.rot / 2) > kCsPairs)) return hipErrorInvalidValue;
+  if (vec > 1 && (p.dim % (2 * vec) || p.rot % (2 * vec) || std::max(p.tw[0], p.tw[1]) * (p.rot / 2) > kCsPairs)) return hipErrorInvalidValue;
   switch (vec) {
-    case 8: return launch_vec<T, MODE, INTER, 8>(p, s);
+    case 8:  // 16 bytes of bf16; fp32 takes 4 values, twice the bytes per lane would spill
+      if constexpr (sizeof(T) == 2) return launch_vec<T, MODE, INTER, 8>(p, s);
+      else return hipErrorInvalidValue;
     case 4: return launch_vec<T, MODE, INTER, 4>(p, s);
     case 2: return launch_vec<T, MODE, INTER, 2>(p, s);
-    default: return p.dim <= kMaxDim ? launch_kernel(qk_plain_kernel<T, MODE, INTER>, dim3((unsigned)p.blocks), p, s, 64)
+    default: return p.dim <= kMaxDim ? launch_kernel(qk_plain_kernel<T, MODE, INTER>, dim3((unsigned)(p.blocks[0] + p.blocks[1])), p, s, 64)
                                      : hipErrorInvalidValue;
   }
 }
@@ -376,37 +374,42 @@ hipError_t launch_type(const QkParams& p, int mode, bool inter, int vec, hipStre
 }
 
 struct WeightSum {
-  const float* partial; int32_t blocks, dim;
+  const float* partial; int32_t blocks[2], dim;
   void* out[2]; int32_t out_dtype;
 };
 
-// dw[q][d] = the blocks' partials in order: 16 threads per value add every
-// sixteenth block, then their sums in order.
-__global__ __launch_bounds__(256) void qk_weight_sum_kernel(const WeightSum p) {
-  __shared__ float red[16][17];
-  const int v = threadIdx.x & 15, part = threadIdx.x >> 4;
-  const int at = blockIdx.x * 16 + v;
+// dw[q][d] = the sum of tensor q's workgroups' partials: 64 threads per value
+// each add every 64th, then the 64 sums are added pairwise.  1024 workgroups of
+// 128 values: 4.8 us (16 threads per value, one load at a time: 20.6 us).
+__global__ __launch_bounds__(1024) void qk_weight_sum_kernel(const WeightSum p) {
+  __shared__ float red[64][17];
+  const int v = threadIdx.x & 15, part = threadIdx.x >> 4, q = blockIdx.y;
+  const int d = blockIdx.x * 16 + v;
+  const float* const src = p.partial + (q ? (int64_t)p.blocks[0] * p.dim : 0);
   float t = 0.f;
-  if (at < 2 * p.dim)
-    for (int b = part; b < p.blocks; b += 16) t += p.partial[(int64_t)b * 2 * p.dim + at];
+  if (d < p.dim) {
+#pragma unroll 8
+    for (int b = part; b < p.blocks[q]; b += 64) t += src[(int64_t)b * p.dim + d];
+  }
   red[part][v] = t;
-  __syncthreads();
-  if (part || at >= 2 * p.dim) return;
-  for (int i = 1; i < 16; ++i) t += red[i][v];
-  const int q = at >= p.dim;
-  if (p.out[q]) store_elem(p.out[q], at - q * p.dim, t, p.out_dtype == MUON_BF16);
+#pragma unroll
+  for (int half = 32; half >= 1; half >>= 1) {
+    __syncthreads();
+    if (part < half) red[part][v] += red[part + half][v];
+  }
+  if (part == 0 && d < p.dim && p.out[q]) store_elem(p.out[q], d, red[0][v], p.out_dtype == MUON_BF16);
 }
 
 }  // namespace
 
 hipError_t launch_qk(const QkParams& p, int mode, bool bf16, bool interleaved, int vec, hipStream_t s) {
-  if (p.blocks <= 0) return hipErrorInvalidValue;
+  if (p.blocks[0] + p.blocks[1] <= 0) return hipErrorInvalidValue;
   return bf16 ? launch_type<uint16_t>(p, mode, interleaved, vec, s) : launch_type<float>(p, mode, interleaved, vec, s);
 }
 
 hipError_t launch_qk_weight_sum(const QkParams& p, void* const out[2], int32_t out_dtype, hipStream_t s) {
-  const WeightSum w{p.partial, p.blocks, p.dim, {out[0], out[1]}, out_dtype};
-  return launch_kernel(qk_weight_sum_kernel, dim3((unsigned)((2 * p.dim + 15) / 16)), w, s, 256);
+  const WeightSum w{p.partial, {p.blocks[0], p.blocks[1]}, p.dim, {out[0], out[1]}, out_dtype};
+  return launch_kernel(qk_weight_sum_kernel, dim3((unsigned)((p.dim + 15) / 16), 2), w, s, 1024);
 }
 
 }  // namespace muon

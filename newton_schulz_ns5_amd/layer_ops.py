@@ -9,11 +9,12 @@ requires a gradient; the ``*_backward`` entry points are the same gradients
 called directly.
 """
 import ctypes
+import struct
 
 import torch
 
-from . import MuonError, _dt, _lib
-from ._lib import LinearGrad, LinearProblem, QkProblem
+from . import MuonError, _lib
+from ._lib import MUON_BF16, MUON_F32
 
 __all__ = ["linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward",
            "ACTIVATIONS"]
@@ -32,38 +33,59 @@ def _act(name):
         raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"activation {name!r} is not one of {sorted(filter(None, ACTIVATIONS))}")
 
 
+_CODE = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+
+# The problem structures of the C ABI, packed in one call each (setting a
+# ctypes structure field by field costs more than the kernel of a small call).
+_LINEAR = struct.Struct("@qqq ii Pq Pq P Pq Pq Pq iiii")
+_GRAD = struct.Struct("@qqq ii Pq Pq Pq Pq Pq Pq P iiiiii")
+_QK = struct.Struct("@qq iiiiii " + "Pqqq" * 6 + " PPPP Pqqq P iiii ff 256s")
+
+
+def _dt(t):
+    code = _CODE.get(t.dtype)
+    if code is None:
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"dtype {t.dtype} is not float32 or bfloat16")
+    return code
+
+
 def _same_device(first, *others):
-    dev = first.device
-    if dev.type != "cuda":
-        _bad(f"tensors must be on a GPU, got {dev}")
+    """The index of the one GPU that holds every tensor."""
+    dev = first.get_device()
+    if dev < 0:
+        _bad(f"tensors must be on a GPU, got {first.device}")
     for t in others:
-        if t is not None and t.device != dev:
-            _bad(f"tensors are on {t.device} and {dev}")
+        if t is not None and t.get_device() != dev:
+            _bad(f"tensors are on {t.device} and {first.device}")
     return dev
+
+
+# The raw handle of a device's current stream (what current_stream().cuda_stream
+# gives, without making a Stream object).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _call(dev, fn, problem, need):
     """Run fn(problem[, workspace]) on the device's current stream.  The device
     is made current for the launch when another one is."""
-    if dev.index is not None and dev.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _call_here(dev, fn, problem, need)
     return _call_here(dev, fn, problem, need)
 
 
 def _call_here(dev, fn, problem, need):
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    p = ctypes.byref(problem)
     if need is None:
-        return _lib.check(fn(p, stream))
+        return _lib.check(fn(problem, _raw_stream(dev)))
     size = ctypes.c_size_t(0)
-    _lib.check(need(p, ctypes.byref(size)))
+    _lib.check(need(problem, ctypes.byref(size)))
     if not size.value:
-        return _lib.check(fn(p, None, 0, stream))
+        return _lib.check(fn(problem, None, 0, _raw_stream(dev)))
     # Taken from torch's allocator for this call: it goes back to the stream that
     # runs the call, and one taken under capture belongs to that graph alone.
-    ws = torch.empty(size.value, dtype=torch.uint8, device=dev)
-    return _lib.check(fn(p, ws.data_ptr(), size.value, stream))
+    ws = torch.empty(size.value, dtype=torch.uint8, device=torch.device("cuda", dev))
+    return _lib.check(fn(problem, ws.data_ptr(), size.value, _raw_stream(dev)))
 
 
 # ---- the linear product ---------------------------------------------------------------
@@ -138,18 +160,18 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
     xp, m, _, ldx = _rows(x, "x", k)
     shape = x.shape[:-1] + (n,)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype if residual is None else residual.dtype, device=dev)
+        out = torch.empty(shape, dtype=x.dtype if residual is None else residual.dtype, device=x.device)
     if (return_preact or preact is not None):
         if preact is None:
-            preact = torch.empty(shape, dtype=x.dtype, device=dev)
+            preact = torch.empty(shape, dtype=x.dtype, device=x.device)
         elif preact.dtype != x.dtype:
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"preact must be {x.dtype} like x")
     yp, ldy = _check_matrix(out, "out", m, n)
-    zp, ldz = _check_matrix(preact, "preact", m, n) if preact is not None else (None, 0)
-    rp, ldr = _check_matrix(residual, "residual", m, n) if residual is not None else (None, 0)
-    bp = _vector(bias, "bias", n) if bias is not None else None
-    prob = LinearProblem(m, n, k, code, act, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz,
-                         _dt(bias) if bias is not None else 0, _dt(residual) if residual is not None else 0, _dt(out), 0)
+    zp, ldz = _check_matrix(preact, "preact", m, n) if preact is not None else (0, 0)
+    rp, ldr = _check_matrix(residual, "residual", m, n) if residual is not None else (0, 0)
+    bp = _vector(bias, "bias", n) if bias is not None else 0
+    prob = _LINEAR.pack(m, n, k, code, act, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz,
+                        _dt(bias) if bias is not None else 0, _dt(residual) if residual is not None else 0, _dt(out), 0)
     L = _lib.lib()
     _call(dev, L.muon_linear, prob, L.muon_linear_workspace_bytes)
     return (out, preact) if return_preact else out
@@ -176,7 +198,7 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
     wp, n, k, ldw = _rows(w, "w")
     xp, m, _, ldx = _rows(x, "x", k)
     gp, ldg = _check_matrix(dy, "dy", m, n)
-    zp, ldz = None, 0
+    zp, ldz = 0, 0
     if act:
         if preact is None:
             _bad("an activation's gradient needs preact")
@@ -186,15 +208,15 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         _bad("accumulate needs the tensors to add to")
     if dx is None and need_dx:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if dw is None and need_dw:
-        dw = torch.empty((n, k), dtype=dw_dtype or w.dtype, device=dev)
+        dw = torch.empty((n, k), dtype=dw_dtype or w.dtype, device=x.device)
     if dbias is None and need_dbias:
-        dbias = torch.empty((n,), dtype=dbias_dtype or w.dtype, device=dev)
-    dxp, lddx = _check_matrix(dx, "dx", m, k) if dx is not None else (None, 0)
-    dwp, lddw = _check_matrix(dw, "dw", n, k) if dw is not None else (None, 0)
-    dbp = _vector(dbias, "dbias", n) if dbias is not None else None
-    prob = LinearGrad(m, n, k, code, act, gp, ldg, xp, ldx, wp, ldw, zp, ldz, dxp, lddx, dwp, lddw, dbp,
+        dbias = torch.empty((n,), dtype=dbias_dtype or w.dtype, device=x.device)
+    dxp, lddx = _check_matrix(dx, "dx", m, k) if dx is not None else (0, 0)
+    dwp, lddw = _check_matrix(dw, "dw", n, k) if dw is not None else (0, 0)
+    dbp = _vector(dbias, "dbias", n) if dbias is not None else 0
+    prob = _GRAD.pack(m, n, k, code, act, gp, ldg, xp, ldx, wp, ldw, zp, ldz, dxp, lddx, dwp, lddw, dbp,
                       _dt(dy), _dt(dx) if dx is not None else 0, _dt(dw) if dw is not None else 0,
                       _dt(dbias) if dbias is not None else 0, int(bool(accumulate)), 0)
     L = _lib.lib()
@@ -239,7 +261,8 @@ class _Linear(torch.autograd.Function):
 
 
 # ---- per-head norms and rotation ----------------------------------------------------------
-_NO_HEADS = (None, 0, 0, 0)
+_NO_HEADS = (0, 0, 0, 0)
+_NO_PAIR = _NO_HEADS * 2
 
 
 def _heads_of(t, name, like=None):
@@ -269,74 +292,68 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"q is {q.dtype} and k {k.dtype}: one type is needed")
     if first.dim() not in (3, 4):
         _bad("q and k must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
-    every = [t for pair in (x, g, y) if pair is not None for t in pair if t is not None]
-    wts = [t for pair in (weight, dweight) for t in pair if t is not None]
-    dev = _same_device(first, positions, inv_freq, *every, *wts)
-    for t in every:
-        if t.dtype != first.dtype:
-            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"head tensors are {t.dtype} and {first.dtype}: one type is needed")
+    dtype = first.dtype
+    fields = []
+    for pair in (x, g, y):
+        if pair is None:
+            fields += _NO_PAIR
+            continue
+        for t, like, name in ((pair[0], q, "q"), (pair[1], k, "k")):
+            if (t is None) != (like is None):
+                _bad("q and k must both be given, or both be left out, in every pair of tensors")
+            if t is not None and t.dtype != dtype:
+                raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"head tensors are {t.dtype} and {dtype}: one type is needed")
+            fields += _heads_of(t, name, like)
+    dev = _same_device(positions, inv_freq, *(x or ()), *(g or ()), *(y or ()), *weight, *dweight)
     batch, tokens = (first.shape[0], first.shape[1]) if first.dim() == 4 else (1, first.shape[0])
     dim = first.shape[-1]
-    p = QkProblem()
-    p.batch, p.tokens, p.dim = batch, tokens, dim
-    p.heads[0] = q.shape[-2] if q is not None else 0
-    p.heads[1] = k.shape[-2] if k is not None else 0
-    p.dtype = _dt(first)
-    for field, pair in ((p.x, x), (p.g, g), (p.y, y)):
-        if pair is not None:
-            for i, like in ((0, q), (1, k)):
-                if (pair[i] is None) != (like is None):
-                    _bad("q and k must both be given, or both be left out, in every pair of tensors")
-                field[i] = _heads_of(pair[i], "qk"[i], like)
-    for i in range(2):
-        if weight[i] is not None:
-            p.weight[i] = _vector(weight[i], f"the norm weight of {'qk'[i]}", dim)
-        if dweight[i] is not None:
-            p.dweight[i] = _vector(dweight[i], f"the weight gradient of {'qk'[i]}", dim)
-    if wts:
-        if any(t.dtype != wts[0].dtype for t in wts):
+    wtype = None
+    for t in weight + dweight:
+        if t is None:
+            fields.append(0)
+            continue
+        if wtype is not None and t.dtype != wtype:
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "the norm weights and their gradients need one type")
-        p.weight_dtype = _dt(wts[0])
+        wtype = t.dtype
+        wcode = _dt(t)
+        fields.append(_vector(t, "a norm weight", dim))
     if inv_freq.dim() != 1 or inv_freq.dtype not in (torch.float32, torch.float64) or not inv_freq.is_contiguous():
         _bad("inv_freq must be a contiguous fp32 or fp64 vector of one frequency per pair")
     pairs = inv_freq.shape[0]
     if 2 * pairs > dim or pairs > _lib.QK_MAX_PAIRS:
         _bad(f"{pairs} pairs do not fit heads of {dim} (at most {_lib.QK_MAX_PAIRS})")
-    p.rotary_dim = 2 * pairs
-    p.inv_freq, p.inv_freq_f64 = inv_freq.data_ptr(), int(inv_freq.dtype == torch.float64)
     if positions.dtype not in (torch.int32, torch.int64):
         raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"positions are {positions.dtype}, not int32 or int64")
-    lead, shape, st = tuple(first.shape[:-2]), tuple(positions.shape), positions.stride()
-    p.axes = 1
+    lead, shape, st = first.shape[:-2], positions.shape, positions.stride()
+    naxes, axis_st, batch_st = 1, 0, 0
     if shape == lead:
-        p.pos_token_stride = st[-1]
-        p.pos_batch_stride = st[0] if len(lead) == 2 else 0
-    elif len(shape) == len(lead) + 1 and shape[1:] == lead:
-        p.axes, p.pos_axis_stride, p.pos_token_stride = shape[0], st[0], st[-1]
-        p.pos_batch_stride = st[1] if len(lead) == 2 else 0
+        token_st = st[-1]
+        batch_st = st[0] if len(lead) == 2 else 0
+    elif shape[1:] == lead:
+        naxes, axis_st, token_st = shape[0], st[0], st[-1]
+        batch_st = st[1] if len(lead) == 2 else 0
     elif len(lead) == 2 and shape == lead[1:]:
-        p.pos_token_stride = st[0]
+        token_st = st[0]
     else:
-        _bad(f"positions {shape} do not go with tokens {lead}")
-    p.positions, p.positions_i64 = positions.data_ptr(), int(positions.dtype == torch.int64)
-    if axes is not None and sections is not None:
-        _bad("give sections or axes, not both")
+        _bad(f"positions {tuple(shape)} do not go with tokens {tuple(lead)}")
+    turns = b""
     if sections is not None:
-        if len(sections) != p.axes or sum(sections) != pairs or min(sections) < 0:
-            _bad(f"sections {list(sections)} do not split {pairs} pairs over {p.axes} axes")
-        turns = b"".join(bytes((i,)) * n for i, n in enumerate(sections))
+        if axes is not None:
+            _bad("give sections or axes, not both")
+        if len(sections) != naxes or sum(sections) != pairs or min(sections) < 0:
+            _bad(f"sections {list(sections)} do not split {pairs} pairs over {naxes} axes")
+        if naxes > 1:
+            turns = b"".join([bytes((i,)) * n for i, n in enumerate(sections)])
     elif axes is not None:
         turns = bytes(axes)
-        if len(turns) != pairs or (turns and max(turns) >= p.axes):
-            _bad(f"axes must name one of {p.axes} axes for each of {pairs} pairs")
-    elif p.axes > 1:
+        if len(turns) != pairs or (turns and max(turns) >= naxes):
+            _bad(f"axes must name one of {naxes} axes for each of {pairs} pairs")
+    elif naxes > 1:
         _bad("positions with several axes need sections or axes")
-    else:
-        turns = b""
-    if turns and p.axes > 1:
-        ctypes.memmove(p.axis, turns, len(turns))
-    p.interleaved, p.scale, p.eps = int(bool(interleaved)), float(scale), float(eps)
-    return dev, p
+    return dev, _QK.pack(batch, tokens, q.shape[-2] if q is not None else 0, k.shape[-2] if k is not None else 0, dim,
+                         2 * pairs, _dt(first), wcode if wtype is not None else 0, *fields, positions.data_ptr(), axis_st,
+                         batch_st, token_st, inv_freq.data_ptr(), positions.dtype is torch.int64,
+                         inv_freq.dtype is torch.float64, bool(interleaved), naxes, scale, eps, turns)
 
 
 def _like(t, out):
@@ -378,7 +395,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     dwt = (_like(q_weight, None), _like(k_weight, None))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), (dq_out, dk_out), y,
                          (q_weight, k_weight), dwt, eps)
-    if p.batch * p.tokens == 0:
+    if all(t is None or not t.numel() for t in (q, k)):  # an empty sum, which the library has no work for
         for t in dwt:
             if t is not None:
                 t.zero_()

@@ -36,6 +36,25 @@ def test_ctypes_structs_match_c_layout():
             assert getattr(py, f).offset == int(lay[f"{c}.{f}"]), (c, f)
 
 
+def test_packed_problems_match_the_structs():
+    from newton_schulz_ns5_amd import layer_ops
+    for packed, py in [(layer_ops._LINEAR, _lib.LinearProblem), (layer_ops._GRAD, _lib.LinearGrad), (layer_ops._QK, _lib.QkProblem)]:
+        assert packed.size == ctypes.sizeof(py)
+    # every field its own number, read back through the structure
+    p = _lib.LinearProblem.from_buffer_copy(layer_ops._LINEAR.pack(*range(1, 21)))
+    assert [getattr(p, f) for f, _ in p._fields_] == list(range(1, 21))
+    p = _lib.LinearGrad.from_buffer_copy(layer_ops._GRAD.pack(*range(1, 25)))
+    assert [getattr(p, f) for f, _ in p._fields_] == list(range(1, 25))
+    nums = list(range(1, 9)) + list(range(100, 124)) + list(range(200, 213)) + [1.5, 2.5, bytes(range(256))]
+    q = _lib.QkProblem.from_buffer_copy(layer_ops._QK.pack(*nums))
+    assert (q.batch, q.tokens, list(q.heads), q.dim, q.rotary_dim, q.dtype, q.weight_dtype) == (1, 2, [3, 4], 5, 6, 7, 8)
+    flat = [v for pair in (q.x, q.g, q.y) for h in pair for v in (h.p, h.batch_stride, h.token_stride, h.head_stride)]
+    assert flat == list(range(100, 124)) and list(q.weight) + list(q.dweight) == [200, 201, 202, 203]
+    assert (q.positions, q.pos_axis_stride, q.pos_batch_stride, q.pos_token_stride, q.inv_freq) == (204, 205, 206, 207, 208)
+    assert (q.positions_i64, q.inv_freq_f64, q.interleaved, q.axes, q.scale, q.eps) == (209, 210, 211, 212, 1.5, 2.5)
+    assert bytes(q.axis) == bytes(range(256))
+
+
 def linear_problem(**over):
     a = dict(m=8, n=16, k=32, dtype=1, activation=0, x=FAKE, x_row_stride=32, w=FAKE + MIB, w_row_stride=32, bias=None,
              residual=None, residual_row_stride=16, y=FAKE + 2 * MIB, y_row_stride=16, preact=None, preact_row_stride=16,
