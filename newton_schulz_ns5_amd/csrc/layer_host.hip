@@ -174,8 +174,9 @@ Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t d
   return o;
 }
 
-// How a product M x N over K runs: columns 0 .. n1 - 1 in tiles `first`, the
-// others in tiles `rest`, and the sum in `split` chunks.
+// How a product M x N over K runs: rows 0 .. m1 - 1 and columns 0 .. n1 - 1 in
+// tiles `first`, the others (rows or columns, not both) in tiles `rest`, and
+// the sum in `split` chunks.
 //
 // Workgroups of a tile run in rounds of as many as the chip holds at once; a
 // round takes a fixed time (pipeline start, epilogue) and a time per slice of
@@ -185,7 +186,7 @@ Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t d
 // rounds), 416 in 256 x 128 (7 rounds), HYB with the last half round of the
 // larger ones in the smaller; 2048 x 4096 over 6144: 132 us in 256 x 256 (half
 // a round), 94 in 256 x 128, 118 in 128, 166 in 64.
-struct Tiling { LinTile first, rest; int64_t n1; int split; };
+struct Tiling { LinTile first, rest; int64_t m1, n1; int split; };
 
 struct TileCost { LinTile tile; int bm, bn, slots; double fixed, u0, u1; };
 constexpr TileCost kCostBf16[] = {{kTile256, 256, 256, 256, 8.0, 1.15, 1.65},
@@ -206,7 +207,7 @@ Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
   const TileCost* costs = bf ? kCostBf16 : kCostF32;
   const int n = bf ? 4 : 2;
   const int64_t slices = std::max<int64_t>(1, cdiv(K, bf ? 64 : 32));
-  Tiling best{kTile64, kTile64, N, 1};
+  Tiling best{kTile64, kTile64, M, N, 1};
   double least = 1e30;
   for (int i = 0; i < n; ++i) {
     const TileCost& c = costs[i];
@@ -218,15 +219,23 @@ Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
       if (split > 1) t += 4.0 + (double)(M * N) * 4.0 * (split + 1) / 4e6;  // a launch, and the products at 4 TB/s
       if (t < least) {
         least = t;
-        best = {c.tile, c.tile, N, split};
+        best = {c.tile, c.tile, M, N, split};
       }
     }
   }
   if (bf) {  // whole rounds of the largest tile, the rest in the next smaller
-    const int64_t tm = cdiv(M, 256), cols = tm <= 256 ? cdiv(N, 256) * tm / 256 * 256 / tm : 0;
-    if (cols > 0 && cols * 256 < N) {
+    const int64_t tm = cdiv(M, 256), tn = cdiv(N, 256), rounds = tm * tn / 256;
+    const int64_t cols = rounds * 256 / tm, rows = rounds * 256 / tn;  // whole columns or rows of tiles in them
+    if (cols > 0 && cols < tn) {
       const double t = tile_time(kCostBf16[0], cols * tm, slices) + tile_time(kCostBf16[1], tm * cdiv(N - cols * 256, 128), slices);
-      if (t < least) best = {kTile256, kTile256x128, cols * 256, 1};
+      if (t < least) {
+        least = t;
+        best = {kTile256, kTile256x128, M, cols * 256, 1};
+      }
+    }
+    if (rows > 0 && rows < tm) {
+      const double t = tile_time(kCostBf16[0], rows * tn, slices) + tile_time(kCostBf16[1], (tm - rows) * cdiv(N, 128), slices);
+      if (t < least) best = {kTile256, kTile256x128, rows * 256, N, 1};
     }
   }
   return best;
@@ -270,17 +279,20 @@ hipError_t run_product(LinGemm g, int32_t dt, LinKind kind, const Tiling& t, cha
   g.part = t.split > 1 ? (float*)part : nullptr;
   g.ldpart = part_ld(g.N);
   hipError_t e;
-  if (t.n1 < g.N) {
-    LinGemm r = g;  // columns n1 .. N - 1
-    const int64_t n1 = t.n1;
+  if (t.n1 < g.N || t.m1 < g.M) {
+    LinGemm r = g;  // rows m1 .. M - 1 or columns n1 .. N - 1
+    const int64_t m1 = t.m1 < g.M ? t.m1 : 0, n1 = t.n1 < g.N ? t.n1 : 0;
     auto past = [&](const void* p, int64_t elems, int32_t d) { return p ? (const char*)p + elems * esize(d) : nullptr; };
+    r.M = g.M - m1;
     r.N = g.N - n1;
+    r.A = past(g.A, kind == kColCol ? m1 : m1 * g.lda, dt);
     r.B = past(g.B, kind == kRowRow ? n1 * g.ldb : n1, dt);
     r.bias = past(g.bias, n1, g.bias_dtype);
-    r.add = past(g.add, n1, g.add_dtype);
-    r.Y = (void*)past(g.Y, n1, g.y_dtype);
-    r.Z = (void*)past(g.Z, n1, dt);
-    g.N = n1;
+    r.add = past(g.add, m1 * g.ldadd + n1, g.add_dtype);
+    r.Y = (void*)past(g.Y, m1 * g.ldy + n1, g.y_dtype);
+    r.Z = (void*)past(g.Z, m1 * g.ldz + n1, dt);
+    if (m1) g.M = m1;
+    if (n1) g.N = n1;
     e = launch_linear_tiles(g, bf, kind, t.first, s);
     return e == hipSuccess ? launch_linear_tiles(r, bf, kind, t.rest, s) : e;
   }
@@ -301,6 +313,7 @@ int vec_flags(const LinGemm& g, int32_t dt) {
 // Work of a forward call: the small kernel for few rows, else tiles.
 struct LinearPlan {
   bool small;
+  int nb;          // small: weight rows per workgroup / 16
   Operand x, w;
   Tiling t;
   size_t part_off, total;
@@ -309,7 +322,20 @@ struct LinearPlan {
 LinearPlan plan_linear(const muon_linear_problem* q) {
   LinearPlan P{};
   P.small = q->m <= kSmallRows;
-  if (P.small || q->m == 0 || q->n == 0) return P;
+  if (q->m == 0 || q->n == 0) return P;
+  if (P.small) {
+    // 64 weight rows per workgroup where that many workgroups, times the
+    // chunks K can be split into (at least two steps per wave each), come near
+    // the 256 CUs; a split pays for its second launch where every workgroup
+    // would read more of the tokens than of a 16-row piece of the weight.
+    const int64_t wgs = cdiv(q->n, 64), steps = cdiv(q->k * esize(q->dtype), 128);
+    const int64_t split = std::max<int64_t>(1, std::min<int64_t>({4, 256 / wgs, steps / 16}));
+    const bool many = q->m > 16 || (q->m > 8 && steps >= 128);
+    P.nb = wgs >= 192 || (many && wgs * split >= 192) ? 4 : 1;
+    P.t.split = P.nb == 4 && wgs < 192 ? (int)split : 1;
+    P.total = part_bytes(q->m, q->n, P.t.split);
+    return P;
+  }
   P.x = operand(q->x, q->m, q->k, q->x_row_stride, q->dtype, true);
   P.w = operand(q->w, q->n, q->k, q->w_row_stride, q->dtype, true);
   P.t = choose_tiling(q->m, q->n, q->k, q->dtype == MUON_BF16);
@@ -406,7 +432,12 @@ int muon_linear(const muon_linear_problem* q, void* workspace, size_t workspace_
   g.split = 1;
   hipError_t e;
   if (P.small) {
-    e = launch_linear_small(g, q->dtype == MUON_BF16, s);
+    const bool bf = q->dtype == MUON_BF16;
+    g.split = P.t.split;
+    g.part = g.split > 1 ? (float*)(ws + P.part_off) : nullptr;
+    g.ldpart = part_ld(g.N);
+    e = launch_linear_small(g, bf, P.nb, s);
+    if (e == hipSuccess && g.split > 1) e = launch_split_finish(g, bf, s);
   } else {
     Operand* ops[] = {&P.x, &P.w};
     if ((e = pack_all(ops, 2, q->dtype, ws, s)) != hipSuccess) return hip_fail(e, "operand copies");

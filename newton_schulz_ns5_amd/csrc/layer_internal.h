@@ -44,9 +44,10 @@ enum LinKind { kRowRow = 0, kRowCol = 1, kColCol = 2 };
 enum LinTile { kTile256 = 0, kTile256x128 = 1, kTile128 = 2, kTile64 = 3 };
 hipError_t launch_linear_tiles(const LinGemm& g, bool bf16, LinKind kind, LinTile tile, hipStream_t s);
 hipError_t launch_split_finish(const LinGemm& g, bool bf16, hipStream_t s);
-// Few rows (M <= kSmallRows), kRowRow: any stride and alignment.
+// Few rows (M <= kSmallRows), kRowRow: any stride and alignment; 16 nb weight
+// rows per workgroup (nb 1 or 4), split as above.
 constexpr int kSmallRows = 64;
-hipError_t launch_linear_small(const LinGemm& g, bool bf16, hipStream_t s);
+hipError_t launch_linear_small(const LinGemm& g, bool bf16, int nb, hipStream_t s);
 // dst [rows][ldd] = src [rows][cols] with zeros in columns cols .. ldd - 1, up
 // to two matrices per launch.
 struct PackJob { const void* src; int64_t lds; void* dst; int64_t ldd; int64_t rows, cols; };

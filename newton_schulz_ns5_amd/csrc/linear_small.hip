@@ -8,7 +8,20 @@
 // from the caches).  The order of K within a step differs between the lanes'
 // layout and memory, but in the same way for both operands, so every product
 // is formed once.  The waves' sums are added in order through LDS and finished
-// there: one launch, nothing through HBM but operands and results.
+// there.
+//
+// Every workgroup reads all tokens, M / (16 NB) of what it reads of the
+// weight, so NB is 4 where that leaves the chip full; a weight with fewer rows
+// has its K split over workgroups (launch_split_finish adds them).  bf16, us,
+// against the weight's bytes at 5.1 TB/s:
+//   rows x K       tokens   bytes   NB 1    2    4    4, split
+//   14336 x 4096       48    23.2      -  40.6  31.9  38.5 (2)
+//   4096 x 14336       48    23.2      -  39.8*    -  32.5 (4)   * split 2
+//   4096 x 14336        1    22.9   23.6     -     -  24.3 (4)
+//   6144 x 4096         1     9.8   12.5     -     -  13.5 (2)
+//   6144 x 4096        48    10.0      -  21.2     -  19.6 (2)
+//   1024 x 1024        16     0.4    4.5   5.3     -     -
+// More steps in flight per wave (two or four loaded together) gained nothing.
 #include "layer_internal.h"
 #include "linear_epilogue.h"
 
@@ -26,8 +39,8 @@ struct Loads<float> { typedef uint32_t v4 __attribute__((ext_vector_type(4), ali
 
 constexpr int NWV = 8;
 
-template <typename T, int MB, int NB, int U>
-__global__ __launch_bounds__(NWV * 64, 4) void linear_small_kernel(const LinGemm p) {
+template <typename T, int MB, int NB>
+__global__ __launch_bounds__(NWV * 64, 2) void linear_small_kernel(const LinGemm p) {
   constexpr bool BF = sizeof(T) == 2;
   constexpr int E = 32 / sizeof(T);        // values of K per lane and step
   constexpr int KS = 4 * E;                // values of K per step
@@ -74,34 +87,28 @@ __global__ __launch_bounds__(NWV * 64, 4) void linear_small_kernel(const LinGemm
           }
         }
   };
-  // Up to 8 whole-step chunks of one row: 16 bytes each at k and k + 16 bytes.
-  const int64_t full = p.K / KS, steps = (p.K + KS - 1) / KS;
-  int64_t s = wave;
-  for (; s + (int64_t)(U - 1) * NWV < full; s += (int64_t)U * NWV) {
-    u32x4 w[U][NB][2], x[U][MB][2];
+  const int64_t all = (p.K + KS - 1) / KS;
+  const int64_t first = p.split > 1 ? (int64_t)blockIdx.y * all / p.split : 0;
+  const int64_t steps = p.split > 1 ? (int64_t)(blockIdx.y + 1) * all / p.split : all;  // this workgroup's, up to here
+  const int64_t full = p.K / KS < steps ? p.K / KS : steps;
+  int64_t s = first + wave;
+  for (; s < full; s += NWV) {
+    u32x4 w[NB][2], x[MB][2];
+    const int64_t k = s * KS;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = (s + (int64_t)u * NWV) * KS;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        w[u][b][0] = *(const v4u*)(wrow[b] + k);
-        w[u][b][1] = *(const v4u*)(wrow[b] + k + E / 2);
-      }
+    for (int b = 0; b < NB; ++b) {
+      w[b][0] = *(const v4u*)(wrow[b] + k);
+      w[b][1] = *(const v4u*)(wrow[b] + k + E / 2);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = (s + (int64_t)u * NWV) * KS;
-#pragma unroll
-      for (int a = 0; a < MB; ++a) {
-        x[u][a][0] = x[u][a][1] = u32x4{0, 0, 0, 0};
-        if (tok[a]) {
-          x[u][a][0] = *(const v4u*)(xrow[a] + k);
-          x[u][a][1] = *(const v4u*)(xrow[a] + k + E / 2);
-        }
+    for (int a = 0; a < MB; ++a) {
+      x[a][0] = x[a][1] = u32x4{0, 0, 0, 0};
+      if (tok[a]) {
+        x[a][0] = *(const v4u*)(xrow[a] + k);
+        x[a][1] = *(const v4u*)(xrow[a] + k + E / 2);
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) products(w[u], x[u]);
+    products(w, x);
   }
   for (; s < steps; s += NWV) {  // the rest, values of K past the end as zeros
     u32x4 w[NB][2], x[MB][2];
@@ -146,37 +153,42 @@ __global__ __launch_bounds__(NWV * 64, 4) void linear_small_kernel(const LinGemm
       for (int w = 1; w < NWV; ++w)
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += red[w][i * PITCH + c8 + e];
+      if (p.part) {
+        float* const d = p.part + ((int64_t)blockIdx.y * p.M + i) * p.ldpart + j;
+        *(f32x4*)d = f32x4{v[0], v[1], v[2], v[3]};
+        *(f32x4*)(d + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        continue;
+      }
       bias8(p, j, valid, b);
       finish8<ACT, BF>(p, i, j, valid, b, v);
     }
   });
 }
 
-template <typename T, int MB, int NB, int U>
+template <typename T, int MB, int NB>
 hipError_t launch_one(const LinGemm& g, hipStream_t s) {
   const int64_t grid = (g.N + 16 * NB - 1) / (16 * NB);
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return launch_kernel(linear_small_kernel<T, MB, NB, U>, dim3((unsigned)grid), g, s, NWV * 64);
+  if (grid > INT32_MAX || g.split < 1 || g.split > 65535 || (g.split > 1 && !g.part)) return hipErrorInvalidValue;
+  return launch_kernel(linear_small_kernel<T, MB, NB>, dim3((unsigned)grid, (unsigned)g.split), g, s, NWV * 64);
 }
 
 template <typename T>
-hipError_t launch_type(const LinGemm& g, hipStream_t s) {
+hipError_t launch_type(const LinGemm& g, int nb, hipStream_t s) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
-  // 32 weight rows per workgroup halve the reads of the tokens; 16 where 32
-  // would leave CUs without work.
-  const bool wide = g.N >= 32 * 256;
-  const int mb = (int)((g.M + 15) / 16);
-  if (mb == 1) return wide ? launch_one<T, 1, 2, 4>(g, s) : launch_one<T, 1, 1, 4>(g, s);
-  if (mb == 2) return wide ? launch_one<T, 2, 2, 2>(g, s) : launch_one<T, 2, 1, 4>(g, s);
-  if (mb == 3) return wide ? launch_one<T, 3, 2, 2>(g, s) : launch_one<T, 3, 1, 2>(g, s);
-  if (mb == 4) return wide ? launch_one<T, 4, 2, 1>(g, s) : launch_one<T, 4, 1, 2>(g, s);
-  return hipErrorInvalidValue;
+  if (nb != 1 && nb != 4) return hipErrorInvalidValue;
+  switch ((g.M + 15) / 16) {
+    case 1: return nb == 4 ? launch_one<T, 1, 4>(g, s) : launch_one<T, 1, 1>(g, s);
+    case 2: return nb == 4 ? launch_one<T, 2, 4>(g, s) : launch_one<T, 2, 1>(g, s);
+    case 3: return nb == 4 ? launch_one<T, 3, 4>(g, s) : launch_one<T, 3, 1>(g, s);
+    case 4: return nb == 4 ? launch_one<T, 4, 4>(g, s) : launch_one<T, 4, 1>(g, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
-hipError_t launch_linear_small(const LinGemm& g, bool bf16, hipStream_t s) {
-  return bf16 ? launch_type<uint16_t>(g, s) : launch_type<float>(g, s);
+hipError_t launch_linear_small(const LinGemm& g, bool bf16, int nb, hipStream_t s) {
+  return bf16 ? launch_type<uint16_t>(g, nb, s) : launch_type<float>(g, nb, s);
 }
 
 }  // namespace muon

@@ -89,7 +89,9 @@ def check_forward(x, w, b, r, act, y, z, what):
 
 SIZES = [(1, 1, 1), (1, 4096, 640), (2, 33, 65), (5, 130, 7), (16, 512, 1000), (17, 64, 64), (31, 1001, 129),
          (48, 768, 256), (65, 200, 513), (127, 127, 127), (128, 256, 384), (130, 64, 300), (257, 320, 260), (300, 8, 1040),
-         (512, 1024, 512)]
+         (512, 1024, 512), (9, 8200, 3200), (24, 4096, 4100), (64, 2050, 12300)]
+# Outputs of a little more than whole rounds of the largest tile: columns, rows.
+BIG = [(4096, 128, 4400), (4400, 128, 4096), (4104, 72, 4104)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
@@ -101,6 +103,27 @@ def test_linear_sizes(m, k, n, dtype):
     check_forward(x, w, None, None, None, ns.linear(x, w), None, "plain")
     y, z = ns.linear(x, w, b, r, activation="silu", return_preact=True)
     check_forward(x, w, b, r, "silu", y, z, "bias, silu, residual")
+
+
+@pytest.mark.parametrize("m,k,n", BIG)
+def test_linear_big_outputs(m, k, n):
+    torch_cuda()
+    x, w = rand((m, k), BF, 1), rand((n, k), BF, 2, 1 / math.sqrt(k))
+    b, r = rand((n,), BF, 3), rand((m, n), F32, 4)
+    y, z = ns.linear(x, w, b, r, activation="gelu_tanh", return_preact=True)
+    check_forward(x, w, b, r, "gelu_tanh", y, z, "forward")
+    dy = rand((m, n), BF, 5)
+    dx, dw, _ = ns.linear_backward(dy, x, w)
+    check_backward(dy, x, w, None, None, dx, dw, None, "backward")
+    # the input gradient of an m x n output over few columns, and the weight gradient of one over few rows
+    x, w, dy = rand((m, n), BF, 6), rand((k, n), BF, 7), rand((m, k), BF, 8)
+    dx, dw, _ = ns.linear_backward(dy, x, w, dw_dtype=F32)
+    check_backward(dy, x, w, None, None, dx, dw, None, "backward, wide")
+    x, w, dy = rand((k, n), BF, 9), rand((m, n), BF, 10), rand((k, m), BF, 11)
+    dw = rand((m, n), BF, 12)
+    base = dw.clone()
+    ns.linear_backward(dy, x, w, need_dx=False, dw=dw, accumulate=True)
+    check_backward(dy, x, w, None, None, None, dw, None, "weight gradient", base)
 
 
 @pytest.mark.parametrize("act", ACTS)
