@@ -370,10 +370,10 @@ GradPlan plan_grad(const muon_linear_grad* q) {
   P.store_g = q->m > 0 && q->n > 0 && (dx || dw) && (q->activation != MUON_ACT_NONE || q->dy_dtype != q->dtype || dy.pack);
   P.colsum = q->dbias && q->n > 0;
   // Rows per workgroup of the elementwise pass: enough workgroups to fill the
-  // chip (256 columns each), at least 32 rows so that partial sums stay few.
+  // chip (256 columns each), at least the 8 rows it takes at once.
   const int64_t cols = std::max<int64_t>(1, cdiv(q->n, 256));
   const int64_t want = std::max<int64_t>(1, 2048 / cols);
-  P.rows_per = std::max<int64_t>(32, cdiv(q->m, want));
+  P.rows_per = std::max<int64_t>(8, cdiv(q->m, want));
   P.chunks = (int)cdiv(q->m, P.rows_per);
   P.ldg = cdiv(q->n, 8) * 8;
   if (P.store_g) P.g_off = take((size_t)(q->m * P.ldg * esize(q->dtype)));

@@ -446,11 +446,15 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackJobs p) {
   at -= p.start[q];
   const int64_t per = w.ldd / E, r = at / per, c = (at - r * per) * E;
   const T* s = (const T*)w.src + r * w.lds + c;
-  T v[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = c + e < w.cols ? s[e] : T(0);
   u32x4 o;
-  __builtin_memcpy(&o, v, 16);
+  if (c + E <= w.cols) {
+    __builtin_memcpy(&o, s, 16);  // rows may start anywhere
+  } else {
+    T v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = c + e < w.cols ? s[e] : T(0);
+    __builtin_memcpy(&o, v, 16);
+  }
   *(u32x4*)((T*)w.dst + r * w.ldd + c) = o;
 }
 

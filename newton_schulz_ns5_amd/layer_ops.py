@@ -66,10 +66,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # tensors on a GPU: it is initialised
+
+
 def _call(dev, fn, problem, need):
     """Run fn(problem[, workspace]) on the device's current stream.  The device
     is made current for the launch when another one is."""
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return _call_here(dev, fn, problem, need)
     return _call_here(dev, fn, problem, need)
@@ -108,7 +111,7 @@ def _rows(t, name, cols=None):
 
 
 def _vector(t, name, n):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         _bad(f"{name} must be a contiguous [{n}] tensor")
     return t.data_ptr()
 
@@ -127,7 +130,11 @@ def _refuse_capture():
 
 
 def _wants_grad(*ts):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=False, out=None, preact=None):
@@ -160,10 +167,10 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
     xp, m, _, ldx = _rows(x, "x", k)
     shape = x.shape[:-1] + (n,)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype if residual is None else residual.dtype, device=x.device)
+        out = (x if residual is None else residual).new_empty(shape)
     if (return_preact or preact is not None):
         if preact is None:
-            preact = torch.empty(shape, dtype=x.dtype, device=x.device)
+            preact = x.new_empty(shape)
         elif preact.dtype != x.dtype:
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"preact must be {x.dtype} like x")
     yp, ldy = _check_matrix(out, "out", m, n)
@@ -208,7 +215,7 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         _bad("accumulate needs the tensors to add to")
     if dx is None and need_dx:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     if dw is None and need_dw:
         dw = torch.empty((n, k), dtype=dw_dtype or w.dtype, device=x.device)
     if dbias is None and need_dbias:
@@ -265,18 +272,14 @@ _NO_HEADS = (0, 0, 0, 0)
 _NO_PAIR = _NO_HEADS * 2
 
 
-def _heads_of(t, name, like=None):
+def _heads_of(t, name, shape):
     """(pointer, batch, token, head stride) of a [tokens, heads, dim] or [batch, tokens, heads, dim] tensor."""
-    if t is None:
-        return _NO_HEADS
-    if like is not None and t.shape != like.shape:
-        _bad(f"{name} is {tuple(t.shape)}, not {tuple(like.shape)}")
-    if t.dim() not in (3, 4):
-        _bad(f"{name} must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
+    if t.shape != shape:
+        _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
     st = t.stride()
-    if t.shape[-1] > 1 and t.numel() and st[-1] != 1:
+    if st[-1] != 1 and shape[-1] > 1 and t.numel():
         _bad(f"{name} needs unit stride in its last dimension")
-    return t.data_ptr(), (st[0] if t.dim() == 4 else 0), st[-3], st[-2]
+    return (t.data_ptr(), 0, *st[:2]) if len(st) == 3 else (t.data_ptr(), *st[:3])
 
 
 def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x, g, y, weight, dweight, eps):
@@ -299,11 +302,14 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
             fields += _NO_PAIR
             continue
         for t, like, name in ((pair[0], q, "q"), (pair[1], k, "k")):
-            if (t is None) != (like is None):
-                _bad("q and k must both be given, or both be left out, in every pair of tensors")
-            if t is not None and t.dtype != dtype:
+            if t is None or like is None:
+                if t is not like:
+                    _bad("q and k must both be given, or both be left out, in every pair of tensors")
+                fields += _NO_HEADS
+                continue
+            if t.dtype != dtype:
                 raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"head tensors are {t.dtype} and {dtype}: one type is needed")
-            fields += _heads_of(t, name, like)
+            fields += _heads_of(t, name, like.shape)
     dev = _same_device(positions, inv_freq, *(x or ()), *(g or ()), *(y or ()), *weight, *dweight)
     batch, tokens = (first.shape[0], first.shape[1]) if first.dim() == 4 else (1, first.shape[0])
     dim = first.shape[-1]
@@ -359,7 +365,7 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
 def _like(t, out):
     if out is not None:
         return out
-    return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps=1e-6, sections=None, axes=None,
