@@ -193,7 +193,7 @@ constexpr TileCost kCostBf16[] = {{kTile256, 256, 256, 256, 8.0, 1.15, 1.65},
                                   {kTile256x128, 256, 128, 256, 6.0, 0.58, 0.87},
                                   {kTile128, 128, 128, 512, 6.0, 0.75, 1.13},
                                   {kTile64, 64, 64, 1024, 4.5, 0.44, 0.75}};
-constexpr TileCost kCostF32[] = {{kTile128, 128, 128, 512, 9.0, 2.1, 3.95}, {kTile64, 64, 64, 1024, 5.0, 0.6, 2.03}};
+constexpr TileCost kCostF32[] = {{kTile256x128, 256, 128, 256, 9.0, 3.6, 3.77}, {kTile64, 64, 64, 1024, 5.0, 0.6, 2.0}};
 
 // Microseconds of `wgs` workgroups of `slices` slices each.
 double tile_time(const TileCost& c, int64_t wgs, int64_t slices) {

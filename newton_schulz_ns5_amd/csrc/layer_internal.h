@@ -37,7 +37,7 @@ struct LinGemm {
 };
 enum LinKind { kRowRow = 0, kRowCol = 1, kColCol = 2 };
 
-// Tiled kernels (fp32: the two smaller tiles).  Operand rows
+// Tiled kernels (fp32: kTile256x128 and kTile64).  Operand rows
 // must start 16-byte aligned, and a row operand's K be a multiple of 16 bytes
 // (launch_pack makes such a copy); with split > 1 the kernel stores the
 // chunks' products and launch_split_finish adds them and runs the epilogue.

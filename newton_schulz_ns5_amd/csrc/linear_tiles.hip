@@ -477,7 +477,7 @@ hipError_t launch_kind(const LinGemm& g, bool bf16, LinTile tile, hipStream_t s)
     }
   }
   switch (tile) {
-    case kTile128: return launch_tile<float, KIND, 128, 128, 2, 2>(g, s);
+    case kTile256x128: return launch_tile<float, KIND, 256, 128, 4, 2>(g, s);
     case kTile64: return launch_tile<float, KIND, 64, 64, 2, 2>(g, s);
     default: return hipErrorInvalidValue;
   }
