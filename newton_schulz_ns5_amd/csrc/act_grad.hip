@@ -22,7 +22,6 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGrad p) {
   const int valid = j >= p.N ? 0 : (p.N - j < 8 ? (int)(p.N - j) : 8);
   const int64_t r0 = (int64_t)blockIdx.y * p.rows_per;
   const int64_t r1 = r0 + p.rows_per < p.M ? r0 + p.rows_per : p.M;
-  const bool vec = p.vec != 0;
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
@@ -32,14 +31,14 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGrad p) {
 #pragma unroll 2
       for (int64_t i = r0 + rg; i < r1; i += 8) {
         float g[8];
-        get8(p.dy, i * p.lddy + j, p.dy_dtype == MUON_BF16, vec, valid, g);
+        get8(p.dy, i * p.lddy + j, p.dy_dtype == MUON_BF16, valid, g);
         if constexpr (ACT != MUON_ACT_NONE) {
           float z[8];
-          get8(p.z, i * p.ldz + j, BF, vec, valid, z);
+          get8(p.z, i * p.ldz + j, BF, valid, z);
 #pragma unroll
           for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(z[e]);
         }
-        if (p.G) put8(p.G, i * p.ldg + j, BF, true, 8, g);  // values past N are zero
+        if (p.G) put8(p.G, i * p.ldg + j, BF, 8, g);  // values past N are zero
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += g[e];
       }
@@ -62,18 +61,21 @@ struct ColSum {
   void* out; int32_t out_dtype; int32_t accumulate;
 };
 
-// Four threads per column add every fourth chunk, then the four sums in order.
+// 16 threads per column add every 16th chunk, then the 16 sums in order.
 __global__ __launch_bounds__(256) void col_sum_kernel(const ColSum p) {
-  __shared__ float red[4][64];
-  const int col = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t j = (int64_t)blockIdx.x * 64 + col;
+  __shared__ float red[16][17];
+  const int col = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int64_t j = (int64_t)blockIdx.x * 16 + col;
   float t = 0.f;
-  if (j < p.n)
-    for (int c = q; c < p.chunks; c += 4) t += p.partial[(int64_t)c * p.n + j];
+  if (j < p.n) {
+#pragma unroll 8
+    for (int c = q; c < p.chunks; c += 16) t += p.partial[(int64_t)c * p.n + j];
+  }
   red[q][col] = t;
   __syncthreads();
   if (q || j >= p.n) return;
-  t = ((red[0][col] + red[1][col]) + red[2][col]) + red[3][col];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) t += red[i][col];
   const bool bf = p.out_dtype == MUON_BF16;
   if (p.accumulate) t += load_elem(p.out, j, bf);
   store_elem(p.out, j, t, bf);
@@ -91,7 +93,7 @@ hipError_t launch_act_grad(const ActGrad& g, bool bf16, hipStream_t s) {
 
 hipError_t launch_col_sum(const float* partial, int chunks, int64_t n, void* out, int32_t out_dtype, bool accumulate,
                           hipStream_t s) {
-  const int64_t blocks = (n + 63) / 64;
+  const int64_t blocks = (n + 15) / 16;
   if (blocks <= 0) return hipSuccess;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const ColSum p{partial, chunks, n, out, out_dtype, accumulate ? 1 : 0};

@@ -149,10 +149,6 @@ int check_linear_grad(const muon_linear_grad* q) {
   return MUON_OK;
 }
 
-bool rows16(const void* p, int64_t ld, int32_t dt) {
-  return ((uintptr_t)p & 15) == 0 && (ld * esize(dt)) % 16 == 0;
-}
-
 // Elements per 16 bytes.
 int64_t per16(int32_t dt) { return 16 / esize(dt); }
 
@@ -301,15 +297,6 @@ hipError_t run_product(LinGemm g, int32_t dt, LinKind kind, const Tiling& t, cha
   return e;
 }
 
-int vec_flags(const LinGemm& g, int32_t dt) {
-  int v = 0;
-  if (g.bias && ((uintptr_t)g.bias & 15) == 0) v |= kVecBias;
-  if (g.add && rows16(g.add, g.ldadd, g.add_dtype)) v |= kVecAdd;
-  if (rows16(g.Y, g.ldy, g.y_dtype)) v |= kVecY;
-  if (g.Z && rows16(g.Z, g.ldz, dt)) v |= kVecZ;
-  return v;
-}
-
 // Work of a forward call: the small kernel for few rows, else tiles.
 struct LinearPlan {
   bool small;
@@ -428,7 +415,6 @@ int muon_linear(const muon_linear_problem* q, void* workspace, size_t workspace_
   g.Y = q->y; g.y_dtype = q->y_dtype; g.ldy = q->y_row_stride;
   g.Z = q->preact; g.ldz = q->preact_row_stride;
   g.act = q->activation;
-  g.vec = vec_flags(g, q->dtype);
   g.split = 1;
   hipError_t e;
   if (P.small) {
@@ -480,7 +466,6 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
     if (P.colsum) a.partial = (float*)(ws + P.partial_off);
     a.chunks = P.chunks; a.rows_per = P.rows_per;
     a.M = q->m; a.N = q->n;
-    a.vec = rows16(a.dy, a.lddy, a.dy_dtype) && (!a.z || rows16(a.z, a.ldz, q->dtype)) ? 1 : 0;
     if ((e = launch_act_grad(a, bf, s)) != hipSuccess) return hip_fail(e, "gradient at the pre-activation");
   }
   if (P.colsum) {
@@ -496,7 +481,6 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
     g.B = P.w.p; g.ldb = P.w.ld;
     g.M = q->m; g.N = q->k; g.K = q->n;
     g.Y = q->dx; g.y_dtype = q->dx_dtype; g.ldy = q->dx_row_stride;
-    g.vec = vec_flags(g, q->dtype);
     if ((e = run_product(g, q->dtype, kRowCol, P.tx, ws + P.part_off, s)) != hipSuccess) return hip_fail(e, "input gradient");
   }
   if (dw) {
@@ -506,7 +490,6 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
     g.M = q->n; g.N = q->k; g.K = q->m;
     g.Y = q->dw; g.y_dtype = q->dw_dtype; g.ldy = q->dw_row_stride;
     if (q->accumulate) { g.add = q->dw; g.add_dtype = q->dw_dtype; g.ldadd = q->dw_row_stride; }
-    g.vec = vec_flags(g, q->dtype);
     if ((e = run_product(g, q->dtype, kColCol, P.tw, ws + P.part_off, s)) != hipSuccess) return hip_fail(e, "weight gradient");
   }
   return ok();

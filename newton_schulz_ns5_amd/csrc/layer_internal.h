@@ -19,8 +19,6 @@ int report(int code, const char* msg) noexcept;
 //   input gradient   g [M][N] row, w [N][K] col  (M x K out, sum over N)
 //   weight gradient  g [M][N] col, x [M][K] col  (N x K out, sum over M)
 // Epilogue: z = C + bias_j; zout = z; y = act(z) + add(i, j).
-// kVec*: every row of that tensor starts 16-byte aligned.
-constexpr int kVecBias = 1, kVecAdd = 2, kVecY = 4, kVecZ = 8;
 struct LinGemm {
   const void* A; int64_t lda;
   const void* B; int64_t ldb;
@@ -31,7 +29,6 @@ struct LinGemm {
   void* Y; int32_t y_dtype; int64_t ldy;
   void* Z; int64_t ldz;                                // pre-activation (operand type), or null
   int32_t act;
-  int32_t vec;                                         // kVec* flags
   float* part; int64_t ldpart;                         // split sum: [split][M][ldpart] fp32, else null
   int32_t split;                                       // chunks of the sum, >= 1
 };
@@ -51,8 +48,8 @@ hipError_t launch_linear_small(const LinGemm& g, bool bf16, int nb, hipStream_t 
 // dst [rows][ldd] = src [rows][cols] with zeros in columns cols .. ldd - 1, up
 // to two matrices per launch.
 struct PackJob { const void* src; int64_t lds; void* dst; int64_t ldd; int64_t rows, cols; };
-struct PackJobs { PackJob job[2]; int32_t n; int64_t start[3]; };
-hipError_t launch_pack(PackJobs& p, bool bf16, hipStream_t s);
+struct PackJobs { PackJob job[2]; int32_t n; };
+hipError_t launch_pack(const PackJobs& p, bool bf16, hipStream_t s);
 
 // ---- gradient at the pre-activation ----------------------------------------------
 // G = round(dy * act'(z)) in the operand type (G null: not stored), with zeros
@@ -66,7 +63,6 @@ struct ActGrad {
   float* partial; int32_t chunks; int64_t rows_per;
   int64_t M, N;
   int32_t act;
-  int32_t vec;                         // 1: every row of dy and z starts 16-byte aligned (G's always do)
 };
 hipError_t launch_act_grad(const ActGrad& g, bool bf16, hipStream_t s);
 // out[j] (+)= sum over chunks of partial[c][j], c ascending.

@@ -31,6 +31,8 @@
 #include "layer_internal.h"
 #include "linear_epilogue.h"
 
+#include <algorithm>
+
 namespace muon {
 namespace {
 
@@ -151,7 +153,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   const int slices = (int)((p.K + KS - 1) / KS);
   const int t0 = p.split > 1 ? (int)((int64_t)sp * slices / p.split) : 0;
   const int t1 = p.split > 1 ? (int)((int64_t)(sp + 1) * slices / p.split) : slices;
-  const int KT = t1 > t0 ? t1 - t0 : 1;             // an empty sum is one slice of zeros
+  const int KT = __builtin_amdgcn_readfirstlane(t1 > t0 ? t1 - t0 : 1);  // an empty sum is one slice of zeros
   const int64_t kbeg = (int64_t)t0 * KS;
   const int64_t kend = (int64_t)t1 * KS < p.K ? (int64_t)t1 * KS : p.K;
   const int Kc = (int)(kend - kbeg);                // K values of this workgroup
@@ -192,18 +194,23 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   };
   const i32x4 ars = rsrc_words(Ab, ACOL ? 0 : span(arows, BM, p.lda));
   const i32x4 brs = rsrc_words(Bb, BCOL ? 0 : span(brows, BN, p.ldb));
-  // Scalar arithmetic only (32-bit compares and products), so that the words
-  // stay in scalar registers.
+  // Scalar arithmetic only (32-bit compares and products of values made uniform
+  // once), so that the words stay in scalar registers.
+  auto uni = [](int v) { return (int)__builtin_amdgcn_readfirstlane(v); };
+  auto uni64 = [&](const char* v) {
+    return (uint64_t)(uint32_t)uni((int)(uint32_t)(uint64_t)v) | ((uint64_t)(uint32_t)uni((int)((uint64_t)v >> 32)) << 32);
+  };
+  const uint64_t Au = uni64(Ab), Bu = uni64(Bb);
   const int kcol = (int)((p.Kcol < kend ? p.Kcol : kend) - kbeg);
   auto col_bytes = [&](int ld, int64_t rows, int ext, int left) {
     const int cols = rows < ext ? ((int)rows + 16 / ES - 1) / (16 / ES) * (16 / ES) : ext;
     return left <= 0 ? 0 : (((left < KS ? left : KS) - 1) * ld + cols) * ES;
   };
   const int left = kcol - (KT - 1) * KS;
-  const int afull = ACOL ? col_bytes(lda, arows, BM, KS) : 0, alast = ACOL ? col_bytes(lda, arows, BM, left) : 0;
-  const int bfull = BCOL ? col_bytes(ldb, brows, BN, KS) : 0, blast = BCOL ? col_bytes(ldb, brows, BN, left) : 0;
-  auto col_rsrc = [&](const char* base, int ld, int full, int end, int t) {
-    const uint64_t a = (uint64_t)base + (uint64_t)(uint32_t)t * (uint32_t)(KS * ld * ES);
+  const int afull = uni(ACOL ? col_bytes(lda, arows, BM, KS) : 0), alast = uni(ACOL ? col_bytes(lda, arows, BM, left) : 0);
+  const int bfull = uni(BCOL ? col_bytes(ldb, brows, BN, KS) : 0), blast = uni(BCOL ? col_bytes(ldb, brows, BN, left) : 0);
+  auto col_rsrc = [&](uint64_t base, int ld, int full, int end, int t) {
+    const uint64_t a = base + (uint64_t)(uint32_t)t * (uint32_t)(KS * ld * ES);
     i32x4 r;
     r[0] = (int)(uint32_t)a;
     r[1] = (int)((uint32_t)(a >> 32) & 0xffffu);
@@ -220,13 +227,13 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   auto load_a = [&](int t, uint32_t slot, int q) {
     const bool last = t >= KT - 1;
     const int tc = last ? KT - 1 : t, at = (wave * DPA + q) * 1024;
-    if constexpr (ACOL) lds_dma16_asm(col_rsrc(Ab, lda, afull, alast, tc), slot + at, avo[q], 0);
+    if constexpr (ACOL) lds_dma16_asm(col_rsrc(Au, lda, afull, alast, tc), slot + at, avo[q], 0);
     else lds_dma16_asm(ars, slot + at, last ? tail(avo[q], at + lane * 16) : avo[q], tc * ROWB);
   };
   auto load_b = [&](int t, uint32_t slot, int q) {
     const bool last = t >= KT - 1;
     const int tc = last ? KT - 1 : t, at = (wave * DPB + q) * 1024;
-    if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bb, ldb, bfull, blast, tc), slot + at, bvo[q], 0);
+    if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bu, ldb, bfull, blast, tc), slot + at, bvo[q], 0);
     else lds_dma16_asm(brs, slot + at, last ? tail(bvo[q], at + lane * 16) : bvo[q], tc * ROWB);
   };
   // Slot of the next slice of the same operand.
@@ -434,28 +441,27 @@ __global__ __launch_bounds__(256) void split_finish_kernel(const LinGemm p) {
   with_act(p.act, [&](auto act_c) { finish8<decltype(act_c)::value, BF>(p, i, j, valid, b, v); });
 }
 
-// Copy with zero padding: consecutive lanes take consecutive 16-byte chunks of
-// the destination.
+// Copy with zero padding: 64 consecutive lanes take consecutive 16-byte chunks
+// of a destination row; a matrix per grid z.
 template <typename T>
 __global__ __launch_bounds__(256) void pack_kernel(const PackJobs p) {
   constexpr int E = 16 / sizeof(T);
-  int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= p.start[p.n]) return;
-  const int q = p.n > 1 && at >= p.start[1];
-  const PackJob& w = p.job[q];
-  at -= p.start[q];
-  const int64_t per = w.ldd / E, r = at / per, c = (at - r * per) * E;
-  const T* s = (const T*)w.src + r * w.lds + c;
-  u32x4 o;
-  if (c + E <= w.cols) {
-    __builtin_memcpy(&o, s, 16);  // rows may start anywhere
-  } else {
-    T v[E];
+  const PackJob& w = p.job[blockIdx.z];
+  const int64_t c = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * E;
+  if (c >= w.ldd) return;
+  for (int64_t r = (int64_t)blockIdx.y * 4 + (threadIdx.x >> 6); r < w.rows; r += (int64_t)gridDim.y * 4) {
+    const T* s = (const T*)w.src + r * w.lds + c;
+    u32x4 o;
+    if (c + E <= w.cols) {
+      o = load16(s);  // rows may start anywhere
+    } else {
+      T v[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = c + e < w.cols ? s[e] : T(0);
-    __builtin_memcpy(&o, v, 16);
+      for (int e = 0; e < E; ++e) v[e] = c + e < w.cols ? s[e] : T(0);
+      __builtin_memcpy(&o, v, 16);
+    }
+    *(u32x4*)((T*)w.dst + r * w.ldd + c) = o;
   }
-  *(u32x4*)((T*)w.dst + r * w.ldd + c) = o;
 }
 
 template <typename T, int KIND, int BM, int BN, int WM, int WN>
@@ -507,18 +513,19 @@ hipError_t launch_split_finish(const LinGemm& g, bool bf16, hipStream_t s) {
               : launch_kernel(split_finish_kernel<false>, dim3((unsigned)grid), g, s);
 }
 
-hipError_t launch_pack(PackJobs& p, bool bf16, hipStream_t s) {
+hipError_t launch_pack(const PackJobs& p, bool bf16, hipStream_t s) {
   const int64_t e = bf16 ? 8 : 4;
-  p.start[0] = 0;
+  int64_t gx = 0, gy = 0;
   for (int i = 0; i < p.n; ++i) {
-    if (p.job[i].ldd % e || ((uintptr_t)p.job[i].dst & 15)) return hipErrorInvalidValue;
-    p.start[i + 1] = p.start[i] + p.job[i].rows * (p.job[i].ldd / e);
+    const PackJob& w = p.job[i];
+    if (w.ldd % e || ((uintptr_t)w.dst & 15)) return hipErrorInvalidValue;
+    if (!w.rows) continue;
+    gx = std::max(gx, (w.ldd / e + 63) / 64);
+    gy = std::max(gy, std::min<int64_t>((w.rows + 3) / 4, 65535));
   }
-  const int64_t grid = (p.start[p.n] + 255) / 256;
-  if (grid <= 0) return hipSuccess;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return bf16 ? launch_kernel(pack_kernel<uint16_t>, dim3((unsigned)grid), p, s)
-              : launch_kernel(pack_kernel<float>, dim3((unsigned)grid), p, s);
+  if (gx <= 0 || gy <= 0) return hipSuccess;
+  const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)p.n);
+  return bf16 ? launch_kernel(pack_kernel<uint16_t>, grid, p, s) : launch_kernel(pack_kernel<float>, grid, p, s);
 }
 
 }  // namespace muon
