@@ -188,7 +188,7 @@ struct TileCost { LinTile tile; int bm, bn, slots; double fixed, u0, u1; };
 constexpr TileCost kCostBf16[] = {{kTile256, 256, 256, 256, 8.0, 1.15, 1.65},
                                   {kTile256x128, 256, 128, 256, 6.0, 0.58, 0.87},
                                   {kTile128, 128, 128, 512, 6.0, 0.75, 1.13},
-                                  {kTile64, 64, 64, 1024, 4.5, 0.44, 0.75}};
+                                  {kTile64, 64, 64, 768, 6.0, 0.30, 0.62}};
 constexpr TileCost kCostF32[] = {{kTile256x128, 256, 128, 256, 9.0, 3.6, 3.77}, {kTile64, 64, 64, 1024, 5.0, 0.6, 2.0}};
 
 // Microseconds of `wgs` workgroups of `slices` slices each.

@@ -9,7 +9,7 @@
 //    block of 16 x 16 products (v_mfma_f32_16x16x32_bf16: 3 % faster here than
 //    the 32x32x16 form, which moves more accumulator values per operation;
 //    fp32: 16x16x4).  256 x 256: eight waves of 128 x 64, two per SIMD;
-//    256 x 128: eight of 64 x 64; 128 and 64: four waves, two and four
+//    256 x 128: eight of 64 x 64; 128 and 64: four waves, two and three or four
 //    workgroups per CU, for outputs with too few large tiles to fill the chip;
 //  - K advances by 128 bytes of a row (64 bf16 or 32 fp32 values) per slice,
 //    brought HBM -> LDS directly into a ring of operand slots, one and a half
@@ -119,7 +119,7 @@ struct Operand {
   }
 };
 
-template <typename T, int KIND, int BM, int BN, int WM, int WN>
+template <typename T, int KIND, int BM, int BN, int WM, int WN, int DEPTH>
 __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinGemm p) {
   constexpr bool BF = sizeof(T) == 2;
   constexpr bool ACOL = KIND == kColCol, BCOL = KIND != kRowRow;
@@ -130,14 +130,14 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   constexpr int WT = BM / WM, WC = BN / WN;      // wave tile
   constexpr int F = WT / 16, FN = WC / 16, FH = F / 2;
   constexpr int DPA = BM / NW / 8, DPB = BN / NW / 8;  // load instructions per wave, operand and slice
-  // Ring: equal operands share five slots (A of slice t in 2 t mod 5, B in
-  // 2 t + 1 mod 5), else each has three.
-  constexpr bool RING5 = BM == BN;
-  constexpr int RING_A = RING5 ? 5 * OA::BYTES : 3 * OA::BYTES;
-  constexpr int RING = RING5 ? RING_A : RING_A + 3 * OB::BYTES;
+  // Ring: DEPTH slots of each operand, or (DEPTH 0) five that both share: A of
+  // slice t in 2 t mod 5, B in 2 t + 1 mod 5.
+  constexpr bool RING5 = DEPTH == 0;
+  constexpr int RING_A = RING5 ? 5 * OA::BYTES : DEPTH * OA::BYTES;
+  constexpr int RING = RING5 ? RING_A : RING_A + DEPTH * OB::BYTES;
   constexpr int RH = BM / 2, PITCH = BN + 4;
   constexpr int LDS_BYTES = RING > RH * PITCH * 4 ? RING : RH * PITCH * 4;
-  static_assert(DPA >= 1 && DPB >= 1 && (!RING5 || DPB % 2 == 0) && F % 2 == 0 && FN % 2 == 0, "tile shape");
+  static_assert(DPA >= 1 && DPB >= 1 && (!RING5 || (DPB % 2 == 0 && BM == BN)) && (RING5 || DEPTH >= 3) && F % 2 == 0 && FN % 2 == 0, "tile shape");
   static_assert((WT & (WT - 1)) == 0 && (WC & (WC - 1)) == 0, "fragment indices are XORed into addresses");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
 
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   };
   auto next_b = [&](uint32_t s) {
     const uint32_t step = RING5 ? 2 * OB::BYTES : OB::BYTES, end = smem_lds + RING;
-    return s + step >= end ? s + step - (RING5 ? RING : 3 * OB::BYTES) : s + step;
+    return s + step >= end ? s + step - (RING5 ? RING : DEPTH * OB::BYTES) : s + step;
   };
 
   f32x4 acc[F][FN];
@@ -320,22 +320,24 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   // waits for its own loads of slice t + 1 and meets the others: that
   // publishes slice t + 1 and frees slice t's slots (the fourth quarter's
   // fragments are in registers).  Loads, each into slots freed before:
-  //   five slots:  B of slice t + 1 in the fourth quarter of slice t - 1 and
-  //                the first of slice t, A of slice t + 2 in the second and third;
-  //   three each:  slice t + 2 in the first three quarters of slice t.
+  //   five shared slots:  B of slice t + 1 in the fourth quarter of slice t - 1
+  //                       and the first of slice t, A of slice t + 2 in the
+  //                       second and third;
+  //   DEPTH each:         slice t + DEPTH - 1 in the first three quarters of
+  //                       slice t (where slice t - 1 was).
   uint32_t sa = smem_lds, sb = smem_lds + (RING5 ? OA::BYTES : RING_A);   // slots of slice t
-  {
-    const uint32_t sa1 = next_a(sa), sb1 = next_b(sb);
+  uint32_t wa = sa, wb = sb;                                              // slots loaded next
+  constexpr int AHEAD = RING5 ? 2 : DEPTH - 1;                            // slices loaded before the loop
 #pragma unroll
-    for (int q = 0; q < DPA; ++q) load_a(0, sa, q);
+  for (int t = 0; t < AHEAD; ++t) {
 #pragma unroll
-    for (int q = 0; q < DPB; ++q) load_b(0, sb, q);
+    for (int q = 0; q < DPA; ++q) load_a(t, wa, q);
 #pragma unroll
-    for (int q = 0; q < DPA; ++q) load_a(1, sa1, q);
-#pragma unroll
-    for (int q = 0; q < (RING5 ? DPB / 2 : DPB); ++q) load_b(1, sb1, q);
+    for (int q = 0; q < (RING5 && t == 1 ? DPB / 2 : DPB); ++q) load_b(t, wb, q);
+    if (!RING5) { wa = next_a(wa); wb = next_b(wb); }
+    else if (t == 0) { wa = next_a(wa); wb = next_b(wb); }
   }
-  wait_vmcnt<DPA + (RING5 ? DPB / 2 : DPB)>();
+  wait_vmcnt<RING5 ? DPA + DPB / 2 : (AHEAD - 1) * (DPA + DPB)>();
   __builtin_amdgcn_s_barrier();
   va = la + sa;
   vb = lb + sb;
@@ -343,17 +345,21 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   for (int u = 0; u < FH + FN; ++u) read(Q3{}, u);
   __builtin_amdgcn_sched_barrier(0);
   for (int t = 0; t < KT; ++t) {
-    const uint32_t sa1 = next_a(sa), sb1 = next_b(sb), sa2 = next_a(sa1), sb2 = next_b(sb1);
+    const uint32_t sa1 = next_a(sa), sb1 = next_b(sb);
     if constexpr (RING5) {
+      const uint32_t sa2 = next_a(sa1), sb2 = next_b(sb1);
       quarter(Q0{}, std::integral_constant<int, DPB / 2>{}, [&](int d) { load_b(t + 1, sb1, DPB / 2 + d); });
       quarter(Q1{}, std::integral_constant<int, DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, d); });
       quarter(Q2{}, std::integral_constant<int, DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, DPA / 2 + d); });
       wait_vmcnt<DPA>();
+      wb = sb2;
     } else {
-      quarter(Q0{}, std::integral_constant<int, DPB>{}, [&](int d) { load_b(t + 2, sb2, d); });
-      quarter(Q1{}, std::integral_constant<int, DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, d); });
-      quarter(Q2{}, std::integral_constant<int, DPA - DPA / 2>{}, [&](int d) { load_a(t + 2, sa2, DPA / 2 + d); });
-      wait_vmcnt<DPA + DPB>();
+      quarter(Q0{}, std::integral_constant<int, DPB>{}, [&](int d) { load_b(t + AHEAD, wb, d); });
+      quarter(Q1{}, std::integral_constant<int, DPA / 2>{}, [&](int d) { load_a(t + AHEAD, wa, d); });
+      quarter(Q2{}, std::integral_constant<int, DPA - DPA / 2>{}, [&](int d) { load_a(t + AHEAD, wa, DPA / 2 + d); });
+      wait_vmcnt<(AHEAD - 1) * (DPA + DPB)>();
+      wa = next_a(wa);
+      wb = next_b(wb);
     }
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's reads of slice t are done
     __builtin_amdgcn_s_barrier();
@@ -363,7 +369,7 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
     va = la + sa;
     vb = lb + sb;
     if constexpr (RING5)
-      quarter(Q3{}, std::integral_constant<int, DPB / 2>{}, [&](int d) { load_b(t + 2, sb2, d); });
+      quarter(Q3{}, std::integral_constant<int, DPB / 2>{}, [&](int d) { load_b(t + 2, wb, d); });
     else
       quarter(Q3{}, std::integral_constant<int, 0>{}, [&](int) {});
   }
@@ -464,27 +470,27 @@ __global__ __launch_bounds__(256) void pack_kernel(const PackJobs p) {
   }
 }
 
-template <typename T, int KIND, int BM, int BN, int WM, int WN>
+template <typename T, int KIND, int BM, int BN, int WM, int WN, int DEPTH>
 hipError_t launch_tile(const LinGemm& g, hipStream_t s) {
   const int64_t grid = ((g.M + BM - 1) / BM) * ((g.N + BN - 1) / BN) * g.split;
   if (grid <= 0) return hipSuccess;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  return launch_kernel(linear_tile_kernel<T, KIND, BM, BN, WM, WN>, dim3((unsigned)grid), g, s, WM * WN * 64);
+  return launch_kernel(linear_tile_kernel<T, KIND, BM, BN, WM, WN, DEPTH>, dim3((unsigned)grid), g, s, WM * WN * 64);
 }
 
 template <int KIND>
 hipError_t launch_kind(const LinGemm& g, bool bf16, LinTile tile, hipStream_t s) {
   if (bf16) {
     switch (tile) {
-      case kTile256: return launch_tile<uint16_t, KIND, 256, 256, 2, 4>(g, s);
-      case kTile256x128: return launch_tile<uint16_t, KIND, 256, 128, 4, 2>(g, s);
-      case kTile128: return launch_tile<uint16_t, KIND, 128, 128, 2, 2>(g, s);
-      default: return launch_tile<uint16_t, KIND, 64, 64, 2, 2>(g, s);
+      case kTile256: return launch_tile<uint16_t, KIND, 256, 256, 2, 4, 0>(g, s);
+      case kTile256x128: return launch_tile<uint16_t, KIND, 256, 128, 4, 2, 3>(g, s);
+      case kTile128: return launch_tile<uint16_t, KIND, 128, 128, 2, 2, 0>(g, s);
+      default: return launch_tile<uint16_t, KIND, 64, 64, 2, 2, 3>(g, s);
     }
   }
   switch (tile) {
-    case kTile256x128: return launch_tile<float, KIND, 256, 128, 4, 2>(g, s);
-    case kTile64: return launch_tile<float, KIND, 64, 64, 2, 2>(g, s);
+    case kTile256x128: return launch_tile<float, KIND, 256, 128, 4, 2, 3>(g, s);
+    case kTile64: return launch_tile<float, KIND, 64, 64, 2, 2, 0>(g, s);
     default: return hipErrorInvalidValue;
   }
 }
