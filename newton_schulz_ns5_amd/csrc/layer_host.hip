@@ -545,11 +545,13 @@ bool same_view(const muon_heads& a, const muon_heads& b, const muon_qk_problem* 
 bool may_meet(const muon_heads& a, int64_t ha, const muon_heads& b, int64_t hb, int32_t dt, const muon_qk_problem* q) {
   const Span x = span_of(a, ha, dt, q), y = span_of(b, hb, dt, q);
   if (x.lo >= y.hi || y.lo >= x.hi) return false;
-  const int64_t S = a.token_stride;
+  // The stride between tokens; with one token per sequence, between sequences
+  // (the stride of an axis of one entry means nothing).
+  const bool one = q->tokens <= 1;
+  const int64_t S = one ? a.batch_stride : a.token_stride, Sb = one ? b.batch_stride : b.token_stride;
   const int64_t wa = (ha - 1) * a.head_stride + q->dim, wb = (hb - 1) * b.head_stride + q->dim;
-  const bool batched = q->batch > 1;
-  if (S != b.token_stride || S <= 0 || wa > S || wb > S) return true;
-  if (batched && (a.batch_stride % S || b.batch_stride % S)) return true;
+  if (S != Sb || S <= 0 || wa > S || wb > S || (one && q->batch <= 1)) return true;
+  if (!one && q->batch > 1 && (a.batch_stride % S || b.batch_stride % S)) return true;
   const int64_t bytes = S * esize(dt);
   const int64_t d = (int64_t)((x.lo >= y.lo ? x.lo - y.lo : (uintptr_t)bytes - (y.lo - x.lo) % (uintptr_t)bytes) % (uintptr_t)bytes);
   return !(d >= wb * esize(dt) && d + wa * esize(dt) <= bytes);

@@ -29,8 +29,11 @@ namespace {
 constexpr int NT = 256;
 constexpr int kCsPairs = 512;  // (cos, sin) pairs of LDS per wave
 
+// Batch entry of a token (a division only where there are several).
+__device__ __forceinline__ int64_t batch_of(const QkParams& p, int64_t tok) { return p.seq == p.tokens ? 0 : tok / p.seq; }
+
 __device__ __forceinline__ int64_t pos_of(const QkParams& p, int64_t tok, int axis) {
-  const int64_t b = tok / p.seq, t = tok - b * p.seq;
+  const int64_t b = batch_of(p, tok), t = tok - b * p.seq;
   const int64_t at = axis * p.pos_sa + b * p.pos_sb + t * p.pos_st;
   return p.pos_i64 ? ((const int64_t*)p.pos)[at] : (int64_t)((const int32_t*)p.pos)[at];
 }
@@ -99,7 +102,7 @@ __device__ __forceinline__ void store_chunk(T* dst, const float* v) {
 
 template <typename T>
 __device__ __forceinline__ T* row_ptr(const QkTensor& x, const QkParams& p, int64_t tok, int head) {
-  const int64_t b = tok / p.seq, t = tok - b * p.seq;
+  const int64_t b = batch_of(p, tok), t = tok - b * p.seq;
   return (T*)x.p + b * x.sb + t * x.st + head * x.sh;
 }
 

@@ -470,7 +470,6 @@ class _Rope(torch.autograd.Function):
     def forward(ctx, q, k, positions, inv_freq, how):
         y = rope(q, k, positions, inv_freq, **how)
         ctx.save_for_backward(positions, inv_freq)
-        ctx.like = [None if t is None else (t.shape, t.dtype, t.device) for t in (q, k)]
         ctx.how = how
         ctx.set_materialize_grads(False)
         return y

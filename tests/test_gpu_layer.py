@@ -194,12 +194,32 @@ def test_linear_empty_sizes():
     y = ns.linear(x, w, b, r, activation="relu")  # no columns: relu(bias) + residual
     want = b.double().clamp(min=0) + r.double()
     close(y, want, want.abs() * (U[BF] + 2.0 ** -20), "k = 0")
+    x = rand((100, 0), BF, 3)
+    y = ns.linear(x, w, b, None)
+    assert torch.equal(y, b.expand(100, 24))
     assert ns.linear(rand((0, 8), BF, 5), rand((24, 8), BF, 6)).shape == (0, 24)
     assert ns.linear(rand((4, 8), BF, 5), rand((0, 8), BF, 6)).shape == (4, 0)
     dx, dw, db = ns.linear_backward(rand((0, 24), BF, 1), rand((0, 8), BF, 2), rand((24, 8), BF, 3), need_dbias=True)
     assert dx.shape == (0, 8) and not dw.any() and not db.any()
     dx, dw, _ = ns.linear_backward(rand((5, 0), BF, 1), rand((5, 8), BF, 2), rand((0, 8), BF, 3))
     assert not dx.any() and dw.shape == (0, 8)
+
+
+def test_linear_beyond_32_bit_offsets():
+    """Operands of more than 2^32 bytes: rows at the end of x, and sums over all of them."""
+    torch_cuda()
+    m, k, n = 70000, 32768, 72
+    x = torch.empty((m, k), dtype=BF, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    w, dy = rand((n, k), BF, 2, 1 / math.sqrt(k)), rand((m, n), BF, 3)
+    y = ns.linear(x, w)
+    tail = slice(m - 300, m)
+    check_forward(x[tail], w, None, None, None, y[tail], None, "last rows")
+    dx, dw, _ = ns.linear_backward(dy, x, w)
+    check_backward(dy[tail], x[tail], w, None, None, dx[tail], None, None, "last rows")
+    cols = slice(k - 64, k)
+    want, size = dy.double().t() @ x[:, cols].double(), dy.double().abs().t() @ x[:, cols].double().abs()
+    close(dw[:, cols], want, size * (m + 8) * 2.0 ** -23 + U[BF] * want.abs(), "dw")
 
 
 def test_linear_leading_dimensions():
@@ -502,6 +522,40 @@ def test_qk_in_place_on_packed_rows(d, pad):
     want = ns.qk_norm_rope_backward(gq, gk, q, k, pos, f)
     ns.qk_norm_rope_backward(gq, gk, q, k, pos, f, dq=gq, dk=gk)
     assert torch.equal(gq, want[0]) and torch.equal(gk, want[1])
+
+
+def test_qk_single_token_rows_in_place():
+    """Decoding: one token per sequence, q and k views of the packed rows, in place, in both shapes."""
+    torch_cuda()
+    B, hq, hk, d = 9, 8, 2, 128
+    buf, q, k = packed(B, hq, hk, d, BF, 1)
+    f, pos = torch.rand(d // 2, device="cuda"), torch.randint(0, 100000, (B,), device="cuda")
+    wq, wk = 1 + rand((d,), F32, 2, 0.1), 1 + rand((d,), F32, 3, 0.1)  # fp32 weights on bf16 heads
+    want = ns.qk_norm_rope(q, k, pos, f, q_weight=wq, k_weight=wk)
+    axes = torch.zeros(d // 2, dtype=torch.int64, device="cuda")
+    check_qk(q, wq, pos[None], f, axes, False, 1.0, 1e-6, want[0], "fp32 weight")
+    again = buf.clone()
+    qv, kv = again[:, :hq * d].view(B, 1, hq, d), again[:, hq * d:(hq + hk) * d].view(B, 1, hk, d)
+    ns.qk_norm_rope(qv, kv, pos.view(B, 1), f, q_weight=wq, k_weight=wk, q_out=qv, k_out=kv)
+    assert torch.equal(qv.reshape(B, hq, d), want[0]) and torch.equal(kv.reshape(B, hk, d), want[1])
+    assert torch.equal(again[:, (hq + hk) * d:], buf[:, (hq + hk) * d:])
+    one = buf[:1].clone()
+    qv, kv = one[:, :hq * d].view(1, hq, d), one[:, hq * d:(hq + hk) * d].view(1, hk, d)
+    ns.qk_norm_rope(qv, kv, pos[:1], f, q_weight=wq, k_weight=wk, q_out=qv, k_out=kv)
+    assert torch.equal(qv, want[0][:1]) and torch.equal(kv, want[1][:1])
+
+
+def test_qk_beyond_32_bit_offsets():
+    torch_cuda()
+    t, h, d = 140000, 128, 128
+    q = torch.empty((t, h, d), dtype=BF, device="cuda")
+    q.normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    f, pos = torch.rand(d // 2, device="cuda"), torch.arange(t, device="cuda")
+    axes = torch.zeros(d // 2, dtype=torch.int64, device="cuda")
+    y, _ = ns.qk_norm_rope(q, None, pos, f)
+    check_qk(q[-50:], None, pos[None, -50:], f, axes, False, 1.0, 1e-6, y[-50:], "last tokens")
+    ns.qk_norm_rope_backward(y, None, q, None, pos, f, dq=y)
+    assert torch.isfinite(y[-50:]).all()
 
 
 def test_qk_far_positions():
