@@ -5,7 +5,8 @@
 // 256 columns of a chunk of rows; a thread owns 8 consecutive columns of every
 // eighth row of it, keeps their sums in registers, and the eight row groups
 // are added in order through LDS, so a column's sum is added in an order that
-// depends on the sizes only.
+// depends on the sizes only.  4096 x 14336 in bf16 (352 MB, 69 us at the rate
+// of a copy): 80 us.
 #include "layer_internal.h"
 #include "linear_epilogue.h"
 

@@ -76,15 +76,20 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* base, int64_t bytes) {
 // operand bound to that register: the compiler writes M0 itself and knows
 // it is read here, so nothing the compiler keeps in M0 is overwritten.
 // The compiler does not look inside the assembly for the wait states that the
-// hardware leaves to software: five between a vector instruction that writes
-// a scalar register (v_readfirstlane) and a memory instruction that reads it,
-// one between a write of M0 and an LDS load.  The s_nop covers both, whatever
-// the compiler put in front.
+// hardware leaves to software, so the assembly starts with WAITS of them.  One
+// is needed between a write of M0 and an LDS load.  Five are needed between a
+// vector instruction that writes a scalar register (v_readfirstlane) and a
+// memory instruction that reads it: a kernel whose descriptor or offset
+// changes from load to load takes five, whatever the compiler puts in front;
+// one whose descriptors are formed once, far from its loads, and whose offsets
+// are scalar arithmetic takes one (five cost its step 1 %).
+template <int WAITS = 1>
 __device__ __forceinline__ void lds_dma16_asm(i32x4 rsrc, uint32_t lds, int voff, int soff) {
-  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  static_assert(WAITS >= 1 && WAITS <= 16, "s_nop's range");
+  asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc),
-                 "s"(__builtin_amdgcn_readfirstlane(soff))
+                 "s"(__builtin_amdgcn_readfirstlane(soff)), "n"(WAITS - 1)
                : "memory");
 }
 

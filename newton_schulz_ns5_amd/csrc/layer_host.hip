@@ -178,10 +178,13 @@ Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t d
 // round takes a fixed time (pipeline start, epilogue) and a time per slice of
 // K, which is bounded by latency (u0) while few workgroups run and by the
 // chip's rate (u1) in a full round.  Measured for every tile with 16 to 1024
-// workgroups; bf16, 4096 x 14336 over 4096: 414 us in 256 x 256 tiles (3.5
-// rounds), 416 in 256 x 128 (7 rounds), HYB with the last half round of the
-// larger ones in the smaller; 2048 x 4096 over 6144: 132 us in 256 x 256 (half
-// a round), 94 in 256 x 128, 118 in 128, 166 in 64.
+// workgroups.  bf16, us in tiles of 256 x 256, 256 x 128, 128 and 64, and with
+// the last, part-empty round of the largest tile in the next (one box):
+//   4096 x 14336 over 4096   417  409  500  704  399
+//   14336 x 4096 over 4096   398  432  546  791  388
+//   6144 x 4096 over 2048    104  101  121  158   96
+//   2048 x 4096 over 6144    129   91  112  161
+//   1037 x 1001 over 2056      -   22*  23*   18      * split, with its addition
 struct Tiling { LinTile first, rest; int64_t m1, n1; int split; };
 
 struct TileCost { LinTile tile; int bm, bn, slots; double fixed, u0, u1; };

@@ -23,7 +23,12 @@
 //  - every LDS address of a lane is one register per operand plus constants: a
 //    version that formed them per read spilled six registers in the product
 //    of two col operands, whose reloads waited out the loads in flight
-//    (537 us where this takes LAST us, 14336 x 4096 over 4096).
+//    (14336 x 4096 over 4096 in 256 x 256 tiles: 537 us where this takes 400 to
+//    433, by the box's clock).
+// What bounds it: 4096 x 4096 over 14336 runs at 1337 TFLOP/s (the library's
+// product at 1263 on the same box) with the matrix units about 70 % busy, at a
+// clock that power holds near 1.65 GHz; the epilogue and the pipeline's start
+// cost about 8 us per round of workgroups.
 // Ragged sizes cost nothing in the loop: rows past the end repeat the last one
 // (their products are not stored), K values past the end are zeros from the
 // buffer descriptor's bounds check (which the loads of the last slice are sent
@@ -227,14 +232,14 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   auto load_a = [&](int t, uint32_t slot, int q) {
     const bool last = t >= KT - 1;
     const int tc = last ? KT - 1 : t, at = (wave * DPA + q) * 1024;
-    if constexpr (ACOL) lds_dma16_asm(col_rsrc(Au, lda, afull, alast, tc), slot + at, avo[q], 0);
-    else lds_dma16_asm(ars, slot + at, last ? tail(avo[q], at + lane * 16) : avo[q], tc * ROWB);
+    if constexpr (ACOL) lds_dma16_asm<5>(col_rsrc(Au, lda, afull, alast, tc), slot + at, avo[q], 0);
+    else lds_dma16_asm<5>(ars, slot + at, last ? tail(avo[q], at + lane * 16) : avo[q], tc * ROWB);
   };
   auto load_b = [&](int t, uint32_t slot, int q) {
     const bool last = t >= KT - 1;
     const int tc = last ? KT - 1 : t, at = (wave * DPB + q) * 1024;
-    if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bu, ldb, bfull, blast, tc), slot + at, bvo[q], 0);
-    else lds_dma16_asm(brs, slot + at, last ? tail(bvo[q], at + lane * 16) : bvo[q], tc * ROWB);
+    if constexpr (BCOL) lds_dma16_asm<5>(col_rsrc(Bu, ldb, bfull, blast, tc), slot + at, bvo[q], 0);
+    else lds_dma16_asm<5>(brs, slot + at, last ? tail(bvo[q], at + lane * 16) : bvo[q], tc * ROWB);
   };
   // Slot of the next slice of the same operand.
   auto next_a = [&](uint32_t s) {
