@@ -448,7 +448,8 @@ typedef struct muon_qk_problem {
 
 int muon_qk_norm_rope(const muon_qk_problem* p, void* stream);
 /* Gradients dq, dk (y) and dweight from the gradients of the outputs (g), the
- * inputs (x) and the weights.  dq and dk may be their own g. */
+ * inputs (x) and the weights.  dq and dk may be their own g.  A call without
+ * tokens or heads writes nothing, dweight included. */
 int muon_qk_norm_rope_backward_workspace_bytes(const muon_qk_problem* p, size_t* bytes);
 int muon_qk_norm_rope_backward(const muon_qk_problem* p, void* workspace, size_t workspace_bytes, void* stream);
 /* The rotation alone, and its gradient: y = scale R^T g (x is not read). */

@@ -125,6 +125,8 @@ int check_linear_grad(const muon_linear_grad* q) {
   if ((rc = check_sizes(q->m, q->n, q->k)) || (rc = check_act(q->activation))) return rc;
   if (!dtype_ok(q->dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype %d is not MUON_F32 or MUON_BF16", q->dtype);
   if ((rc = check_matrix("dy", q->dy, q->dy_dtype, q->m, q->n, q->dy_row_stride))) return rc;
+  // the gradient at the pre-activation is a matrix of the operands' type
+  if (q->n * esize(q->dtype) > kMaxRowBytes) return fail(MUON_ERR_INVALID_ARG, "rows of n elements of dtype must be at most 2^23 - 32 bytes");
   const bool act = q->activation != MUON_ACT_NONE;
   if (act && (rc = check_matrix("preact", q->preact, q->dtype, q->m, q->n, q->preact_row_stride))) return rc;
   if (q->dw && (rc = check_matrix("x", q->x, q->dtype, q->m, q->k, q->x_row_stride))) return rc;

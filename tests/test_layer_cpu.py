@@ -114,6 +114,8 @@ def grad_problem(**over):
     (dict(dy_dtype=3), -2), (dict(activation=17), -2), (dict(accumulate=2), -1), (dict(reserved=3), -1),
     (dict(dx=FAKE), -1), (dict(dw=FAKE + MIB), -1), (dict(dbias=FAKE + 5 * MIB), -1), (dict(dx=FAKE + 3 * MIB), -1),
     (dict(dx=FAKE + 2 * MIB), -1),
+    # bf16 gradients whose fp32 copy would have rows of 2^23 bytes
+    (dict(dtype=0, activation=0, n=1 << 21, dy_row_stride=1 << 21, dx_dtype=0, dw=None, dbias=None), -1),
 ])
 def test_linear_backward_refusals(over, code):
     L = _lib.lib()
