@@ -17,12 +17,33 @@ __device__ __forceinline__ float gelu_arg(float z) {
   return 1.59576912160573f * z * (1.f + 0.044715f * z * z);
 }
 
+// The normal distribution function of z, and its density through `pdf`, with
+// one exponential for both: 1/2 erfc(x) = 1/2 P(t) exp(-x^2), x = |z| / sqrt 2,
+// t = 1 / (1 + 0.3275911 x) (Abramowitz and Stegun, 7.1.26: within 1.5e-7 of
+// erf, at a third of the instructions of the library's erff, which cost the
+// epilogue of a 4096 x 14336 product 20 us).
+__device__ __forceinline__ float normal_cdf(float z, float& pdf) {
+  const float e = __builtin_amdgcn_exp2f(-0.721347520444482f * z * z);
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.231641888f * fabsf(z));
+  float q = 1.061405429f;
+  q = q * t - 1.453152027f;
+  q = q * t + 1.421413741f;
+  q = q * t - 0.284496736f;
+  q = q * t + 0.254829592f;
+  const float h = 0.5f * q * t * e;
+  pdf = 0.398942280401433f * e;
+  return z > 0.f ? 1.f - h : h;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_fwd(float z) {
   if constexpr (ACT == MUON_ACT_RELU) return z <= 0.f ? 0.f : z;  // a NaN stays one
   if constexpr (ACT == MUON_ACT_RELU2) return z <= 0.f ? 0.f : z * z;
   if constexpr (ACT == MUON_ACT_SILU) return z * logistic(z);
-  if constexpr (ACT == MUON_ACT_GELU) return 0.5f * z * (1.f + erff(0.707106781186548f * z));
+  if constexpr (ACT == MUON_ACT_GELU) {
+    float pdf;
+    return z * normal_cdf(z, pdf);
+  }
   if constexpr (ACT == MUON_ACT_GELU_TANH) return z * logistic(gelu_arg(z));
   return z;
 }
@@ -39,9 +60,11 @@ __device__ __forceinline__ float act_slope(float z) {
       const float s = logistic(c);
       return s * (1.f + c * (1.f - s));
     }
-    if constexpr (ACT == MUON_ACT_GELU)
-      return 0.5f * (1.f + erff(0.707106781186548f * c)) +
-             0.398942280401433f * c * __builtin_amdgcn_exp2f(-0.721347520444482f * c * c);
+    if constexpr (ACT == MUON_ACT_GELU) {
+      float pdf;
+      const float cdf = normal_cdf(c, pdf);
+      return cdf + c * pdf;
+    }
     const float s = logistic(gelu_arg(c));
     return s + c * s * (1.f - s) * 1.59576912160573f * (1.f + 0.134145f * c * c);
   }
