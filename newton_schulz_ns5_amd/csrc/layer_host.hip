@@ -458,7 +458,7 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
   hipError_t e;
   // the gradient at the pre-activation; dy itself where they are the same
   const void* G = q->m && q->n ? q->dy : nullptr;
-  int64_t ldg = q->m > 1 ? q->dy_row_stride : P.ldg;
+  int64_t ldg = q->m > 1 && q->n ? q->dy_row_stride : P.ldg;  // (the stride of one row, or of none, means nothing)
   if (P.store_g || (P.colsum && P.chunks > 0)) {
     ActGrad a{};
     a.dy = q->dy; a.dy_dtype = q->dy_dtype; a.lddy = q->dy_row_stride;

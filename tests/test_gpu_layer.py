@@ -205,6 +205,22 @@ def test_linear_empty_sizes():
     assert not dx.any() and dw.shape == (0, 8)
 
 
+def test_empty_sum_ignores_its_operands_strides():
+    """The C entry point with n = 0: dx is zero whatever the strides of the empty dy and w."""
+    torch_cuda()
+    import ctypes
+    from newton_schulz_ns5_amd import _lib
+    dx = torch.full((70, 24), 7.0, dtype=BF, device="cuda")
+    p = _lib.LinearGrad(m=70, n=0, k=24, dtype=1, dy_dtype=1, dx_dtype=1, dy_row_stride=5, w_row_stride=3,
+                        dx=dx.data_ptr(), dx_row_stride=24)
+    need = ctypes.c_size_t()
+    _lib.check(_lib.lib().muon_linear_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)))
+    ws = torch.empty(max(need.value, 256), dtype=torch.uint8, device="cuda")
+    _lib.check(_lib.lib().muon_linear_backward(ctypes.byref(p), ws.data_ptr(), ws.numel(),
+                                               torch.cuda.current_stream().cuda_stream))
+    assert not dx.any()
+
+
 def test_linear_beyond_32_bit_offsets():
     """Operands of more than 2^32 bytes: rows at the end of x, and sums over all of them."""
     torch_cuda()
