@@ -371,9 +371,10 @@ int muon_linear(const muon_linear_problem* p, void* workspace, size_t workspace_
  *   dx = g w,  dw = g^T x,  dbias = sum over rows of g
  * (the residual's gradient is dy).  Outputs that are NULL are not computed;
  * x is read for dw only, w for dx only, preact only with an activation.
- * g is rounded to `dtype` where an activation (or dy of another type) makes
- * it differ from dy, since it is an operand of both products; dbias sums the
- * unrounded g in fp32.  dw and dbias are what a step takes as gradients: dw
+ * Where an activation (or dy of another type) makes g differ from dy, a dx or
+ * dw in bf16 takes g rounded to `dtype`, since it is an operand of the product;
+ * one in fp32 takes g to 2^-16 (bf16 operands: as the sum of two bf16 terms, at
+ * twice the products).  dbias sums the unrounded g in fp32.  dw and dbias are what a step takes as gradients: dw
  * contiguous in bf16 or fp32.  With accumulate they are added to what the
  * outputs hold (in fp32, one rounding on store).  m == 0 gives zero dw and
  * dbias.  Results do not depend on anything but the arguments: sums are added

@@ -40,6 +40,17 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGrad p) {
           for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(z[e]);
         }
         if (p.G) put8(p.G, i * p.ldg + j, BF, 8, g);  // values past N are zero
+        if constexpr (BF) {
+          if (p.low) {  // what the rounding left (nothing where it overflowed)
+            float l[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float h = bf2f(f2bf(g[e]));
+              l[e] = fabsf(h) < __builtin_huge_valf() ? g[e] - h : 0.f;
+            }
+            put8(p.low, i * p.ldg + j, true, 8, l);
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += g[e];
       }

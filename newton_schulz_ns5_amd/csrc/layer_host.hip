@@ -343,14 +343,18 @@ LinearPlan plan_linear(const muon_linear_problem* q) {
 // pre-activation differs from dy (an activation, or dy of another type than
 // the operands), when dy's rows cannot be loaded in place, or when the bias
 // gradient is wanted.  The split sums of dx and dw use one region in turn.
+// With bf16 operands g = dy act'(z) has more bits than an operand.  A gradient
+// in bf16 takes g rounded to bf16, whose error (2^-8 of each term) is the one
+// that its own rounding has.  A gradient in fp32 takes two terms, the rounded g
+// and what that leaves, rounded: 2^-16 of each term, at twice the products.
 struct GradPlan {
-  bool store_g, colsum;
+  bool store_g, colsum, low;
   int64_t ldg;
   int chunks;
   int64_t rows_per;
   Operand x, w;
   Tiling tx, tw;
-  size_t g_off, partial_off, part_off, total;
+  size_t g_off, low_off, partial_off, part_off, total;
 };
 
 GradPlan plan_grad(const muon_linear_grad* q) {
@@ -369,6 +373,9 @@ GradPlan plan_grad(const muon_linear_grad* q) {
   P.chunks = (int)cdiv(q->m, P.rows_per);
   P.ldg = cdiv(q->n, 8) * 8;
   if (P.store_g) P.g_off = take((size_t)(q->m * P.ldg * esize(q->dtype)));
+  P.low = P.store_g && q->dtype == MUON_BF16 && (q->activation != MUON_ACT_NONE || q->dy_dtype != MUON_BF16) &&
+          ((dx && q->dx_dtype == MUON_F32) || (dw && q->dw_dtype == MUON_F32));
+  if (P.low) P.low_off = take((size_t)(q->m * P.ldg * 2));
   if (P.colsum) P.partial_off = take((size_t)P.chunks * (size_t)q->n * 4);
   const bool bf = q->dtype == MUON_BF16;
   size_t part = 0;
@@ -468,6 +475,7 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
       a.G = ws + P.g_off; a.ldg = P.ldg;
       G = a.G; ldg = P.ldg;
     }
+    if (P.low) a.low = ws + P.low_off;
     if (P.colsum) a.partial = (float*)(ws + P.partial_off);
     a.chunks = P.chunks; a.rows_per = P.rows_per;
     a.M = q->m; a.N = q->n;
@@ -486,7 +494,13 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
     g.B = P.w.p; g.ldb = P.w.ld;
     g.M = q->m; g.N = q->k; g.K = q->n;
     g.Y = q->dx; g.y_dtype = q->dx_dtype; g.ldy = q->dx_row_stride;
-    if ((e = run_product(g, q->dtype, kRowCol, P.tx, ws + P.part_off, s)) != hipSuccess) return hip_fail(e, "input gradient");
+    e = run_product(g, q->dtype, kRowCol, P.tx, ws + P.part_off, s);
+    if (e == hipSuccess && P.low && q->dx_dtype == MUON_F32) {
+      g.A = ws + P.low_off;
+      g.add = q->dx; g.add_dtype = q->dx_dtype; g.ldadd = q->dx_row_stride;
+      e = run_product(g, q->dtype, kRowCol, P.tx, ws + P.part_off, s);
+    }
+    if (e != hipSuccess) return hip_fail(e, "input gradient");
   }
   if (dw) {
     LinGemm g{};
@@ -495,7 +509,13 @@ int muon_linear_backward(const muon_linear_grad* q, void* workspace, size_t work
     g.M = q->n; g.N = q->k; g.K = q->m;
     g.Y = q->dw; g.y_dtype = q->dw_dtype; g.ldy = q->dw_row_stride;
     if (q->accumulate) { g.add = q->dw; g.add_dtype = q->dw_dtype; g.ldadd = q->dw_row_stride; }
-    if ((e = run_product(g, q->dtype, kColCol, P.tw, ws + P.part_off, s)) != hipSuccess) return hip_fail(e, "weight gradient");
+    e = run_product(g, q->dtype, kColCol, P.tw, ws + P.part_off, s);
+    if (e == hipSuccess && P.low && q->dw_dtype == MUON_F32) {
+      g.A = ws + P.low_off;
+      g.add = q->dw; g.add_dtype = q->dw_dtype; g.ldadd = q->dw_row_stride;
+      e = run_product(g, q->dtype, kColCol, P.tw, ws + P.part_off, s);
+    }
+    if (e != hipSuccess) return hip_fail(e, "weight gradient");
   }
   return ok();
 }

@@ -53,13 +53,15 @@ hipError_t launch_pack(const PackJobs& p, bool bf16, hipStream_t s);
 
 // ---- gradient at the pre-activation ----------------------------------------------
 // G = round(dy * act'(z)) in the operand type (G null: not stored), with zeros
-// in columns N .. ldg - 1 (ldg the next multiple of 8), and, when
+// in columns N .. ldg - 1 (ldg the next multiple of 8); low (bf16 operands, may
+// be null) = round(dy * act'(z) - G), laid out the same; and, when
 // partial is not null, partial[c][j] = the sum over row chunk c of dy * act'(z)
 // (unrounded), rows c * rows_per .. of M.
 struct ActGrad {
   const void* dy; int32_t dy_dtype; int64_t lddy;
   const void* z; int64_t ldz;          // operand type; null: act' = 1
   void* G; int64_t ldg;
+  void* low;
   float* partial; int32_t chunks; int64_t rows_per;
   int64_t M, N;
   int32_t act;
