@@ -140,6 +140,13 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _written(*tensors):
+    """Tell autograd that these tensors (None: left out) were written through
+    their pointers, so that a backward pass that saved one of them raises
+    instead of reading the new values."""
+    _torch().autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def ns_workspace_bytes(n, rows, cols, cfg):
     out = ctypes.c_size_t(0)
     _lib.check(lib().muon_ns_workspace_bytes(int(n), int(rows), int(cols), ctypes.byref(cfg), ctypes.byref(out)))
@@ -187,6 +194,7 @@ def ns_batched(x, out=None, *, steps=5, coeffs=QUINTIC, eps=1e-7, compute_dtype=
         _ptr(x3), _dt(x3), x3.stride(0), x3.stride(1),
         _ptr(y3), _dt(y3), y3.stride(0), y3.stride(1),
         n, rows, cols, ctypes.byref(cfg), _ptr(ws), ws.numel(), _stream(x)))
+    _written(out)
     return out
 
 
@@ -210,6 +218,7 @@ def ns_batched_noalloc(x, out=None, *, steps=5, coeffs=QUINTIC, eps=1e-7, comput
         _ptr(x3), _dt(x3), x3.stride(0), x3.stride(1),
         _ptr(y3), _dt(y3), y3.stride(0), y3.stride(1),
         n, rows, cols, ctypes.byref(cfg), _stream(x)))
+    _written(out)
     return out
 
 
@@ -258,6 +267,7 @@ def ns_groups(xs, outs=None, *, steps=5, coeffs=QUINTIC, eps=1e-7, compute_dtype
     need = ns_groups_workspace_bytes([tuple(_as3(x).shape) for x in xs], cfg)
     ws = workspace if workspace is not None else _workspace(xs[0].device, need)
     _lib.check(lib().muon_ns_groups(probs, len(xs), ctypes.byref(cfg), _ptr(ws), ws.numel(), _stream(xs[0])))
+    _written(*outs)
     return outs
 
 
@@ -275,6 +285,7 @@ def normuon_normalize(o, v, beta2=0.95, eps=1e-8, workspace=None):
     _lib.check(lib().normuon_normalize(
         _ptr(o3), _dt(o3), o3.stride(0), o3.stride(1), n, rows, cols,
         _ptr(v2), v2.stride(0), float(beta2), float(eps), _ptr(ws), ws.numel(), _stream(o)))
+    _written(o, v)
     return o
 
 
@@ -344,6 +355,7 @@ def step_group(w_master, grads, moms, variances=None, w_model=None, *, heads=1, 
     _lib.check(lib().muon_step_group(ctypes.byref(g), ctypes.byref(hp), _ptr(ws), ws.numel(),
                                      _stream(w_master[0])))
     del keep
+    _written(*w_master, *moms, *(variances or ()), *(w_model or ()))
     return None
 
 
@@ -374,6 +386,8 @@ def step_groups(groups, *, hp=None, workspace=None, **kw):
     ws = workspace if workspace is not None else _workspace(first.device, need.value)
     _lib.check(lib().muon_step_groups(arr, len(made), ctypes.byref(hp), _ptr(ws), ws.numel(), _stream(first)))
     del made
+    for d in groups:
+        _written(*d["w_master"], *d["moms"], *(d.get("variances") or ()), *(d.get("w_model") or ()))
     return None
 
 
@@ -501,6 +515,7 @@ class MuonNS5:
                 "split_rows": list(sp) if sp else None,
             })
         step_groups(todo, hp=self.hp)
+        _written(*(p for p in self.params if p.grad is not None))  # p.data has a version counter of its own
         # Parameters whose storage the library does not write: copy the new
         # values in (a layout change only, on the same stream).
         with torch.no_grad():

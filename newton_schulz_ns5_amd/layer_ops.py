@@ -13,7 +13,7 @@ import struct
 
 import torch
 
-from . import MuonError, _lib
+from . import MuonError, _lib, _written
 from ._lib import MUON_BF16, MUON_F32
 
 __all__ = ["linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward",
@@ -166,6 +166,7 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
     wp, n, k, ldw = _rows(w, "w")
     xp, m, _, ldx = _rows(x, "x", k)
     shape = x.shape[:-1] + (n,)
+    given = [t for t in (out, preact) if t is not None]
     if out is None:
         out = (x if residual is None else residual).new_empty(shape)
     if (return_preact or preact is not None):
@@ -181,6 +182,8 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
                         _dt(bias) if bias is not None else 0, _dt(residual) if residual is not None else 0, _dt(out), 0)
     L = _lib.lib()
     _call(dev, L.muon_linear, prob, L.muon_linear_workspace_bytes)
+    if given:
+        _written(*given)
     return (out, preact) if return_preact else out
 
 
@@ -214,6 +217,7 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
         zp, ldz = _check_matrix(preact, "preact", m, n)
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         _bad("accumulate needs the tensors to add to")
+    given = [t for t in (dx, dw, dbias) if t is not None]
     if dx is None and need_dx:
         dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     if dw is None and need_dw:
@@ -228,6 +232,8 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
                       _dt(dbias) if dbias is not None else 0, int(bool(accumulate)), 0)
     L = _lib.lib()
     _call(dev, L.muon_linear_backward, prob, L.muon_linear_backward_workspace_bytes)
+    if given:
+        _written(*given)
     return dx, dw, dbias
 
 
@@ -390,6 +396,8 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
                          (q_weight, k_weight), (None, None), eps)
     _call(dev, _lib.lib().muon_qk_norm_rope, p, None)
+    if q_out is not None or k_out is not None:
+        _written(q_out, k_out)
     return y
 
 
@@ -407,6 +415,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
                 t.zero_()
     L = _lib.lib()
     _call(dev, L.muon_qk_norm_rope_backward, p, L.muon_qk_norm_rope_backward_workspace_bytes)
+    if dq is not None or dk is not None:
+        _written(dq, dk)
     return y + dwt
 
 
@@ -422,6 +432,8 @@ def rope(q, k, positions, inv_freq, *, sections=None, axes=None, interleaved=Fal
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
                          (None, None), (None, None), 0.0)
     _call(dev, _lib.lib().muon_rope, p, None)
+    if q_out is not None or k_out is not None:
+        _written(q_out, k_out)
     return y
 
 
@@ -432,6 +444,8 @@ def rope_backward(dq_out, dk_out, positions, inv_freq, *, sections=None, axes=No
     dev, p = _qk_problem(dq_out, dk_out, positions, inv_freq, sections, axes, interleaved, scale, None,
                          (dq_out, dk_out), y, (None, None), (None, None), 0.0)
     _call(dev, _lib.lib().muon_rope_backward, p, None)
+    if dq is not None or dk is not None:
+        _written(dq, dk)
     return y
 
 

@@ -49,3 +49,73 @@ def test_fp32_gradients_behind_an_infinite_one():
     _, dw, _ = ns.linear_backward(dy, x, w, activation="relu", preact=z, need_dx=False, dw_dtype=F32)
     assert torch.isinf(dw[5]).all() and torch.equal(dw[5] > 0, x[7] > 0)
     assert torch.isfinite(dw[:5]).all() and torch.isfinite(dw[6:]).all()
+
+
+# ---- buffers written through their pointers ------------------------------------------
+def versions(ts, call):
+    """call() and which of ts it moved on."""
+    before = [t._version for t in ts]
+    call()
+    return [t._version > b for t, b in zip(ts, before)]
+
+
+def test_written_outputs_move_their_version_counters():
+    torch_cuda()
+    x, w, dy, z = rand((20, 64), BF, 1), rand((48, 64), BF, 2), rand((20, 48), BF, 3), rand((20, 48), BF, 4)
+    out, pre = torch.empty_like(dy), torch.empty_like(dy)
+    assert versions([out, pre, x, w], lambda: ns.linear(x, w, activation="silu", out=out, preact=pre, return_preact=True)) == \
+        [True, True, False, False]
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(48, dtype=BF, device="cuda")
+    assert all(versions([dx, dw, db], lambda: ns.linear_backward(dy, x, w, dx=dx, dw=dw, dbias=db, need_dbias=True)))
+    assert versions([dw, dy], lambda: ns.linear_backward(dy, x, w, need_dx=False, dw=dw, accumulate=True)) == [True, False]
+    q, k, gq, gk = (rand((6, h, 64), BF, i) for i, h in enumerate((4, 2, 4, 2)))
+    pos, f = torch.arange(6, device="cuda"), torch.rand(32, device="cuda")
+    for fn in (ns.rope, ns.qk_norm_rope):
+        assert versions([q, k], lambda: fn(q, k, pos, f, q_out=q)) == [True, False]
+        assert all(versions([q, k], lambda: fn(q, k, pos, f, q_out=q, k_out=k)))
+    assert versions([gq, gk], lambda: ns.rope_backward(gq, gk, pos, f, dk=gk)) == [False, True]
+    assert versions([gq, gk, q], lambda: ns.qk_norm_rope_backward(gq, gk, q, k, pos, f, dq=gq, dk=gk)) == [True, True, False]
+    buf = rand((6, 8 * 64), BF, 5)  # a view's buffer with it
+    assert versions([buf], lambda: ns.rope(buf[:, :256].view(6, 4, 64), None, pos, f, q_out=buf[:, :256].view(6, 4, 64))) == [True]
+
+
+def test_backward_after_a_saved_buffer_was_written_raises():
+    torch_cuda()
+    x, w = rand((6, 128), BF, 1), rand((32, 128), BF, 2).requires_grad_()
+    pos, f = torch.arange(6, device="cuda"), torch.rand(32, device="cuda")
+    h = ns.linear(x, w)
+    ns.rope(x.view(6, 2, 64), None, pos, f, q_out=x.view(6, 2, 64))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        h.sum().backward()
+    with torch.inference_mode():  # tensors without a counter are written like any other
+        y = rand((6, 32), BF, 3)
+        ns.linear(x, w.detach(), out=y)
+    assert torch.equal(y, ns.linear(x, w.detach()))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_backward_after_the_step_raises(dtype):
+    """The step writes the weight that linear saved."""
+    torch_cuda()
+    x, w = rand((8, 64), dtype, 1).requires_grad_(), rand((32, 64), dtype, 2).requires_grad_()
+    opt = ns.MuonNS5([w], lr=0.05)
+    h = ns.linear(x, w)
+    h.sum().backward(retain_graph=True)
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        h.sum().backward()
+
+
+def test_step_and_newton_schulz_outputs_move_their_version_counters():
+    torch_cuda()
+    shape = (64, 96)
+    w, g, m, v, wm = rand(shape, F32, 1), rand(shape, BF, 2), rand(shape, BF, 3), torch.ones(64, device="cuda"), rand(shape, BF, 4)
+    ts = [w, m, v, wm, g]
+    assert versions(ts, lambda: ns.step_group([w], [g], [m], [v], [wm], normuon=True)) == [True] * 4 + [False]
+    one = {"w_master": [w], "grads": [g], "moms": [m], "variances": [v], "w_model": [wm]}
+    assert versions(ts, lambda: ns.step_groups([one], normuon=True)) == [True] * 4 + [False]
+    out = torch.empty_like(g)
+    assert versions([out, g], lambda: ns.ns_batched(g, out)) == [True, False]
+    assert versions([out, g], lambda: ns.ns_batched_noalloc(g, out)) == [True, False]
+    assert versions([out, g], lambda: ns.ns_groups([g], [out])) == [True, False]
+    assert versions([out, v], lambda: ns.normuon_normalize(out, v)) == [True, True]
