@@ -6,12 +6,14 @@ Thin marshalling like the rest of the binding: shapes and strides in, raw
 pointers to the library, work enqueued on the current stream.  ``linear``,
 ``qk_norm_rope`` and ``rope`` record themselves for autograd when an input
 requires a gradient; the ``*_backward`` entry points are the same gradients
-called directly.
+called directly, and their results carry no gradient of their own.  Inputs of
+forward-mode differentiation are refused.
 """
 import ctypes
 import struct
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from . import MuonError, _lib, _written
 from ._lib import MUON_BF16, MUON_F32
@@ -129,7 +131,17 @@ def _refuse_capture():
                         "autograd is not recorded under stream capture: call the *_backward entry point there")
 
 
+def _refuse_tangents(*ts):
+    """These operators have no forward-mode derivative: a result would silently come without its tangent."""
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        for t in ts:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "forward-mode automatic differentiation is not supported")
+
+
 def _wants_grad(*ts):
+    """Whether to record the call for autograd."""
+    _refuse_tangents(*ts)
     if torch.is_grad_enabled():
         for t in ts:
             if t is not None and t.requires_grad:
@@ -198,6 +210,7 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
     bf16 and fp32 are both what a step takes as a gradient.  Given outputs are
     written in place, and with ``accumulate`` dw and dbias are added to.
     """
+    _refuse_tangents(dy, x, w, preact)
     act = _act(activation)
     dev = _same_device(dy, x, w, preact, dx, dw, dbias)
     code = _dt(x)
@@ -386,6 +399,7 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     says which pair turns by which.  ``inv_freq`` [rotary pairs] is fp32 or
     fp64.  Returns (q_out, k_out); an output may be its own input.
     """
+    _refuse_tangents(inv_freq)
     if _wants_grad(q, k, q_weight, k_weight):
         if q_out is not None or k_out is not None:
             _bad("q_out and k_out cannot be given when an input requires a gradient")
@@ -405,6 +419,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
                           sections=None, axes=None, interleaved=False, scale=1.0, dq=None, dk=None):
     """(dq, dk, dq_weight, dk_weight) of :func:`qk_norm_rope` for the gradients of its outputs; None for what
     was not given.  dq may be dq_out, and dk dk_out."""
+    _refuse_tangents(dq_out, dk_out, q, k, q_weight, k_weight)
     y = (_like(q, dq), _like(k, dk))
     dwt = (_like(q_weight, None), _like(k_weight, None))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), (dq_out, dk_out), y,
@@ -422,6 +437,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
 
 def rope(q, k, positions, inv_freq, *, sections=None, axes=None, interleaved=False, scale=1.0, q_out=None, k_out=None):
     """The position rotation of :func:`qk_norm_rope` without its norm (see muon_rope)."""
+    _refuse_tangents(inv_freq)
     if _wants_grad(q, k):
         if q_out is not None or k_out is not None:
             _bad("q_out and k_out cannot be given when an input requires a gradient")
@@ -440,6 +456,7 @@ def rope(q, k, positions, inv_freq, *, sections=None, axes=None, interleaved=Fal
 def rope_backward(dq_out, dk_out, positions, inv_freq, *, sections=None, axes=None, interleaved=False, scale=1.0,
                   dq=None, dk=None):
     """(dq, dk) of :func:`rope`: the rotation by the opposite angles.  dq may be dq_out, and dk dk_out."""
+    _refuse_tangents(dq_out, dk_out)
     y = (_like(dq_out, dq), _like(dk_out, dk))
     dev, p = _qk_problem(dq_out, dk_out, positions, inv_freq, sections, axes, interleaved, scale, None,
                          (dq_out, dk_out), y, (None, None), (None, None), 0.0)

@@ -216,3 +216,31 @@ def test_python_refusals():
     pos, f = torch.zeros(4, dtype=torch.int64), torch.ones(4)
     assert code_of(lambda: ns.qk_norm_rope(q, q, pos, f)) == -1
     assert code_of(lambda: ns.rope(None, None, pos, f)) == -1
+
+
+# ---- calls that would lose what their caller asked for, refused before the device is looked at ----
+def heads_call():
+    q = torch.randn(4, 2, 8)
+    return q, torch.arange(4), torch.ones(4)
+
+
+def test_forward_mode_is_refused():
+    """The result would come without its tangent."""
+    from torch.autograd import forward_ad as fwd
+    x, w, b, r = torch.randn(4, 8), torch.randn(16, 8), torch.randn(16), torch.randn(4, 16)
+    q, pos, f = heads_call()
+    with fwd.dual_level():
+        def dual(t):
+            return fwd.make_dual(t, torch.ones_like(t))
+        for args in ((dual(x), w, b, r), (x, dual(w), b, r), (x, w, dual(b), r), (x, w, b, dual(r))):
+            assert code_of(lambda: ns.linear(*args)) == -2
+        assert code_of(lambda: ns.linear_backward(dual(r), x, w)) == -2
+        assert code_of(lambda: ns.rope(dual(q), None, pos, f)) == -2
+        assert code_of(lambda: ns.rope(q, q, pos, dual(f))) == -2
+        assert code_of(lambda: ns.rope_backward(None, dual(q), pos, f)) == -2
+        assert code_of(lambda: ns.qk_norm_rope(q, dual(q), pos, f)) == -2
+        assert code_of(lambda: ns.qk_norm_rope(q, None, pos, f, q_weight=dual(torch.ones(8)))) == -2
+        assert code_of(lambda: ns.qk_norm_rope_backward(q, None, dual(q), None, pos, f)) == -2
+        with torch.no_grad():
+            assert code_of(lambda: ns.linear(dual(x), w)) == -2
+        assert code_of(lambda: ns.linear(x, w)) == -1  # no dual tensor: only the device is wrong
