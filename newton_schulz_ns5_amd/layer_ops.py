@@ -51,8 +51,24 @@ def _dt(t):
     return code
 
 
+_tracing_state = torch._C._get_tracing_state
+_dispatch_modes = torch._C._len_torch_dispatch_stack
+
+
+def _refuse_tracing():
+    """A tracer records the allocation of a result but not the launch that writes
+    it: its replays would return memory that nobody wrote."""
+    if _tracing_state() is not None:
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "torch.jit.trace cannot record this operator")
+    if _dispatch_modes():
+        from torch.fx.experimental.proxy_tensor import get_proxy_mode
+        if get_proxy_mode() is not None:
+            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "torch.fx tracing cannot record this operator")
+
+
 def _same_device(first, *others):
     """The index of the one GPU that holds every tensor."""
+    _refuse_tracing()
     dev = first.get_device()
     if dev < 0:
         _bad(f"tensors must be on a GPU, got {first.device}")

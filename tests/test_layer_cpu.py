@@ -244,3 +244,18 @@ def test_forward_mode_is_refused():
         with torch.no_grad():
             assert code_of(lambda: ns.linear(dual(x), w)) == -2
         assert code_of(lambda: ns.linear(x, w)) == -1  # no dual tensor: only the device is wrong
+
+
+def test_tracing_is_refused():
+    """A trace would hold the result's allocation without the launch that writes it."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    x, w = torch.randn(4, 8), torch.randn(16, 8)
+    q, pos, f = heads_call()
+    calls = [(lambda a: ns.linear(a, w), x), (lambda a: ns.linear_backward(torch.ones(4, 16), a, w)[0], x),
+             (lambda a: ns.rope(a, None, pos, f)[0], q), (lambda a: ns.rope_backward(a, None, pos, f)[0], q),
+             (lambda a: ns.qk_norm_rope(a, None, pos, f)[0], q),
+             (lambda a: ns.qk_norm_rope_backward(a, None, a, None, pos, f)[0], q)]
+    for call, a in calls:
+        assert code_of(lambda: torch.jit.trace(call, (a,), check_trace=False)) == -2
+        assert code_of(lambda: make_fx(call)(a)) == -2
+        assert code_of(lambda: call(a)) == -1  # not traced: only the device is wrong
