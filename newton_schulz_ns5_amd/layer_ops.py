@@ -172,7 +172,8 @@ def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=Fal
     The result has the residual's type, or x's without one, unless ``out`` is
     given (``out`` may be the residual).  ``return_preact=True`` returns
     (y, x @ w.T + bias), the second in x's type, which
-    :func:`linear_backward` takes when there is an activation.
+    :func:`linear_backward` takes when there is an activation.  Both carry
+    gradients.
     """
     if _wants_grad(x, w, bias, residual):
         if out is not None or preact is not None:
@@ -283,22 +284,26 @@ class _Linear(torch.autograd.Function):
         ctx.activation = activation
         ctx.bias_dtype = bias.dtype if bias is not None else None
         ctx.set_materialize_grads(False)
-        if z is not None:
+        if z is not None and not return_preact:
             ctx.mark_non_differentiable(z)
         return y, z
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, dy, _):
-        if dy is None:
+    def backward(ctx, dy, dz):
+        if dy is None and dz is None:
             return (None,) * 6
         _refuse_capture()
         x, w, z = ctx.saved_tensors
         need = ctx.needs_input_grad
         dx = dw = db = None
         if need[0] or need[1] or need[2]:
-            dx, dw, db = linear_backward(_rowable(dy), x, w, activation=ctx.activation, preact=z, need_dx=need[0],
-                                         need_dw=need[1], need_dbias=need[2], dbias_dtype=ctx.bias_dtype)
+            how = dict(need_dx=need[0], need_dw=need[1], need_dbias=need[2], dbias_dtype=ctx.bias_dtype)
+            if dy is not None:
+                dx, dw, db = linear_backward(_rowable(dy), x, w, activation=ctx.activation, preact=z, **how)
+            if dz is not None:  # the returned pre-activation's own gradient, added onto y's
+                more, dw, db = linear_backward(_rowable(dz), x, w, dw=dw, dbias=db, accumulate=dy is not None, **how)
+                dx = more if dx is None else dx.add_(more) if need[0] else None
         return dx, dw, db, (dy if need[3] else None), None, None
 
 

@@ -119,3 +119,42 @@ def test_step_and_newton_schulz_outputs_move_their_version_counters():
     assert versions([out, g], lambda: ns.ns_batched_noalloc(g, out)) == [True, False]
     assert versions([out, g], lambda: ns.ns_groups([g], [out])) == [True, False]
     assert versions([out, v], lambda: ns.normuon_normalize(out, v)) == [True, True]
+
+
+# ---- autograd --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act", [None, "silu", "gelu"])
+def test_the_returned_preactivation_carries_its_gradient(act, dtype):
+    """A loss on y and on z, on z alone and on y alone, against the sum of the two
+    gradients called directly: bf16 sums of two bf16 gradients, one more rounding."""
+    torch_cuda()
+    x, w, b, r = rand((2, 33, 48), dtype, 1), rand((80, 48), dtype, 2), rand((80,), F32, 3), rand((2, 33, 80), F32, 4)
+    gy, gz = rand((2, 33, 80), F32, 5), rand((2, 33, 80), dtype, 6)
+    _, z = ns.linear(x, w, b, r, activation=act, return_preact=True)
+    of_y = ns.linear_backward(gy, x, w, activation=act, preact=z if act else None, need_dbias=True, dbias_dtype=F32)
+    of_z = ns.linear_backward(gz, x, w, need_dbias=True, dbias_dtype=F32)
+    for on in ((gy, gz), (None, gz), (gy, None)):
+        leaves = [t.clone().requires_grad_() for t in (x, w, b, r)]
+        y, z = ns.linear(*leaves, activation=act, return_preact=True)
+        assert z.requires_grad
+        torch.autograd.backward([t for t, g in zip((y, z), on) if g is not None], [g for g in on if g is not None])
+        for leaf, p, q in zip(leaves, of_y, of_z):
+            parts = [t.double().view(leaf.shape) for t, g in ((p, on[0]), (q, on[1])) if g is not None]
+            size = sum(t.abs() for t in parts)
+            close(leaf.grad, sum(parts), 2 * U[leaf.dtype] * size + 2.0 ** -20 * size, (act, on[0] is None, on[1] is None))
+        assert (leaves[3].grad is None) if on[0] is None else torch.equal(leaves[3].grad, gy)
+
+
+def test_gradient_through_the_preactivation_against_fp64():
+    torch_cuda()
+    x, w, b = rand((40, 64), F32, 1), rand((72, 64), F32, 2, 1 / 8), rand((72,), F32, 3)
+    gy, gz = rand((40, 72), F32, 4), rand((40, 72), F32, 5)
+    leaves = [t.clone().requires_grad_() for t in (x, w, b)]
+    y, z = ns.linear(*leaves, activation="silu", return_preact=True)
+    torch.autograd.backward([y, z], [gy, gz])
+    exact = [t.double().requires_grad_() for t in (x, w, b)]
+    z = exact[0] @ exact[1].t() + exact[2]
+    torch.autograd.backward([z * torch.sigmoid(z), z], [gy.double(), gz.double()])
+    for a, e in zip(leaves, exact):
+        # sums of at most 72 fp32 terms, twice, and the activation's slope: well under 200 units
+        assert float((a.grad.double() - e.grad).norm() / e.grad.norm()) <= 200 * 2.0 ** -24
