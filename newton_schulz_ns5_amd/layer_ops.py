@@ -155,6 +155,13 @@ def _refuse_tangents(*ts):
                 raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "forward-mode automatic differentiation is not supported")
 
 
+def _no_gradient(inv_freq):
+    """The frequencies are constants of the rotation."""
+    _refuse_tangents(inv_freq)
+    if torch.is_grad_enabled() and inv_freq.requires_grad:
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "inv_freq has no gradient here: detach it")
+
+
 def _wants_grad(*ts):
     """Whether to record the call for autograd."""
     _refuse_tangents(*ts)
@@ -418,9 +425,9 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     (int32 or int64), or has a leading dimension of up to four axes, and then
     ``sections`` (pairs per axis, in order) or ``axes`` (one axis per pair)
     says which pair turns by which.  ``inv_freq`` [rotary pairs] is fp32 or
-    fp64.  Returns (q_out, k_out); an output may be its own input.
+    fp64, and has no gradient.  Returns (q_out, k_out); an output may be its own input.
     """
-    _refuse_tangents(inv_freq)
+    _no_gradient(inv_freq)
     if _wants_grad(q, k, q_weight, k_weight):
         if q_out is not None or k_out is not None:
             _bad("q_out and k_out cannot be given when an input requires a gradient")
@@ -458,7 +465,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
 
 def rope(q, k, positions, inv_freq, *, sections=None, axes=None, interleaved=False, scale=1.0, q_out=None, k_out=None):
     """The position rotation of :func:`qk_norm_rope` without its norm (see muon_rope)."""
-    _refuse_tangents(inv_freq)
+    _no_gradient(inv_freq)
     if _wants_grad(q, k):
         if q_out is not None or k_out is not None:
             _bad("q_out and k_out cannot be given when an input requires a gradient")

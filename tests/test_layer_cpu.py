@@ -259,3 +259,15 @@ def test_tracing_is_refused():
         assert code_of(lambda: torch.jit.trace(call, (a,), check_trace=False)) == -2
         assert code_of(lambda: make_fx(call)(a)) == -2
         assert code_of(lambda: call(a)) == -1  # not traced: only the device is wrong
+
+
+def test_frequencies_that_require_a_gradient_are_refused():
+    """The rotation has none for them; it would be dropped."""
+    q, pos, f = heads_call()
+    g = f.clone().requires_grad_()
+    for fn in (ns.rope, ns.qk_norm_rope):
+        assert code_of(lambda: fn(q, None, pos, g)) == -2
+        assert code_of(lambda: fn(q.clone().requires_grad_(), None, pos, g)) == -2
+        assert code_of(lambda: fn(q, None, pos, g.detach())) == -1  # only the device is wrong
+        with torch.no_grad():
+            assert code_of(lambda: fn(q, None, pos, g)) == -1
