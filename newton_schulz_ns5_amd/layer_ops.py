@@ -172,6 +172,17 @@ def _wants_grad(*ts):
     return False
 
 
+def _given(*outs):
+    """The outputs that the caller gave.  Writing into one that is part of an
+    autograd graph would leave its old history on it."""
+    outs = [t for t in outs if t is not None]
+    if outs and torch.is_grad_enabled():
+        for t in outs:
+            if t.requires_grad:
+                _bad("a given output requires a gradient: detach it")
+    return outs
+
+
 def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=False, out=None, preact=None):
     """``activation(x @ w.T + bias) + residual`` for x [..., k] and w [n, k] (see muon_linear).
 
@@ -193,6 +204,7 @@ def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=Fal
 
 def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=None):
     act = _act(activation)
+    given = _given(out, preact)
     dev = _same_device(x, w, bias, residual, out, preact)
     code = _dt(x)
     if w.dtype != x.dtype:
@@ -202,7 +214,6 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
     wp, n, k, ldw = _rows(w, "w")
     xp, m, _, ldx = _rows(x, "x", k)
     shape = x.shape[:-1] + (n,)
-    given = [t for t in (out, preact) if t is not None]
     if out is None:
         out = (x if residual is None else residual).new_empty(shape)
     if (return_preact or preact is not None):
@@ -236,6 +247,7 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
     """
     _refuse_tangents(dy, x, w, preact)
     act = _act(activation)
+    given = _given(dx, dw, dbias)
     dev = _same_device(dy, x, w, preact, dx, dw, dbias)
     code = _dt(x)
     if w.dtype != x.dtype:
@@ -254,7 +266,6 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
         zp, ldz = _check_matrix(preact, "preact", m, n)
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         _bad("accumulate needs the tensors to add to")
-    given = [t for t in (dx, dw, dbias) if t is not None]
     if dx is None and need_dx:
         dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     if dw is None and need_dw:
@@ -434,12 +445,13 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
         _refuse_capture()
         how = dict(eps=eps, sections=sections, axes=axes, interleaved=interleaved, scale=scale)
         return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, how)
+    given = _given(q_out, k_out)
     y = (_like(q, q_out), _like(k, k_out))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
                          (q_weight, k_weight), (None, None), eps)
     _call(dev, _lib.lib().muon_qk_norm_rope, p, None)
-    if q_out is not None or k_out is not None:
-        _written(q_out, k_out)
+    if given:
+        _written(*given)
     return y
 
 
@@ -448,6 +460,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     """(dq, dk, dq_weight, dk_weight) of :func:`qk_norm_rope` for the gradients of its outputs; None for what
     was not given.  dq may be dq_out, and dk dk_out."""
     _refuse_tangents(dq_out, dk_out, q, k, q_weight, k_weight)
+    given = _given(dq, dk)
     y = (_like(q, dq), _like(k, dk))
     dwt = (_like(q_weight, None), _like(k_weight, None))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), (dq_out, dk_out), y,
@@ -458,8 +471,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
                 t.zero_()
     L = _lib.lib()
     _call(dev, L.muon_qk_norm_rope_backward, p, L.muon_qk_norm_rope_backward_workspace_bytes)
-    if dq is not None or dk is not None:
-        _written(dq, dk)
+    if given:
+        _written(*given)
     return y + dwt
 
 
@@ -472,12 +485,13 @@ def rope(q, k, positions, inv_freq, *, sections=None, axes=None, interleaved=Fal
         _refuse_capture()
         how = dict(sections=sections, axes=axes, interleaved=interleaved, scale=scale)
         return _Rope.apply(q, k, positions, inv_freq, how)
+    given = _given(q_out, k_out)
     y = (_like(q, q_out), _like(k, k_out))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
                          (None, None), (None, None), 0.0)
     _call(dev, _lib.lib().muon_rope, p, None)
-    if q_out is not None or k_out is not None:
-        _written(q_out, k_out)
+    if given:
+        _written(*given)
     return y
 
 
@@ -485,12 +499,13 @@ def rope_backward(dq_out, dk_out, positions, inv_freq, *, sections=None, axes=No
                   dq=None, dk=None):
     """(dq, dk) of :func:`rope`: the rotation by the opposite angles.  dq may be dq_out, and dk dk_out."""
     _refuse_tangents(dq_out, dk_out)
+    given = _given(dq, dk)
     y = (_like(dq_out, dq), _like(dk_out, dk))
     dev, p = _qk_problem(dq_out, dk_out, positions, inv_freq, sections, axes, interleaved, scale, None,
                          (dq_out, dk_out), y, (None, None), (None, None), 0.0)
     _call(dev, _lib.lib().muon_rope_backward, p, None)
-    if dq is not None or dk is not None:
-        _written(dq, dk)
+    if given:
+        _written(*given)
     return y
 
 

@@ -271,3 +271,27 @@ def test_frequencies_that_require_a_gradient_are_refused():
         assert code_of(lambda: fn(q, None, pos, g.detach())) == -1  # only the device is wrong
         with torch.no_grad():
             assert code_of(lambda: fn(q, None, pos, g)) == -1
+
+
+def test_given_outputs_that_require_a_gradient_are_refused():
+    """They would keep a history that their new values do not have."""
+    def msg(f):
+        with pytest.raises(ns.MuonError) as e:
+            f()
+        return "given output requires a gradient" in str(e.value)
+
+    x, w, dy = torch.randn(4, 8), torch.randn(16, 8), torch.randn(4, 16)
+    q, pos, f = heads_call()
+
+    def leaf(t):
+        return torch.empty_like(t).requires_grad_()
+
+    calls = [lambda o: ns.linear(x, w, out=o(dy)), lambda o: ns.linear(x, w, preact=o(dy)),
+             lambda o: ns.linear_backward(dy, x, w, dx=o(x)), lambda o: ns.linear_backward(dy, x, w, dw=o(w)),
+             lambda o: ns.linear_backward(dy, x, w, dbias=o(dy[0])), lambda o: ns.rope(q, q, pos, f, q_out=o(q)),
+             lambda o: ns.rope_backward(q, q, pos, f, dk=o(q)), lambda o: ns.qk_norm_rope(q, q, pos, f, k_out=o(q)),
+             lambda o: ns.qk_norm_rope_backward(q, q, q, q, pos, f, dq=o(q))]
+    for call in calls:
+        assert msg(lambda: call(leaf)) and not msg(lambda: call(torch.empty_like))
+        with torch.no_grad():
+            assert not msg(lambda: call(leaf))
