@@ -301,6 +301,7 @@ class _Linear(torch.autograd.Function):
         ctx.save_for_backward(x, w, z if keep else None)
         ctx.activation = activation
         ctx.bias_dtype = bias.dtype if bias is not None else None
+        ctx.residual_shape = residual.shape if residual is not None else None
         ctx.set_materialize_grads(False)
         if z is not None and not return_preact:
             ctx.mark_non_differentiable(z)
@@ -322,7 +323,9 @@ class _Linear(torch.autograd.Function):
             if dz is not None:  # the returned pre-activation's own gradient, added onto y's
                 more, dw, db = linear_backward(_rowable(dz), x, w, dw=dw, dbias=db, accumulate=dy is not None, **how)
                 dx = more if dx is None else dx.add_(more) if need[0] else None
-        return dx, dw, db, (dy if need[3] else None), None, None
+        # the residual may have other leading dimensions than x, of as many rows
+        dr = dy.reshape(ctx.residual_shape) if need[3] and dy is not None else None
+        return dx, dw, db, dr, None, None
 
 
 # ---- per-head norms and rotation ----------------------------------------------------------

@@ -158,3 +158,19 @@ def test_gradient_through_the_preactivation_against_fp64():
     for a, e in zip(leaves, exact):
         # sums of at most 72 fp32 terms, twice, and the activation's slope: well under 200 units
         assert float((a.grad.double() - e.grad).norm() / e.grad.norm()) <= 200 * 2.0 ** -24
+
+
+def test_residual_of_other_leading_dimensions():
+    """The residual's rows are x's, its leading dimensions need not be."""
+    torch_cuda()
+    x, w = rand((2, 33, 48), BF, 1), rand((80, 48), BF, 2)
+    gy = rand((2, 33, 80), F32, 4)
+    for shape in ((66, 80), (2, 33, 80), (6, 11, 80), (1, 66, 80)):
+        r = rand(shape, F32, 3).requires_grad_()
+        y = ns.linear(x, w, None, r)
+        assert torch.equal(y, ns.linear(x, w, None, r.detach().view(2, 33, 80)))
+        y.backward(gy)
+        assert torch.equal(r.grad, gy.view(shape))
+    r = rand((80,), F32, 5).requires_grad_()
+    ns.linear(x[0, :1], w, None, r).backward(gy[0, :1])
+    assert torch.equal(r.grad, gy[0, 0])
