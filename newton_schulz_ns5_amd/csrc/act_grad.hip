@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGrad p) {
           float z[8];
           get8(p.z, i * p.ldz + j, BF, valid, z);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT>(z[e]);
+          for (int e = 0; e < 8; ++e) g[e] *= act_slope<ACT, BF>(z[e]);
         }
         if (p.G) put8(p.G, i * p.ldg + j, BF, 8, g);  // values past N are zero
         if constexpr (BF) {

@@ -77,7 +77,7 @@ __device__ __forceinline__ void finish8(const LinGemm& p, int64_t i, int64_t j, 
   if (p.Z) put8(p.Z, i * p.ldz + j, BF, valid, v);
   if constexpr (ACT != MUON_ACT_NONE) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = act_fwd<ACT>(v[e]);
+    for (int e = 0; e < 8; ++e) v[e] = act_fwd<ACT, BF>(v[e]);
   }
   if (p.add) {
 #pragma unroll

@@ -174,3 +174,64 @@ def test_residual_of_other_leading_dimensions():
     r = rand((80,), F32, 5).requires_grad_()
     ns.linear(x[0, :1], w, None, r).backward(gy[0, :1])
     assert torch.equal(r.grad, gy[0, 0])
+
+
+# ---- the activations' values and slopes, in their tails too -----------------------------
+def exact_act(z, name):
+    """Value and slope in fp64, and the magnitudes that the slope is a sum of."""
+    if name == "gelu":
+        cdf, zp = 0.5 * torch.erfc(-z / math.sqrt(2)), z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        return z * cdf, cdf + zp, cdf + zp.abs(), 0 * z
+    t, dt = z, torch.ones_like(z)
+    if name == "gelu_tanh":
+        c = 2 * math.sqrt(2 / math.pi)
+        t, dt = c * (z + 0.044715 * z ** 3), c * (1 + 3 * 0.044715 * z * z)
+    s, r = torch.sigmoid(t), torch.sigmoid(-t)
+    # 1 - s is off by 2^-24 where s is near one
+    return z * s, s + z * s * r * dt, s + (z * s * r * dt).abs(), (z * s * dt).abs() * 2.0 ** -23
+
+
+# silu and gelu: the fp32 functions and three roundings beside them, under 16 units of 2^-24; bf16 operands:
+# exponentials whose argument a is rounded, |a| 2^-23 of the result, and |a| <= 104 here.  gelu_tanh: its argument
+# is a product of fp32 numbers, each rounding of it |2 u| 2^-24 of the result, three of them, and 2 u >= -87 here.
+TAILS = [("gelu", -12, 12, 2.0 ** -20), ("silu", -80, 80, 2.0 ** -20), ("gelu_tanh", -9.5, 9.5, 2.0 ** -15)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act,lo,hi,rel", TAILS)
+def test_activation_values_in_their_tails(act, lo, hi, rel, dtype):
+    """The bias alone, in fp32, is the pre-activation: values relative to themselves."""
+    torch_cuda()
+    z = torch.cat([torch.linspace(lo, hi, 60001, device="cuda"), torch.linspace(-1e-2, 1e-2, 2001, device="cuda")])
+    x, w = torch.zeros((1, 8), dtype=dtype, device="cuda"), torch.zeros((z.numel(), 8), dtype=dtype, device="cuda")
+    y = ns.linear(x, w, z, activation=act, out=torch.empty((1, z.numel()), device="cuda"))
+    want = exact_act(z.double(), act)[0][None]
+    close(y, want, want.abs() * max(rel, 2.0 ** -17 if dtype == BF else 0), (act, "value"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("act,lo,hi,rel", TAILS)
+def test_activation_slopes_in_their_tails(act, lo, hi, rel, dtype):
+    """The bias gradient of one row of ones is the slope at its pre-activation."""
+    torch_cuda()
+    z = torch.linspace(lo, hi, 60001, device="cuda").to(dtype)[None]
+    x, w = torch.zeros((1, 8), dtype=dtype, device="cuda"), torch.zeros((z.numel(), 8), dtype=dtype, device="cuda")
+    _, _, db = ns.linear_backward(torch.ones_like(z), x, w, activation=act, preact=z, need_dx=False, need_dw=False,
+                                  need_dbias=True, dbias_dtype=F32)
+    _, want, size, more = exact_act(z.double(), act)
+    close(db[None], want, size * 2 * max(rel, 2.0 ** -17 if dtype == BF else 0) + more, (act, "slope"))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_slopes_far_out_are_zero_and_one(act, dtype):
+    torch_cuda()
+    z = torch.tensor([[-float("inf"), -1e30, -300.0, -120.0, 120.0, 1e30, float("inf")]], device="cuda").to(dtype)
+    x, w = torch.zeros((1, 8), dtype=dtype, device="cuda"), torch.zeros((7, 8), dtype=dtype, device="cuda")
+    _, _, db = ns.linear_backward(torch.ones_like(z), x, w, activation=act, preact=z, need_dx=False, need_dw=False,
+                                  need_dbias=True, dbias_dtype=F32)
+    assert (db[:4].abs() <= 2.0 ** -126).all() and torch.equal(db[4:], torch.ones(3, device="cuda"))
+    s = torch.tensor([[-40.0]], device="cuda", dtype=dtype)  # between: silu's slope there is -1.66e-16
+    _, _, db = ns.linear_backward(torch.ones_like(s), x, w[:1], activation=act, preact=s, need_dx=False, need_dw=False,
+                                  need_dbias=True, dbias_dtype=F32)
+    assert abs(float(db[0]) - (-40 * math.exp(-40) if act == "silu" else 0.0)) <= 1e-17
