@@ -22,9 +22,12 @@
 // compiler spills (63 us).  Loading the next row while this one is turned gave
 // the last 10 %; loading four rows at once cost more in waves than it gained.
 //
-// The angle is formed in fp64, in turns: pos * (inv_freq / 2 pi) less its
-// nearest integer, which leaves fp32's full precision at any position below
-// 2^40 or so; a product in fp32 would be off by whole radians at 10^7.
+// The angle is formed in turns: pos * (inv_freq / 2 pi) less its nearest
+// integer, in a fused multiply-add, the factor in two fp64 terms, so that sine
+// and cosine are fp32's at any position that fp64 holds (2^53).  A rounded fp64
+// product would be off by pos 2^-52 radians, one in fp32 by whole radians at
+// 10^7.  What rounding the turns to fp32 leaves turns the sine and cosine once
+// more, to first order.
 #include "layer_internal.h"
 #include "device_util.h"
 #include "muon_mi355x.h"
@@ -48,9 +51,13 @@ __device__ __forceinline__ int64_t pos_of(const QkParams& p, int64_t tok, int ax
 
 __device__ __forceinline__ f32x2_t cos_sin(const QkParams& p, int64_t tok, int pair) {
   const double f = p.inv_freq_f64 ? ((const double*)p.inv_freq)[pair] : (double)((const float*)p.inv_freq)[pair];
-  const double turns = (double)pos_of(p, tok, p.axis[pair]) * (f * 0.15915494309189533577);
-  float s, c;
-  sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+  const double pos = (double)pos_of(p, tok, p.axis[pair]);
+  const double h = f * 0.15915494309189535, l = fma(f, 0.15915494309189535, -h) + f * -9.839338337591243e-18;  // f / 2 pi
+  const double half = 2.0 * (fma(pos, h, -rint(pos * h)) + pos * l);  // in half turns
+  const float x = (float)half, d = (float)((half - (double)x) * 3.14159265358979323846);
+  float s0, c0;
+  sincospif(x, &s0, &c0);
+  const float c = c0 - s0 * d, s = s0 + c0 * d;
   return f32x2_t{c * p.scale, s * p.scale * p.sign};
 }
 

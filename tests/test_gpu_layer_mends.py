@@ -235,3 +235,29 @@ def test_slopes_far_out_are_zero_and_one(act, dtype):
     _, _, db = ns.linear_backward(torch.ones_like(s), x, w[:1], activation=act, preact=s, need_dx=False, need_dw=False,
                                   need_dbias=True, dbias_dtype=F32)
     assert abs(float(db[0]) - (-40 * math.exp(-40) if act == "silu" else 0.0)) <= 1e-17
+
+
+# ---- far positions ---------------------------------------------------------------------
+def turn_of(pos, f):
+    """cos and sin of pos * f, the angle reduced in exact rational arithmetic."""
+    from fractions import Fraction
+    pi = Fraction(314159265358979323846264338327950288419716939937510582097494459, 10 ** 62)
+    turns = Fraction(pos) * Fraction(f) / (2 * pi)
+    a = 2 * math.pi * float(turns - round(turns))
+    return math.cos(a), math.sin(a)
+
+
+def test_angles_of_far_positions():
+    """Rotations of (1, 0) are the cosine and sine themselves: within two units of 2^-23
+    (the library's sine and cosine of a reduced angle, and the last rounding) at any position
+    that fp64 holds, against angles from rational arithmetic."""
+    torch_cuda()
+    pos = [0, 1, -1, 12345, 10 ** 7 + 3, 2 ** 28 - 1, 2 ** 30 + 7, 10 ** 9 + 1, 2 ** 34 + 5, 2 ** 40 + 11, -(2 ** 45) - 9, 2 ** 53]
+    for dtype in (torch.float64, F32):
+        f = torch.pow(10000.0, -torch.arange(64, device="cuda", dtype=torch.float64) / 64).to(dtype)
+        q = torch.zeros((len(pos), 1, 128), device="cuda")
+        q[..., :64] = 1
+        y, _ = ns.rope(q, None, torch.tensor(pos, device="cuda"), f)
+        want = torch.tensor([[turn_of(p, g) for g in f.tolist()] for p in pos], dtype=torch.float64, device="cuda")
+        close(y[:, 0, :64], want[..., 0], torch.full_like(want[..., 0], 2.0 ** -22), "cos")
+        close(y[:, 0, 64:], want[..., 1], torch.full_like(want[..., 0], 2.0 ** -22), "sin")
