@@ -60,15 +60,15 @@ def _refuse_tracing():
     it: its replays would return memory that nobody wrote."""
     if _tracing_state() is not None:
         raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "torch.jit.trace cannot record this operator")
-    if _dispatch_modes():
-        from torch.fx.experimental.proxy_tensor import get_proxy_mode
-        if get_proxy_mode() is not None:
-            raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "torch.fx tracing cannot record this operator")
+    from torch.fx.experimental.proxy_tensor import get_proxy_mode
+    if get_proxy_mode() is not None:
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "torch.fx tracing cannot record this operator")
 
 
 def _same_device(first, *others):
     """The index of the one GPU that holds every tensor."""
-    _refuse_tracing()
+    if _tracing_state() is not None or _dispatch_modes():
+        _refuse_tracing()
     dev = first.get_device()
     if dev < 0:
         _bad(f"tensors must be on a GPU, got {first.device}")
@@ -155,13 +155,6 @@ def _refuse_tangents(*ts):
                 raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "forward-mode automatic differentiation is not supported")
 
 
-def _no_gradient(inv_freq):
-    """The frequencies are constants of the rotation."""
-    _refuse_tangents(inv_freq)
-    if torch.is_grad_enabled() and inv_freq.requires_grad:
-        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "inv_freq has no gradient here: detach it")
-
-
 def _wants_grad(*ts):
     """Whether to record the call for autograd."""
     _refuse_tangents(*ts)
@@ -172,14 +165,19 @@ def _wants_grad(*ts):
     return False
 
 
+def _refuse_frequency_gradient(inv_freq):
+    """The frequencies are constants of the rotation."""
+    if inv_freq.requires_grad:
+        raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "inv_freq has no gradient here: detach it")
+
+
 def _given(*outs):
     """The outputs that the caller gave.  Writing into one that is part of an
     autograd graph would leave its old history on it."""
     outs = [t for t in outs if t is not None]
-    if outs and torch.is_grad_enabled():
-        for t in outs:
-            if t.requires_grad:
-                _bad("a given output requires a gradient: detach it")
+    for t in outs:
+        if t.requires_grad and torch.is_grad_enabled():
+            _bad("a given output requires a gradient: detach it")
     return outs
 
 
@@ -204,7 +202,7 @@ def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=Fal
 
 def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=None):
     act = _act(activation)
-    given = _given(out, preact)
+    given = () if out is None and preact is None else _given(out, preact)
     dev = _same_device(x, w, bias, residual, out, preact)
     code = _dt(x)
     if w.dtype != x.dtype:
@@ -441,14 +439,14 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_weight=None, k_weight=None, eps
     says which pair turns by which.  ``inv_freq`` [rotary pairs] is fp32 or
     fp64, and has no gradient.  Returns (q_out, k_out); an output may be its own input.
     """
-    _no_gradient(inv_freq)
-    if _wants_grad(q, k, q_weight, k_weight):
+    if _wants_grad(q, k, q_weight, k_weight, inv_freq):
+        _refuse_frequency_gradient(inv_freq)
         if q_out is not None or k_out is not None:
             _bad("q_out and k_out cannot be given when an input requires a gradient")
         _refuse_capture()
         how = dict(eps=eps, sections=sections, axes=axes, interleaved=interleaved, scale=scale)
         return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, how)
-    given = _given(q_out, k_out)
+    given = () if q_out is None and k_out is None else _given(q_out, k_out)
     y = (_like(q, q_out), _like(k, k_out))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
                          (q_weight, k_weight), (None, None), eps)
@@ -463,7 +461,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
     """(dq, dk, dq_weight, dk_weight) of :func:`qk_norm_rope` for the gradients of its outputs; None for what
     was not given.  dq may be dq_out, and dk dk_out."""
     _refuse_tangents(dq_out, dk_out, q, k, q_weight, k_weight)
-    given = _given(dq, dk)
+    given = () if dq is None and dk is None else _given(dq, dk)
     y = (_like(q, dq), _like(k, dk))
     dwt = (_like(q_weight, None), _like(k_weight, None))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), (dq_out, dk_out), y,
@@ -481,14 +479,14 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
 
 def rope(q, k, positions, inv_freq, *, sections=None, axes=None, interleaved=False, scale=1.0, q_out=None, k_out=None):
     """The position rotation of :func:`qk_norm_rope` without its norm (see muon_rope)."""
-    _no_gradient(inv_freq)
-    if _wants_grad(q, k):
+    if _wants_grad(q, k, inv_freq):
+        _refuse_frequency_gradient(inv_freq)
         if q_out is not None or k_out is not None:
             _bad("q_out and k_out cannot be given when an input requires a gradient")
         _refuse_capture()
         how = dict(sections=sections, axes=axes, interleaved=interleaved, scale=scale)
         return _Rope.apply(q, k, positions, inv_freq, how)
-    given = _given(q_out, k_out)
+    given = () if q_out is None and k_out is None else _given(q_out, k_out)
     y = (_like(q, q_out), _like(k, k_out))
     dev, p = _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, (q, k), None, y,
                          (None, None), (None, None), 0.0)
@@ -502,7 +500,7 @@ def rope_backward(dq_out, dk_out, positions, inv_freq, *, sections=None, axes=No
                   dq=None, dk=None):
     """(dq, dk) of :func:`rope`: the rotation by the opposite angles.  dq may be dq_out, and dk dk_out."""
     _refuse_tangents(dq_out, dk_out)
-    given = _given(dq, dk)
+    given = () if dq is None and dk is None else _given(dq, dk)
     y = (_like(dq_out, dq), _like(dk_out, dk))
     dev, p = _qk_problem(dq_out, dk_out, positions, inv_freq, sections, axes, interleaved, scale, None,
                          (dq_out, dk_out), y, (None, None), (None, None), 0.0)
