@@ -76,21 +76,32 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* base, int64_t bytes) {
 // operand bound to that register: the compiler writes M0 itself and knows
 // it is read here, so nothing the compiler keeps in M0 is overwritten.
 // The compiler does not look inside the assembly for the wait states that the
-// hardware leaves to software, so the assembly starts with WAITS of them.  One
-// is needed between a write of M0 and an LDS load.  Five are needed between a
-// vector instruction that writes a scalar register (v_readfirstlane) and a
-// memory instruction that reads it: a kernel whose descriptor or offset
-// changes from load to load takes five, whatever the compiler puts in front;
-// one whose descriptors are formed once, far from its loads, and whose offsets
-// are scalar arithmetic takes one (five cost its step 1 %).
-template <int WAITS = 1>
-__device__ __forceinline__ void lds_dma16_asm(i32x4 rsrc, uint32_t lds, int voff, int soff) {
-  static_assert(WAITS >= 1 && WAITS <= 16, "s_nop's range");
+// hardware leaves to software, so the assembly starts with them.  One is needed
+// between a write of M0 and an LDS load.  Five are needed between a vector
+// instruction that writes a scalar register (v_readfirstlane) and a memory
+// instruction that reads it, so a load of a descriptor just formed takes five.
+// A kernel whose descriptors stay the same from load to load passes them
+// through settled() once, which waits the five there; its loads, whose offsets
+// must be scalar arithmetic on values made uniform before, then take one (five
+// on every load cost such a kernel's step 1 %).
+struct SettledRsrc { i32x4 words; };
+__device__ __forceinline__ SettledRsrc settled(i32x4 rsrc) {
+  asm volatile("s_nop 4" : "+s"(rsrc));  // reads and writes the words: after their v_readfirstlane, before every use
+  return {rsrc};
+}
+template <int WAITS>
+__device__ __forceinline__ void lds_dma16_waits(i32x4 rsrc, uint32_t lds, int voff, int soff) {
   asm volatile("s_nop %4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
                : "{m0}"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rsrc),
                  "s"(__builtin_amdgcn_readfirstlane(soff)), "n"(WAITS - 1)
                : "memory");
+}
+__device__ __forceinline__ void lds_dma16_asm(i32x4 rsrc, uint32_t lds, int voff, int soff) {
+  lds_dma16_waits<5>(rsrc, lds, voff, soff);
+}
+__device__ __forceinline__ void lds_dma16_asm(const SettledRsrc& rsrc, uint32_t lds, int voff, int soff) {
+  lds_dma16_waits<1>(rsrc.words, lds, voff, soff);
 }
 
 // Launch a kernel taking one parameter block by value, `threads` (256 unless

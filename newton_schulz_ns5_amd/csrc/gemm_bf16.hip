@@ -196,8 +196,8 @@ __global__ __launch_bounds__(NW * 64, 1) void gemm_nt_bf16_kernel(const GemmGrou
   const int64_t qbytes = (NN ? (int64_t)p.K : (int64_t)BT) * p.ldq * 2;
   const __amdgpu_buffer_rsrc_t prs = make_rsrc(Pg, (int64_t)BT * p.ldp * 2);
   const __amdgpu_buffer_rsrc_t qrs = make_rsrc(Qg, qbytes);
-  const i32x4 prw = rsrc_words(Pg, (int64_t)BT * p.ldp * 2);
-  const i32x4 qrw = rsrc_words(Qg, qbytes);
+  const SettledRsrc prw = settled(rsrc_words(Pg, (int64_t)BT * p.ldp * 2));
+  const SettledRsrc qrw = settled(rsrc_words(Qg, qbytes));
 
   // LDS layout: a slot holds BT rows of 128 bytes (64 K values of one
   // operand row); its eight 16-byte chunks are XOR-swizzled by (row / 2) mod

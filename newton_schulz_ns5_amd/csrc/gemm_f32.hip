@@ -73,8 +73,8 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(const GemmParams p) {
   const float* Pg = (const float*)p.P + (int64_t)b * p.sP + (int64_t)tm * BT * ldp;
   const float* Qg = NN ? (const float*)p.Q + (int64_t)b * p.sQ + (int64_t)tn * BT
                        : (const float*)p.Q + (int64_t)b * p.sQ + (int64_t)tn * BT * ldq;
-  const i32x4 prw = rsrc_words(Pg, (int64_t)BT * ldp * 4);
-  const i32x4 qrw = rsrc_words(Qg, NN ? (int64_t)p.K * ldq * 4 : (int64_t)BT * ldq * 4);
+  const SettledRsrc prw = settled(rsrc_words(Pg, (int64_t)BT * ldp * 4));
+  const SettledRsrc qrw = settled(rsrc_words(Qg, NN ? (int64_t)p.K * ldq * 4 : (int64_t)BT * ldq * 4));
   const uint32_t lds0 =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem);
   const uint32_t wbase = lds0 + (uint32_t)(wave * WAVE_LDS);

@@ -232,14 +232,14 @@ __global__ __launch_bounds__(WM * WN * 64, 1) void linear_tile_kernel(const LinG
   auto load_a = [&](int t, uint32_t slot, int q) {
     const bool last = t >= KT - 1;
     const int tc = last ? KT - 1 : t, at = (wave * DPA + q) * 1024;
-    if constexpr (ACOL) lds_dma16_asm<5>(col_rsrc(Au, lda, afull, alast, tc), slot + at, avo[q], 0);
-    else lds_dma16_asm<5>(ars, slot + at, last ? tail(avo[q], at + lane * 16) : avo[q], tc * ROWB);
+    if constexpr (ACOL) lds_dma16_asm(col_rsrc(Au, lda, afull, alast, tc), slot + at, avo[q], 0);
+    else lds_dma16_asm(ars, slot + at, last ? tail(avo[q], at + lane * 16) : avo[q], tc * ROWB);
   };
   auto load_b = [&](int t, uint32_t slot, int q) {
     const bool last = t >= KT - 1;
     const int tc = last ? KT - 1 : t, at = (wave * DPB + q) * 1024;
-    if constexpr (BCOL) lds_dma16_asm<5>(col_rsrc(Bu, ldb, bfull, blast, tc), slot + at, bvo[q], 0);
-    else lds_dma16_asm<5>(brs, slot + at, last ? tail(bvo[q], at + lane * 16) : bvo[q], tc * ROWB);
+    if constexpr (BCOL) lds_dma16_asm(col_rsrc(Bu, ldb, bfull, blast, tc), slot + at, bvo[q], 0);
+    else lds_dma16_asm(brs, slot + at, last ? tail(bvo[q], at + lane * 16) : bvo[q], tc * ROWB);
   };
   // Slot of the next slice of the same operand.
   auto next_a = [&](uint32_t s) {

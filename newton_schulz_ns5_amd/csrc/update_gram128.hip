@@ -137,8 +137,8 @@ __global__ __launch_bounds__(512, 1) void updgram128_kernel(const UpdGram128Grou
   const uint16_t* const Xg = (const uint16_t*)p.X + (int64_t)b * p.x_bs + (int64_t)j0 * SUB;
   uint16_t* const Yg = (uint16_t*)p.Y + (int64_t)b * p.y_bs + (int64_t)j0 * SUB;
   const int64_t chunk_bytes = ((int64_t)(M - 1) * ldx + (int64_t)nsub * SUB) * 2;
-  const i32x4 brw = rsrc_words(Bg, (int64_t)M * M * 2);
-  const i32x4 xrw = rsrc_words(Xg, chunk_bytes);
+  const SettledRsrc brw = settled(rsrc_words(Bg, (int64_t)M * M * 2));
+  const SettledRsrc xrw = settled(rsrc_words(Xg, chunk_bytes));
   const __amdgpu_buffer_rsrc_t yrs = __builtin_amdgcn_make_buffer_rsrc(
       (void*)Yg, (short)0, __builtin_amdgcn_readfirstlane((int)chunk_bytes), 0x00020000);
   // LDS byte addresses (the ds instructions take a 32-bit address plus an
