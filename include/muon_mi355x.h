@@ -422,7 +422,8 @@ typedef struct muon_heads {
  * pair turns by.  Angles are formed in fp64, the rest is fp32 with one rounding
  * on store.
  * heads[i] == 0 leaves tensor i out.  An output may be its own input (the same
- * view); any other overlap of an output is refused. */
+ * view); any other overlap of an output, dweight among them, with an input or
+ * another output is refused. */
 #define MUON_QK_MAX_DIM 1024
 #define MUON_QK_MAX_PAIRS 256
 #define MUON_QK_MAX_AXES 4

@@ -582,6 +582,67 @@ bool may_meet(const muon_heads& a, int64_t ha, const muon_heads& b, int64_t hb, 
   return !(d >= wb * esize(dt) && d + wa * esize(dt) <= bytes);
 }
 
+// One index of a strided tensor: its stride in bytes and its first and last value.
+struct Index { int64_t stride, lo, hi; };
+
+// Whether `at` plus a multiple of every stride lies strictly between two
+// bounds.  Largest stride first, each index is tried only where the smaller
+// ones can still reach the bounds; more than `tries` of them count as a yes.
+bool reaches(int64_t at, const Index* d, int n, int64_t above, int64_t below, int& tries) {
+  if (n == 0) return at > above && at < below;
+  int64_t lo = 0, hi = 0;  // what the smaller strides add
+  for (int i = 1; i < n; ++i) { lo += d[i].lo * d[i].stride; hi += d[i].hi * d[i].stride; }
+  const int64_t s = d[0].stride;
+  if (s <= 0) return reaches(at, d + 1, n - 1, above, below, tries);
+  auto floordiv = [](int64_t a, int64_t b) { return a / b - (a % b != 0 && a < 0); };
+  const int64_t first = std::max(d[0].lo, floordiv(above - hi - at, s) + 1), last = std::min(d[0].hi, -floordiv(at + lo - below, s) - 1);
+  for (int64_t k = first; k <= last; ++k) {
+    if (--tries < 0) return true;
+    if (reaches(at + k * s, d + 1, n - 1, above, below, tries)) return true;
+  }
+  return false;
+}
+
+// Whether a head row of `t` shares a byte with the range of `bytes` from p on.
+bool meets_range(const muon_heads& t, int64_t heads, int32_t dt, const muon_qk_problem* q, const void* p, int64_t bytes) {
+  if (!p || bytes <= 0 || !heads) return false;
+  const int64_t e = esize(dt);
+  Index d[3] = {{t.batch_stride * e, 0, q->batch - 1}, {t.token_stride * e, 0, q->tokens - 1}, {t.head_stride * e, 0, heads - 1}};
+  std::sort(d, d + 3, [](const Index& a, const Index& b) { return a.stride > b.stride; });
+  int tries = 4096;
+  return reaches((int64_t)((uintptr_t)t.p - (uintptr_t)p), d, 3, -q->dim * e, bytes, tries);
+}
+
+bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
+  return a && b && na > 0 && nb > 0 && (uintptr_t)a < (uintptr_t)b + (uintptr_t)nb && (uintptr_t)b < (uintptr_t)a + (uintptr_t)na;
+}
+
+// The outputs against the vectors: the weights, the positions, the frequencies,
+// and, backward, the weights' gradients, which are outputs themselves.
+int check_vectors(const muon_qk_problem* q, bool backward, bool norm) {
+  struct Range { const char* name; const void* p; int64_t bytes; };
+  const int64_t wb = q->dim * esize(q->weight_dtype), pe = q->positions_i64 ? 8 : 4;
+  const int64_t pos = (q->axes - 1) * q->pos_axis_stride + (q->batch - 1) * q->pos_batch_stride + (q->tokens - 1) * q->pos_token_stride + 1;
+  const bool rot = q->rotary_dim > 0;
+  const Range in[] = {{"the weight of q", norm ? q->weight[0] : nullptr, wb},
+                      {"the weight of k", norm ? q->weight[1] : nullptr, wb},
+                      {"positions", rot ? q->positions : nullptr, pos * pe},
+                      {"inv_freq", rot ? q->inv_freq : nullptr, q->rotary_dim / 2 * (int64_t)(q->inv_freq_f64 ? 8 : 4)}};
+  for (int i = 0; i < 2; ++i) {
+    for (const Range& r : in)
+      if (meets_range(q->y[i], q->heads[i], q->dtype, q, r.p, r.bytes)) return fail(MUON_ERR_INVALID_ARG, "output of %s overlaps %s", kQ[i], r.name);
+    const void* const dw = backward && norm ? q->dweight[i] : nullptr;
+    if (!dw) continue;
+    for (const Range& r : in)
+      if (ranges_meet(dw, wb, r.p, r.bytes)) return fail(MUON_ERR_INVALID_ARG, "dweight of %s overlaps %s", kQ[i], r.name);
+    for (int k = 0; k < 2; ++k)
+      for (const muon_heads* t : {&q->x[k], &q->g[k], &q->y[k]})
+        if (meets_range(*t, q->heads[k], q->dtype, q, dw, wb)) return fail(MUON_ERR_INVALID_ARG, "dweight of %s overlaps a tensor of %s", kQ[i], kQ[k]);
+    if (i == 1 && ranges_meet(dw, wb, q->dweight[0], wb)) return fail(MUON_ERR_INVALID_ARG, "the dweights overlap");
+  }
+  return MUON_OK;
+}
+
 int check_qk(const muon_qk_problem* q, bool backward, bool norm) {
   if (!q) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
   if (q->batch < 0 || q->tokens < 0) return fail(MUON_ERR_INVALID_ARG, "negative batch or tokens");
@@ -630,7 +691,7 @@ int check_qk(const muon_qk_problem* q, bool backward, bool norm) {
   }
   if (q->heads[0] && q->heads[1] && may_meet(q->y[0], q->heads[0], q->y[1], q->heads[1], q->dtype, q))
     return fail(MUON_ERR_INVALID_ARG, "outputs of q and k overlap");
-  return MUON_OK;
+  return check_vectors(q, backward, norm);
 }
 
 // Launch geometry of one call: chunk size, tokens per wave item, row parts,

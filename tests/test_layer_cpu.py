@@ -295,3 +295,57 @@ def test_given_outputs_that_require_a_gradient_are_refused():
         assert msg(lambda: call(leaf)) and not msg(lambda: call(torch.empty_like))
         with torch.no_grad():
             assert not msg(lambda: call(leaf))
+
+
+# ---- overlaps ---------------------------------------------------------------------------
+ROW = (4 + 2 * 2) * 64 * 2  # bytes of a packed row of qk_problem
+
+
+def with_vectors(**over):
+    """qk_problem with weights, and their gradients, of their own."""
+    p = qk_problem(**{k: v for k, v in over.items() if k not in ("weight", "dweight")})
+    for i in range(2):
+        p.weight[i] = over.get("weight", (FAKE + 3 * MIB, FAKE + 4 * MIB))[i]
+        p.dweight[i] = over.get("dweight", (FAKE + 5 * MIB, FAKE + 6 * MIB))[i]
+    return p
+
+
+@pytest.mark.parametrize("over", [
+    dict(weight=(QKV, FAKE + 4 * MIB)),                     # q's weight is q's first head
+    dict(weight=(FAKE + 4 * MIB, QKV + 2 * ROW + 100)),     # k's weight is in q's heads of the third token
+    dict(weight=(QKV - 126, None)),                         # its last value is q's first
+    dict(positions=QKV + 8), dict(positions=QKV - 32), dict(inv_freq=QKV + 4 * ROW), dict(inv_freq=QKV - 248),
+])
+def test_qk_outputs_over_the_vectors_are_refused(over):
+    L = _lib.lib()
+    p = with_vectors(**over)
+    assert L.muon_qk_norm_rope(ctypes.byref(p), None) == -1 and b"overlaps" in L.muon_last_error()
+    if "weight" not in over:
+        assert L.muon_rope(ctypes.byref(p), None) == -1 and b"overlaps" in L.muon_last_error()
+    assert L.muon_qk_norm_rope_backward(ctypes.byref(p), FAKE + 64 * MIB, 1 << 30, None) == -1
+
+
+@pytest.mark.parametrize("over", [
+    dict(dweight=(FAKE + 3 * MIB, None)), dict(dweight=(None, FAKE + 3 * MIB)),     # a weight
+    dict(dweight=(FAKE + 5 * MIB, FAKE + 5 * MIB + 126)),                           # each other
+    dict(dweight=(QKV, None)), dict(dweight=(None, QKV + 4 * ROW + 640)),           # head rows
+    dict(dweight=(FAKE, None)), dict(dweight=(FAKE + MIB + 8, None)),               # positions, inv_freq
+])
+def test_qk_weight_gradients_over_other_tensors_are_refused(over):
+    L = _lib.lib()
+    p = with_vectors(**over)
+    need = ctypes.c_size_t()
+    assert L.muon_qk_norm_rope_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == -1
+    assert L.muon_qk_norm_rope_backward(ctypes.byref(p), FAKE + 64 * MIB, 1 << 30, None) == -1
+    assert b"overlap" in L.muon_last_error()
+
+
+def test_qk_vectors_beside_and_between_the_rows_are_taken():
+    """Up to the first and from the last byte on, and in the v heads between the rows of q and k."""
+    L = _lib.lib()
+    need = ctypes.c_size_t()
+    for over in (dict(weight=(QKV - 128, QKV + 5 * ROW)), dict(positions=QKV - 40), dict(inv_freq=QKV + 5 * ROW),
+                 dict(weight=(QKV + 6 * 128, QKV + ROW + 6 * 128)), dict(dweight=(QKV + 7 * 128, QKV + 4 * ROW + 6 * 128)),
+                 dict(positions=QKV + 2 * ROW + 6 * 128)):
+        p = with_vectors(**over)
+        assert L.muon_qk_norm_rope_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0, (over, L.muon_last_error())
