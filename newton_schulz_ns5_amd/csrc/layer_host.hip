@@ -564,24 +564,6 @@ bool same_view(const muon_heads& a, const muon_heads& b, const muon_qk_problem* 
          (q->tokens <= 1 || a.token_stride == b.token_stride) && (heads <= 1 || a.head_stride == b.head_stride);
 }
 
-// Whether two tensors may share a byte.  Views of one packed buffer with the
-// same token stride, each token's heads within it, are told apart by their
-// place within that stride; others by their whole extent.
-bool may_meet(const muon_heads& a, int64_t ha, const muon_heads& b, int64_t hb, int32_t dt, const muon_qk_problem* q) {
-  const Span x = span_of(a, ha, dt, q), y = span_of(b, hb, dt, q);
-  if (x.lo >= y.hi || y.lo >= x.hi) return false;
-  // The stride between tokens; with one token per sequence, between sequences
-  // (the stride of an axis of one entry means nothing).
-  const bool one = q->tokens <= 1;
-  const int64_t S = one ? a.batch_stride : a.token_stride, Sb = one ? b.batch_stride : b.token_stride;
-  const int64_t wa = (ha - 1) * a.head_stride + q->dim, wb = (hb - 1) * b.head_stride + q->dim;
-  if (S != Sb || S <= 0 || wa > S || wb > S || (one && q->batch <= 1)) return true;
-  if (!one && q->batch > 1 && (a.batch_stride % S || b.batch_stride % S)) return true;
-  const int64_t bytes = S * esize(dt);
-  const int64_t d = (int64_t)((x.lo >= y.lo ? x.lo - y.lo : (uintptr_t)bytes - (y.lo - x.lo) % (uintptr_t)bytes) % (uintptr_t)bytes);
-  return !(d >= wb * esize(dt) && d + wa * esize(dt) <= bytes);
-}
-
 // One index of a strided tensor: its stride in bytes and its first and last value.
 struct Index { int64_t stride, lo, hi; };
 
@@ -601,6 +583,42 @@ bool reaches(int64_t at, const Index* d, int n, int64_t above, int64_t below, in
     if (reaches(at + k * s, d + 1, n - 1, above, below, tries)) return true;
   }
   return false;
+}
+
+// Whether two tensors may share a byte.  Views with the same strides, such as q
+// and k in packed rows or in a heads-first buffer, are compared row by row: the
+// distance of two head rows is that of the tensors plus a multiple of every
+// stride.  Else views with the same token stride, each token's heads within it,
+// are told apart by their place within that stride; others by their whole
+// extent.
+bool may_meet(const muon_heads& a, int64_t ha, const muon_heads& b, int64_t hb, int32_t dt, const muon_qk_problem* q) {
+  const Span x = span_of(a, ha, dt, q), y = span_of(b, hb, dt, q);
+  if (x.lo >= y.hi || y.lo >= x.hi) return false;
+  const int64_t e = esize(dt);
+  const struct { int64_t sa, sb, na, nb; } axes[3] = {{a.batch_stride, b.batch_stride, q->batch, q->batch},
+                                                      {a.token_stride, b.token_stride, q->tokens, q->tokens},
+                                                      {a.head_stride, b.head_stride, ha, hb}};
+  Index ix[3];
+  bool alike = true;
+  for (int i = 0; i < 3; ++i) {
+    alike &= axes[i].na <= 1 || axes[i].nb <= 1 || axes[i].sa == axes[i].sb;
+    ix[i] = {(axes[i].na > 1 ? axes[i].sa : axes[i].sb) * e, 1 - axes[i].na, axes[i].nb - 1};
+  }
+  if (alike) {
+    std::sort(ix, ix + 3, [](const Index& p, const Index& r) { return p.stride > r.stride; });
+    int tries = 4096;
+    return reaches((int64_t)(y.lo - x.lo), ix, 3, -q->dim * e, q->dim * e, tries);
+  }
+  // The stride between tokens; with one token per sequence, between sequences
+  // (the stride of an axis of one entry means nothing).
+  const bool one = q->tokens <= 1;
+  const int64_t S = one ? a.batch_stride : a.token_stride, Sb = one ? b.batch_stride : b.token_stride;
+  const int64_t wa = (ha - 1) * a.head_stride + q->dim, wb = (hb - 1) * b.head_stride + q->dim;
+  if (S != Sb || S <= 0 || wa > S || wb > S || (one && q->batch <= 1)) return true;
+  if (!one && q->batch > 1 && (a.batch_stride % S || b.batch_stride % S)) return true;
+  const int64_t bytes = S * esize(dt);
+  const int64_t d = (int64_t)((x.lo >= y.lo ? x.lo - y.lo : (uintptr_t)bytes - (y.lo - x.lo) % (uintptr_t)bytes) % (uintptr_t)bytes);
+  return !(d >= wb * esize(dt) && d + wa * esize(dt) <= bytes);
 }
 
 // Whether a head row of `t` shares a byte with the range of `bytes` from p on.

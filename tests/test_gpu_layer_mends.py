@@ -261,3 +261,18 @@ def test_angles_of_far_positions():
         want = torch.tensor([[turn_of(p, g) for g in f.tolist()] for p in pos], dtype=torch.float64, device="cuda")
         close(y[:, 0, :64], want[..., 0], torch.full_like(want[..., 0], 2.0 ** -22), "cos")
         close(y[:, 0, 64:], want[..., 1], torch.full_like(want[..., 0], 2.0 ** -22), "sin")
+
+
+@pytest.mark.parametrize("B,S", [(1, 9), (3, 9), (4, 1)])
+def test_qk_in_place_in_a_heads_first_buffer(B, S):
+    torch_cuda()
+    hq, hk, d = 4, 2, 64
+    buf = rand((B, hq + 2 * hk, S, d), BF, 1)
+    f, pos = torch.rand(d // 2, device="cuda"), torch.arange(S, device="cuda")
+    want = ns.qk_norm_rope(buf[:, :hq].transpose(1, 2), buf[:, hq:hq + hk].transpose(1, 2), pos, f)
+    rest = buf[:, hq + hk:].clone()
+    q, k = buf[:, :hq].transpose(1, 2), buf[:, hq:hq + hk].transpose(1, 2)
+    ns.qk_norm_rope(q, k, pos, f, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(buf[:, hq + hk:], rest)
+    with pytest.raises(ns.MuonError):
+        ns.rope(q, k, pos, f, k_out=buf[:, hq - 1:hq - 1 + hk].transpose(1, 2))

@@ -349,3 +349,68 @@ def test_qk_vectors_beside_and_between_the_rows_are_taken():
                  dict(positions=QKV + 2 * ROW + 6 * 128)):
         p = with_vectors(**over)
         assert L.muon_qk_norm_rope_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0, (over, L.muon_last_error())
+
+
+def packed_problem(B, S, hq, hk, dim, heads_first, at=(0, 0)):
+    """q and k of one buffer, in place, k's output `at` values off its input."""
+    p = qk_problem(heads=(hq, hk), batch=B, tokens=S, dim=dim, rotary_dim=0)
+    n = hq + 2 * hk
+    st = (n * S * dim, dim, S * dim) if heads_first else (n * S * dim, n * dim, dim)
+    for i, h0 in enumerate((0, hq)):
+        first = QKV + 2 * h0 * st[2]
+        p.x[i] = p.g[i] = _lib.Heads(first, *st)
+        p.y[i] = _lib.Heads(first + 2 * at[i], *st)
+    return p
+
+
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_qk_in_place_views_of_one_buffer_are_told_apart(heads_first):
+    """q and k of packed rows ([B, S, heads, D]) and of a heads-first buffer
+    ([B, heads, S, D]) are disjoint, for any number of sequences; moved by a
+    value, by a head or by a row they are not."""
+    L = _lib.lib()
+    need = ctypes.c_size_t()
+
+    def status(*a, **k):
+        p = packed_problem(*a, **k)
+        return L.muon_qk_norm_rope_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need))
+
+    for B, S, hq, hk, dim in [(1, 7, 4, 2, 64), (3, 7, 4, 2, 64), (5, 1, 8, 2, 128), (4, 9, 1, 1, 63), (2, 1000, 32, 8, 128), (1, 1, 2, 1, 8)]:
+        assert status(B, S, hq, hk, dim, heads_first) == 0, L.muon_last_error()
+        step = S * dim if heads_first else dim
+        assert status(B, S, hq, hk, dim, heads_first, at=(0, 1)) == -1       # by one value, over its own input
+        assert status(B, S, hq, hk, dim, heads_first, at=(0, -step)) == -1   # onto q's last head
+        assert status(B, S, hq, hk, dim, heads_first, at=(step * hq, 0)) == -1
+
+
+def test_qk_overlap_agrees_with_the_sets_of_elements():
+    """Against the elements written down, for small tensors of random strides: nothing that
+    shares an element is taken; where the strides are the same, nothing else is refused."""
+    import random
+    L, rng, need = _lib.lib(), random.Random(5), ctypes.c_size_t()
+    seen = set()
+    for _ in range(4000):
+        B, S, hq, hk, dim = (rng.randint(1, 3) for _ in range(5))
+        p = qk_problem(heads=(hq, hk), batch=B, tokens=S, dim=dim, rotary_dim=0)
+
+        def strides():
+            order, st, reach = rng.sample(range(3), 3), [0] * 3, dim
+            for i in order:
+                st[i] = reach + rng.randint(0, 6)
+                reach += (max(B, S, hq, hk) - 1) * st[i]
+            return st
+
+        st = strides()
+        same = rng.random() < 0.7
+        offs = [0, rng.randint(0, 60)]
+        all_st = [st, st if same else strides()]
+        for i in range(2):
+            p.y[i] = _lib.Heads(QKV + 2 * offs[i], *all_st[i])
+            p.x[i] = p.g[i] = _lib.Heads(FAKE + (9 + i) * MIB, S * hq * hk * 8, hq * hk * 8, 8)
+        sets = [{offs[i] + b * all_st[i][0] + s * all_st[i][1] + h * all_st[i][2] + e for b in range(B) for s in range(S)
+                 for h in range((hq, hk)[i]) for e in range(dim)} for i in range(2)]
+        rc = L.muon_qk_norm_rope_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need))
+        meets = bool(sets[0] & sets[1])
+        assert rc == (-1 if meets else 0) or (rc == -1 and not same), (B, S, hq, hk, dim, all_st, offs, rc, L.muon_last_error())
+        seen.add((same, meets, rc))
+    assert {(True, True, -1), (True, False, 0), (False, True, -1), (False, False, 0)} <= seen
