@@ -532,10 +532,16 @@ const char* kQ[2] = {"q", "k"};
 // not negative.
 struct Span { uintptr_t lo, hi; };
 
+// Whether n positions `stride` apart stay below 2^54 bytes in all (with at most
+// four such terms, every offset fits 64 bits).
+bool extent_ok(int64_t n, int64_t stride) { return n <= 1 || stride <= ((int64_t)1 << 54) / 8 / (n - 1); }
+
 int check_heads(const char* what, int i, const muon_heads* t, int32_t dt, const muon_qk_problem* q) {
   if (!t->p) return fail(MUON_ERR_INVALID_ARG, "%s of %s is NULL", what, kQ[i]);
   if (t->batch_stride < 0 || t->token_stride < 0 || t->head_stride < 0)
     return fail(MUON_ERR_INVALID_ARG, "%s of %s has a negative stride", what, kQ[i]);
+  if (!extent_ok(q->batch, t->batch_stride) || !extent_ok(q->tokens, t->token_stride) || !extent_ok(q->heads[i], t->head_stride))
+    return fail(MUON_ERR_INVALID_ARG, "%s of %s reaches too far", what, kQ[i]);
   if ((uintptr_t)t->p % esize(dt)) return fail(MUON_ERR_INVALID_ARG, "%s of %s is not aligned to its element size", what, kQ[i]);
   return MUON_OK;
 }
@@ -684,6 +690,8 @@ int check_qk(const muon_qk_problem* q, bool backward, bool norm) {
     if ((uintptr_t)q->positions % (q->positions_i64 ? 8 : 4) || (uintptr_t)q->inv_freq % (q->inv_freq_f64 ? 8 : 4))
       return fail(MUON_ERR_INVALID_ARG, "positions or inv_freq is not aligned to its element size");
     if (q->pos_axis_stride < 0 || q->pos_batch_stride < 0 || q->pos_token_stride < 0) return fail(MUON_ERR_INVALID_ARG, "positions has a negative stride");
+    if (!extent_ok(q->axes, q->pos_axis_stride) || !extent_ok(q->batch, q->pos_batch_stride) || !extent_ok(q->tokens, q->pos_token_stride))
+      return fail(MUON_ERR_INVALID_ARG, "positions reach too far");
   }
   int rc;
   for (int i = 0; i < 2; ++i) {

@@ -414,3 +414,17 @@ def test_qk_overlap_agrees_with_the_sets_of_elements():
         assert rc == (-1 if meets else 0) or (rc == -1 and not same), (B, S, hq, hk, dim, all_st, offs, rc, L.muon_last_error())
         seen.add((same, meets, rc))
     assert {(True, True, -1), (True, False, 0), (False, True, -1), (False, False, 0)} <= seen
+
+
+def test_qk_strides_that_pass_64_bits_are_refused():
+    """Their offsets wrapped round, and the overlap checks with them."""
+    L = _lib.lib()
+    for st in ((1 << 61, 512, 64), (0, 1 << 62, 64), (0, 512, 1 << 62), (0, 1 << 54, 64)):
+        p = qk_problem(batch=8 if st[0] else 1)
+        for t in (*p.x, *p.y):
+            t.batch_stride = 5 * 512
+        p.x[1] = _lib.Heads(FAKE + 8 * MIB, *st)
+        assert L.muon_qk_norm_rope(ctypes.byref(p), None) == -1 and b"too far" in L.muon_last_error()
+    for over in (dict(pos_token_stride=1 << 61), dict(pos_batch_stride=1 << 61, batch=8), dict(pos_axis_stride=1 << 62, axes=4)):
+        p = qk_problem(**over)
+        assert L.muon_rope(ctypes.byref(p), None) == -1 and b"too far" in L.muon_last_error()
