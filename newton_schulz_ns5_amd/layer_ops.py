@@ -128,6 +128,17 @@ def _rows(t, name, cols=None):
     return t.data_ptr(), r, c, (t.stride(0) if r > 1 and c else c)
 
 
+# Elements that rows may be apart for the library (2^23 - 32 bytes).  Inputs
+# whose rows are further apart, such as one token of every long sequence
+# (h[:, -1]), are copied first.
+_FAR = {MUON_F32: (2 ** 23 - 32) // 4, MUON_BF16: (2 ** 23 - 32) // 2}
+
+
+def _near(t, ld):
+    """The tensor to read in place of t, whose row stride is ld."""
+    return t.contiguous() if ld > _FAR.get(_CODE.get(t.dtype), ld) else t
+
+
 def _vector(t, name, n):
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         _bad(f"{name} must be a contiguous [{n}] tensor")
@@ -184,6 +195,8 @@ def _given(*outs):
 def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=False, out=None, preact=None):
     """``activation(x @ w.T + bias) + residual`` for x [..., k] and w [n, k] (see muon_linear).
 
+    Rows of any stride; inputs whose rows are 8 MiB or more apart are copied first.
+
     ``activation`` is None, "relu", "relu2", "silu", "gelu" or "gelu_tanh".
     The result has the residual's type, or x's without one, unless ``out`` is
     given (``out`` may be the residual).  ``return_preact=True`` returns
@@ -211,6 +224,9 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
         _bad("w must be [n, k]")
     wp, n, k, ldw = _rows(w, "w")
     xp, m, _, ldx = _rows(x, "x", k)
+    if ldw > _FAR[code] or ldx > _FAR[code]:
+        w, x = _near(w, ldw), _near(x, ldx)
+        (wp, _, _, ldw), (xp, _, _, ldx) = _rows(w, "w"), _rows(x, "x", k)
     shape = x.shape[:-1] + (n,)
     if out is None:
         out = (x if residual is None else residual).new_empty(shape)
@@ -222,6 +238,9 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
     yp, ldy = _check_matrix(out, "out", m, n)
     zp, ldz = _check_matrix(preact, "preact", m, n) if preact is not None else (0, 0)
     rp, ldr = _check_matrix(residual, "residual", m, n) if residual is not None else (0, 0)
+    if ldr > 1 << 20 and residual is not out:
+        residual = _near(residual, ldr)
+        rp, ldr = _check_matrix(residual, "residual", m, n)
     bp = _vector(bias, "bias", n) if bias is not None else 0
     prob = _LINEAR.pack(m, n, k, code, act, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz,
                         _dt(bias) if bias is not None else 0, _dt(residual) if residual is not None else 0, _dt(out), 0)
@@ -254,7 +273,13 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
         _bad("w must be [n, k]")
     wp, n, k, ldw = _rows(w, "w")
     xp, m, _, ldx = _rows(x, "x", k)
+    if ldw > _FAR[code] or ldx > _FAR[code]:
+        w, x = _near(w, ldw), _near(x, ldx)
+        (wp, _, _, ldw), (xp, _, _, ldx) = _rows(w, "w"), _rows(x, "x", k)
     gp, ldg = _check_matrix(dy, "dy", m, n)
+    if ldg > 1 << 20:
+        dy = _near(dy, ldg)
+        gp, ldg = _check_matrix(dy, "dy", m, n)
     zp, ldz = 0, 0
     if act:
         if preact is None:
@@ -262,6 +287,9 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
         if preact.dtype != x.dtype:
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"preact must be {x.dtype} like x")
         zp, ldz = _check_matrix(preact, "preact", m, n)
+        if ldz > 1 << 20:
+            preact = _near(preact, ldz)
+            zp, ldz = _check_matrix(preact, "preact", m, n)
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         _bad("accumulate needs the tensors to add to")
     if dx is None and need_dx:

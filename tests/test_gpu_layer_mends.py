@@ -276,3 +276,33 @@ def test_qk_in_place_in_a_heads_first_buffer(B, S):
     assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(buf[:, hq + hk:], rest)
     with pytest.raises(ns.MuonError):
         ns.rope(q, k, pos, f, k_out=buf[:, hq - 1:hq - 1 + hk].transpose(1, 2))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_rows_far_apart(dtype):
+    """The last token of every long sequence, 8 MiB and more apart; every input so, and their gradients."""
+    torch_cuda()
+
+    def spread(rows, cols, seed):
+        gap = 2 ** 23 // (2 if dtype == BF else 4)
+        buf = torch.empty(rows * gap, dtype=dtype, device="cuda")
+        view = buf.as_strided((rows, cols), (gap, 1))
+        view.copy_(rand((rows, cols), dtype, seed))
+        return view
+
+    for m, k, n in ((4, 72, 40), (70, 72, 40)):
+        x, w, r, z = spread(m, k, 1), spread(n, k, 2), spread(m, n, 3), spread(m, n, 4)
+        want = ns.linear(x.contiguous(), w.contiguous(), None, r.contiguous(), activation="silu")
+        assert torch.equal(ns.linear(x, w, None, r, activation="silu"), want)
+        assert torch.equal(ns.linear(x, w.contiguous()), ns.linear(x.contiguous(), w.contiguous()))
+        want = ns.linear_backward(r.contiguous(), x.contiguous(), w.contiguous(), activation="gelu", preact=z.contiguous())
+        got = ns.linear_backward(r, x, w, activation="gelu", preact=z)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    h = rand((4, 1024, 4096), dtype, 5)
+    w = rand((96, 4096), dtype, 6)
+    assert torch.equal(ns.linear(h[:, -1], w), ns.linear(h[:, -1].contiguous(), w))
+    leaf = h.clone().requires_grad_()
+    ns.linear(leaf[:, -1], w).sum().backward()
+    assert not leaf.grad[:, :-1].any() and leaf.grad[:, -1].any()
+    with pytest.raises(ns.MuonError):  # an output is not copied
+        ns.linear(h[:, -1].contiguous(), w, out=torch.empty(4 * 2 ** 22, dtype=dtype, device="cuda").as_strided((4, 96), (2 ** 22, 1)))
