@@ -10,6 +10,7 @@ called directly, and their results carry no gradient of their own.  Inputs of
 forward-mode differentiation are refused.
 """
 import ctypes
+import operator
 import struct
 
 import torch
@@ -369,6 +370,26 @@ def _heads_of(t, name, shape):
     return (t.data_ptr(), 0, *st[:2]) if len(st) == 3 else (t.data_ptr(), *st[:3])
 
 
+def _integers(name, values):
+    try:
+        return [operator.index(v) for v in values]
+    except TypeError:
+        _bad(f"{name} must be a sequence of integers, not {values!r}")
+
+
+def _float(name, value):
+    """value as the library's fp32 takes it."""
+    try:
+        if value == 0 or -_F32_MAX <= value <= _F32_MAX:
+            return value
+    except (TypeError, RuntimeError):
+        pass
+    _bad(f"{name} must be a number that fp32 holds, not {value!r}")
+
+
+_F32_MAX = 3.4028234663852886e38
+
+
 def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x, g, y, weight, dweight, eps):
     """The problem of one call; q and k (either may be None) give the shapes, x,
     g and y are pairs of tensors or None."""
@@ -433,16 +454,19 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
     if sections is not None:
         if axes is not None:
             _bad("give sections or axes, not both")
-        if len(sections) != naxes or sum(sections) != pairs or min(sections) < 0:
-            _bad(f"sections {list(sections)} do not split {pairs} pairs over {naxes} axes")
+        sections = _integers("sections", sections)
+        if len(sections) != naxes or sum(sections) != pairs or any(n < 0 for n in sections):
+            _bad(f"sections {sections} do not split {pairs} pairs over {naxes} axes")
         if naxes > 1:
             turns = b"".join([bytes((i,)) * n for i, n in enumerate(sections)])
     elif axes is not None:
-        turns = bytes(axes)
-        if len(turns) != pairs or (turns and max(turns) >= naxes):
+        axes = _integers("axes", axes)
+        if len(axes) != pairs or not all(0 <= a < naxes for a in axes):
             _bad(f"axes must name one of {naxes} axes for each of {pairs} pairs")
+        turns = bytes(axes)
     elif naxes > 1:
         _bad("positions with several axes need sections or axes")
+    scale, eps = _float("scale", scale), _float("eps", eps)
     return dev, _QK.pack(batch, tokens, q.shape[-2] if q is not None else 0, k.shape[-2] if k is not None else 0, dim,
                          2 * pairs, _dt(first), wcode if wtype is not None else 0, *fields, positions.data_ptr(), axis_st,
                          batch_st, token_st, inv_freq.data_ptr(), positions.dtype is torch.int64,

@@ -306,3 +306,27 @@ def test_rows_far_apart(dtype):
     assert not leaf.grad[:, :-1].any() and leaf.grad[:, -1].any()
     with pytest.raises(ns.MuonError):  # an output is not copied
         ns.linear(h[:, -1].contiguous(), w, out=torch.empty(4 * 2 ** 22, dtype=dtype, device="cuda").as_strided((4, 96), (2 ** 22, 1)))
+
+
+def test_axes_sections_and_numbers_that_are_not():
+    torch_cuda()
+    q, f = rand((4, 2, 16), BF, 1), torch.ones(8, device="cuda")
+    pos = torch.zeros((2, 4), dtype=torch.int64, device="cuda")
+
+    def status(**how):
+        with pytest.raises(ns.MuonError) as e:
+            ns.rope(q, None, pos, f, **how)
+        return e.value.status
+
+    for axes in (8, [0] * 7, [0] * 7 + [2], [0] * 7 + [256], [0] * 7 + [-1], [0.0] * 8, ["0"] * 8, "00000000", torch.ones(8)):
+        assert status(axes=axes) == -1
+    for sections in (8, [8], [4, 5], [9, -1], [4.0, 4.0], "44", [4, 4, 0], None, []):
+        assert status(sections=sections) == -1
+    for number in (float("nan"), float("inf"), 1e39, "1", None, [1.0]):
+        assert status(axes=[0] * 8, scale=number) == -1
+        with pytest.raises(ns.MuonError):
+            ns.qk_norm_rope(q, None, pos[0], f, eps=number)
+    want = ns.rope(q, None, pos, f, axes=[0, 1] * 4)[0]
+    for axes in ((0, 1) * 4, torch.tensor([0, 1] * 4), bytes([0, 1] * 4)):
+        assert torch.equal(ns.rope(q, None, pos, f, axes=axes)[0], want)
+    assert torch.equal(ns.rope(q, None, pos, f, sections=torch.tensor([3, 5]), scale=2)[0], ns.rope(q, None, pos, f, sections=(3, 5), scale=2.0)[0])
