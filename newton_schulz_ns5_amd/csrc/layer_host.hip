@@ -189,18 +189,33 @@ Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t d
 //   1037 x 1001 over 2056      -   22*  23*   18      * split, with its addition
 struct Tiling { LinTile first, rest; int64_t m1, n1; int split; };
 
-struct TileCost { LinTile tile; int bm, bn, slots; double fixed, u0, u1; };
-constexpr TileCost kCostBf16[] = {{kTile256, 256, 256, 256, 8.0, 1.15, 1.65},
-                                  {kTile256x128, 256, 128, 256, 6.0, 0.58, 0.87},
-                                  {kTile128, 128, 128, 512, 6.0, 0.75, 1.13},
-                                  {kTile64, 64, 64, 768, 6.0, 0.30, 0.62}};
-constexpr TileCost kCostF32[] = {{kTile256x128, 256, 128, 256, 9.0, 3.6, 3.77}, {kTile64, 64, 64, 1024, 5.0, 0.6, 2.0}};
+//
+// fp32 64-edge tiles, four to a CU: the last round takes as long as its fullest
+// CU, so their rate goes by whole workgroups per CU, and their start and
+// epilogue run under each other's products.  us, the tiles chosen without and
+// with that in the model, and the library's product:
+//   260 x 4096 over 14336   474  297  255
+//   227 x 9174 over 4920    238  197  193
+//   87 x 8583 over 4288     110   91   66
+//   16 x 6812 over 7680      91   68   40
+//   2339 x 704 over 4736    160  137  121
+//   7680 x 6812 over 16      81   62   77
+//   260 x 14336 over 4096   326  326  239
+struct TileCost { LinTile tile; int bm, bn, slots; double fixed, u0, u1; bool by_cu; };
+constexpr TileCost kCostBf16[] = {{kTile256, 256, 256, 256, 8.0, 1.15, 1.65, false},
+                                  {kTile256x128, 256, 128, 256, 6.0, 0.58, 0.87, false},
+                                  {kTile128, 128, 128, 512, 6.0, 0.75, 1.13, false},
+                                  {kTile64, 64, 64, 768, 6.0, 0.30, 0.62, false}};
+constexpr TileCost kCostF32[] = {{kTile256x128, 256, 128, 256, 9.0, 3.6, 3.77, false},
+                                 {kTile64, 64, 64, 1024, 3.0, 0.5, 2.0, true}};
 
 // Microseconds of `wgs` workgroups of `slices` slices each.
 double tile_time(const TileCost& c, int64_t wgs, int64_t slices) {
   const int64_t full = wgs / c.slots, last = wgs % c.slots;
   double t = (double)full * (c.fixed + (double)slices * c.u1);
-  if (last) t += c.fixed + (double)slices * std::max(c.u0, c.u1 * (double)last / c.slots);
+  const int cus = 256, per_cu = c.slots / cus;
+  const double share = c.by_cu ? (double)cdiv(last, cus) / per_cu : (double)last / c.slots;
+  if (last) t += c.fixed + (double)slices * std::max(c.u0, c.u1 * share);
   return t;
 }
 

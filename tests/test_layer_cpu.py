@@ -428,3 +428,20 @@ def test_qk_strides_that_pass_64_bits_are_refused():
     for over in (dict(pos_token_stride=1 << 61), dict(pos_batch_stride=1 << 61, batch=8), dict(pos_axis_stride=1 << 62, axes=4)):
         p = qk_problem(**over)
         assert L.muon_rope(ctypes.byref(p), None) == -1 and b"too far" in L.muon_last_error()
+
+
+# ---- how products are divided: the workspace holds split products of m x n, one per chunk ----
+def split_of(m, n, k, dtype):
+    """Chunks that the sum of aligned operands is divided into."""
+    L, need = _lib.lib(), ctypes.c_size_t()
+    p = linear_problem(m=m, n=n, k=k, dtype=dtype, y_dtype=dtype, x_row_stride=k, w_row_stride=k, y_row_stride=n,
+                       w=FAKE + (1 << 38), y=FAKE + (1 << 39))
+    assert L.muon_linear_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0, L.muon_last_error()
+    return max(1, need.value // (m * -(-n // 8) * 8 * 4))
+
+
+def test_fp32_products_with_half_empty_rounds_are_split():
+    """Where the tiles fill the CUs unevenly, chunks of the sum even them out (474 to 297 us and
+    238 to 197 us at the first two); where they fill whole rounds they are not split."""
+    assert split_of(260, 4096, 14336, 0) >= 3 and split_of(227, 9174, 4920, 0) >= 3 and split_of(87, 8584, 4288, 0) >= 4
+    assert split_of(4096, 4096, 4096, 0) == 1 and split_of(1024, 4096, 4096, 0) == 1
