@@ -331,15 +331,26 @@ LinearPlan plan_linear(const muon_linear_problem* q) {
   P.small = q->m <= kSmallRows;
   if (q->m == 0 || q->n == 0) return P;
   if (P.small) {
-    // 64 weight rows per workgroup where that many workgroups, times the
-    // chunks K can be split into (at least two steps per wave each), come near
-    // the 256 CUs; a split pays for its second launch where every workgroup
-    // would read more of the tokens than of a 16-row piece of the weight.
-    const int64_t wgs = cdiv(q->n, 64), steps = cdiv(q->k * esize(q->dtype), 128);
-    const int64_t split = std::max<int64_t>(1, std::min<int64_t>({4, 256 / wgs, steps / 16}));
-    const bool many = q->m > 16 || (q->m > 8 && steps >= 128);
-    P.nb = wgs >= 192 || (many && wgs * split >= 192) ? 4 : 1;
-    P.t.split = P.nb == 4 && wgs < 192 ? (int)split : 1;
+    // Workgroups of 64 weight rows read the tokens least often; of 16, the weight
+    // with the most workgroups.  Chunks of K, of two steps per wave at least,
+    // make up to the 256 CUs' worth of either, and cost a second launch (4 us).
+    const int64_t steps = cdiv(q->k * esize(q->dtype), 128);
+    const int64_t wide = cdiv(q->n, 64), narrow = cdiv(q->n, 16);
+    auto chunks = [&](int64_t wgs, int64_t most) { return std::max<int64_t>(1, std::min<int64_t>({most, 256 / wgs, steps / 16})); };
+    const int64_t split4 = chunks(wide, 8), split1 = chunks(narrow, 16);
+    // 64 rows: enough workgroups without a split, or, where the tokens are many
+    // enough to count (more than 16, or 8 of a weight that is wide too), half a
+    // chip of them with one.
+    const bool many = q->m > 16 || (q->m > 8 && wide >= 80);
+    P.nb = wide >= 192 || (many && wide * split4 >= 128) ? 4 : 1;
+    if (P.nb == 4) {
+      P.t.split = wide >= 192 ? 1 : (int)split4;
+    } else {
+      // a wave's time per step grows with the tokens; the steps that a split
+      // saves it are worth more than the launch
+      const double per_step = 0.4 + (double)q->m / 40, saved = (double)steps / 8 * (1 - 1.0 / (double)split1) * per_step;
+      P.t.split = saved > 6 ? (int)split1 : 1;
+    }
     P.total = part_bytes(q->m, q->n, P.t.split);
     return P;
   }

@@ -12,15 +12,28 @@
 //
 // Every workgroup reads all tokens, M / (16 NB) of what it reads of the
 // weight, so NB is 4 where that leaves the chip full; a weight with fewer rows
-// has its K split over workgroups (launch_split_finish adds them).  bf16, us,
-// against the weight's bytes at 5.1 TB/s:
-//   rows x K       tokens   bytes   NB 1    2    4    4, split
-//   14336 x 4096       48    23.2      -  40.6  31.9  38.5 (2)
-//   4096 x 14336       48    23.2      -  39.8*    -  32.5 (4)   * split 2
-//   4096 x 14336        1    22.9   23.6     -     -  24.3 (4)
-//   6144 x 4096         1     9.8   12.5     -     -  13.5 (2)
-//   6144 x 4096        48    10.0      -  21.2     -  19.6 (2)
-//   1024 x 1024        16     0.4    4.5   5.3     -     -
+// has its K split over workgroups (launch_split_finish adds them).  us by NB and
+// split, against the weight's bytes at 5.1 TB/s (a call of one launch takes 8
+// at least, of two 11):
+//   bf16, rows x K  tokens   bytes   1/1   1/2   1/4   1/8   4/1   4/2   4/4   4/8
+//   14336 x 4096        48    23.2     -     -     -     -  31.9  38.5     -     -
+//   6144 x 4096          1     9.8  12.5  15.3  15.2  17.7  18.4  15.0  15.0  16.4
+//   6144 x 4096         10     9.8  15.6  16.1  16.8  19.2  19.9  15.8  15.9  17.4
+//   6144 x 4096         16     9.8  18.3  17.7  18.3  20.5  20.9  16.1  16.5  18.1
+//   6144 x 4096         38     9.8  28.4  26.4  26.8  30.3  28.5  20.6  23.0  23.6
+//   4096 x 8192         16    13.1  20.1  24.2  22.8  25.7  38.8  25.2  20.9  19.5
+//   4096 x 8192         24    13.1  22.4  27.3  26.3  29.1  43.9  27.6  21.8  20.0
+//   1024 x 8192          1     3.3  11.3  11.1  11.1  11.1  32.1  20.2  12.8  11.0
+//   1024 x 8192         16     3.3  16.6  12.9  11.1  11.3  37.4  23.4  14.7  11.2
+//   1024 x 16384         1     6.5  20.0  14.1  12.2  12.4  61.2  34.8  20.2  13.3
+//   512 x 14336         64     2.9  63.7  36.7  21.5  14.6  99.5  55.0  31.1  19.7
+//   5921 x 10391*       38    23.9   169   133   133   134   160    87    89    76
+//   fp32, rows x K
+//   576 x 3456           4     1.5  11.2  12.3  12.4  12.1  32.9  21.7  13.9  12.3
+//   576 x 3456          16     1.5  14.6  12.4  12.3  12.3  35.3  23.0  14.5  12.3
+//   384 x 13973*        62     4.2   123  66.9  37.6  23.1   329   173  92.8  52.5
+//   9472 x 2504         40    18.5  61.1  56.1  56.5  56.4  58.9  63.5  54.6  56.0
+// (* rows that are not 16-byte aligned: every load takes two lines.)
 // More steps in flight per wave (two or four loaded together) gained nothing.
 #include "layer_internal.h"
 #include "linear_epilogue.h"

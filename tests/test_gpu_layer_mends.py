@@ -12,7 +12,7 @@ import torch
 
 import newton_schulz_ns5_amd as ns
 from gpu_util import torch_cuda
-from test_gpu_layer import ACTS, BF, F32, U, act64, close, rand
+from test_gpu_layer import ACTS, BF, F32, U, act64, check_forward, close, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -330,3 +330,17 @@ def test_axes_sections_and_numbers_that_are_not():
     for axes in ((0, 1) * 4, torch.tensor([0, 1] * 4), bytes([0, 1] * 4)):
         assert torch.equal(ns.rope(q, None, pos, f, axes=axes)[0], want)
     assert torch.equal(ns.rope(q, None, pos, f, sections=torch.tensor([3, 5]), scale=2)[0], ns.rope(q, None, pos, f, sections=(3, 5), scale=2.0)[0])
+
+
+# ---- few rows times narrow weights: 16 or 64 weight rows per workgroup, K divided over workgroups --------
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("m", [1, 5, 16, 17, 33, 40, 49, 64])
+@pytest.mark.parametrize("k,n", [(8200, 70), (14336, 512), (13973, 37), (6016, 2051), (4160, 5100), (12300, 100)])
+def test_few_rows_divided_sums(m, k, n, dtype):
+    torch_cuda()
+    x, w = rand((m, k), dtype, 1), rand((n, k), dtype, 2, 1 / math.sqrt(k))
+    b, r = rand((n,), dtype, 3), rand((m, n), dtype, 4)
+    check_forward(x, w, None, None, None, ns.linear(x, w), None, "plain")
+    y, z = ns.linear(x, w, b, r, activation="gelu", return_preact=True)
+    check_forward(x, w, b, r, "gelu", y, z, "bias, gelu, residual")
+    assert torch.equal(ns.linear(x, w), ns.linear(x, w))

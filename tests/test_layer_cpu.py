@@ -445,3 +445,12 @@ def test_fp32_products_with_half_empty_rounds_are_split():
     238 to 197 us at the first two); where they fill whole rounds they are not split."""
     assert split_of(260, 4096, 14336, 0) >= 3 and split_of(227, 9174, 4920, 0) >= 3 and split_of(87, 8584, 4288, 0) >= 4
     assert split_of(4096, 4096, 4096, 0) == 1 and split_of(1024, 4096, 4096, 0) == 1
+
+
+def test_few_rows_times_narrow_weights_are_split():
+    """A weight with few rows leaves most CUs without a workgroup unless its K is divided
+    (123 to 23 us and 64 to 15 us at the first two); few steps, or a full chip, are not split."""
+    assert split_of(62, 384, 13972, 0) >= 8 and split_of(64, 512, 14336, 1) >= 8 and split_of(38, 5920, 10392, 1) >= 2
+    assert split_of(1, 1024, 16384, 1) >= 2
+    for m, n, k, t in ((1, 6144, 4096, 1), (48, 14336, 4096, 1), (4, 576, 3456, 0), (16, 1024, 1024, 0), (64, 1024, 1024, 1)):
+        assert split_of(m, n, k, t) == 1
