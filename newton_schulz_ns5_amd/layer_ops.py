@@ -361,11 +361,12 @@ _NO_PAIR = _NO_HEADS * 2
 
 
 def _heads_of(t, name, shape):
-    """(pointer, batch, token, head stride) of a [tokens, heads, dim] or [batch, tokens, heads, dim] tensor."""
-    if t.shape != shape:
+    """(pointer, batch, token, head stride) of a [tokens, heads, dim] or [batch, tokens, heads, dim] tensor
+    of this shape (None: it is where the shape comes from)."""
+    if shape is not None and t.shape != shape:
         _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
     st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1 and t.numel():
+    if st[-1] != 1 and t.shape[-1] > 1 and t.numel():
         _bad(f"{name} needs unit stride in its last dimension")
     return (t.data_ptr(), 0, *st[:2]) if len(st) == 3 else (t.data_ptr(), *st[:3])
 
@@ -377,31 +378,20 @@ def _integers(name, values):
         _bad(f"{name} must be a sequence of integers, not {values!r}")
 
 
-def _float(name, value):
-    """value as the library's fp32 takes it."""
-    try:
-        if value == 0 or -_F32_MAX <= value <= _F32_MAX:
-            return value
-    except (TypeError, RuntimeError):
-        pass
-    _bad(f"{name} must be a number that fp32 holds, not {value!r}")
-
-
-_F32_MAX = 3.4028234663852886e38
-
-
 def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x, g, y, weight, dweight, eps):
     """The problem of one call; q and k (either may be None) give the shapes, x,
     g and y are pairs of tensors or None."""
     first = q if q is not None else k
     if first is None:
         _bad("q and k are both None")
+    qs, ks = q.shape if q is not None else None, k.shape if k is not None else None
     if q is not None and k is not None:
-        if q.dim() != k.dim() or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
-            _bad(f"q {tuple(q.shape)} and k {tuple(k.shape)} differ in more than their heads")
+        if len(qs) != len(ks) or qs[:-2] != ks[:-2] or qs[-1] != ks[-1]:
+            _bad(f"q {tuple(qs)} and k {tuple(ks)} differ in more than their heads")
         if q.dtype != k.dtype:
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"q is {q.dtype} and k {k.dtype}: one type is needed")
-    if first.dim() not in (3, 4):
+    fs = qs if qs is not None else ks
+    if len(fs) not in (3, 4):
         _bad("q and k must be [tokens, heads, dim] or [batch, tokens, heads, dim]")
     dtype = first.dtype
     fields = []
@@ -409,7 +399,7 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
         if pair is None:
             fields += _NO_PAIR
             continue
-        for t, like, name in ((pair[0], q, "q"), (pair[1], k, "k")):
+        for t, like, shape, name in ((pair[0], q, qs, "q"), (pair[1], k, ks, "k")):
             if t is None or like is None:
                 if t is not like:
                     _bad("q and k must both be given, or both be left out, in every pair of tensors")
@@ -417,10 +407,10 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
                 continue
             if t.dtype != dtype:
                 raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"head tensors are {t.dtype} and {dtype}: one type is needed")
-            fields += _heads_of(t, name, like.shape)
+            fields += _heads_of(t, name, shape if t is not like else None)
     dev = _same_device(positions, inv_freq, *(x or ()), *(g or ()), *(y or ()), *weight, *dweight)
-    batch, tokens = (first.shape[0], first.shape[1]) if first.dim() == 4 else (1, first.shape[0])
-    dim = first.shape[-1]
+    batch, tokens = (fs[0], fs[1]) if len(fs) == 4 else (1, fs[0])
+    dim = fs[-1]
     wtype = None
     for t in weight + dweight:
         if t is None:
@@ -438,7 +428,7 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
         _bad(f"{pairs} pairs do not fit heads of {dim} (at most {_lib.QK_MAX_PAIRS})")
     if positions.dtype not in (torch.int32, torch.int64):
         raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"positions are {positions.dtype}, not int32 or int64")
-    lead, shape, st = first.shape[:-2], positions.shape, positions.stride()
+    lead, shape, st = fs[:-2], positions.shape, positions.stride()
     naxes, axis_st, batch_st = 1, 0, 0
     if shape == lead:
         token_st = st[-1]
@@ -466,11 +456,13 @@ def _qk_problem(q, k, positions, inv_freq, sections, axes, interleaved, scale, x
         turns = bytes(axes)
     elif naxes > 1:
         _bad("positions with several axes need sections or axes")
-    scale, eps = _float("scale", scale), _float("eps", eps)
-    return dev, _QK.pack(batch, tokens, q.shape[-2] if q is not None else 0, k.shape[-2] if k is not None else 0, dim,
-                         2 * pairs, _dt(first), wcode if wtype is not None else 0, *fields, positions.data_ptr(), axis_st,
-                         batch_st, token_st, inv_freq.data_ptr(), positions.dtype is torch.int64,
-                         inv_freq.dtype is torch.float64, bool(interleaved), naxes, scale, eps, turns)
+    try:
+        return dev, _QK.pack(batch, tokens, qs[-2] if qs is not None else 0, ks[-2] if ks is not None else 0, dim,
+                             2 * pairs, _dt(first), wcode if wtype is not None else 0, *fields, positions.data_ptr(),
+                             axis_st, batch_st, token_st, inv_freq.data_ptr(), positions.dtype is torch.int64,
+                             inv_freq.dtype is torch.float64, bool(interleaved), naxes, scale, eps, turns)
+    except (OverflowError, struct.error, TypeError):  # every other field is a size or an address
+        _bad(f"scale and eps must be numbers that fp32 holds, not {scale!r} and {eps!r}")
 
 
 def _like(t, out):
