@@ -114,6 +114,7 @@ SIGNATURES = {
     "muon_step_groups": (c_i32, [ctypes.POINTER(Group), c_i64, ctypes.POINTER(HParams), c_vp, c_sz, c_vp]),
     "muon_linear_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
     "muon_linear": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
+    "muon_linear_plan": (c_i32, [c_i64, c_i64, c_i64, c_i32, c_i32, ctypes.POINTER(c_i32 * 4)]),
     "muon_linear_backward_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
     "muon_linear_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "muon_qk_norm_rope": (c_i32, [c_vp, c_vp]),

@@ -317,6 +317,27 @@ hipError_t run_product(LinGemm g, int32_t dt, LinKind kind, const Tiling& t, cha
   return e;
 }
 
+// Few rows: weight rows per workgroup / 16 through nb, and the chunks of K.
+int few_rows(int64_t m, int64_t n, int64_t k, int32_t dtype, int& nb) {
+  // Workgroups of 64 weight rows read the tokens least often; of 16, the weight
+  // with the most workgroups.  Chunks of K, of two steps per wave at least,
+  // make up to the 256 CUs' worth of either, and cost a second launch (4 us).
+  const int64_t steps = cdiv(k * esize(dtype), 128);
+  const int64_t wide = cdiv(n, 64), narrow = cdiv(n, 16);
+  auto chunks = [&](int64_t wgs, int64_t most) { return std::max<int64_t>(1, std::min<int64_t>({most, 256 / wgs, steps / 16})); };
+  const int64_t split4 = chunks(wide, 8), split1 = chunks(narrow, 16);
+  // 64 rows: enough workgroups without a split, or, where the tokens are many
+  // enough to count (more than 16, or 8 of a weight that is wide too), half a
+  // chip of them with one.
+  const bool many = m > 16 || (m > 8 && wide >= 80);
+  nb = wide >= 192 || (many && wide * split4 >= 128) ? 4 : 1;
+  if (nb == 4) return wide >= 192 ? 1 : (int)split4;
+  // a wave's time per step grows with the tokens; the steps that a split
+  // saves it are worth more than the launch
+  const double per_step = 0.4 + (double)m / 40, saved = (double)steps / 8 * (1 - 1.0 / (double)split1) * per_step;
+  return saved > 6 ? (int)split1 : 1;
+}
+
 // Work of a forward call: the small kernel for few rows, else tiles.
 struct LinearPlan {
   bool small;
@@ -331,26 +352,7 @@ LinearPlan plan_linear(const muon_linear_problem* q) {
   P.small = q->m <= kSmallRows;
   if (q->m == 0 || q->n == 0) return P;
   if (P.small) {
-    // Workgroups of 64 weight rows read the tokens least often; of 16, the weight
-    // with the most workgroups.  Chunks of K, of two steps per wave at least,
-    // make up to the 256 CUs' worth of either, and cost a second launch (4 us).
-    const int64_t steps = cdiv(q->k * esize(q->dtype), 128);
-    const int64_t wide = cdiv(q->n, 64), narrow = cdiv(q->n, 16);
-    auto chunks = [&](int64_t wgs, int64_t most) { return std::max<int64_t>(1, std::min<int64_t>({most, 256 / wgs, steps / 16})); };
-    const int64_t split4 = chunks(wide, 8), split1 = chunks(narrow, 16);
-    // 64 rows: enough workgroups without a split, or, where the tokens are many
-    // enough to count (more than 16, or 8 of a weight that is wide too), half a
-    // chip of them with one.
-    const bool many = q->m > 16 || (q->m > 8 && wide >= 80);
-    P.nb = wide >= 192 || (many && wide * split4 >= 128) ? 4 : 1;
-    if (P.nb == 4) {
-      P.t.split = wide >= 192 ? 1 : (int)split4;
-    } else {
-      // a wave's time per step grows with the tokens; the steps that a split
-      // saves it are worth more than the launch
-      const double per_step = 0.4 + (double)q->m / 40, saved = (double)steps / 8 * (1 - 1.0 / (double)split1) * per_step;
-      P.t.split = saved > 6 ? (int)split1 : 1;
-    }
+    P.t.split = few_rows(q->m, q->n, q->k, q->dtype, P.nb);
     P.total = part_bytes(q->m, q->n, P.t.split);
     return P;
   }
@@ -470,6 +472,25 @@ int muon_linear(const muon_linear_problem* q, void* workspace, size_t workspace_
     e = run_product(g, q->dtype, kRowRow, P.t, ws + P.part_off, s);
   }
   return e == hipSuccess ? ok() : hip_fail(e, "linear kernels");
+}
+
+int muon_linear_plan(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t kind, int32_t plan[4]) {
+  if (!plan) return fail(MUON_ERR_INVALID_ARG, "plan is NULL");
+  if (kind < 0 || kind > 2) return fail(MUON_ERR_INVALID_ARG, "kind %d is not in 0..2", kind);
+  if (!dtype_ok(dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype %d is not MUON_F32 or MUON_BF16", dtype);
+  const int rc = check_sizes(m, n, k);
+  if (rc) return rc;
+  if (kind == 0 && m <= kSmallRows) {
+    int nb = 1;
+    plan[2] = few_rows(m, n, k, dtype, nb);
+    plan[0] = 0; plan[1] = 16 * nb; plan[3] = 0;
+    return ok();
+  }
+  const int64_t M = kind == 2 ? n : m, N = kind == 0 ? n : k, K = kind == 0 ? k : (kind == 1 ? n : m);
+  const Tiling t = choose_tiling(M, N, K, dtype == MUON_BF16);
+  const int edge[4][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 64}};
+  plan[0] = edge[t.first][0]; plan[1] = edge[t.first][1]; plan[2] = t.split; plan[3] = t.m1 < M || t.n1 < N;
+  return ok();
 }
 
 int muon_linear_backward_workspace_bytes(const muon_linear_grad* q, size_t* bytes) {

@@ -12,7 +12,7 @@ import torch
 
 import newton_schulz_ns5_amd as ns
 from gpu_util import torch_cuda
-from test_gpu_layer import ACTS, BF, F32, U, act64, check_forward, close, rand
+from test_gpu_layer import ACTS, BF, F32, U, act64, check_backward, check_forward, close, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -333,9 +333,12 @@ def test_axes_sections_and_numbers_that_are_not():
 
 
 # ---- few rows times narrow weights: 16 or 64 weight rows per workgroup, K divided over workgroups --------
+FEW_ROWS = [(m, k, n) for m in (1, 5, 16, 17, 33, 40, 49, 64)
+            for k, n in ((8200, 70), (14336, 512), (13973, 37), (6016, 2051), (4160, 5100), (12300, 100))]
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("m", [1, 5, 16, 17, 33, 40, 49, 64])
-@pytest.mark.parametrize("k,n", [(8200, 70), (14336, 512), (13973, 37), (6016, 2051), (4160, 5100), (12300, 100)])
+@pytest.mark.parametrize("m,k,n", FEW_ROWS)
 def test_few_rows_divided_sums(m, k, n, dtype):
     torch_cuda()
     x, w = rand((m, k), dtype, 1), rand((n, k), dtype, 2, 1 / math.sqrt(k))
@@ -344,3 +347,38 @@ def test_few_rows_divided_sums(m, k, n, dtype):
     y, z = ns.linear(x, w, b, r, activation="gelu", return_preact=True)
     check_forward(x, w, b, r, "gelu", y, z, "bias, gelu, residual")
     assert torch.equal(ns.linear(x, w), ns.linear(x, w))
+
+
+# ---- every kernel that a call can choose (test_layer_cpu says which sizes reach which) ---------------------
+TILE_SIZES = {
+    F32: [(69, 360, 72), (67, 62, 358), (355, 81, 65), (3150, 229, 2241), (2549, 2766, 897), (2226, 3299, 226), (1239, 1868, 2771),
+          (231, 2572, 2790), (2387, 1102, 2303)],
+    BF: [(67, 1001, 66), (71, 63, 992), (1005, 83, 69), (3176, 65, 2465), (1876, 4160, 67), (66, 3318, 2334), (774, 60, 3617),
+         (2527, 1155, 65), (65, 910, 3010), (2386, 3965, 67), (2588, 67, 3612), (2505, 66, 3988), (2576, 60, 3123), (3370, 2374, 65),
+         (65, 3417, 2324), (4134, 63, 4181), (4153, 4079, 73), (66, 4100, 4124), (65, 4096, 6144)],
+}
+FEW_ROWS_WHOLE = [(m, k, n) for m in (3, 23, 42, 60) for k, n in ((72, 12300), (1030, 16400), (200, 99))]
+
+
+@pytest.mark.parametrize("dtype,m,k,n", [(t, *s) for t in (BF, F32) for s in TILE_SIZES[t]])
+def test_every_tile(dtype, m, k, n):
+    torch_cuda()
+    x, w, b, r = rand((m, k), dtype, 1), rand((n, k), dtype, 2, 1 / math.sqrt(k)), rand((n,), F32, 3), rand((m, n), dtype, 4)
+    y, z = ns.linear(x, w, b, r, activation="silu", return_preact=True)
+    check_forward(x, w, b, r, "silu", y, z, "forward")
+    check_forward(x, w, None, None, None, ns.linear(x, w), None, "plain")
+    dy, base = rand((m, n), dtype, 5), rand((n, k), F32, 6)
+    dx, dw, db = ns.linear_backward(dy, x, w, activation="silu", preact=z, need_dbias=True)
+    check_backward(dy, x, w, z, "silu", dx, dw, db, "backward")
+    dw = base.clone()
+    dx, _, _ = ns.linear_backward(dy, x, w, dw=dw, accumulate=True)
+    check_backward(dy, x, w, None, None, dx, dw, None, "accumulated", base)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("m,k,n", FEW_ROWS_WHOLE)
+def test_few_rows_undivided_sums(m, k, n, dtype):
+    torch_cuda()
+    x, w, b, r = rand((m, k), dtype, 1), rand((n, k), dtype, 2, 1 / math.sqrt(k)), rand((n,), dtype, 3), rand((m, n), F32, 4)
+    y, z = ns.linear(x, w, b, r, activation="relu2", return_preact=True)
+    check_forward(x, w, b, r, "relu2", y, z, "undivided")

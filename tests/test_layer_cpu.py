@@ -454,3 +454,40 @@ def test_few_rows_times_narrow_weights_are_split():
     assert split_of(1, 1024, 16384, 1) >= 2
     for m, n, k, t in ((1, 6144, 4096, 1), (48, 14336, 4096, 1), (4, 576, 3456, 0), (16, 1024, 1024, 0), (64, 1024, 1024, 1)):
         assert split_of(m, n, k, t) == 1
+
+
+def test_the_gpu_tests_reach_every_kernel_of_the_products():
+    """Each type, layout, tile, with and without a divided sum and a last round of smaller tiles;
+    for few rows each number of token and weight blocks: by the plan of the sizes that the GPU tests run."""
+    import test_gpu_layer as old
+    import test_gpu_layer_mends as new
+    L = _lib.lib()
+
+    def plan(m, n, k, dtype, kind):
+        p = (ctypes.c_int32 * 4)()
+        assert L.muon_linear_plan(m, n, k, dtype, kind, ctypes.byref(p)) == 0
+        return tuple(p)
+
+    code = {torch.float32: 0, torch.bfloat16: 1}
+    runs = [(code[t], m, k, n) for t in code for m, k, n in old.SIZES + new.TILE_SIZES[t] + new.FEW_ROWS + new.FEW_ROWS_WHOLE]
+    tiles, few = set(), set()
+    for dtype, m, k, n in runs:
+        for kind in range(3):
+            rows, cols, split, last = plan(m, n, k, dtype, kind)
+            if rows:
+                tiles.add((dtype, kind, rows, cols, split > 1, last))
+            else:
+                few.add((dtype, -(-m // 16), cols, split > 1))
+    every = {(t, mb, cols, split) for t in (0, 1) for mb in (1, 2, 3, 4) for cols in (16, 64) for split in (False, True)}
+    assert few == every, sorted(every - few)
+    want = {(0, kind, rows, cols, split, 0) for kind in range(3) for rows, cols in ((64, 64), (256, 128)) for split in (False, True)}
+    want |= {(1, kind, rows, cols, split, 0) for kind in range(3) for rows, cols in ((64, 64), (256, 128)) for split in (False, True)}
+    want |= {(1, kind, rows, rows, False, last) for kind in range(3) for rows, last in ((128, 0), (256, 0), (256, 1))}
+    assert not want - tiles, sorted(want - tiles)
+
+
+def test_plan_refusals():
+    L, p = _lib.lib(), (ctypes.c_int32 * 4)()
+    assert L.muon_linear_plan(1, 1, 1, 0, 0, None) == -1
+    assert L.muon_linear_plan(1, 1, 1, 0, 3, ctypes.byref(p)) == -1 and L.muon_linear_plan(1, 1, 1, 0, -1, ctypes.byref(p)) == -1
+    assert L.muon_linear_plan(1, 1, 1, 2, 0, ctypes.byref(p)) == -2 and L.muon_linear_plan(-1, 1, 1, 0, 0, ctypes.byref(p)) == -1
