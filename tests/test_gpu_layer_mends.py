@@ -382,3 +382,28 @@ def test_few_rows_undivided_sums(m, k, n, dtype):
     x, w, b, r = rand((m, k), dtype, 1), rand((n, k), dtype, 2, 1 / math.sqrt(k)), rand((n,), dtype, 3), rand((m, n), F32, 4)
     y, z = ns.linear(x, w, b, r, activation="relu2", return_preact=True)
     check_forward(x, w, b, r, "relu2", y, z, "undivided")
+
+
+@pytest.mark.filterwarnings("ignore")
+def test_inside_torch_compile():
+    """A compiled function breaks its graph at these calls: every call with new tensors gives what the plain call gives."""
+    torch_cuda()
+    w = rand((96, 64), BF, 1)
+    pos, f = torch.arange(40, device="cuda"), torch.rand(32, device="cuda")
+
+    def fn(x, w, q):
+        y = ns.linear(x * 2, w, activation="silu") + 1
+        a, _ = ns.rope(q, None, pos, f)
+        return y.float().sum(-1) + a.float().sum((1, 2))
+
+    compiled = torch.compile(fn, backend="eager")
+    for i in range(3):
+        for grad in (False, True):
+            x, q = rand((40, 64), BF, 10 + i), rand((40, 2, 64), BF, 20 + i)
+            a, b = [t.clone().requires_grad_(grad) for t in (x, w, q)], [t.clone().requires_grad_(grad) for t in (x, w, q)]
+            got, want = compiled(*a), fn(*b)
+            assert torch.equal(got, want)
+            if grad:
+                got.sum().backward()
+                want.sum().backward()
+                assert all(torch.equal(s.grad, t.grad) for s, t in zip(a, b))
