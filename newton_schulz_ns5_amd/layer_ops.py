@@ -111,6 +111,10 @@ def _call_here(dev, fn, problem, need):
 
 
 # ---- the linear product ---------------------------------------------------------------
+class _Uneven(MuonError):
+    """Rows that are not one stride apart."""
+
+
 def _rows(t, name, cols=None):
     """(pointer, rows, columns, row stride) of a [..., columns] tensor seen as rows."""
     if t.dim() < 1:
@@ -120,7 +124,7 @@ def _rows(t, name, cols=None):
             t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(-1, t.shape[-1]) if t.shape[-1] else \
                 t.new_empty((t.shape[:-1].numel(), 0))
         except RuntimeError:
-            _bad(f"the leading dimensions of {name} cannot be seen as one")
+            raise _Uneven(_lib.MUON_ERR_INVALID_ARG, f"the leading dimensions of {name} cannot be seen as one")
     r, c = t.shape
     if cols is not None and c != cols:
         _bad(f"{name} has {c} columns, not {cols}")
@@ -129,15 +133,32 @@ def _rows(t, name, cols=None):
     return t.data_ptr(), r, c, (t.stride(0) if r > 1 and c else c)
 
 
-# Elements that rows may be apart for the library (2^23 - 32 bytes).  Inputs
-# whose rows are further apart, such as one token of every long sequence
-# (h[:, -1]), are copied first.
+# Elements that rows may be apart for the library (2^23 - 32 bytes).
 _FAR = {MUON_F32: (2 ** 23 - 32) // 4, MUON_BF16: (2 ** 23 - 32) // 2}
 
 
-def _near(t, ld):
-    """The tensor to read in place of t, whose row stride is ld."""
-    return t.contiguous() if ld > _FAR.get(_CODE.get(t.dtype), ld) else t
+def _input(t, name, cols=None):
+    """(tensor, pointer, rows, columns, row stride) of an input seen as rows.  The
+    tensor is t, or a copy where the library cannot take its rows: leading
+    dimensions that are not one, rows that share elements (expanded), rows too
+    far apart (one token of every long sequence, h[:, -1]).  The caller holds it
+    until the launch."""
+    try:
+        p, r, c, ld = _rows(t, name, cols)
+        if r <= 1 or (c <= ld and (ld <= 1 << 20 or ld <= _FAR[_dt(t)])):
+            return t, p, r, c, ld
+    except _Uneven:
+        if t.stride(-1) != 1:
+            _bad(f"{name} needs unit column stride")
+    t = t.contiguous()
+    return (t, *_rows(t, name, cols))
+
+
+def _input_matrix(t, name, rows, cols):
+    t, p, r, c, ld = _input(t, name)
+    if (r, c) != (rows, cols):
+        _bad(f"{name} is [{r}, {c}], not [{rows}, {cols}]")
+    return t, p, ld
 
 
 def _vector(t, name, n):
@@ -196,7 +217,8 @@ def _given(*outs):
 def linear(x, w, bias=None, residual=None, *, activation=None, return_preact=False, out=None, preact=None):
     """``activation(x @ w.T + bias) + residual`` for x [..., k] and w [n, k] (see muon_linear).
 
-    Rows of any stride; inputs whose rows are 8 MiB or more apart are copied first.
+    Columns are contiguous, rows of any stride.  Inputs whose rows share elements (expanded), are 8 MiB or
+    more apart, or are not evenly spaced are copied first.
 
     ``activation`` is None, "relu", "relu2", "silu", "gelu" or "gelu_tanh".
     The result has the residual's type, or x's without one, unless ``out`` is
@@ -223,11 +245,8 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
         raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"x is {x.dtype} and w {w.dtype}: one type is needed")
     if w.dim() != 2:
         _bad("w must be [n, k]")
-    wp, n, k, ldw = _rows(w, "w")
-    xp, m, _, ldx = _rows(x, "x", k)
-    if ldw > _FAR[code] or ldx > _FAR[code]:
-        w, x = _near(w, ldw), _near(x, ldx)
-        (wp, _, _, ldw), (xp, _, _, ldx) = _rows(w, "w"), _rows(x, "x", k)
+    w, wp, n, k, ldw = _input(w, "w")
+    x, xp, m, _, ldx = _input(x, "x", k)
     shape = x.shape[:-1] + (n,)
     if out is None:
         out = (x if residual is None else residual).new_empty(shape)
@@ -238,10 +257,11 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"preact must be {x.dtype} like x")
     yp, ldy = _check_matrix(out, "out", m, n)
     zp, ldz = _check_matrix(preact, "preact", m, n) if preact is not None else (0, 0)
-    rp, ldr = _check_matrix(residual, "residual", m, n) if residual is not None else (0, 0)
-    if ldr > 1 << 20 and residual is not out:
-        residual = _near(residual, ldr)
-        rp, ldr = _check_matrix(residual, "residual", m, n)
+    rp, ldr = 0, 0
+    if residual is out and out is not None:
+        rp, ldr = yp, ldy
+    elif residual is not None:
+        residual, rp, ldr = _input_matrix(residual, "residual", m, n)
     bp = _vector(bias, "bias", n) if bias is not None else 0
     prob = _LINEAR.pack(m, n, k, code, act, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz,
                         _dt(bias) if bias is not None else 0, _dt(residual) if residual is not None else 0, _dt(out), 0)
@@ -272,25 +292,16 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
         raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"x is {x.dtype} and w {w.dtype}: one type is needed")
     if w.dim() != 2:
         _bad("w must be [n, k]")
-    wp, n, k, ldw = _rows(w, "w")
-    xp, m, _, ldx = _rows(x, "x", k)
-    if ldw > _FAR[code] or ldx > _FAR[code]:
-        w, x = _near(w, ldw), _near(x, ldx)
-        (wp, _, _, ldw), (xp, _, _, ldx) = _rows(w, "w"), _rows(x, "x", k)
-    gp, ldg = _check_matrix(dy, "dy", m, n)
-    if ldg > 1 << 20:
-        dy = _near(dy, ldg)
-        gp, ldg = _check_matrix(dy, "dy", m, n)
+    w, wp, n, k, ldw = _input(w, "w")
+    x, xp, m, _, ldx = _input(x, "x", k)
+    dy, gp, ldg = _input_matrix(dy, "dy", m, n)
     zp, ldz = 0, 0
     if act:
         if preact is None:
             _bad("an activation's gradient needs preact")
         if preact.dtype != x.dtype:
             raise MuonError(_lib.MUON_ERR_UNSUPPORTED, f"preact must be {x.dtype} like x")
-        zp, ldz = _check_matrix(preact, "preact", m, n)
-        if ldz > 1 << 20:
-            preact = _near(preact, ldz)
-            zp, ldz = _check_matrix(preact, "preact", m, n)
+        preact, zp, ldz = _input_matrix(preact, "preact", m, n)
     if accumulate and ((need_dw and dw is None) or (need_dbias and dbias is None)):
         _bad("accumulate needs the tensors to add to")
     if dx is None and need_dx:

@@ -407,3 +407,31 @@ def test_inside_torch_compile():
                 got.sum().backward()
                 want.sum().backward()
                 assert all(torch.equal(s.grad, t.grad) for s, t in zip(a, b))
+
+
+def test_inputs_that_share_rows_or_are_unevenly_spaced():
+    torch_cuda()
+    x, w, z = rand((5, 7, 64), BF, 1), rand((48, 64), BF, 2), rand((5, 7, 48), BF, 3)
+    t, u = x.transpose(0, 1), z.transpose(0, 1)  # [S, B, E] in [B, S, E] memory
+    want = ns.linear(t.contiguous(), w, None, u.contiguous(), activation="silu")
+    assert torch.equal(ns.linear(t, w, None, u, activation="silu"), want)
+    want = ns.linear_backward(u.contiguous(), t.contiguous(), w, activation="gelu", preact=u.contiguous())
+    got = ns.linear_backward(u, t, w, activation="gelu", preact=u)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for m in (5, 100):
+        row, line = rand((1, 64), BF, 4), rand((1, 48), F32, 5)
+        got = ns.linear(row.expand(m, 64), w, None, line.expand(m, 48))
+        assert torch.equal(got, ns.linear(row.repeat(m, 1), w, None, line.repeat(m, 1)))
+        got = ns.linear_backward(line.expand(m, 48), row.expand(m, 64), w)
+        want = ns.linear_backward(line.repeat(m, 1), row.repeat(m, 1), w)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    leaf = x.clone().requires_grad_()
+    ns.linear(leaf.transpose(0, 1), w).sum().backward()
+    want = ns.linear_backward(torch.ones(35, 48, dtype=BF, device="cuda"), x.view(35, 64), w)[0]
+    assert torch.equal(leaf.grad, want.view(5, 7, 64))
+    for bad in (lambda: ns.linear(x.transpose(1, 2), rand((48, 7), BF, 6)),           # columns are not contiguous
+                lambda: ns.linear(x, w, out=u.transpose(0, 1).transpose(0, 1)),       # an output is not copied
+                lambda: ns.linear(x.view(35, 64), w, out=torch.empty(48, dtype=BF, device="cuda").expand(35, 48))):
+        with pytest.raises(ns.MuonError) as e:
+            bad()
+        assert e.value.status == -1
