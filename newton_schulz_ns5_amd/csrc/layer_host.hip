@@ -480,13 +480,15 @@ int muon_linear_plan(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t kin
   if (!dtype_ok(dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype %d is not MUON_F32 or MUON_BF16", dtype);
   const int rc = check_sizes(m, n, k);
   if (rc) return rc;
+  const int64_t M = kind == 2 ? n : m, N = kind == 0 ? n : k, K = kind == 0 ? k : (kind == 1 ? n : m);
+  for (int i = 0; i < 4; ++i) plan[i] = 0;  // an empty output runs nothing
+  if (M == 0 || N == 0) return ok();
   if (kind == 0 && m <= kSmallRows) {
     int nb = 1;
     plan[2] = few_rows(m, n, k, dtype, nb);
-    plan[0] = 0; plan[1] = 16 * nb; plan[3] = 0;
+    plan[1] = 16 * nb;
     return ok();
   }
-  const int64_t M = kind == 2 ? n : m, N = kind == 0 ? n : k, K = kind == 0 ? k : (kind == 1 ? n : m);
   const Tiling t = choose_tiling(M, N, K, dtype == MUON_BF16);
   const int edge[4][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 64}};
   plan[0] = edge[t.first][0]; plan[1] = edge[t.first][1]; plan[2] = t.split; plan[3] = t.m1 < M || t.n1 < N;

@@ -491,3 +491,15 @@ def test_plan_refusals():
     assert L.muon_linear_plan(1, 1, 1, 0, 0, None) == -1
     assert L.muon_linear_plan(1, 1, 1, 0, 3, ctypes.byref(p)) == -1 and L.muon_linear_plan(1, 1, 1, 0, -1, ctypes.byref(p)) == -1
     assert L.muon_linear_plan(1, 1, 1, 2, 0, ctypes.byref(p)) == -2 and L.muon_linear_plan(-1, 1, 1, 0, 0, ctypes.byref(p)) == -1
+
+
+def test_plan_of_empty_and_largest_sizes():
+    L, p = _lib.lib(), (ctypes.c_int32 * 4)()
+    for dtype in (0, 1):
+        for kind in range(3):
+            for m, n, k in ((0, 5, 5), (5, 0, 5), (5, 5, 0), (0, 0, 0), (100, 0, 7), (100, 7, 0), (0, 100, 100)):
+                assert L.muon_linear_plan(m, n, k, dtype, kind, ctypes.byref(p)) == 0
+                empty = {0: m and n, 1: m and k, 2: n and k}[kind] == 0
+                assert (tuple(p) == (0, 0, 0, 0)) == empty
+            for m, n, k in ((1 << 30, 64, 64), (64, 1 << 22, 64), (1 << 20, 1 << 15, 1 << 20), (1, 1, 1 << 30)):
+                assert L.muon_linear_plan(m, n, k, dtype, kind, ctypes.byref(p)) == 0 and p[2] >= 1
