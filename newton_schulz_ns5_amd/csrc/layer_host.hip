@@ -228,6 +228,7 @@ Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
   for (int i = 0; i < n; ++i) {
     const TileCost& c = costs[i];
     const int64_t tiles = cdiv(M, c.bm) * cdiv(N, c.bn);
+    if (tiles >= (int64_t)1 << 23) continue;  // a launch has fewer than 2^32 threads, of up to 512 per tile
     for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
       // chunks of at least two slices, and at most two rounds of them
       if (split > 1 && (split > slices / 2 || tiles * split > 2 * c.slots)) break;

@@ -503,3 +503,19 @@ def test_plan_of_empty_and_largest_sizes():
                 assert (tuple(p) == (0, 0, 0, 0)) == empty
             for m, n, k in ((1 << 30, 64, 64), (64, 1 << 22, 64), (1 << 20, 1 << 15, 1 << 20), (1, 1, 1 << 30)):
                 assert L.muon_linear_plan(m, n, k, dtype, kind, ctypes.byref(p)) == 0 and p[2] >= 1
+
+
+def test_no_grid_passes_2_32_threads():
+    """An fp32 product of 2^30 rows by 8 columns (34 GB) chose more 64-edge tiles than a launch has threads."""
+    L, p = _lib.lib(), (ctypes.c_int32 * 4)()
+    threads = {(256, 256): 512, (256, 128): 512, (128, 128): 256, (64, 64): 256}
+    for dtype in (0, 1):
+        for kind in range(3):
+            for m in ((1 << 30), (1 << 30) - 64, 1 << 29, (1 << 28) + 1):
+                for n in (1, 8, 64):
+                    a, b, c = (m, n, 8) if kind != 2 else (8, m, n)
+                    if L.muon_linear_plan(a, b, c, dtype, kind, ctypes.byref(p)) or not p[0]:
+                        continue
+                    M, N = {0: (a, b), 1: (a, c), 2: (b, c)}[kind]
+                    tiles = -(-M // p[0]) * -(-N // p[1]) * p[2]
+                    assert tiles * threads[p[0], p[1]] < 1 << 32, (dtype, kind, m, n, tuple(p))
