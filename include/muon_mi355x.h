@@ -481,7 +481,8 @@ int muon_rope_backward(const muon_qk_problem* p, void* stream);
 #define MUON_K_APPLY 7      /* weight update (or NorMuon in-place scaling) */
 #define MUON_K_COUNT 8
 
-/* When enabled, every launch is bracketed by HIP events on its stream, and
+/* When enabled, every launch of Newton-Schulz, NorMuon and the step (the
+ * classes above) is bracketed by HIP events on its stream, and
  * the launch count, summed event time and summed algorithmic FLOPs and bytes
  * are kept per kernel class.  Off by default; enabling or disabling clears
  * nothing.  Reading synchronizes on the recorded events. */

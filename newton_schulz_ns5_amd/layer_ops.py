@@ -280,8 +280,10 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
 
     ``preact`` is the pre-activation that linear returned (needed with an
     activation).  ``dw_dtype`` and ``dbias_dtype`` default to w's type;
-    bf16 and fp32 are both what a step takes as a gradient.  Given outputs are
-    written in place, and with ``accumulate`` dw and dbias are added to.
+    bf16 and fp32 are both what a step takes as a gradient; in fp32 they have
+    its precision, which with bf16 operands behind an activation takes a second
+    product.  Given outputs are asked for by being given, and written in place;
+    with ``accumulate`` dw and dbias are added to.
     """
     _refuse_tangents(dy, x, w, preact)
     act = _act(activation)
