@@ -187,7 +187,7 @@ Operand operand(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t d
 //   6144 x 4096 over 2048    104  101  121  158   96
 //   2048 x 4096 over 6144    129   91  112  161
 //   1037 x 1001 over 2056      -   22*  23*   18      * split, with its addition
-struct Tiling { LinTile first, rest; int64_t m1, n1; int split; };
+struct Tiling { LinTile first, rest; int64_t m1, n1; int split; double us; };  // us: by the model above
 
 //
 // fp32 64-edge tiles, four to a CU: the last round takes as long as its fullest
@@ -223,7 +223,7 @@ Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
   const TileCost* costs = bf ? kCostBf16 : kCostF32;
   const int n = bf ? 4 : 2;
   const int64_t slices = std::max<int64_t>(1, cdiv(K, bf ? 64 : 32));
-  Tiling best{kTile64, kTile64, M, N, 1};
+  Tiling best{kTile64, kTile64, M, N, 1, 0};
   double least = 1e30;
   for (int i = 0; i < n; ++i) {
     const TileCost& c = costs[i];
@@ -236,7 +236,7 @@ Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
       if (split > 1) t += 4.0 + (double)(M * N) * 4.0 * (split + 1) / 4e6;  // a launch, and the products at 4 TB/s
       if (t < least) {
         least = t;
-        best = {c.tile, c.tile, M, N, split};
+        best = {c.tile, c.tile, M, N, split, t};
       }
     }
   }
@@ -247,12 +247,12 @@ Tiling choose_tiling(int64_t M, int64_t N, int64_t K, bool bf) {
       const double t = tile_time(kCostBf16[0], cols * tm, slices) + tile_time(kCostBf16[1], tm * cdiv(N - cols * 256, 128), slices);
       if (t < least) {
         least = t;
-        best = {kTile256, kTile256x128, M, cols * 256, 1};
+        best = {kTile256, kTile256x128, M, cols * 256, 1, t};
       }
     }
     if (rows > 0 && rows < tm) {
       const double t = tile_time(kCostBf16[0], rows * tn, slices) + tile_time(kCostBf16[1], (tm - rows) * cdiv(N, 128), slices);
-      if (t < least) best = {kTile256, kTile256x128, rows * 256, N, 1};
+      if (t < least) best = {kTile256, kTile256x128, rows * 256, N, 1, t};
     }
   }
   return best;
@@ -318,8 +318,9 @@ hipError_t run_product(LinGemm g, int32_t dt, LinKind kind, const Tiling& t, cha
   return e;
 }
 
-// Few rows: weight rows per workgroup / 16 through nb, and the chunks of K.
-int few_rows(int64_t m, int64_t n, int64_t k, int32_t dtype, int& nb) {
+// Few rows: weight rows per workgroup / 16 through nb, and the chunks of K;
+// `us` receives the time of an fp32 product.
+int few_rows(int64_t m, int64_t n, int64_t k, int32_t dtype, int& nb, double& us) {
   // Workgroups of 64 weight rows read the tokens least often; of 16, the weight
   // with the most workgroups.  Chunks of K, of two steps per wave at least,
   // make up to the 256 CUs' worth of either, and cost a second launch (4 us).
@@ -332,11 +333,33 @@ int few_rows(int64_t m, int64_t n, int64_t k, int32_t dtype, int& nb) {
   // chip of them with one.
   const bool many = m > 16 || (m > 8 && wide >= 80);
   nb = wide >= 192 || (many && wide * split4 >= 128) ? 4 : 1;
-  if (nb == 4) return wide >= 192 ? 1 : (int)split4;
+  if (nb == 4) {
+    // a workgroup per CU; its eight waves take a step each at once, which takes
+    // so many us by the blocks of 16 tokens (fp32)
+    const double step[] = {2.9, 4.0, 5.5, 6.5};
+    const int64_t split = wide >= 192 ? 1 : split4;
+    us = 5 + (double)(cdiv(wide * split, 256) * cdiv(cdiv(steps, split), 8)) * step[(m - 1) / 16] + (split > 1 ? 4 : 0);
+    return (int)split;
+  }
   // a wave's time per step grows with the tokens; the steps that a split
   // saves it are worth more than the launch
   const double per_step = 0.4 + (double)m / 40, saved = (double)steps / 8 * (1 - 1.0 / (double)split1) * per_step;
-  return saved > 6 ? (int)split1 : 1;
+  const int64_t split = saved > 6 ? split1 : 1;
+  us = 5 + (double)cdiv(steps, split * 8) * per_step + (split > 1 ? 4 : 0);
+  return (int)split;
+}
+
+// fp32, 17 to 64 rows: whether the tiles are faster.  They read the weight at
+// 2.4 TB/s at most with so few rows, and pad the rows to 64; the few-row kernel
+// multiplies rows padded to 16, one step per wave at a time.  us, few-row
+// kernel and tiles, at 24, 40 and 64 rows:
+//   9472 x 2504    45 37   59 38   77 39
+//   6144 x 4096    39 34   52 35   61 36
+//   1024 x 8192    22 18   27 18   32 18
+//   4096 x 4096    25 34   31 34   37 35
+//   14336 x 4096   67 106  92 107  108 107
+bool tiles_for_few(int64_t m, int64_t n, int64_t k, int32_t dtype, const Tiling& t, double few_us) {
+  return dtype == MUON_F32 && m > 16 && 1.1 * std::max(t.us, (double)n * (double)k * 4 / 2.4e6) < few_us;
 }
 
 // Work of a forward call: the small kernel for few rows, else tiles.
@@ -352,14 +375,23 @@ LinearPlan plan_linear(const muon_linear_problem* q) {
   LinearPlan P{};
   P.small = q->m <= kSmallRows;
   if (q->m == 0 || q->n == 0) return P;
-  if (P.small) {
-    P.t.split = few_rows(q->m, q->n, q->k, q->dtype, P.nb);
-    P.total = part_bytes(q->m, q->n, P.t.split);
-    return P;
-  }
   P.x = operand(q->x, q->m, q->k, q->x_row_stride, q->dtype, true);
   P.w = operand(q->w, q->n, q->k, q->w_row_stride, q->dtype, true);
-  P.t = choose_tiling(q->m, q->n, q->k, q->dtype == MUON_BF16);
+  if (P.small) {
+    double us = 0;
+    const int split = few_rows(q->m, q->n, q->k, q->dtype, P.nb, us);
+    if (q->dtype == MUON_F32 && q->m > 16 && !P.x.pack && !P.w.pack) {
+      P.t = choose_tiling(q->m, q->n, q->k, false);
+      P.small = !tiles_for_few(q->m, q->n, q->k, q->dtype, P.t, us);
+    }
+    if (P.small) {
+      P.t.split = split;
+      P.total = part_bytes(q->m, q->n, split);
+      return P;
+    }
+  } else {
+    P.t = choose_tiling(q->m, q->n, q->k, q->dtype == MUON_BF16);
+  }
   size_t off = 0;
   P.x.off = off; off += pack_bytes(P.x, q->dtype);
   P.w.off = off; off += pack_bytes(P.w, q->dtype);
@@ -484,13 +516,16 @@ int muon_linear_plan(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t kin
   const int64_t M = kind == 2 ? n : m, N = kind == 0 ? n : k, K = kind == 0 ? k : (kind == 1 ? n : m);
   for (int i = 0; i < 4; ++i) plan[i] = 0;  // an empty output runs nothing
   if (M == 0 || N == 0) return ok();
+  const Tiling t = choose_tiling(M, N, K, dtype == MUON_BF16);
   if (kind == 0 && m <= kSmallRows) {
     int nb = 1;
-    plan[2] = few_rows(m, n, k, dtype, nb);
-    plan[1] = 16 * nb;
-    return ok();
+    double us = 0;
+    const int split = few_rows(m, n, k, dtype, nb, us);
+    if (k % per16(dtype) || !tiles_for_few(m, n, k, dtype, t, us)) {
+      plan[1] = 16 * nb; plan[2] = split;
+      return ok();
+    }
   }
-  const Tiling t = choose_tiling(M, N, K, dtype == MUON_BF16);
   const int edge[4][2] = {{256, 256}, {256, 128}, {128, 128}, {64, 64}};
   plan[0] = edge[t.first][0]; plan[1] = edge[t.first][1]; plan[2] = t.split; plan[3] = t.m1 < M || t.n1 < N;
   return ok();

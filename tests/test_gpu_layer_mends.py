@@ -334,7 +334,7 @@ def test_axes_sections_and_numbers_that_are_not():
 
 # ---- few rows times narrow weights: 16 or 64 weight rows per workgroup, K divided over workgroups --------
 FEW_ROWS = [(m, k, n) for m in (1, 5, 16, 17, 33, 40, 49, 64)
-            for k, n in ((8200, 70), (14336, 512), (13973, 37), (6016, 2051), (4160, 5100), (12300, 100))]
+            for k, n in ((8200, 70), (14336, 512), (13973, 37), (6016, 2051), (4160, 5100), (4161, 5100), (12300, 100))]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])

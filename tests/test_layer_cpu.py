@@ -519,3 +519,13 @@ def test_no_grid_passes_2_32_threads():
                     M, N = {0: (a, b), 1: (a, c), 2: (b, c)}[kind]
                     tiles = -(-M // p[0]) * -(-N // p[1]) * p[2]
                     assert tiles * threads[p[0], p[1]] < 1 << 32, (dtype, kind, m, n, tuple(p))
+
+
+def test_fp32_few_rows_take_the_faster_kernel():
+    """Both measured, few-row kernel and tiles: 59 and 38 us, 52 and 35 us, 32 and 18 us, 92 and 107 us at the first four."""
+    L, p = _lib.lib(), (ctypes.c_int32 * 4)()
+    for m, n, k, tiles in ((40, 9472, 2504, True), (40, 6144, 4096, True), (64, 1024, 8192, True), (40, 14336, 4096, False),
+                           (24, 4096, 4096, False), (16, 9472, 2504, False), (40, 9472, 2501, False)):
+        assert L.muon_linear_plan(m, n, k, 0, 0, ctypes.byref(p)) == 0
+        assert (p[0] > 0) == tiles, (m, n, k, tuple(p))
+    assert L.muon_linear_plan(40, 9472, 2504, 1, 0, ctypes.byref(p)) == 0 and p[0] == 0  # bf16 as before
