@@ -88,25 +88,33 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)  # tensors on a GPU: it is initialised
 
 
-def _call(dev, fn, problem, need):
+def _call(dev, fn, problem, need, likely=False):
     """Run fn(problem[, workspace]) on the device's current stream.  The device
-    is made current for the launch when another one is."""
+    is made current for the launch when another one is.  likely: the call will
+    want a workspace."""
     if dev != _current_device():
         with torch.cuda.device(dev):
-            return _call_here(dev, fn, problem, need)
-    return _call_here(dev, fn, problem, need)
+            return _call_here(dev, fn, problem, need, likely)
+    return _call_here(dev, fn, problem, need, likely)
 
 
-def _call_here(dev, fn, problem, need):
+_NO_WORKSPACE = 256  # an aligned address that stands for an empty workspace
+
+
+def _call_here(dev, fn, problem, need, likely):
     if need is None:
         return _lib.check(fn(problem, _raw_stream(dev)))
+    if not likely:
+        # Most small calls need no workspace: an empty one is offered first, and the
+        # library, which enqueues nothing without what it needs, says if it is too small.
+        status = fn(problem, _NO_WORKSPACE, 0, _raw_stream(dev))
+        if status != _lib.MUON_ERR_WORKSPACE:
+            return _lib.check(status)
     size = ctypes.c_size_t(0)
     _lib.check(need(problem, ctypes.byref(size)))
-    if not size.value:
-        return _lib.check(fn(problem, None, 0, _raw_stream(dev)))
     # Taken from torch's allocator for this call: it goes back to the stream that
     # runs the call, and one taken under capture belongs to that graph alone.
-    ws = torch.empty(size.value, dtype=torch.uint8, device=torch.device("cuda", dev))
+    ws = torch.empty(max(size.value, 1), dtype=torch.uint8, device=torch.device("cuda", dev))
     return _lib.check(fn(problem, ws.data_ptr(), size.value, _raw_stream(dev)))
 
 
@@ -125,12 +133,12 @@ def _rows(t, name, cols=None):
                 t.new_empty((t.shape[:-1].numel(), 0))
         except RuntimeError:
             raise _Uneven(_lib.MUON_ERR_INVALID_ARG, f"the leading dimensions of {name} cannot be seen as one")
-    r, c = t.shape
+    (r, c), (row, col) = t.shape, t.stride()
     if cols is not None and c != cols:
         _bad(f"{name} has {c} columns, not {cols}")
-    if r and c > 1 and t.stride(1) != 1:
+    if col != 1 and r and c > 1:
         _bad(f"{name} needs unit column stride")
-    return t.data_ptr(), r, c, (t.stride(0) if r > 1 and c else c)
+    return t.data_ptr(), r, c, (row if r > 1 and c else c)
 
 
 # Elements that rows may be apart for the library (2^23 - 32 bytes).
@@ -180,9 +188,13 @@ def _refuse_capture():
                         "autograd is not recorded under stream capture: call the *_backward entry point there")
 
 
+# Where the level of forward-mode differentiation stands (below 0: none is open).
+_dual = vars(_forward_ad) if "_current_level" in vars(_forward_ad) else {"_current_level": 0}
+
+
 def _refuse_tangents(*ts):
     """These operators have no forward-mode derivative: a result would silently come without its tangent."""
-    if getattr(_forward_ad, "_current_level", 0) >= 0:
+    if _dual["_current_level"] >= 0:
         for t in ts:
             if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
                 raise MuonError(_lib.MUON_ERR_UNSUPPORTED, "forward-mode automatic differentiation is not supported")
@@ -190,7 +202,8 @@ def _refuse_tangents(*ts):
 
 def _wants_grad(*ts):
     """Whether to record the call for autograd."""
-    _refuse_tangents(*ts)
+    if _dual["_current_level"] >= 0:
+        _refuse_tangents(*ts)
     if torch.is_grad_enabled():
         for t in ts:
             if t is not None and t.requires_grad:
@@ -319,7 +332,7 @@ def linear_backward(dy, x, w, *, activation=None, preact=None, need_dx=True, nee
                       _dt(dy), _dt(dx) if dx is not None else 0, _dt(dw) if dw is not None else 0,
                       _dt(dbias) if dbias is not None else 0, int(bool(accumulate)), 0)
     L = _lib.lib()
-    _call(dev, L.muon_linear_backward, prob, L.muon_linear_backward_workspace_bytes)
+    _call(dev, L.muon_linear_backward, prob, L.muon_linear_backward_workspace_bytes, act != 0 or dbias is not None)
     if given:
         _written(*given)
     return dx, dw, dbias
@@ -528,7 +541,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, *, q_weight
             if t is not None:
                 t.zero_()
     L = _lib.lib()
-    _call(dev, L.muon_qk_norm_rope_backward, p, L.muon_qk_norm_rope_backward_workspace_bytes)
+    _call(dev, L.muon_qk_norm_rope_backward, p, L.muon_qk_norm_rope_backward_workspace_bytes, True)
     if given:
         _written(*given)
     return y + dwt
