@@ -341,10 +341,11 @@ int few_rows(int64_t m, int64_t n, int64_t k, int32_t dtype, int& nb, double& us
     us = 5 + (double)(cdiv(wide * split, 256) * cdiv(cdiv(steps, split), 8)) * step[(m - 1) / 16] + (split > 1 ? 4 : 0);
     return (int)split;
   }
-  // a wave's time per step grows with the tokens; the steps that a split
-  // saves it are worth more than the launch
-  const double per_step = 0.4 + (double)m / 40, saved = (double)steps / 8 * (1 - 1.0 / (double)split1) * per_step;
-  const int64_t split = saved > 6 ? split1 : 1;
+  // A wave's time per step grows with the tokens.  A split pays where the steps
+  // it saves are worth more than its launch, and the call takes longer than one
+  // of two launches from Python, workspace included (13 us).
+  const double per_step = 0.4 + (double)m / 40, whole = 5 + (double)steps / 8 * per_step;
+  const int64_t split = whole > 16 && (whole - 5) * (1 - 1.0 / (double)split1) > 6 ? split1 : 1;
   us = 5 + (double)cdiv(steps, split * 8) * per_step + (split > 1 ? 4 : 0);
   return (int)split;
 }

@@ -279,7 +279,7 @@ def _linear(x, w, bias, residual, activation, return_preact, out=None, preact=No
     prob = _LINEAR.pack(m, n, k, code, act, xp, ldx, wp, ldw, bp, rp, ldr, yp, ldy, zp, ldz,
                         _dt(bias) if bias is not None else 0, _dt(residual) if residual is not None else 0, _dt(out), 0)
     L = _lib.lib()
-    _call(dev, L.muon_linear, prob, L.muon_linear_workspace_bytes)
+    _call(dev, L.muon_linear, prob, L.muon_linear_workspace_bytes, m > 64)  # copies, or a divided sum
     if given:
         _written(*given)
     return (out, preact) if return_preact else out
