@@ -370,12 +370,11 @@ int muon_linear_workspace_bytes(const muon_linear_problem* p, size_t* bytes);
  * MUON_ERR_WORKSPACE, MUON_ERR_HIP. */
 int muon_linear(const muon_linear_problem* p, void* workspace, size_t workspace_bytes, void* stream);
 
-/* How a product of these sizes runs, its rows dense and, if k allows it, 16-byte
- * aligned; for tests and tuning.  kind 0: the forward product, 1: the input
- * gradient, 2: the weight gradient.  plan receives rows and columns of the
- * output per workgroup (the kernel of few forward rows: 0 and the weight rows),
- * the chunks its sum is divided into, and 1 where a last round of smaller tiles
- * follows; zeros for an empty output. */
+/* How a product of these sizes runs, for tests and tuning.  kind 0: the forward
+ * product, 1: the input gradient, 2: the weight gradient.  plan receives rows
+ * and columns of the output per workgroup (the kernel of few forward rows: 0 and
+ * the weight rows), the chunks its sum is divided into, and 1 where a last round
+ * of smaller tiles follows; zeros for an empty output. */
 int muon_linear_plan(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t kind, int32_t plan[4]);
 
 /* Gradients of muon_linear.  With g = dy act'(preact):

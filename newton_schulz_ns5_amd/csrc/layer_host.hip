@@ -352,15 +352,18 @@ int few_rows(int64_t m, int64_t n, int64_t k, int32_t dtype, int& nb, double& us
 
 // fp32, 17 to 64 rows: whether the tiles are faster.  They read the weight at
 // 2.4 TB/s at most with so few rows, and pad the rows to 64; the few-row kernel
-// multiplies rows padded to 16, one step per wave at a time.  us, few-row
-// kernel and tiles, at 24, 40 and 64 rows:
+// multiplies rows padded to 16, one step per wave at a time, and takes a K that
+// is not whole chunks without a copy.  By the sizes alone, so that a result
+// does not depend on its operands' alignment.  us, few-row kernel and tiles, at
+// 24, 40 and 64 rows:
 //   9472 x 2504    45 37   59 38   77 39
 //   6144 x 4096    39 34   52 35   61 36
 //   1024 x 8192    22 18   27 18   32 18
 //   4096 x 4096    25 34   31 34   37 35
 //   14336 x 4096   67 106  92 107  108 107
 bool tiles_for_few(int64_t m, int64_t n, int64_t k, int32_t dtype, const Tiling& t, double few_us) {
-  return dtype == MUON_F32 && m > 16 && 1.1 * std::max(t.us, (double)n * (double)k * 4 / 2.4e6) < few_us;
+  return dtype == MUON_F32 && m > 16 && k % per16(dtype) == 0 &&
+         1.1 * std::max(t.us, (double)n * (double)k * 4 / 2.4e6) < few_us;
 }
 
 // Work of a forward call: the small kernel for few rows, else tiles.
@@ -381,7 +384,7 @@ LinearPlan plan_linear(const muon_linear_problem* q) {
   if (P.small) {
     double us = 0;
     const int split = few_rows(q->m, q->n, q->k, q->dtype, P.nb, us);
-    if (q->dtype == MUON_F32 && q->m > 16 && !P.x.pack && !P.w.pack) {
+    if (q->dtype == MUON_F32 && q->m > 16) {
       P.t = choose_tiling(q->m, q->n, q->k, false);
       P.small = !tiles_for_few(q->m, q->n, q->k, q->dtype, P.t, us);
     }
@@ -522,7 +525,7 @@ int muon_linear_plan(int64_t m, int64_t n, int64_t k, int32_t dtype, int32_t kin
     int nb = 1;
     double us = 0;
     const int split = few_rows(m, n, k, dtype, nb, us);
-    if (k % per16(dtype) || !tiles_for_few(m, n, k, dtype, t, us)) {
+    if (!tiles_for_few(m, n, k, dtype, t, us)) {
       plan[1] = 16 * nb; plan[2] = split;
       return ok();
     }

@@ -435,3 +435,21 @@ def test_inputs_that_share_rows_or_are_unevenly_spaced():
         with pytest.raises(ns.MuonError) as e:
             bad()
         assert e.value.status == -1
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_bits_do_not_depend_on_alignment(dtype):
+    """Views of odd strides and addresses give the bits of dense operands, whichever kernel their sizes choose."""
+    torch_cuda()
+
+    def odd(t):
+        buf = torch.zeros(t.shape[0], t.shape[1] + 3, dtype=t.dtype, device="cuda")
+        buf[:, 1:1 + t.shape[1]] = t
+        return buf[:, 1:1 + t.shape[1]]
+
+    for m, k, n in ((3, 256, 200), (24, 2504, 9472), (40, 4096, 1100), (64, 8192, 1024), (70, 264, 520), (300, 1000, 2000)):
+        x, w, dy = rand((m, k), dtype, 1), rand((n, k), dtype, 2), rand((m, n), dtype, 3)
+        want = ns.linear(x, w)
+        assert torch.equal(ns.linear(odd(x), w), want) and torch.equal(ns.linear(x, odd(w)), want)
+        a, b = ns.linear_backward(dy, x, w), ns.linear_backward(odd(dy), odd(x), odd(w))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
