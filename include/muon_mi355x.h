@@ -468,6 +468,36 @@ int muon_qk_norm_rope_backward(const muon_qk_problem* p, void* workspace, size_t
 int muon_rope(const muon_qk_problem* p, void* stream);
 int muon_rope_backward(const muon_qk_problem* p, void* stream);
 
+/* ---- the norm over all gradients, and clipping ------------------------------- */
+
+#define MUON_NORM_2 0    /* sqrt of the sum of squares */
+#define MUON_NORM_MAX 1  /* the largest magnitude; a NaN anywhere gives NaN */
+
+/* The norm over n tensors (0..2^20) of numel[i] contiguous elements each, of
+ * MUON_F32 or MUON_BF16.  x, x_dtype and numel are host arrays.  Tensors need
+ * only be aligned to their element size; empty ones are left out.
+ * norm (may be NULL) receives the norm in fp32, square (MUON_NORM_2, may be
+ * NULL) the sum of squares in fp64, which is what ranks that hold different
+ * gradients add up.  Squares are formed and added in fp64, in an order that
+ * depends on the sizes only. */
+int muon_grad_norm_workspace_bytes(int64_t n, const int64_t* numel, size_t* bytes);
+int muon_grad_norm(int64_t n, const void* const* x, const int32_t* x_dtype, const int64_t* numel, int32_t kind,
+                   float* norm, double* square, void* workspace, size_t workspace_bytes, void* stream);
+
+/* y[i] = f x[i] with f = 1 where max_norm >= N + eps, else max_norm / (N + eps)
+ * (formed in fp64, applied in fp32, one rounding on store).  N is the norm of
+ * the call's tensors, or that of `total` (device memory): the norm itself
+ * (fp32), or with total_f64 the sum of squares (MUON_NORM_2); then no
+ * workspace is needed.  norm (may be NULL) receives N.  A NaN norm makes every
+ * y NaN; an infinite one zero (NaN where x is infinite), unless max_norm is
+ * infinite.  y[i] may be x[i] itself (of the same type), and is then not
+ * written where f is 1; any other overlap of an output with a tensor of the
+ * call is refused, the same tensor twice among them. */
+int muon_clip_grad_norm(int64_t n, const void* const* x, const int32_t* x_dtype, const int64_t* numel,
+                        void* const* y, const int32_t* y_dtype, int32_t kind, double max_norm, double eps,
+                        const void* total, int32_t total_f64, float* norm,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- launch timing ------------------------------------------------------ */
 
 /* Kernel classes the library launches. */

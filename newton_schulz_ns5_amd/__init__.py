@@ -26,7 +26,9 @@ Entry points (same names as the C ABI):
   form a step takes);
 * ``qk_norm_rope``, ``rope`` and their ``_backward`` -- per-head norms of queries
   and keys with the position rotation (one or several axes) in the same pass,
-  and the rotation alone.
+  and the rotation alone;
+* ``grad_norm``, ``clip_grad_norm`` -- the norm over all gradients and their
+  clipping (``MuonNS5.clip_grad_norm`` for an optimizer's own).
 """
 import ctypes
 import math
@@ -497,6 +499,14 @@ class MuonNS5:
                     if st[k] is not None:
                         st[k].copy_(e[k])
 
+    def clip_grad_norm(self, max_norm, *, extra=(), norm_type=2, eps=1e-6, total=None):
+        """Clip the gradients of this optimizer's parameters, and the gradient tensors of ``extra`` with them
+        (those of parameters that another optimizer steps), by the norm of all of them; returns the norm.
+        ``total`` as for :func:`clip_grad_norm`, whose other rules hold too."""
+        from .pass_ops import clip_grad_norm
+        return clip_grad_norm([p.grad for p in self.params] + list(extra), max_norm, norm_type=norm_type, eps=eps,
+                              total=total)
+
     def step(self):
         torch = _torch()
         todo = []
@@ -553,16 +563,22 @@ def profile_query(kernel_class):
     return {"launches": n.value, "ms": ms.value, "flop": fl.value, "bytes": by.value}
 
 
-# ---- layer operators ---------------------------------------------------------------
-_LAYER_OPS = ("linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward", "ACTIVATIONS")
+# ---- layer operators and those around them in a pass -----------------------------------
+_TORCH_OPS = {
+    "layer_ops": ("linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward",
+                  "ACTIVATIONS"),
+    "pass_ops": ("grad_norm", "clip_grad_norm"),
+}
 
 
 def __getattr__(name):
-    # The layer operators are defined with torch (autograd functions), which
-    # this module itself imports on first use only.
-    if name in _LAYER_OPS:
-        from . import layer_ops
-        for n in _LAYER_OPS:
-            globals()[n] = getattr(layer_ops, n)
-        return globals()[name]
+    # These operators are defined with torch (autograd functions), which this
+    # module itself imports on first use only.
+    for module, names in _TORCH_OPS.items():
+        if name in names:
+            import importlib
+            m = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -19,6 +19,9 @@ MUON_ERR_HIP = -4
 MUON_F32 = 0
 MUON_BF16 = 1
 
+MUON_NORM_2 = 0
+MUON_NORM_MAX = 1
+
 KERNEL_CLASSES = ("prep", "norm", "gram", "poly", "update", "rowstat", "rho", "apply")
 MUON_K_UPDATE = 4
 
@@ -122,6 +125,10 @@ SIGNATURES = {
     "muon_qk_norm_rope_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "muon_rope": (c_i32, [c_vp, c_vp]),
     "muon_rope_backward": (c_i32, [c_vp, c_vp]),
+    "muon_grad_norm_workspace_bytes": (c_i32, [c_i64, c_vp, ctypes.POINTER(c_sz)]),
+    "muon_grad_norm": (c_i32, [c_i64, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "muon_clip_grad_norm": (c_i32, [c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_f64, c_f64, c_vp, c_i32, c_vp, c_vp,
+                                    c_sz, c_vp]),
     "muon_profile_enable": (c_i32, [c_i32]),
     "muon_profile_classes": (c_i32, [ctypes.c_uint32]),
     "muon_profile_reset": (c_i32, []),

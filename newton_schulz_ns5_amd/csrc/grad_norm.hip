@@ -1,0 +1,232 @@
+// The norm over all gradients and their clipping:
+//   N = sqrt(sum over tensors of sum g^2), or the largest |g|;
+//   y = f g, f = 1 where max_norm >= N + eps, else max_norm / (N + eps).
+//
+// Bound by HBM: the norm reads every gradient once, clipping reads them again
+// and writes them.  Squares are added in fp64, so that neither values whose
+// squares leave fp32's range nor the length of the sum cost digits; the matrix
+// units and fp32 would not be faster, since the loads bound it.  The order of
+// the additions depends on the sizes alone: lanes, waves and workgroups take
+// fixed items, and the partials are added in order.
+#include "linear_epilogue.h"
+#include "pass_internal.h"
+
+namespace muon {
+namespace {
+
+constexpr int NT = 256;
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const uint32_t o = __shfl_xor(v, off, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// The tensor that holds an item, and the item's first element in it.
+__device__ __forceinline__ int find_item(const TensorList& l, int item, int64_t& first) {
+  int lo = 0, hi = l.n - 1;  // the first i with end[i] > item
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (l.end[mid] > item) hi = mid;
+    else lo = mid + 1;
+  }
+  first = (int64_t)(item - (lo ? l.end[lo - 1] : 0)) * kListItem;
+  return lo;
+}
+__device__ __forceinline__ bool bit(const uint64_t* words, int i) { return (words[i >> 6] >> (i & 63)) & 1; }
+
+// What a lane adds up: squares, or the largest pattern of a magnitude (a NaN's
+// is larger than infinity's, so a NaN stays).
+template <bool MAX>
+struct Acc {
+  double sum[2] = {0.0, 0.0};
+  uint32_t top = 0;
+  __device__ __forceinline__ void add(float v, int e) {
+    if constexpr (MAX) {
+      const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+      top = b > top ? b : top;
+    } else {
+      const double d = (double)v;
+      sum[e & 1] = fma(d, d, sum[e & 1]);
+    }
+  }
+};
+
+template <bool MAX, bool BF>
+__device__ __forceinline__ void add_item(const void* base, int64_t first, int64_t n, int lane, Acc<MAX>& acc) {
+  constexpr int W = BF ? 8 : 4;            // elements of a 16-byte load
+  constexpr int U = 8;                     // loads in flight
+  const char* const p = (const char*)base + first * (BF ? 2 : 4);
+  auto use = [&](u32x4 a) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if constexpr (BF) {
+        acc.add(__uint_as_float(a[w] << 16), 0);
+        acc.add(__uint_as_float(a[w] & 0xffff0000u), 1);
+      } else {
+        acc.add(__uint_as_float(a[w]), w);
+      }
+    }
+  };
+  if (n >= kListItem) {
+#pragma unroll
+    for (int r = 0; r < kListItem / (64 * W * U); ++r) {
+      u32x4 a[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) a[u] = load16(p + (int64_t)((r * U + u) * 64 + lane) * 16);
+#pragma unroll
+      for (int u = 0; u < U; ++u) use(a[u]);
+    }
+    return;
+  }
+  const int whole = (int)n / W;
+  for (int v = lane; v < whole; v += 64) use(load16(p + (int64_t)v * 16));
+  for (int e = whole * W + lane; e < n; e += 64) acc.add(load_elem(p, e, BF), 0);
+}
+
+template <bool MAX>
+__global__ __launch_bounds__(NT) void norm_partial_kernel(const NormPartial p) {
+  __shared__ uint64_t red[NT / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  Acc<MAX> acc;
+  for (int item = __builtin_amdgcn_readfirstlane((int)blockIdx.x * (NT / 64) + wave); item < p.list.items; item += gridDim.x * (NT / 64)) {
+    int64_t first;
+    const int t = find_item(p.list, item, first);
+    const int64_t left = p.list.numel[t] - first;
+    if (bit(p.list.x_bf16, t)) add_item<MAX, true>(p.list.x[t], first, left, lane, acc);
+    else add_item<MAX, false>(p.list.x[t], first, left, lane, acc);
+  }
+  uint64_t v;
+  if constexpr (MAX) v = wave_max(acc.top);
+  else v = __builtin_bit_cast(uint64_t, wave_sum64(acc.sum[0] + acc.sum[1]));
+  if (lane == 0) red[wave] = v;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if constexpr (MAX) {
+#pragma unroll
+      for (int w = 1; w < NT / 64; ++w) v = red[w] > v ? red[w] : v;
+    } else {
+      double t = __builtin_bit_cast(double, v);
+#pragma unroll
+      for (int w = 1; w < NT / 64; ++w) t += __builtin_bit_cast(double, red[w]);
+      v = __builtin_bit_cast(uint64_t, t);
+    }
+    p.partial[blockIdx.x] = v;
+  }
+}
+
+// The norm, the same in every thread of the workgroup; the sum of squares
+// through `square` (kind 2 only).
+__device__ __forceinline__ double total_norm(const NormTotal& p, double& square) {
+  __shared__ uint64_t red[NT / 64];
+  square = 0.0;
+  if (p.total) {
+    if (!p.total_f64) return (double)*(const float*)p.total;
+    square = *(const double*)p.total;
+    return sqrt(square);
+  }
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (p.max_norm_kind) {
+    uint32_t top = 0;
+    for (int64_t i = threadIdx.x; i < p.count; i += NT) {
+      const uint32_t b = (uint32_t)p.partial[i];
+      top = b > top ? b : top;
+    }
+    top = wave_max(top);
+    if (lane == 0) red[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) top = (uint32_t)red[w] > top ? (uint32_t)red[w] : top;
+    return (double)__uint_as_float(top);
+  }
+  double t = 0.0;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x; i < p.count; i += NT) t += __builtin_bit_cast(double, p.partial[i]);
+  t = wave_sum64(t);
+  if (lane == 0) red[wave] = __builtin_bit_cast(uint64_t, t);
+  __syncthreads();
+  t = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) t += __builtin_bit_cast(double, red[w]);
+  square = t;
+  return sqrt(t);
+}
+
+__global__ __launch_bounds__(NT) void norm_total_kernel(const NormTotal p) {
+  double square;
+  const double norm = total_norm(p, square);
+  if (threadIdx.x == 0) {
+    if (p.norm) *p.norm = (float)norm;
+    if (p.square) *p.square = square;
+    if (p.store) *p.store = p.max_norm_kind ? __float_as_uint((float)norm) : __builtin_bit_cast(uint64_t, square);
+  }
+}
+
+template <bool XBF, bool YBF>
+__device__ __forceinline__ void scale_item(const void* x, void* y, int64_t first, int64_t n, int lane, float f) {
+  constexpr int U = 4;
+  if (n >= kListItem) {
+#pragma unroll
+    for (int r = 0; r < kListItem / (64 * 8 * U); ++r) {
+      float v[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) get8(x, first + ((r * U + u) * 64 + lane) * 8, XBF, 8, v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] *= f;
+        put8(y, first + ((r * U + u) * 64 + lane) * 8, YBF, 8, v[u]);
+      }
+    }
+    return;
+  }
+  for (int at = lane * 8; at < n; at += 64 * 8) {
+    const int valid = n - at < 8 ? (int)(n - at) : 8;
+    float v[8];
+    get8(x, first + at, XBF, valid, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= f;
+    put8(y, first + at, YBF, valid, v);
+  }
+}
+
+__global__ __launch_bounds__(NT) void clip_kernel(const ClipParams p) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double square;
+  const double norm = total_norm(p.total, square);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.total.norm) *p.total.norm = (float)norm;
+  // a NaN norm gives a NaN factor, an infinite one zero (and NaN from infinite gradients)
+  const float f = p.max_norm >= norm + p.eps ? 1.f : (float)(p.max_norm / (norm + p.eps));
+  if (f == 1.f && p.in_place) return;
+  for (int item = __builtin_amdgcn_readfirstlane((int)blockIdx.x * (NT / 64) + wave); item < p.list.items; item += gridDim.x * (NT / 64)) {
+    int64_t first;
+    const int t = find_item(p.list, item, first);
+    const int64_t left = p.list.numel[t] - first;
+    const bool xb = bit(p.list.x_bf16, t), yb = bit(p.list.y_bf16, t);
+    const void* const x = p.list.x[t];
+    void* const y = p.list.y[t];
+    if (xb && yb) scale_item<true, true>(x, y, first, left, lane, f);
+    else if (xb) scale_item<true, false>(x, y, first, left, lane, f);
+    else if (yb) scale_item<false, true>(x, y, first, left, lane, f);
+    else scale_item<false, false>(x, y, first, left, lane, f);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_norm_partial(const NormPartial& p, int blocks, hipStream_t s) {
+  return p.max_norm_kind ? launch_kernel(norm_partial_kernel<true>, dim3(blocks), p, s, NT)
+                         : launch_kernel(norm_partial_kernel<false>, dim3(blocks), p, s, NT);
+}
+hipError_t launch_norm_total(const NormTotal& p, hipStream_t s) { return launch_kernel(norm_total_kernel, dim3(1), p, s, NT); }
+hipError_t launch_clip(const ClipParams& p, int blocks, hipStream_t s) { return launch_kernel(clip_kernel, dim3(blocks), p, s, NT); }
+
+}  // namespace muon

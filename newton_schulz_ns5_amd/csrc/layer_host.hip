@@ -2,63 +2,15 @@
 // sequences of the linear product, its gradients and the per-head norms with
 // rotation.  Every argument is checked before anything is enqueued.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <algorithm>
 
+#include "host_check.h"
 #include "layer_internal.h"
 #include "muon_mi355x.h"
 
 using namespace muon;
 
 namespace {
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  return report(code, buf);
-}
-int ok() { return report(MUON_OK, ""); }
-int hip_fail(hipError_t e, const char* what) { return fail(MUON_ERR_HIP, "%s: %s", what, hipGetErrorString(e)); }
-
-bool dtype_ok(int32_t d) { return d == MUON_F32 || d == MUON_BF16; }
-int64_t esize(int32_t d) { return d == MUON_BF16 ? 2 : 4; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-int check_workspace(const void* ws, size_t have, size_t need) {
-  if (!need) return MUON_OK;
-  if (!ws) return fail(MUON_ERR_INVALID_ARG, "workspace is NULL");
-  if ((uintptr_t)ws & 255) return fail(MUON_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  if (have < need) return fail(MUON_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, have);
-  return MUON_OK;
-}
-
-// Bytes a strided set of rows reaches: rows of `width` bytes, `stride` bytes apart.
-struct Rows {
-  const char* name;
-  uintptr_t at;
-  int64_t rows, width, stride;
-};
-Rows rows_of(const char* name, const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld) {
-  return {name, (uintptr_t)p, rows, cols * esize(dt), rows > 1 ? ld * esize(dt) : cols * esize(dt)};
-}
-// Whether two sets may share a byte.  Sets with one common stride are told
-// apart by their place within it (columns of one packed buffer), others by
-// their whole extent.
-bool meet(const Rows& a, const Rows& b) {
-  if (!a.at || !b.at || !a.rows || !b.rows || !a.width || !b.width) return false;
-  const uintptr_t ae = a.at + (uintptr_t)((a.rows - 1) * a.stride + a.width);
-  const uintptr_t be = b.at + (uintptr_t)((b.rows - 1) * b.stride + b.width);
-  if (a.at >= be || b.at >= ae) return false;
-  const int64_t S = a.rows > 1 ? a.stride : b.stride;
-  if ((a.rows > 1 && b.rows > 1 && a.stride != b.stride) || a.width > S || b.width > S) return true;
-  const int64_t d = (int64_t)((a.at >= b.at ? a.at - b.at : S - (int64_t)((b.at - a.at) % (uintptr_t)S)) % (uintptr_t)S);
-  return !(d >= b.width && d + a.width <= S);
-}
 
 // ---- the linear product -------------------------------------------------------------
 // Dimensions stay below 2^30 and a row stride (rounded up to 32 bytes, as
@@ -724,10 +676,6 @@ bool meets_range(const muon_heads& t, int64_t heads, int32_t dt, const muon_qk_p
   std::sort(d, d + 3, [](const Index& a, const Index& b) { return a.stride > b.stride; });
   int tries = 4096;
   return reaches((int64_t)((uintptr_t)t.p - (uintptr_t)p), d, 3, -q->dim * e, bytes, tries);
-}
-
-bool ranges_meet(const void* a, int64_t na, const void* b, int64_t nb) {
-  return a && b && na > 0 && nb > 0 && (uintptr_t)a < (uintptr_t)b + (uintptr_t)nb && (uintptr_t)b < (uintptr_t)a + (uintptr_t)na;
 }
 
 // The outputs against the vectors: the weights, the positions, the frequencies,

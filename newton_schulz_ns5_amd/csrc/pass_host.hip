@@ -1,0 +1,245 @@
+// Host side of the operators around a layer's products: validation, workspace
+// carve-up and launch sequences of the gradient norm and clipping.  Every
+// argument is checked before anything is enqueued.
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "host_check.h"
+#include "pass_internal.h"
+
+using namespace muon;
+
+namespace {
+
+// ---- gradient norm and clipping -------------------------------------------------------
+constexpr int64_t kMaxTensors = (int64_t)1 << 20;
+constexpr int kNormBlocks = 2048;  // workgroups of a launch: eight per CU
+
+// Tensors [begin, end) of a list, one launch's: at most kListMax that are not
+// empty, and 2^30 items.
+struct ListPart { int64_t begin, end, items; };
+
+int blocks_of(int64_t items) { return (int)std::min<int64_t>(cdiv(items, 4), kNormBlocks); }
+
+// Calls f(part) for every launch of a list.
+template <class F>
+int each_part(int64_t n, const int64_t* numel, F&& f) {
+  ListPart part{0, 0, 0};
+  int held = 0;
+  auto flush = [&](int64_t at) {
+    part.end = at;
+    const int rc = part.items ? f(part) : MUON_OK;
+    part = {at, at, 0};
+    held = 0;
+    return rc;
+  };
+  for (int64_t i = 0; i < n; ++i) {
+    const int64_t items = cdiv(numel[i], kListItem);
+    if (!items) continue;
+    if (held == kListMax || part.items + items > ((int64_t)1 << 30)) {
+      const int rc = flush(i);
+      if (rc) return rc;
+    }
+    part.items += items;
+    ++held;
+  }
+  return flush(n);
+}
+
+struct ListPlan { int64_t parts = 0, partials = 0; };
+ListPlan plan_list(int64_t n, const int64_t* numel) {
+  ListPlan P;
+  each_part(n, numel, [&](const ListPart& part) {
+    ++P.parts;
+    P.partials += blocks_of(part.items);
+    return MUON_OK;
+  });
+  return P;
+}
+// The partials, and their sum behind them.
+size_t list_bytes(const ListPlan& P) { return align256((size_t)(P.partials + 1) * 8); }
+
+int check_list(int64_t n, const int64_t* numel) {
+  if (n < 0 || n > kMaxTensors) return fail(MUON_ERR_INVALID_ARG, "a list has 0 to 2^20 tensors, not %lld", (long long)n);
+  if (n && !numel) return fail(MUON_ERR_INVALID_ARG, "numel is NULL");
+  for (int64_t i = 0; i < n; ++i) {
+    if (numel[i] < 0) return fail(MUON_ERR_INVALID_ARG, "tensor %lld has a negative size", (long long)i);
+    if (numel[i] > ((int64_t)1 << 40)) return fail(MUON_ERR_INVALID_ARG, "tensor %lld has more than 2^40 elements", (long long)i);
+  }
+  return MUON_OK;
+}
+
+int check_tensors(const char* name, int64_t n, const void* const* p, const int32_t* dtype, const int64_t* numel) {
+  if (n && (!p || !dtype)) return fail(MUON_ERR_INVALID_ARG, "the pointers or types of every %s are NULL", name);
+  for (int64_t i = 0; i < n; ++i) {
+    if (!dtype_ok(dtype[i])) return fail(MUON_ERR_UNSUPPORTED, "%s %lld: dtype %d is not MUON_F32 or MUON_BF16", name, (long long)i, dtype[i]);
+    if (!numel[i]) continue;
+    if (!p[i]) return fail(MUON_ERR_INVALID_ARG, "%s %lld is NULL", name, (long long)i);
+    if ((uintptr_t)p[i] % esize(dtype[i])) return fail(MUON_ERR_INVALID_ARG, "%s %lld is not aligned to its element size", name, (long long)i);
+  }
+  return MUON_OK;
+}
+
+// No output shares a byte with another tensor or the scalars, but with its own
+// input as a whole.
+int check_apart(int64_t n, const void* const* x, const int32_t* xt, const int64_t* numel, void* const* y, const int32_t* yt,
+                const void* total, int64_t total_bytes, const void* norm) {
+  struct Span { uintptr_t lo, hi; int64_t tensor; bool out; };
+  std::vector<Span> spans;
+  spans.reserve((size_t)(2 * n + 2));
+  auto add = [&](const void* p, int64_t bytes, int64_t i, bool out) {
+    if (p && bytes) spans.push_back({(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, i, out});
+  };
+  for (int64_t i = 0; i < n; ++i) {
+    add(y[i], numel[i] * esize(yt[i]), i, true);
+    if (!(x[i] == y[i] && xt[i] == yt[i])) add(x[i], numel[i] * esize(xt[i]), i, false);
+  }
+  add(total, total_bytes, -1, false);
+  add(norm, 4, -2, true);
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  uintptr_t all = 0, outs = 0;  // ends of what came before
+  for (const Span& s : spans) {
+    if (s.lo < outs || (s.out && s.lo < all)) {
+      if (s.tensor < 0) return fail(MUON_ERR_INVALID_ARG, "%s overlaps a tensor of the call", s.tensor == -1 ? "the given total" : "norm");
+      return fail(MUON_ERR_INVALID_ARG, "%s %lld overlaps another tensor of the call", s.out ? "output" : "gradient", (long long)s.tensor);
+    }
+    all = std::max(all, s.hi);
+    if (s.out) outs = std::max(outs, s.hi);
+  }
+  return MUON_OK;
+}
+
+void fill_list(TensorList& l, const ListPart& part, const void* const* x, const int32_t* xt, void* const* y, const int32_t* yt,
+               const int64_t* numel) {
+  l = TensorList{};
+  int64_t items = 0;
+  for (int64_t i = part.begin; i < part.end; ++i) {
+    if (!numel[i]) continue;
+    const int k = l.n++;
+    l.x[k] = x[i];
+    l.numel[k] = numel[i];
+    if (xt[i] == MUON_BF16) l.x_bf16[k >> 6] |= (uint64_t)1 << (k & 63);
+    if (y) {
+      l.y[k] = y[i];
+      if (yt[i] == MUON_BF16) l.y_bf16[k >> 6] |= (uint64_t)1 << (k & 63);
+    }
+    items += cdiv(numel[i], kListItem);
+    l.end[k] = (int32_t)items;
+  }
+  l.items = (int32_t)items;
+}
+
+int check_kind(int32_t kind) {
+  if (kind != MUON_NORM_2 && kind != MUON_NORM_MAX) return fail(MUON_ERR_UNSUPPORTED, "norm kind %d is not MUON_NORM_2 or MUON_NORM_MAX", kind);
+  return MUON_OK;
+}
+
+// The partials of a list into the workspace.
+int run_partials(int64_t n, const void* const* x, const int32_t* xt, const int64_t* numel, int32_t kind, uint64_t* partial, hipStream_t s) {
+  return each_part(n, numel, [&](const ListPart& part) {
+    NormPartial p;
+    fill_list(p.list, part, x, xt, nullptr, nullptr, numel);
+    const int blocks = blocks_of(part.items);
+    p.partial = partial;
+    p.max_norm_kind = kind == MUON_NORM_MAX;
+    partial += blocks;
+    const hipError_t e = launch_norm_partial(p, blocks, s);
+    return e == hipSuccess ? MUON_OK : hip_fail(e, "gradient norm");
+  });
+}
+
+int clip(int64_t n, const void* const* x, const int32_t* xt, const int64_t* numel, void* const* y, const int32_t* yt, int32_t kind,
+         double max_norm, double eps, const void* total, int32_t total_f64, float* norm, void* workspace, size_t workspace_bytes, hipStream_t s) {
+  int rc;
+  if ((rc = check_list(n, numel)) || (rc = check_kind(kind)) || (rc = check_tensors("gradient", n, x, xt, numel)) ||
+      (rc = check_tensors("output", n, (const void* const*)y, yt, numel)))
+    return rc;
+  if (!(max_norm >= 0)) return fail(MUON_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if (!(eps >= 0) || std::isinf(eps)) return fail(MUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (total_f64 != 0 && total_f64 != 1) return fail(MUON_ERR_INVALID_ARG, "total_f64 must be 0 or 1");
+  if (total && total_f64 && kind != MUON_NORM_2) return fail(MUON_ERR_INVALID_ARG, "an fp64 total is a sum of squares, which MUON_NORM_MAX has not");
+  if ((total && (uintptr_t)total % (total_f64 ? 8 : 4)) || (uintptr_t)norm % 4) return fail(MUON_ERR_INVALID_ARG, "norm or total is not aligned to its element size");
+  if ((rc = check_apart(n, x, xt, numel, y, yt, total, total_f64 ? 8 : 4, norm))) return rc;
+  const ListPlan P = plan_list(n, numel);
+  NormTotal t{};
+  t.total = total; t.total_f64 = total_f64;
+  t.max_norm_kind = kind == MUON_NORM_MAX;
+  t.norm = norm;
+  if (!total && P.parts) {
+    if ((rc = check_workspace(workspace, workspace_bytes, list_bytes(P)))) return rc;
+    uint64_t* const partial = (uint64_t*)workspace;
+    if ((rc = run_partials(n, x, xt, numel, kind, partial, s))) return rc;
+    t.partial = partial; t.count = P.partials;
+    // The partials of one launch are added by every workgroup of the next one
+    // (one launch less); those of several once, in between.
+    if (P.parts > 1) t.store = partial + P.partials;
+  }
+  if ((t.store || !P.parts) && (t.store || norm)) {
+    const hipError_t e = launch_norm_total(t, s);
+    if (e != hipSuccess) return hip_fail(e, "gradient norm");
+    t.partial = t.store; t.count = 1;
+    t.store = nullptr; t.norm = nullptr;
+  }
+  return each_part(n, numel, [&](const ListPart& part) {
+    ClipParams p{};
+    fill_list(p.list, part, x, xt, y, yt, numel);
+    p.total = t;
+    t.norm = nullptr;  // written once
+    p.max_norm = max_norm; p.eps = eps;
+    p.in_place = 1;
+    for (int i = 0; i < p.list.n; ++i) p.in_place &= p.list.x[i] == p.list.y[i];
+    const hipError_t e = launch_clip(p, blocks_of(part.items), s);
+    return e == hipSuccess ? MUON_OK : hip_fail(e, "clipping");
+  });
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_grad_norm_workspace_bytes(int64_t n, const int64_t* numel, size_t* bytes) {
+  if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+  const int rc = check_list(n, numel);
+  if (rc) return rc;
+  const ListPlan P = plan_list(n, numel);
+  *bytes = P.parts ? list_bytes(P) : 0;
+  return ok();
+}
+
+int muon_grad_norm(int64_t n, const void* const* x, const int32_t* x_dtype, const int64_t* numel, int32_t kind, float* norm,
+                   double* square, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc;
+  if ((rc = check_list(n, numel)) || (rc = check_kind(kind)) || (rc = check_tensors("gradient", n, x, x_dtype, numel))) return rc;
+  if (!norm && !square) return fail(MUON_ERR_INVALID_ARG, "norm and square are both NULL");
+  if (square && kind != MUON_NORM_2) return fail(MUON_ERR_INVALID_ARG, "MUON_NORM_MAX has no sum of squares");
+  if ((uintptr_t)norm % 4 || (uintptr_t)square % 8) return fail(MUON_ERR_INVALID_ARG, "norm or square is not aligned to its element size");
+  if (ranges_meet(norm, 4, square, 8)) return fail(MUON_ERR_INVALID_ARG, "norm overlaps square");
+  for (int64_t i = 0; i < n; ++i)
+    if (ranges_meet(norm, 4, x[i], numel[i] * esize(x_dtype[i])) || ranges_meet(square, 8, x[i], numel[i] * esize(x_dtype[i])))
+      return fail(MUON_ERR_INVALID_ARG, "norm or square overlaps gradient %lld", (long long)i);
+  const ListPlan P = plan_list(n, numel);
+  if (P.parts && (rc = check_workspace(workspace, workspace_bytes, list_bytes(P)))) return rc;
+  if ((rc = run_partials(n, x, x_dtype, numel, kind, (uint64_t*)workspace, (hipStream_t)stream))) return rc;
+  NormTotal t{};
+  t.partial = (const uint64_t*)workspace; t.count = P.partials;
+  t.max_norm_kind = kind == MUON_NORM_MAX;
+  t.norm = norm; t.square = square;
+  const hipError_t e = launch_norm_total(t, (hipStream_t)stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "gradient norm");
+}
+
+int muon_clip_grad_norm(int64_t n, const void* const* x, const int32_t* x_dtype, const int64_t* numel, void* const* y,
+                        const int32_t* y_dtype, int32_t kind, double max_norm, double eps, const void* total, int32_t total_f64,
+                        float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+  try {
+    const int rc = clip(n, x, x_dtype, numel, y, y_dtype, kind, max_norm, eps, total, total_f64, norm, workspace, workspace_bytes,
+                        (hipStream_t)stream);
+    return rc ? rc : ok();
+  } catch (const std::bad_alloc&) {
+    return fail(MUON_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+}  // extern "C"
