@@ -468,6 +468,59 @@ int muon_qk_norm_rope_backward(const muon_qk_problem* p, void* workspace, size_t
 int muon_rope(const muon_qk_problem* p, void* stream);
 int muon_rope_backward(const muon_qk_problem* p, void* stream);
 
+/* ---- the norms before and after a block, its gate and its residual ------------ */
+
+/* For every row, b the output of a block and x the residual stream before it:
+ *   u = b / sqrt(mean(b^2) + eps) * (post_weight + weight_offset)   (post_norm), else b
+ *   s = residual_scale x + scale gate u          (no residual: 0; no gate: 1)
+ *   y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset)        (norm)
+ * the stream behind the block and what the next block reads.  Weights [cols]
+ * may be NULL: ones, without the offset.  gate [gate_rows][cols] has one row
+ * for rows / gate_rows consecutive rows each: one for all, one per sequence, or
+ * one per row.  Everything is formed in fp32 and rounded once on store; y is
+ * formed from s before its rounding.
+ * Rows have unit column stride; row strides are in elements, only alignment to
+ * the element size is required (16-byte aligned rows are fastest).
+ * Forward: stream may be NULL with norm.  Backward reads stream as the forward
+ * pass stored it, takes the gradients of y (dy, with norm) and of the stream
+ * (dstream, or NULL), and writes those outputs that are not NULL; block is read
+ * with post_norm or a gate only, the residual never.  dweight, dpost_weight and
+ * dgate have the types of what they are gradients of and are sums in fp32 in an
+ * order that depends on the sizes only.  A call without rows or columns writes
+ * nothing, dweight among it.
+ * An output of rows may be an input of rows (the same view and type); any other
+ * overlap of an output with another tensor is refused. */
+#define MUON_NORM_MAX_COLS 16384
+typedef struct muon_residual_norm_problem {
+  int64_t rows, cols;          /* rows at most 2^30, cols at most MUON_NORM_MAX_COLS */
+  int32_t dtype;               /* of block, y, dy and dblock */
+  int32_t stream_dtype;        /* of residual, stream, dstream and dresidual */
+  int32_t weight_dtype;        /* of weight, post_weight and their gradients */
+  int32_t gate_dtype;          /* of gate and dgate */
+  int32_t post_norm, norm;     /* 0 or 1 */
+  const void* block; int64_t block_row_stride;
+  const void* residual; int64_t residual_row_stride;  /* or NULL */
+  void* stream; int64_t stream_row_stride;            /* forward: output; backward: input */
+  void* y; int64_t y_row_stride;
+  const void* weight;          /* or NULL */
+  const void* post_weight;     /* or NULL */
+  const void* gate; int64_t gate_rows, gate_row_stride;  /* or NULL; gate_rows divides rows */
+  float scale, residual_scale, eps, weight_offset;
+  const void* dy; int64_t dy_row_stride;              /* backward, from here on */
+  const void* dstream; int64_t dstream_row_stride;    /* or NULL */
+  void* dblock; int64_t dblock_row_stride;            /* or NULL */
+  void* dresidual; int64_t dresidual_row_stride;      /* or NULL */
+  void* dweight;               /* [cols], or NULL */
+  void* dpost_weight;          /* [cols], or NULL */
+  void* dgate; int64_t dgate_row_stride;              /* as the gate, or NULL */
+  int64_t reserved;            /* must be 0 */
+} muon_residual_norm_problem;
+
+int muon_residual_norm(const muon_residual_norm_problem* p, void* stream);
+int muon_residual_norm_backward_workspace_bytes(const muon_residual_norm_problem* p, size_t* bytes);
+int muon_residual_norm_backward(const muon_residual_norm_problem* p, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
 /* ---- the norm over all gradients, and clipping ------------------------------- */
 
 #define MUON_NORM_2 0    /* sqrt of the sum of squares */

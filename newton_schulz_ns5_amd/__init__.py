@@ -27,6 +27,8 @@ Entry points (same names as the C ABI):
 * ``qk_norm_rope``, ``rope`` and their ``_backward`` -- per-head norms of queries
   and keys with the position rotation (one or several axes) in the same pass,
   and the rotation alone;
+* ``residual_norm``, ``residual_norm_backward`` -- the norms before and after a
+  block with its gate and its residual stream;
 * ``grad_norm``, ``clip_grad_norm`` -- the norm over all gradients and their
   clipping (``MuonNS5.clip_grad_norm`` for an optimizer's own).
 """
@@ -567,7 +569,7 @@ def profile_query(kernel_class):
 _TORCH_OPS = {
     "layer_ops": ("linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward",
                   "ACTIVATIONS"),
-    "pass_ops": ("grad_norm", "clip_grad_norm"),
+    "pass_ops": ("residual_norm", "residual_norm_backward", "grad_norm", "clip_grad_norm"),
 }
 
 

@@ -92,6 +92,18 @@ class QkProblem(ctypes.Structure):
                 ("scale", c_f32), ("eps", c_f32), ("axis", ctypes.c_uint8 * QK_MAX_PAIRS)]
 
 
+class ResidualNormProblem(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("cols", c_i64), ("dtype", c_i32), ("stream_dtype", c_i32), ("weight_dtype", c_i32),
+                ("gate_dtype", c_i32), ("post_norm", c_i32), ("norm", c_i32), ("block", c_vp), ("block_row_stride", c_i64),
+                ("residual", c_vp), ("residual_row_stride", c_i64), ("stream", c_vp), ("stream_row_stride", c_i64),
+                ("y", c_vp), ("y_row_stride", c_i64), ("weight", c_vp), ("post_weight", c_vp), ("gate", c_vp),
+                ("gate_rows", c_i64), ("gate_row_stride", c_i64), ("scale", c_f32), ("residual_scale", c_f32),
+                ("eps", c_f32), ("weight_offset", c_f32), ("dy", c_vp), ("dy_row_stride", c_i64), ("dstream", c_vp),
+                ("dstream_row_stride", c_i64), ("dblock", c_vp), ("dblock_row_stride", c_i64), ("dresidual", c_vp),
+                ("dresidual_row_stride", c_i64), ("dweight", c_vp), ("dpost_weight", c_vp), ("dgate", c_vp),
+                ("dgate_row_stride", c_i64), ("reserved", c_i64)]
+
+
 SIGNATURES = {
     "muon_ns_default_config": (None, [ctypes.POINTER(NSConfig)]),
     "muon_default_hparams": (None, [ctypes.POINTER(HParams)]),
@@ -125,6 +137,9 @@ SIGNATURES = {
     "muon_qk_norm_rope_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "muon_rope": (c_i32, [c_vp, c_vp]),
     "muon_rope_backward": (c_i32, [c_vp, c_vp]),
+    "muon_residual_norm": (c_i32, [c_vp, c_vp]),
+    "muon_residual_norm_backward_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
+    "muon_residual_norm_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "muon_grad_norm_workspace_bytes": (c_i32, [c_i64, c_vp, ctypes.POINTER(c_sz)]),
     "muon_grad_norm": (c_i32, [c_i64, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "muon_clip_grad_norm": (c_i32, [c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_f64, c_f64, c_vp, c_i32, c_vp, c_vp,

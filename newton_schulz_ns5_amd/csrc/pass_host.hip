@@ -1,6 +1,6 @@
 // Host side of the operators around a layer's products: validation, workspace
-// carve-up and launch sequences of the gradient norm and clipping.  Every
-// argument is checked before anything is enqueued.
+// carve-up and launch sequences of the gradient norm and clipping and of the
+// norms around a block.  Every argument is checked before anything is enqueued.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -240,6 +240,211 @@ int muon_clip_grad_norm(int64_t n, const void* const* x, const int32_t* x_dtype,
   } catch (const std::bad_alloc&) {
     return fail(MUON_ERR_INVALID_ARG, "out of host memory");
   }
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- norms around a block ----------------------------------------------------------------
+constexpr int64_t kMaxNormRows = (int64_t)1 << 30;
+
+int check_rows(const char* name, const void* p, int32_t dt, int64_t rows, int64_t cols, int64_t ld) {
+  if (!p) return fail(MUON_ERR_INVALID_ARG, "%s is NULL", name);
+  if (rows > 1 && ld < cols) return fail(MUON_ERR_INVALID_ARG, "%s row stride %lld is smaller than its %lld columns", name, (long long)ld, (long long)cols);
+  if (rows > 1 && ld > ((int64_t)1 << 54) / 8 / (rows - 1)) return fail(MUON_ERR_INVALID_ARG, "%s reaches too far", name);
+  if ((uintptr_t)p % esize(dt)) return fail(MUON_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
+  return MUON_OK;
+}
+
+// Gate rows are read gate_each rows long; 1 stands for one for all rows.
+int64_t gate_each(const muon_residual_norm_problem* q) { return q->gate_rows > 1 ? q->rows / q->gate_rows : q->rows; }
+
+int check_norms(const muon_residual_norm_problem* q, bool backward) {
+  if (!q) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
+  if (q->rows < 0 || q->cols < 0) return fail(MUON_ERR_INVALID_ARG, "negative rows or cols");
+  if (q->rows > kMaxNormRows) return fail(MUON_ERR_INVALID_ARG, "rows must be at most 2^30");
+  if (q->cols > kNormMaxCols) return fail(MUON_ERR_INVALID_ARG, "cols must be at most %d", kNormMaxCols);
+  if (!dtype_ok(q->dtype) || !dtype_ok(q->stream_dtype)) return fail(MUON_ERR_UNSUPPORTED, "dtype and stream_dtype must be MUON_F32 or MUON_BF16");
+  const bool weights = q->weight || q->post_weight || (backward && (q->dweight || q->dpost_weight));
+  if (weights && !dtype_ok(q->weight_dtype)) return fail(MUON_ERR_UNSUPPORTED, "weight_dtype %d is not MUON_F32 or MUON_BF16", q->weight_dtype);
+  if (q->gate && !dtype_ok(q->gate_dtype)) return fail(MUON_ERR_UNSUPPORTED, "gate_dtype %d is not MUON_F32 or MUON_BF16", q->gate_dtype);
+  if ((q->norm != 0 && q->norm != 1) || (q->post_norm != 0 && q->post_norm != 1)) return fail(MUON_ERR_INVALID_ARG, "norm and post_norm must be 0 or 1");
+  if (q->reserved) return fail(MUON_ERR_INVALID_ARG, "reserved must be 0");
+  if (!std::isfinite(q->scale) || !std::isfinite(q->residual_scale) || !std::isfinite(q->weight_offset))
+    return fail(MUON_ERR_INVALID_ARG, "scale, residual_scale and weight_offset must be finite");
+  if (!(std::isfinite(q->eps) && q->eps >= 0)) return fail(MUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (q->gate && (q->gate_rows < 1 || q->rows % q->gate_rows)) return fail(MUON_ERR_INVALID_ARG, "gate_rows must divide the rows");
+  if (q->weight && !q->norm) return fail(MUON_ERR_INVALID_ARG, "weight goes with norm");
+  if (q->post_weight && !q->post_norm) return fail(MUON_ERR_INVALID_ARG, "post_weight goes with post_norm");
+  if (backward) {
+    if (!q->norm && !q->dstream) return fail(MUON_ERR_INVALID_ARG, "without a norm there is no gradient but dstream");
+    if (q->dweight && !q->norm) return fail(MUON_ERR_INVALID_ARG, "dweight goes with norm");
+    if (q->dpost_weight && !q->post_norm) return fail(MUON_ERR_INVALID_ARG, "dpost_weight goes with post_norm");
+    if (q->dgate && !q->gate) return fail(MUON_ERR_INVALID_ARG, "dgate goes with a gate");
+  }
+  if (!q->rows || !q->cols) return MUON_OK;
+  // Row tensors first, the vectors behind them.
+  struct Tensor { const char* name; const void* p; int32_t dt; int64_t rows, ld; bool needed; };
+  const int64_t R = q->rows;
+  const bool need_b = q->post_norm || q->gate;
+  const Tensor fin[] = {{"block", q->block, q->dtype, R, q->block_row_stride, true},
+                        {"residual", q->residual, q->stream_dtype, R, q->residual_row_stride, false}};
+  const Tensor fout[] = {{"stream", q->stream, q->stream_dtype, R, q->stream_row_stride, !q->norm},
+                         {"y", q->norm ? q->y : nullptr, q->dtype, R, q->y_row_stride, q->norm != 0}};
+  const Tensor bin[] = {{"block", need_b ? q->block : nullptr, q->dtype, R, q->block_row_stride, need_b},
+                        {"stream", q->norm ? q->stream : nullptr, q->stream_dtype, R, q->stream_row_stride, q->norm != 0},
+                        {"dy", q->norm ? q->dy : nullptr, q->dtype, R, q->dy_row_stride, q->norm != 0},
+                        {"dstream", q->dstream, q->stream_dtype, R, q->dstream_row_stride, false}};
+  const Tensor bout[] = {{"dblock", q->dblock, q->dtype, R, q->dblock_row_stride, false},
+                         {"dresidual", q->dresidual, q->stream_dtype, R, q->dresidual_row_stride, false}};
+  const Tensor vin[] = {{"weight", q->weight, q->weight_dtype, 1, q->cols, false},
+                        {"post_weight", q->post_weight, q->weight_dtype, 1, q->cols, false},
+                        {"gate", q->gate, q->gate_dtype, q->gate_rows, q->gate_row_stride, false}};
+  const Tensor vout[] = {{"dweight", q->dweight, q->weight_dtype, 1, q->cols, false},
+                         {"dpost_weight", q->dpost_weight, q->weight_dtype, 1, q->cols, false},
+                         {"dgate", q->dgate, q->gate_dtype, q->gate_rows, q->dgate_row_stride, false}};
+  const Tensor* const in = backward ? bin : fin;
+  const Tensor* const out = backward ? bout : fout;
+  const int nin = backward ? 4 : 2, nv = backward ? 3 : 0;
+  int rc;
+  auto look = [&](const Tensor& t) { return !t.p && !t.needed ? MUON_OK : check_rows(t.name, t.p, t.dt, t.rows, q->cols, t.ld); };
+  for (int i = 0; i < nin; ++i)
+    if ((rc = look(in[i]))) return rc;
+  for (int i = 0; i < 2; ++i)
+    if ((rc = look(out[i]))) return rc;
+  for (const Tensor& t : vin)
+    if ((rc = look(t))) return rc;
+  for (int i = 0; i < nv; ++i)
+    if ((rc = look(vout[i]))) return rc;
+  auto span = [&](const Tensor& t) { return rows_of(t.name, t.p, t.dt, t.p ? t.rows : 0, q->cols, t.ld); };
+  auto apart = [&](const Tensor& a, const Tensor& b, bool same_ok) {
+    if (!a.p || !b.p) return MUON_OK;
+    if (same_ok && a.p == b.p && a.dt == b.dt && (R <= 1 || a.ld == b.ld)) return MUON_OK;
+    if (meet(span(a), span(b))) return fail(MUON_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+    return MUON_OK;
+  };
+  for (int o = 0; o < 2; ++o) {
+    for (int i = 0; i < nin; ++i)
+      if ((rc = apart(out[o], in[i], true))) return rc;
+    for (const Tensor& t : vin)
+      if ((rc = apart(out[o], t, false))) return rc;
+  }
+  if ((rc = apart(out[0], out[1], false))) return rc;
+  for (int o = 0; o < nv; ++o) {
+    for (int i = 0; i < nin; ++i)
+      if ((rc = apart(vout[o], in[i], false))) return rc;
+    for (int i = 0; i < 2; ++i)
+      if ((rc = apart(vout[o], out[i], false))) return rc;
+    for (const Tensor& t : vin)
+      if ((rc = apart(vout[o], t, false))) return rc;
+    for (int i = 0; i < o; ++i)
+      if ((rc = apart(vout[o], vout[i], false))) return rc;
+  }
+  return MUON_OK;
+}
+
+// Launch geometry of the gradients; it depends on the sizes only.
+struct NormPlan {
+  int blocks = 0;
+  int64_t units = 0, unit_rows = 0, span = 0, gates = 0;
+  int chunks = 1;
+  size_t off[3] = {0, 0, 0}, bytes = 0;
+  bool part[3] = {false, false, false};
+};
+
+NormPlan plan_norm_grad(const muon_residual_norm_problem* q) {
+  NormPlan P;
+  const NormShape shape = norm_shape(q->cols);
+  const int threads = norm_threads(shape), rpw = threads / shape.group;
+  const int target = 256 * (1024 / threads);
+  const int64_t each = gate_each(q);
+  const bool gate_sum = q->gate && (each > 1 || q->rows == 1);
+  P.gates = gate_sum ? q->rows / each : 1;
+  P.span = q->rows / P.gates;
+  const int64_t chunks = std::min<int64_t>(cdiv(P.span, rpw), P.gates < target ? cdiv(target, P.gates) : 1);
+  P.unit_rows = cdiv(cdiv(P.span, chunks), rpw) * rpw;
+  P.chunks = (int)cdiv(P.span, P.unit_rows);
+  P.units = P.gates * P.chunks;
+  P.blocks = (int)std::min<int64_t>(P.units, target);
+  P.part[0] = q->dweight != nullptr;
+  P.part[1] = q->dpost_weight != nullptr;
+  P.part[2] = q->dgate && gate_sum && P.chunks > 1;
+  for (int i = 0; i < 3; ++i) {
+    if (!P.part[i]) continue;
+    P.off[i] = P.bytes;
+    P.bytes += align256((size_t)(i < 2 ? P.blocks : P.units) * q->cols * 4);
+  }
+  return P;
+}
+
+ResidualNorm norm_params(const muon_residual_norm_problem* q) {
+  ResidualNorm p{};
+  p.rows = q->rows; p.cols = (int32_t)q->cols;
+  p.post = q->post_norm; p.norm = q->norm;
+  p.block = q->block; p.ldb = q->block_row_stride;
+  p.residual = q->residual; p.ldr = q->residual_row_stride;
+  p.stream = q->stream; p.lds = q->stream_row_stride;
+  p.y = q->y; p.ldy = q->y_row_stride;
+  p.weight = q->weight; p.post_weight = q->post_weight; p.weight_bf16 = q->weight_dtype == MUON_BF16;
+  p.gate = q->gate; p.ldg = q->gate_row_stride; p.gate_bf16 = q->gate_dtype == MUON_BF16;
+  p.gate_each = gate_each(q);
+  p.scale = q->scale; p.residual_scale = q->residual_scale; p.eps = q->eps; p.offset = q->weight_offset;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_residual_norm(const muon_residual_norm_problem* q, void* stream) {
+  const int rc = check_norms(q, false);
+  if (rc) return rc;
+  if (!q->rows || !q->cols) return ok();
+  const NormShape shape = norm_shape(q->cols);
+  const int threads = norm_threads(shape), rpw = threads / shape.group;
+  const int blocks = (int)std::min<int64_t>(cdiv(q->rows, rpw), 256 * (2048 / threads));
+  const hipError_t e = launch_residual_norm(norm_params(q), q->dtype == MUON_BF16, q->stream_dtype == MUON_BF16, blocks, (hipStream_t)stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "norms around a block");
+}
+
+int muon_residual_norm_backward_workspace_bytes(const muon_residual_norm_problem* q, size_t* bytes) {
+  if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+  const int rc = check_norms(q, true);
+  if (rc) return rc;
+  *bytes = q->rows && q->cols ? plan_norm_grad(q).bytes : 0;
+  return ok();
+}
+
+int muon_residual_norm_backward(const muon_residual_norm_problem* q, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_norms(q, true);
+  if (rc) return rc;
+  if (!q->rows || !q->cols) return ok();
+  const NormPlan P = plan_norm_grad(q);
+  if ((rc = check_workspace(workspace, workspace_bytes, P.bytes))) return rc;
+  ResidualNorm p = norm_params(q);
+  p.dy = q->dy; p.lddy = q->dy_row_stride;
+  p.dstream = q->dstream; p.ldds = q->dstream_row_stride;
+  p.dblock = q->dblock; p.lddb = q->dblock_row_stride;
+  p.dresidual = q->dresidual; p.lddr = q->dresidual_row_stride;
+  p.dgate = q->dgate; p.lddg = q->dgate_row_stride;
+  for (int i = 0; i < 3; ++i) p.part[i] = P.part[i] ? (float*)((char*)workspace + P.off[i]) : nullptr;
+  p.units = P.units; p.unit_rows = P.unit_rows; p.span = P.span; p.gate_chunks = P.chunks;
+  hipError_t e = launch_residual_norm_grad(p, q->dtype == MUON_BF16, q->stream_dtype == MUON_BF16, P.blocks, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "gradients of the norms around a block");
+  NormSums n{};
+  void* const outs[3] = {q->dweight, q->dpost_weight, q->dgate};
+  for (int i = 0; i < 3; ++i) {
+    n.part[i] = p.part[i];
+    n.out[i] = outs[i];
+    n.ld[i] = i == 2 ? q->dgate_row_stride : 0;
+    n.count[i] = i == 2 ? P.chunks : P.blocks;
+    n.groups[i] = P.part[i] ? (i == 2 ? (int)P.gates : 1) : 0;
+    n.bf16[i] = (i == 2 ? q->gate_dtype : q->weight_dtype) == MUON_BF16;
+  }
+  n.cols = (int32_t)q->cols;
+  e = launch_norm_sums(n, (hipStream_t)stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "gradients of the norms' vectors");
 }
 
 }  // extern "C"

@@ -48,4 +48,46 @@ hipError_t launch_norm_partial(const NormPartial& p, int blocks, hipStream_t s);
 hipError_t launch_norm_total(const NormTotal& p, hipStream_t s);
 hipError_t launch_clip(const ClipParams& p, int blocks, hipStream_t s);
 
+// ---- norms around a block -----------------------------------------------------------
+// A row is held by kGroup threads, 8 consecutive columns per chunk, K chunks per
+// thread (columns 8 (j + k kGroup) of thread j).
+constexpr int kNormMaxCols = 16384;
+struct ResidualNorm {
+  int64_t rows;
+  int32_t cols;
+  int32_t post, norm;                      // norm of the block's output, norm of the stream
+  const void* block; int64_t ldb;
+  const void* residual; int64_t ldr;       // may be null
+  void* stream; int64_t lds;               // forward: may be null; backward: read
+  void* y; int64_t ldy;
+  const void *weight, *post_weight; int32_t weight_bf16;  // may be null: ones
+  const void* gate; int64_t ldg; int32_t gate_bf16;       // may be null
+  int64_t gate_each;                       // rows that share a row of the gate
+  float scale, residual_scale, eps, offset;
+  // backward
+  const void* dy; int64_t lddy;
+  const void* dstream; int64_t ldds;       // may be null
+  void* dblock; int64_t lddb;              // may be null
+  void* dresidual; int64_t lddr;           // may be null
+  void* dgate; int64_t lddg;               // written here where a workgroup has all rows of a gate's row
+  float* part[3];                          // of dweight, dpost_weight [workgroup][cols], of dgate [unit][cols]; may be null
+  // Units of rows: gate_chunks for every row of the gate (or for all rows), of
+  // unit_rows each but the last.
+  int64_t units, unit_rows, span;          // span: rows that gate_chunks units cover
+  int32_t gate_chunks;
+};
+// threads that hold a row, and chunks of 8 columns each
+struct NormShape { int group, chunks; };
+NormShape norm_shape(int64_t cols);
+int norm_threads(const NormShape& s);      // of a workgroup
+hipError_t launch_residual_norm(const ResidualNorm& p, bool bf16, bool stream_bf16, int blocks, hipStream_t s);
+hipError_t launch_residual_norm_grad(const ResidualNorm& p, bool bf16, bool stream_bf16, int blocks, hipStream_t s);
+// out[o][j] = the sum over count[o] rows of part[o], for each of groups[o]
+// consecutive sets of rows.
+struct NormSums {
+  const float* part[3]; void* out[3]; int64_t ld[3];
+  int32_t count[3], groups[3], bf16[3], cols;
+};
+hipError_t launch_norm_sums(const NormSums& p, hipStream_t s);
+
 }  // namespace muon

@@ -1,5 +1,6 @@
-"""The operators around a layer's products in a pass: the norm over all
-gradients and their clipping.
+"""The operators around a layer's products in a pass: the norms before and
+after a block with its gate and its residual, the norm over all gradients and
+their clipping.
 
 Marshalling like :mod:`layer_ops`, whose rules hold here too: raw pointers to
 the library, work enqueued on the current stream of the tensors' device,
@@ -15,10 +16,10 @@ import torch
 
 from . import MuonError, _lib, _written
 from ._lib import MUON_NORM_2, MUON_NORM_MAX
-from .layer_ops import (_CODE, _NO_WORKSPACE, _bad, _current_device, _dual, _given, _raw_stream, _refuse_tangents,
-                        _same_device)
+from .layer_ops import (_CODE, _NO_WORKSPACE, _Uneven, _bad, _call, _current_device, _dt, _dual, _given, _raw_stream,
+                        _refuse_capture, _refuse_tangents, _rows, _same_device, _vector, _wants_grad)
 
-__all__ = ["grad_norm", "clip_grad_norm"]
+__all__ = ["residual_norm", "residual_norm_backward", "grad_norm", "clip_grad_norm"]
 
 
 def _unsupported(text):
@@ -31,6 +32,271 @@ def _on(dev, fn):
         with torch.cuda.device(dev):
             return fn()
     return fn()
+
+
+# ---- the norms before and after a block, its gate and its residual ---------------------
+_NORM = struct.Struct("@qq iiiiii Pq Pq Pq Pq PP Pqq ffff Pq Pq Pq Pq PP Pq q")
+
+
+def _input_rows(t, name, shape):
+    """(tensor, pointer, row stride) of an input of this shape, copied where its rows are not evenly spaced or share
+    elements."""
+    if t.shape != shape:
+        _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
+        _bad(f"{name} needs unit column stride")
+    try:
+        p, r, c, ld = _rows(t, name)
+        if r <= 1 or ld >= c:
+            return t, p, ld
+    except _Uneven:
+        pass
+    t = t.contiguous()
+    p, _, _, ld = _rows(t, name)
+    return t, p, ld
+
+
+def _output_rows(t, name, shape, dtype):
+    if t.shape != shape:
+        _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        _unsupported(f"{name} is {t.dtype}, not {dtype}")
+    p, _, _, ld = _rows(t, name)
+    return p, ld
+
+
+def _gate_rows(gate, shape):
+    """(tensor, pointer, rows, row stride) of a gate for rows of this shape: [cols], or as many dimensions as the
+    rows have, of which the leading ones agree and the others are 1."""
+    lead, own = shape[:-1], gate.shape[:-1]
+    if gate.dim() < 1 or gate.shape[-1] != shape[-1]:
+        _bad(f"gate {tuple(gate.shape)} does not go with rows {tuple(shape)}")
+    if len(own):
+        same = 0
+        while same < len(lead) and same < len(own) and own[same] == lead[same]:
+            same += 1
+        if len(own) != len(lead) or any(n != 1 for n in own[same:]):
+            _bad(f"gate {tuple(gate.shape)} does not go with rows {tuple(shape)}: its leading dimensions are theirs, then 1")
+    t, p, ld = _input_rows(gate, "gate", gate.shape)
+    return t, p, max(own.numel(), 1), ld
+
+
+def _norm_vectors(weight, post_weight, cols):
+    if weight is not None and post_weight is not None and weight.dtype != post_weight.dtype:
+        _unsupported(f"weight is {weight.dtype} and post_weight {post_weight.dtype}: one type is needed")
+    first = weight if weight is not None else post_weight
+    return (_dt(first) if first is not None else 0, _vector(weight, "weight", cols) if weight is not None else 0,
+            _vector(post_weight, "post_weight", cols) if post_weight is not None else 0)
+
+
+def _pack_norm(*fields):
+    try:
+        return _NORM.pack(*fields)
+    except (OverflowError, struct.error, TypeError):  # every other field is a size or an address
+        _bad("scale, residual_scale, eps and weight_offset must be numbers that fp32 holds")
+
+
+def _norm_flags(norm, post_norm, weight, post_weight):
+    post = post_weight is not None if post_norm is None else bool(post_norm)
+    if weight is not None and not norm:
+        _bad("weight goes with norm")
+    if post_weight is not None and not post:
+        _bad("post_weight goes with post_norm")
+    return bool(norm), post
+
+
+def residual_norm(block, residual=None, *, weight=None, post_weight=None, gate=None, norm=True, post_norm=None,
+                  scale=1.0, residual_scale=1.0, eps=1e-6, weight_offset=0.0, stream=None, out=None):
+    """The join of a block with its residual stream and the norm before the next block (see muon_residual_norm):
+
+    ``u = block``, or with ``post_norm`` (on when ``post_weight`` is given) its RMS norm times
+    ``post_weight + weight_offset``; ``s = residual_scale * residual + scale * gate * u``; with ``norm``
+    ``y = `` the RMS norm of ``s`` times ``weight + weight_offset``.  Returns (s, y); y is None without ``norm``.
+
+    ``block`` is [..., cols] in fp32 or bf16 (y has its type), ``residual`` of the same shape, whose type, fp32 or
+    bf16, the stream keeps.  Weights are [cols] (None: ones), ``gate`` is [cols], or has block's dimensions with
+    trailing leading ones of 1 ([batch, 1, cols]: one per sequence; block's shape: one per row).  Columns are
+    contiguous, rows of any stride; rows that share elements or are not evenly spaced are copied first.  Without
+    a residual, a norm after the block, a gate and a scale the stream is ``block`` itself: the first norm of a
+    model.  ``stream`` and ``out`` may be given, and be the inputs themselves.
+    """
+    if _wants_grad(block, residual, weight, post_weight, gate):
+        if stream is not None or out is not None:
+            _bad("stream and out cannot be given when an input requires a gradient")
+        _refuse_capture()
+        how = dict(norm=norm, post_norm=post_norm, scale=scale, residual_scale=residual_scale, eps=eps,
+                   weight_offset=weight_offset)
+        s, y = _ResidualNorm.apply(block, residual, weight, post_weight, gate, how)
+        return (block if s is None else s), y
+    return _residual_norm(block, residual, weight, post_weight, gate, norm, post_norm, scale, residual_scale, eps,
+                          weight_offset, stream, out)
+
+
+def _is_block(residual, gate, post, scale, stream):
+    """Whether the stream is the block's output itself."""
+    return residual is None and gate is None and not post and scale == 1 and stream is None
+
+
+def _residual_norm(block, residual, weight, post_weight, gate, norm, post_norm, scale, residual_scale, eps,
+                   weight_offset, stream=None, out=None):
+    norm, post = _norm_flags(norm, post_norm, weight, post_weight)
+    given = () if stream is None and out is None else _given(stream, out)
+    dev = _same_device(block, residual, weight, post_weight, gate, stream, out)
+    code, shape = _dt(block), block.shape
+    if not shape:
+        _bad("block needs at least one dimension")
+    cols = shape[-1]
+    same = _is_block(residual, gate, post, scale, stream)
+    wcode, wp, pwp = _norm_vectors(weight, post_weight, cols)
+    source = block
+    block, bp, ldb = _input_rows(block, "block", shape)
+    rp = ldr = gp = grows = ldg = gcode = 0
+    kept = residual
+    if residual is not None:
+        kept, rp, ldr = _input_rows(residual, "residual", shape)
+    if gate is not None:
+        gate, gp, grows, ldg = _gate_rows(gate, shape)
+        gcode = _dt(gate)
+    st = residual.dtype if residual is not None else stream.dtype if stream is not None else block.dtype
+    sp = lds = yp = ldy = 0
+    if same:
+        stream = source
+    else:
+        if stream is None:
+            stream = torch.empty(shape, dtype=st, device=block.device)
+        sp, lds = _output_rows(stream, "stream", shape, st)
+    if norm:
+        if out is None:
+            out = torch.empty(shape, dtype=block.dtype, device=block.device)
+        yp, ldy = _output_rows(out, "out", shape, block.dtype)
+    elif out is not None:
+        _bad("out goes with norm")
+    if norm or not same:
+        prob = _pack_norm(shape[:-1].numel(), cols, code, _dt(stream), wcode, gcode, post, norm, bp, ldb, rp, ldr, sp, lds,
+                          yp, ldy, wp, pwp, gp, grows, ldg, scale, residual_scale, eps, weight_offset,
+                          0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+        _call(dev, _lib.lib().muon_residual_norm, prob, None)
+    if given:
+        _written(*given)
+    return stream, out
+
+
+def residual_norm_backward(dy, dstream, stream, block, *, weight=None, post_weight=None, gate=None, norm=True,
+                           post_norm=None, scale=1.0, residual_scale=1.0, eps=1e-6, weight_offset=0.0,
+                           need_dblock=True, need_dresidual=True, need_dweight=None, need_dpost_weight=None,
+                           need_dgate=None, dblock=None, dresidual=None):
+    """(dblock, dresidual, dweight, dpost_weight, dgate) of :func:`residual_norm` for the gradients ``dy`` of y and
+    ``dstream`` of the stream (either may be None); None for those not asked for.
+
+    ``stream`` is what the forward pass returned (read where ``dy`` is), ``block`` its input (read with a norm
+    after the block or a gate; may be None else).  The vectors' gradients are asked for by default where
+    there is a vector.  Where dblock and dresidual are equal (no norm after the block, no gate, equal scales,
+    one type) and neither is given, both are the same tensor.  Given outputs are written in place, and may be
+    the input gradients themselves.
+    """
+    _refuse_tangents(dy, dstream, stream, block, weight, post_weight, gate)
+    _, post = _norm_flags(norm, post_norm, weight, post_weight)
+    if not norm and dy is not None:
+        _bad("without norm there is no dy")
+    norm = dy is not None  # a result that nothing depends on
+    if dy is None and dstream is None:
+        _bad("dy and dstream are both None")
+    need_b = post or gate is not None
+    if norm and stream is None:
+        _bad("a gradient of the norm needs stream")
+    if need_b and block is None:
+        _bad("a norm after the block and a gate need block")
+    given = () if dblock is None and dresidual is None else _given(dblock, dresidual)
+    first = dy if dy is not None else dstream
+    dev = _same_device(first, dstream, stream, block, weight, post_weight, gate, dblock, dresidual)
+    shape, cols = first.shape, first.shape[-1] if first.dim() else _bad("gradients need at least one dimension")
+    t = block.dtype if block is not None else dy.dtype if dy is not None else dblock.dtype if dblock is not None else dstream.dtype
+    st = dstream.dtype if dstream is not None else stream.dtype
+    for x, name, want in ((dy, "dy", t), (block, "block", t), (stream if norm else None, "stream", st)):
+        if x is not None and x.dtype != want:
+            _unsupported(f"{name} is {x.dtype}, not {want}")
+    wcode, wp, pwp = _norm_vectors(weight, post_weight, cols)
+    keep = []
+
+    def rows(x, name, read):
+        if x is None or not read:
+            return 0, 0
+        x, p, ld = _input_rows(x, name, shape)
+        keep.append(x)
+        return p, ld
+    dyp, dsp, sp, bp = rows(dy, "dy", norm), rows(dstream, "dstream", True), rows(stream, "stream", norm), rows(block, "block", need_b)
+    gp = grows = ldg = gcode = 0
+    if gate is not None:
+        gate_shape = gate.shape
+        gate, gp, grows, ldg = _gate_rows(gate, shape)
+        gcode = _dt(gate)
+    device = first.device
+    shared = (need_dblock and need_dresidual and not need_b and scale == residual_scale and t == st and dblock is None
+              and dresidual is None)
+    if dblock is None and need_dblock and not shared:
+        dblock = torch.empty(shape, dtype=t, device=device)
+    if dresidual is None and need_dresidual:
+        dresidual = torch.empty(shape, dtype=st, device=device)
+    dbp = _output_rows(dblock, "dblock", shape, t) if dblock is not None else (0, 0)
+    drp = _output_rows(dresidual, "dresidual", shape, st) if dresidual is not None else (0, 0)
+    dw = torch.empty_like(weight) if weight is not None and need_dweight is not False else None
+    dpw = torch.empty_like(post_weight) if post_weight is not None and need_dpost_weight is not False else None
+    dg = torch.empty(gate_shape, dtype=gate.dtype, device=device) if gate is not None and need_dgate is not False else None
+    if (need_dweight and weight is None) or (need_dpost_weight and post_weight is None) or (need_dgate and gate is None):
+        _bad("there is no vector to give the gradient of")
+    dgp, lddg = _output_rows(dg, "dgate", gate_shape, gate.dtype) if dg is not None else (0, 0)
+    if not norm and dw is not None:
+        dw.zero_()
+    nrows = shape[:-1].numel()
+    if not nrows or not cols:  # empty sums, which the library has no work for
+        for v in (dw, dpw, dg):
+            if v is not None:
+                v.zero_()
+    prob = _pack_norm(nrows, cols, _CODE.get(t, -1), _CODE.get(st, -1), wcode, gcode, post, norm, *bp, 0, 0, *sp, 0, 0,
+                      wp if norm else 0, pwp, gp, grows, ldg, scale, residual_scale, eps, weight_offset, *dyp, *dsp, *dbp,
+                      *drp, dw.data_ptr() if dw is not None and norm else 0, dpw.data_ptr() if dpw is not None else 0,
+                      dgp, lddg, 0)
+    L = _lib.lib()
+    _call(dev, L.muon_residual_norm_backward, prob, L.muon_residual_norm_backward_workspace_bytes, True)
+    if given:
+        _written(*given)
+    return (dresidual if shared else dblock), dresidual, dw, dpw, dg
+
+
+def _row_grad(g):
+    """A gradient whose columns are contiguous (autograd may hand over expanded or transposed ones)."""
+    return g if g is None or g.shape[-1] <= 1 or g.stride(-1) == 1 else g.contiguous()
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, block, residual, weight, post_weight, gate, how):
+        s, y = _residual_norm(block, residual, weight, post_weight, gate, how["norm"], how["post_norm"], how["scale"],
+                              how["residual_scale"], how["eps"], how["weight_offset"])
+        same = s is block
+        post = post_weight is not None if how["post_norm"] is None else bool(how["post_norm"])
+        ctx.save_for_backward(block if post or gate is not None else None, s if how["norm"] else None, weight, post_weight, gate)
+        ctx.how = how
+        ctx.block_dtype = block.dtype
+        ctx.set_materialize_grads(False)
+        return (None if same else s), y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, ds, dy):
+        if ds is None and dy is None:
+            return (None,) * 6
+        _refuse_capture()
+        block, s, weight, post_weight, gate = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dblock = None
+        if dy is None and block is None and need[0]:
+            # only the stream's gradient: its type need not be the block's
+            dblock = torch.empty(ds.shape, dtype=ctx.block_dtype, device=ds.device)
+        got = residual_norm_backward(_row_grad(dy), _row_grad(ds), s, block, weight=weight, post_weight=post_weight, gate=gate,
+                                     need_dblock=need[0], need_dresidual=need[1], need_dweight=need[2],
+                                     need_dpost_weight=need[3], need_dgate=need[4], dblock=dblock, **ctx.how)
+        return got + (None,)
 
 
 # ---- the norm over all gradients, and clipping ---------------------------------------

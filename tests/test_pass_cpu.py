@@ -80,6 +80,115 @@ def test_norm_workspace():
     assert L.muon_grad_norm_workspace_bytes(1, struct.pack("q", 1), None) == -1
 
 
+# ---- norms around a block ----------------------------------------------------------------
+def test_ctypes_struct_matches_c_layout():
+    import os
+    import subprocess
+    import tempfile
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    lines = []
+    structs = [("muon_residual_norm_problem", _lib.ResidualNormProblem)]
+    for c, py in structs:
+        lines.append(f'printf("{c} %zu\\n", sizeof({c}));')
+        lines += [f'printf("{c}.{f} %zu\\n", offsetof({c}, {f}));' for f, _ in py._fields_]
+    src = '#include <stdio.h>\n#include <stddef.h>\n#include "muon_mi355x.h"\nint main(void) {' + "\n".join(lines) + "return 0; }"
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "l.c"), os.path.join(d, "l")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", "-std=c99", "-I", os.path.join(root, "include"), c, "-o", exe], check=True)
+        lay = dict(x.split() for x in subprocess.run([exe], check=True, capture_output=True, text=True).stdout.splitlines())
+    for c, py in structs:
+        assert ctypes.sizeof(py) == int(lay[c]), c
+        for f, _ in py._fields_:
+            assert getattr(py, f).offset == int(lay[f"{c}.{f}"]), (c, f)
+
+
+def test_packed_norm_problem_matches_the_struct():
+    from newton_schulz_ns5_amd import pass_ops
+    assert pass_ops._NORM.size == ctypes.sizeof(_lib.ResidualNormProblem)
+    fields = [f for f, _ in _lib.ResidualNormProblem._fields_]
+    p = _lib.ResidualNormProblem.from_buffer_copy(pass_ops._NORM.pack(*range(1, len(fields) + 1)))
+    assert [getattr(p, f) for f in fields] == list(range(1, len(fields) + 1))
+
+
+def norm_problem(**over):
+    a = dict(rows=6, cols=64, dtype=1, stream_dtype=0, weight_dtype=1, gate_dtype=1, post_norm=1, norm=1, block=FAKE,
+             block_row_stride=64, residual=FAKE + MIB, residual_row_stride=64, stream=FAKE + 2 * MIB, stream_row_stride=64,
+             y=FAKE + 3 * MIB, y_row_stride=64, weight=FAKE + 4 * MIB, post_weight=FAKE + 5 * MIB, gate=FAKE + 6 * MIB,
+             gate_rows=2, gate_row_stride=64, scale=1.0, residual_scale=1.0, eps=1e-6, weight_offset=0.0,
+             dy=FAKE + 7 * MIB, dy_row_stride=64, dstream=FAKE + 8 * MIB, dstream_row_stride=64, dblock=FAKE + 9 * MIB,
+             dblock_row_stride=64, dresidual=FAKE + 10 * MIB, dresidual_row_stride=64, dweight=FAKE + 11 * MIB,
+             dpost_weight=FAKE + 12 * MIB, dgate=FAKE + 13 * MIB, dgate_row_stride=64, reserved=0)
+    a.update(over)
+    p = _lib.ResidualNormProblem()
+    for k, v in a.items():
+        setattr(p, k, v)
+    return p
+
+
+BOTH = [
+    (dict(rows=-1), -1), (dict(cols=-1), -1), (dict(rows=(1 << 30) + 1, gate=None), -1), (dict(cols=16385), -1),
+    (dict(dtype=2), -2), (dict(stream_dtype=-1), -2), (dict(weight_dtype=4), -2), (dict(gate_dtype=5), -2),
+    (dict(norm=2), -1), (dict(post_norm=3), -1), (dict(reserved=1), -1), (dict(scale=math.inf), -1),
+    (dict(residual_scale=math.nan), -1), (dict(eps=-1.0), -1), (dict(eps=math.nan), -1), (dict(weight_offset=math.inf), -1),
+    (dict(gate_rows=4), -1), (dict(gate_rows=0), -1), (dict(norm=0), -1), (dict(post_norm=0), -1), (dict(block=None), -1),
+    (dict(block_row_stride=63), -1), (dict(gate_row_stride=63), -1), (dict(block=FAKE + 1), -1), (dict(stream=FAKE + 2 * MIB + 2), -1),
+    (dict(weight=FAKE + 4 * MIB + 1), -1), (dict(stream_row_stride=1 << 60), -1), (dict(gate=FAKE + 1), -1),
+]
+
+
+@pytest.mark.parametrize("over,code", BOTH + [
+    (dict(y=None), -1), (dict(y=FAKE + 2), -1), (dict(y=FAKE, y_row_stride=65), -1), (dict(stream=FAKE), -1),
+    (dict(stream=FAKE + MIB, stream_row_stride=80), -1), (dict(y=FAKE + 2 * MIB), -1), (dict(y=FAKE + 4 * MIB), -1),
+    (dict(stream=FAKE + 5 * MIB), -1), (dict(y=FAKE + 6 * MIB), -1), (dict(y_row_stride=8), -1), (dict(y=FAKE + MIB), -1),
+    (dict(norm=0, weight=None, stream=None), -1), (dict(residual=FAKE + MIB + 2), -1),
+])
+def test_residual_norm_refusals(over, code):
+    assert _lib.lib().muon_residual_norm(ctypes.byref(norm_problem(**over)), None) == code
+    assert _lib.lib().muon_last_error()
+
+
+@pytest.mark.parametrize("over,code", BOTH + [
+    (dict(dy=None), -1), (dict(stream=None), -1), (dict(dy_row_stride=1), -1), (dict(norm=0, weight=None), -1),
+    (dict(norm=0, weight=None, dweight=None, dstream=None), -1), (dict(post_norm=0, post_weight=None), -1),
+    (dict(gate=None), -1), (dict(dblock=FAKE + 2), -1), (dict(dblock=FAKE + 8 * MIB), -1), (dict(dresidual=FAKE + 7 * MIB), -1),
+    (dict(dresidual=FAKE + 9 * MIB), -1), (dict(dweight=FAKE), -1), (dict(dweight=FAKE + 4 * MIB), -1),
+    (dict(dpost_weight=FAKE + 11 * MIB), -1), (dict(dgate=FAKE + 6 * MIB), -1), (dict(dgate=FAKE + 12 * MIB), -1),
+    (dict(dgate=FAKE + 10 * MIB), -1), (dict(dgate_row_stride=3), -1), (dict(dweight=FAKE + 11 * MIB + 1), -1),
+    (dict(dblock=FAKE + 4 * MIB), -1), (dict(dstream=FAKE + 8 * MIB + 2), -1),
+])
+def test_residual_norm_backward_refusals(over, code):
+    assert _lib.lib().muon_residual_norm_backward(ctypes.byref(norm_problem(**over)), FAKE + 20 * MIB, 1 << 40, None) == code
+    assert _lib.lib().muon_last_error()
+
+
+def test_residual_norm_empty_calls_and_workspace():
+    L = _lib.lib()
+    need = ctypes.c_size_t(7)
+    for over in (dict(rows=0, gate_rows=1), dict(cols=0)):
+        p = norm_problem(**over)
+        assert L.muon_residual_norm(ctypes.byref(p), None) == 0
+        assert L.muon_residual_norm_backward(ctypes.byref(p), None, 0, None) == 0
+        assert L.muon_residual_norm_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0 and need.value == 0
+    p = norm_problem()
+    assert L.muon_residual_norm_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0 and need.value > 0
+    assert L.muon_residual_norm_backward(ctypes.byref(p), FAKE + 20 * MIB, need.value - 1, None) == -3
+    assert L.muon_residual_norm_backward(ctypes.byref(p), FAKE + 20 * MIB + 16, need.value, None) == -1
+    assert L.muon_residual_norm(None, None) == -1
+    assert L.muon_residual_norm_backward(None, None, 0, None) == -1
+
+
+def test_residual_norm_bindings_refuse():
+    b, w = torch.ones(2, 3, 8), torch.ones(8)
+    refused(ns.residual_norm, b, code=-1)  # not on a GPU
+    refused(ns.residual_norm, b, weight=w, norm=False, code=-1)
+    refused(ns.residual_norm, b, post_weight=w, post_norm=False, code=-1)
+    refused(ns.residual_norm_backward, None, None, None, b, code=-1)
+    refused(ns.residual_norm_backward, b, None, None, b, code=-1)
+    refused(ns.residual_norm_backward, b, None, b, b, norm=False, code=-1)
+    refused(ns.residual_norm_backward, b, None, b, None, gate=w, code=-1)
+
+
 def refused(fn, *a, code, **kw):
     with pytest.raises(ns.MuonError) as e:
         fn(*a, **kw)
