@@ -468,6 +468,40 @@ int muon_qk_norm_rope_backward(const muon_qk_problem* p, void* workspace, size_t
 int muon_rope(const muon_qk_problem* p, void* stream);
 int muon_rope_backward(const muon_qk_problem* p, void* stream);
 
+/* ---- the embedding and its gradient ---------------------------------------------- */
+
+/* y[t] = scale * w[ids[t] - first] for first <= ids[t] < first + rows, and zeros
+ * for every other id: a shard of a vocabulary looks up what it holds, and a
+ * masked id (-1, -100) gives zeros.  w [rows][dim], y [tokens][dim], each of its
+ * own type; formed in fp32, rounded once.
+ * Backward: w is the gradient, dw[v] = scale * the sum of y[t] (the gradient of
+ * the lookup's y) over the tokens with ids[t] - first == v, rows without a token
+ * zero; with accumulate it is added to what dw holds, and rows without a token
+ * are not touched.  Tokens with the id `padding` (has_padding) count as without
+ * a row.  Sums are fp32, a row's tokens in their order within pieces of fixed
+ * length, one rounding on store; the order depends on the sizes and the ids, so
+ * the same call gives the same bits.
+ * Rows have unit column stride; strides are in elements; only alignment to the
+ * element size is required.  Outputs overlap no input. */
+typedef struct muon_embedding_problem {
+  int64_t tokens, rows, dim;   /* at most 2^28, 2^28 and 65536 */
+  const void* ids;             /* [tokens] */
+  int64_t first;
+  int64_t padding;             /* backward */
+  void* w; int64_t w_row_stride;   /* forward: read; backward: dw, written */
+  void* y; int64_t y_row_stride;   /* forward: written; backward: dy, read */
+  int32_t w_dtype, y_dtype;
+  int32_t ids_i64;             /* 1: int64, 0: int32 */
+  int32_t has_padding;         /* 0 or 1 */
+  int32_t accumulate;          /* backward: 0 or 1 */
+  float scale;
+  int64_t reserved;            /* must be 0 */
+} muon_embedding_problem;
+
+int muon_embedding(const muon_embedding_problem* p, void* stream);
+int muon_embedding_backward_workspace_bytes(const muon_embedding_problem* p, size_t* bytes);
+int muon_embedding_backward(const muon_embedding_problem* p, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- the norms before and after a block, its gate and its residual ------------ */
 
 /* For every row, b the output of a block and x the residual stream before it:

@@ -27,6 +27,8 @@ Entry points (same names as the C ABI):
 * ``qk_norm_rope``, ``rope`` and their ``_backward`` -- per-head norms of queries
   and keys with the position rotation (one or several axes) in the same pass,
   and the rotation alone;
+* ``embedding``, ``embedding_backward`` -- the lookup of token rows with scaling
+  (whole or a shard of a vocabulary), and its gradient by sorted tokens;
 * ``residual_norm``, ``residual_norm_backward`` -- the norms before and after a
   block with its gate and its residual stream;
 * ``grad_norm``, ``clip_grad_norm`` -- the norm over all gradients and their
@@ -569,7 +571,8 @@ def profile_query(kernel_class):
 _TORCH_OPS = {
     "layer_ops": ("linear", "linear_backward", "qk_norm_rope", "qk_norm_rope_backward", "rope", "rope_backward",
                   "ACTIVATIONS"),
-    "pass_ops": ("residual_norm", "residual_norm_backward", "grad_norm", "clip_grad_norm"),
+    "pass_ops": ("embedding", "embedding_backward", "residual_norm", "residual_norm_backward", "grad_norm",
+                 "clip_grad_norm"),
 }
 
 

@@ -104,6 +104,13 @@ class ResidualNormProblem(ctypes.Structure):
                 ("dgate_row_stride", c_i64), ("reserved", c_i64)]
 
 
+class EmbeddingProblem(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("rows", c_i64), ("dim", c_i64), ("ids", c_vp), ("first", c_i64), ("padding", c_i64),
+                ("w", c_vp), ("w_row_stride", c_i64), ("y", c_vp), ("y_row_stride", c_i64), ("w_dtype", c_i32),
+                ("y_dtype", c_i32), ("ids_i64", c_i32), ("has_padding", c_i32), ("accumulate", c_i32), ("scale", c_f32),
+                ("reserved", c_i64)]
+
+
 SIGNATURES = {
     "muon_ns_default_config": (None, [ctypes.POINTER(NSConfig)]),
     "muon_default_hparams": (None, [ctypes.POINTER(HParams)]),
@@ -137,6 +144,9 @@ SIGNATURES = {
     "muon_qk_norm_rope_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "muon_rope": (c_i32, [c_vp, c_vp]),
     "muon_rope_backward": (c_i32, [c_vp, c_vp]),
+    "muon_embedding": (c_i32, [c_vp, c_vp]),
+    "muon_embedding_backward_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
+    "muon_embedding_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),
     "muon_residual_norm": (c_i32, [c_vp, c_vp]),
     "muon_residual_norm_backward_workspace_bytes": (c_i32, [c_vp, ctypes.POINTER(c_sz)]),
     "muon_residual_norm_backward": (c_i32, [c_vp, c_vp, c_sz, c_vp]),

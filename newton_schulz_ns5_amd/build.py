@@ -16,7 +16,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmuon_mi355x.so")
 SOURCES = ["gemm_bf16.hip", "gemm_f32.hip", "elementwise.hip", "poly_small.hip", "update_gram128.hip",
            "muon_host.hip", "linear_tiles.hip", "linear_small.hip", "act_grad.hip", "qk_norm_rope.hip", "layer_host.hip",
-           "grad_norm.hip", "residual_norm.hip", "residual_norm_grad.hip", "pass_host.hip"]
+           "embedding.hip", "grad_norm.hip", "residual_norm.hip", "residual_norm_grad.hip", "pass_host.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-mcode-object-version=5", "-O3", "-std=c++17", "-fPIC",

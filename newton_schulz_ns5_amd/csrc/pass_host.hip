@@ -1,6 +1,7 @@
 // Host side of the operators around a layer's products: validation, workspace
-// carve-up and launch sequences of the gradient norm and clipping and of the
-// norms around a block.  Every argument is checked before anything is enqueued.
+// carve-up and launch sequences of the gradient norm and clipping, of the norms
+// around a block and of the embedding with its gradient.  Every argument is
+// checked before anything is enqueued.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -445,6 +446,144 @@ int muon_residual_norm_backward(const muon_residual_norm_problem* q, void* works
   n.cols = (int32_t)q->cols;
   e = launch_norm_sums(n, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "gradients of the norms' vectors");
+}
+
+}  // extern "C"
+
+namespace {
+
+// ---- embedding ----------------------------------------------------------------------------
+constexpr int64_t kMaxTokens = (int64_t)1 << 28, kMaxVocab = (int64_t)1 << 28, kMaxWidth = 65536;
+
+int check_embedding(const muon_embedding_problem* q, bool backward) {
+  if (!q) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
+  if (q->tokens < 0 || q->rows < 0 || q->dim < 0) return fail(MUON_ERR_INVALID_ARG, "negative tokens, rows or dim");
+  if (q->tokens > kMaxTokens || q->rows > kMaxVocab) return fail(MUON_ERR_INVALID_ARG, "tokens and rows must be at most 2^28");
+  if (q->dim > kMaxWidth) return fail(MUON_ERR_INVALID_ARG, "dim must be at most %lld", (long long)kMaxWidth);
+  if (!dtype_ok(q->y_dtype) || !dtype_ok(q->w_dtype)) return fail(MUON_ERR_UNSUPPORTED, "w_dtype and y_dtype must be MUON_F32 or MUON_BF16");
+  if (!std::isfinite(q->scale)) return fail(MUON_ERR_INVALID_ARG, "scale must be finite");
+  for (int32_t f : {q->ids_i64, q->has_padding, q->accumulate})
+    if (f != 0 && f != 1) return fail(MUON_ERR_INVALID_ARG, "ids_i64, has_padding and accumulate must be 0 or 1");
+  if (q->reserved) return fail(MUON_ERR_INVALID_ARG, "reserved must be 0");
+  int rc;
+  if (q->tokens && q->dim) {
+    if (!q->ids) return fail(MUON_ERR_INVALID_ARG, "ids is NULL");
+    if ((uintptr_t)q->ids % (q->ids_i64 ? 8 : 4)) return fail(MUON_ERR_INVALID_ARG, "ids is not aligned to its element size");
+    if ((rc = check_rows(backward ? "dy" : "y", q->y, q->y_dtype, q->tokens, q->dim, q->y_row_stride))) return rc;
+  }
+  const bool table = q->rows && q->dim && (backward || q->tokens);
+  if (table && (rc = check_rows(backward ? "dw" : "w", q->w, q->w_dtype, q->rows, q->dim, q->w_row_stride))) return rc;
+  if (!q->dim || !q->tokens) return MUON_OK;
+  const Rows y = rows_of("y", q->y, q->y_dtype, q->tokens, q->dim, q->y_row_stride);
+  const Rows w = rows_of("w", q->w, q->w_dtype, table ? q->rows : 0, q->dim, q->w_row_stride);
+  Rows ids = rows_of("ids", q->ids, MUON_F32, 1, q->tokens, q->tokens);
+  ids.width = ids.stride = q->tokens * (q->ids_i64 ? 8 : 4);
+  if (meet(y, w)) return fail(MUON_ERR_INVALID_ARG, backward ? "dw overlaps dy" : "y overlaps w");
+  if (meet(backward ? w : y, ids)) return fail(MUON_ERR_INVALID_ARG, backward ? "dw overlaps ids" : "y overlaps ids");
+  return MUON_OK;
+}
+
+EmbedIds ids_of(const muon_embedding_problem* q) {
+  return EmbedIds{q->ids, q->ids_i64, q->first, q->rows, q->padding, q->has_padding};
+}
+
+// How the gradient's tokens are sorted and summed; it depends on the sizes only.
+struct EmbedPlan {
+  int passes = 0, bits = 0, rounds = 0, tiles = 0, scanned = 0;
+  int piece = 0, sum_blocks = 0, col_blocks = 0;
+  int64_t pieces = 0;
+  size_t key[2] = {0, 0}, tok[2] = {0, 0}, hist = 0, totals = 0, slots = 0, bytes = 0;
+};
+
+EmbedPlan plan_embed(const muon_embedding_problem* q) {
+  EmbedPlan P;
+  const int64_t n = q->tokens;
+  if (!n || !q->rows || !q->dim) return P;
+  int width = 1;  // bits of the largest key, which is `rows`
+  while ((q->rows >> width) != 0) ++width;
+  P.passes = (width + kSortBits - 1) / kSortBits;
+  P.bits = (width + P.passes - 1) / P.passes;
+  P.rounds = n <= 131072 ? 8 : 32;
+  P.tiles = (int)cdiv(n, 256 * P.rounds);
+  P.scanned = P.tiles > 64;
+  const int group = embed_group(q->dim), per = 256 / group;
+  P.col_blocks = (int)cdiv(q->dim, 8 * group);
+  P.piece = 16;
+  while (cdiv(cdiv(n, P.piece), per) * P.col_blocks > 4096) P.piece *= 2;
+  P.pieces = cdiv(n, P.piece);
+  P.sum_blocks = (int)(cdiv(P.pieces, per) * P.col_blocks);
+  auto take = [&](size_t bytes) {
+    const size_t at = P.bytes;
+    P.bytes += align256(bytes);
+    return at;
+  };
+  for (int i = 0; i < 2; ++i) {
+    P.key[i] = take((size_t)n * 4);
+    P.tok[i] = take((size_t)n * 4);
+  }
+  P.hist = take((size_t)P.tiles * kSortBins * 4);
+  P.totals = take((size_t)kSortBins * 4);
+  P.slots = take((size_t)P.pieces * 2 * q->dim * 4);
+  return P;
+}
+
+}  // namespace
+
+extern "C" {
+
+int muon_embedding(const muon_embedding_problem* q, void* stream) {
+  const int rc = check_embedding(q, false);
+  if (rc) return rc;
+  if (!q->tokens || !q->dim) return ok();
+  const Embed p{ids_of(q), q->tokens, (int32_t)q->dim, q->w, q->w_row_stride, q->y, q->y_row_stride, q->scale};
+  const hipError_t e = launch_embed(p, q->w_dtype == MUON_BF16, q->y_dtype == MUON_BF16, (hipStream_t)stream);
+  return e == hipSuccess ? ok() : hip_fail(e, "embedding");
+}
+
+int muon_embedding_backward_workspace_bytes(const muon_embedding_problem* q, size_t* bytes) {
+  if (!bytes) return fail(MUON_ERR_INVALID_ARG, "bytes is NULL");
+  const int rc = check_embedding(q, true);
+  if (rc) return rc;
+  *bytes = plan_embed(q).bytes;
+  return ok();
+}
+
+int muon_embedding_backward(const muon_embedding_problem* q, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_embedding(q, true);
+  if (rc) return rc;
+  if (!q->rows || !q->dim || (!q->tokens && q->accumulate)) return ok();
+  const EmbedPlan P = plan_embed(q);
+  if ((rc = check_workspace(workspace, workspace_bytes, P.bytes))) return rc;
+  const hipStream_t s = (hipStream_t)stream;
+  char* const ws = (char*)workspace;
+  hipError_t e;
+  int from = 1;
+  for (int pass = 0; pass < P.passes; ++pass) {
+    EmbedSort p{};
+    p.ids = ids_of(q);
+    p.key_in = (const uint32_t*)(ws + P.key[from]); p.tok_in = (const uint32_t*)(ws + P.tok[from]);
+    p.key_out = (uint32_t*)(ws + P.key[from ^ 1]); p.tok_out = (uint32_t*)(ws + P.tok[from ^ 1]);
+    p.hist = (uint32_t*)(ws + P.hist); p.totals = (uint32_t*)(ws + P.totals);
+    p.first_pass = pass == 0; p.shift = pass * P.bits; p.bits = P.bits; p.rounds = P.rounds; p.scanned = P.scanned;
+    p.n = q->tokens;
+    if ((e = launch_sort_hist(p, P.tiles, s)) != hipSuccess) return hip_fail(e, "token counts");
+    if (P.scanned && (e = launch_sort_scan(p, P.tiles, s)) != hipSuccess) return hip_fail(e, "token counts");
+    if ((e = launch_sort_scatter(p, P.tiles, s)) != hipSuccess) return hip_fail(e, "token sort");
+    from ^= 1;
+  }
+  EmbedGrad g{};
+  g.key = (const uint32_t*)(ws + P.key[from]); g.tok = (const uint32_t*)(ws + P.tok[from]);
+  g.n = q->tokens; g.rows = q->rows; g.dim = (int32_t)q->dim; g.piece = P.piece ? P.piece : 1;
+  g.dy = q->y; g.lddy = q->y_row_stride;
+  g.dw = q->w; g.lddw = q->w_row_stride;
+  g.scale = q->scale; g.accumulate = q->accumulate;
+  g.slots = (float*)(ws + P.slots);
+  g.sum_blocks = P.sum_blocks; g.col_blocks = P.col_blocks;
+  const int clear = q->accumulate ? 0 : (int)cdiv(q->rows, 64);
+  e = launch_embed_grad(g, q->y_dtype == MUON_BF16, q->w_dtype == MUON_BF16, P.sum_blocks + clear, s);
+  if (e != hipSuccess) return hip_fail(e, "embedding gradient");
+  if (P.pieces > 1 && (e = launch_embed_join(g, q->w_dtype == MUON_BF16, s)) != hipSuccess) return hip_fail(e, "embedding gradient");
+  return ok();
 }
 
 }  // extern "C"

@@ -90,4 +90,56 @@ struct NormSums {
 };
 hipError_t launch_norm_sums(const NormSums& p, hipStream_t s);
 
+// ---- embedding -------------------------------------------------------------------------
+// A group of threads holds a row, 8 columns each; kEmbedCols columns per
+// workgroup at most.
+constexpr int kEmbedCols = 2048;
+struct EmbedIds {
+  const void* ids; int32_t i64;
+  int64_t first, rows, padding;            // padding: an id without a gradient (has_padding)
+  int32_t has_padding;
+};
+struct Embed {
+  EmbedIds ids;
+  int64_t tokens;
+  int32_t dim;
+  const void* w; int64_t ldw;
+  void* y; int64_t ldy;
+  float scale;
+};
+hipError_t launch_embed(const Embed& p, bool w_bf16, bool y_bf16, hipStream_t s);
+
+// Sorting token numbers by their row, stable: digits of `bits` bits from the
+// lowest on, by tiles of 256 * rounds tokens.  A token without a row has the
+// key `rows`.
+constexpr int kSortBits = 9, kSortBins = 1 << kSortBits;
+struct EmbedSort {
+  EmbedIds ids;                            // first pass: where keys come from
+  const uint32_t *key_in, *tok_in;         // later passes
+  uint32_t *key_out, *tok_out;
+  uint32_t* hist;                          // [tiles][kSortBins]
+  uint32_t* totals;                        // [kSortBins], where hist holds sums over the tiles before
+  int32_t first_pass, shift, bits, rounds, scanned;
+  int64_t n;
+};
+hipError_t launch_sort_hist(const EmbedSort& p, int tiles, hipStream_t s);
+hipError_t launch_sort_scan(const EmbedSort& p, int tiles, hipStream_t s);
+hipError_t launch_sort_scatter(const EmbedSort& p, int tiles, hipStream_t s);
+
+// Sums over the sorted tokens, by pieces of `piece` of them.
+struct EmbedGrad {
+  const uint32_t *key, *tok;               // sorted
+  int64_t n, rows;
+  int32_t dim, piece;
+  const void* dy; int64_t lddy;
+  void* dw; int64_t lddw;
+  float scale;
+  int32_t accumulate;
+  float* slots;                            // [pieces][2][dim]: sums that go on in the next or come from the last piece
+  int32_t sum_blocks, col_blocks;          // workgroups of the sums; those behind them clear rows without tokens
+};
+int embed_group(int64_t dim);              // threads of a group
+hipError_t launch_embed_grad(const EmbedGrad& p, bool dy_bf16, bool dw_bf16, int blocks, hipStream_t s);
+hipError_t launch_embed_join(const EmbedGrad& p, bool dw_bf16, hipStream_t s);
+
 }  // namespace muon

@@ -1,6 +1,6 @@
-"""The operators around a layer's products in a pass: the norms before and
-after a block with its gate and its residual, the norm over all gradients and
-their clipping.
+"""The operators around a layer's products in a pass: the embedding with its
+gradient, the norms before and after a block with its gate and its residual,
+the norm over all gradients and their clipping.
 
 Marshalling like :mod:`layer_ops`, whose rules hold here too: raw pointers to
 the library, work enqueued on the current stream of the tensors' device,
@@ -10,6 +10,7 @@ inputs refused.
 """
 import ctypes
 import math
+import operator
 import struct
 
 import torch
@@ -19,7 +20,7 @@ from ._lib import MUON_NORM_2, MUON_NORM_MAX
 from .layer_ops import (_CODE, _NO_WORKSPACE, _Uneven, _bad, _call, _current_device, _dt, _dual, _given, _raw_stream,
                         _refuse_capture, _refuse_tangents, _rows, _same_device, _vector, _wants_grad)
 
-__all__ = ["residual_norm", "residual_norm_backward", "grad_norm", "clip_grad_norm"]
+__all__ = ["embedding", "embedding_backward", "residual_norm", "residual_norm_backward", "grad_norm", "clip_grad_norm"]
 
 
 def _unsupported(text):
@@ -32,6 +33,109 @@ def _on(dev, fn):
         with torch.cuda.device(dev):
             return fn()
     return fn()
+
+
+# ---- the embedding and its gradient ------------------------------------------------------
+_EMBED = struct.Struct("@qqq P qq Pq Pq iiiiif q")
+
+
+def _embed_pack(tokens, rows, dim, ids, first, padding, table, values, wcode, ycode, accumulate, scale):
+    try:
+        return _EMBED.pack(tokens, rows, dim, ids.data_ptr(), operator.index(first), operator.index(padding if padding is not None else 0),
+                           *table, *values, wcode, ycode, ids.dtype is torch.int64, padding is not None, bool(accumulate), scale, 0)
+    except (OverflowError, struct.error, TypeError):  # every other field is a size or an address
+        _bad(f"first and padding_idx must be 64-bit integers and scale a number that fp32 holds, not {first!r}, {padding!r} and {scale!r}")
+
+
+def _token_ids(ids):
+    if ids.dtype not in (torch.int32, torch.int64):
+        _unsupported(f"ids are {ids.dtype}, not int32 or int64")
+    return ids if ids.is_contiguous() else ids.contiguous()
+
+
+def embedding(ids, weight, *, scale=1.0, first=0, padding_idx=None, dtype=None, out=None):
+    """``scale * weight[ids - first]``, and zeros for ids outside [first, first + rows) (see muon_embedding).
+
+    ``ids`` is int32 or int64 of any shape, ``weight`` [rows, dim] in fp32 or bf16; the result [..., dim] has
+    weight's type unless ``dtype`` or ``out`` says otherwise.  ``first`` is the first id of a shard of a vocabulary.
+    ``padding_idx`` is an id that gives weight no gradient.
+    """
+    if _wants_grad(weight):
+        if out is not None:
+            _bad("out cannot be given when weight requires a gradient")
+        _refuse_capture()
+        return _Embedding.apply(ids, weight, scale, first, padding_idx, dtype)
+    return _embedding(ids, weight, scale, first, padding_idx, dtype, out)
+
+
+def _embedding(ids, weight, scale, first, padding_idx, dtype, out=None):
+    given = () if out is None else _given(out)
+    dev = _same_device(weight, ids, out)
+    if weight.dim() != 2:
+        _bad("weight must be [rows, dim]")
+    wcode = _dt(weight)
+    rows, dim = weight.shape
+    ids = _token_ids(ids)
+    weight, wp, ldw = _input_rows(weight, "weight", weight.shape)
+    shape = ids.shape + (dim,)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or weight.dtype, device=weight.device)
+    y = _output_rows(out, "out", shape, dtype or out.dtype)
+    prob = _embed_pack(ids.numel(), rows, dim, ids, first, padding_idx, (wp, ldw), y, wcode, _dt(out), False, scale)
+    _call(dev, _lib.lib().muon_embedding, prob, None)
+    if given:
+        _written(*given)
+    return out
+
+
+def embedding_backward(dy, ids, rows, *, scale=1.0, first=0, padding_idx=None, dw_dtype=None, dw=None, accumulate=False):
+    """dw [rows, dim] of :func:`embedding` for the gradient ``dy`` of its result (see muon_embedding_backward).
+
+    ``dw_dtype`` defaults to dy's type.  A given ``dw`` is written in place, and added to with ``accumulate``
+    (rows without a token are then not touched).  No atomics: the same call gives the same bits.
+    """
+    _refuse_tangents(dy, dw)
+    given = () if dw is None else _given(dw)
+    dev = _same_device(dy, ids, dw)
+    code = _dt(dy)
+    if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
+        _bad(f"dy {tuple(dy.shape)} does not go with ids {tuple(ids.shape)}")
+    if accumulate and dw is None:
+        _bad("accumulate needs the tensor to add to")
+    try:
+        rows = operator.index(rows)
+    except TypeError:
+        _bad(f"rows must be an integer, not {rows!r}")
+    if rows < 0:
+        _bad("rows must not be negative")
+    dim = dy.shape[-1]
+    ids = _token_ids(ids)
+    dy, dyp, lddy = _input_rows(dy, "dy", dy.shape)
+    if dw is None:
+        dw = torch.empty((rows, dim), dtype=dw_dtype or dy.dtype, device=dy.device)
+    w = _output_rows(dw, "dw", (rows, dim), dw_dtype or dw.dtype)
+    prob = _embed_pack(ids.numel(), rows, dim, ids, first, padding_idx, w, (dyp, lddy), _dt(dw), code, accumulate, scale)
+    L = _lib.lib()
+    _call(dev, L.muon_embedding_backward, prob, L.muon_embedding_backward_workspace_bytes, True)
+    if given:
+        _written(*given)
+    return dw
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, weight, scale, first, padding_idx, dtype):
+        ctx.save_for_backward(ids)
+        ctx.rows, ctx.dtype = weight.shape[0] if weight.dim() else 0, weight.dtype
+        ctx.how = dict(scale=scale, first=first, padding_idx=padding_idx)
+        return _embedding(ids, weight, scale, first, padding_idx, dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        _refuse_capture()
+        ids, = ctx.saved_tensors
+        return None, embedding_backward(_row_grad(dy), ids, ctx.rows, dw_dtype=ctx.dtype, **ctx.how), None, None, None, None
 
 
 # ---- the norms before and after a block, its gate and its residual ---------------------

@@ -87,7 +87,7 @@ def test_ctypes_struct_matches_c_layout():
     import tempfile
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     lines = []
-    structs = [("muon_residual_norm_problem", _lib.ResidualNormProblem)]
+    structs = [("muon_residual_norm_problem", _lib.ResidualNormProblem), ("muon_embedding_problem", _lib.EmbeddingProblem)]
     for c, py in structs:
         lines.append(f'printf("{c} %zu\\n", sizeof({c}));')
         lines += [f'printf("{c}.{f} %zu\\n", offsetof({c}, {f}));' for f, _ in py._fields_]
@@ -103,11 +103,15 @@ def test_ctypes_struct_matches_c_layout():
             assert getattr(py, f).offset == int(lay[f"{c}.{f}"]), (c, f)
 
 
-def test_packed_norm_problem_matches_the_struct():
+def test_packed_problems_match_the_structs():
     from newton_schulz_ns5_amd import pass_ops
     assert pass_ops._NORM.size == ctypes.sizeof(_lib.ResidualNormProblem)
     fields = [f for f, _ in _lib.ResidualNormProblem._fields_]
     p = _lib.ResidualNormProblem.from_buffer_copy(pass_ops._NORM.pack(*range(1, len(fields) + 1)))
+    assert [getattr(p, f) for f in fields] == list(range(1, len(fields) + 1))
+    assert pass_ops._EMBED.size == ctypes.sizeof(_lib.EmbeddingProblem)
+    fields = [f for f, _ in _lib.EmbeddingProblem._fields_]
+    p = _lib.EmbeddingProblem.from_buffer_copy(pass_ops._EMBED.pack(*range(1, len(fields) + 1)))
     assert [getattr(p, f) for f in fields] == list(range(1, len(fields) + 1))
 
 
@@ -187,6 +191,60 @@ def test_residual_norm_bindings_refuse():
     refused(ns.residual_norm_backward, b, None, None, b, code=-1)
     refused(ns.residual_norm_backward, b, None, b, b, norm=False, code=-1)
     refused(ns.residual_norm_backward, b, None, b, None, gate=w, code=-1)
+
+
+# ---- embedding ------------------------------------------------------------------------------
+def embed_problem(**over):
+    a = dict(tokens=10, rows=20, dim=16, ids=FAKE, first=0, padding=0, w=FAKE + MIB, w_row_stride=16, y=FAKE + 2 * MIB,
+             y_row_stride=16, w_dtype=1, y_dtype=1, ids_i64=1, has_padding=0, accumulate=0, scale=1.0, reserved=0)
+    a.update(over)
+    p = _lib.EmbeddingProblem()
+    for k, v in a.items():
+        setattr(p, k, v)
+    return p
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(tokens=-1), -1), (dict(rows=-1), -1), (dict(dim=-1), -1), (dict(tokens=(1 << 28) + 1), -1), (dict(rows=(1 << 28) + 1), -1),
+    (dict(dim=65537), -1), (dict(w_dtype=2), -2), (dict(y_dtype=-1), -2), (dict(scale=math.nan), -1), (dict(ids_i64=2), -1),
+    (dict(has_padding=-1), -1), (dict(accumulate=2), -1), (dict(reserved=1), -1), (dict(ids=None), -1), (dict(ids=FAKE + 4), -1),
+    (dict(ids_i64=0, ids=FAKE + 2), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(w=FAKE + MIB + 1), -1), (dict(y=FAKE + 1), -1),
+    (dict(w_row_stride=15), -1), (dict(y_row_stride=15), -1), (dict(y_row_stride=1 << 58), -1), (dict(y=FAKE + MIB + 32), -1),
+])
+def test_embedding_refusals(over, code):
+    L = _lib.lib()
+    assert L.muon_embedding(ctypes.byref(embed_problem(**over)), None) == code
+    assert L.muon_last_error()
+    assert L.muon_embedding_backward(ctypes.byref(embed_problem(**over)), FAKE + 20 * MIB, 1 << 40, None) == code
+
+
+def test_embedding_outputs_over_the_ids():
+    L = _lib.lib()
+    assert L.muon_embedding(ctypes.byref(embed_problem(y=FAKE + 72)), None) == -1
+    assert L.muon_embedding_backward(ctypes.byref(embed_problem(w=FAKE + 72)), FAKE + 20 * MIB, 1 << 40, None) == -1
+
+
+def test_embedding_empty_calls_and_workspace():
+    L = _lib.lib()
+    need = ctypes.c_size_t(7)
+    assert L.muon_embedding(None, None) == -1 and L.muon_embedding_backward(None, None, 0, None) == -1
+    for over in (dict(tokens=0, ids=None, y=None), dict(dim=0)):
+        assert L.muon_embedding(ctypes.byref(embed_problem(**over)), None) == 0
+    for over in (dict(tokens=0, ids=None, y=None, accumulate=1), dict(dim=0), dict(rows=0, w=None)):
+        p = embed_problem(**over)
+        assert L.muon_embedding_backward(ctypes.byref(p), None, 0, None) == 0
+        assert L.muon_embedding_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0 and need.value == 0
+    p = embed_problem()
+    assert L.muon_embedding_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == 0 and need.value > 0
+    assert L.muon_embedding_backward(ctypes.byref(p), FAKE + 20 * MIB, need.value - 1, None) == -3
+    assert L.muon_embedding_backward(ctypes.byref(p), FAKE + 20 * MIB + 16, need.value, None) == -1
+    assert L.muon_embedding_backward_workspace_bytes(ctypes.byref(p), None) == -1
+
+
+def test_embedding_bindings_refuse():
+    ids, w = torch.zeros(3, dtype=torch.int64), torch.ones(4, 8)
+    refused(ns.embedding, ids, w, code=-1)  # not on a GPU
+    refused(ns.embedding_backward, torch.ones(3, 8), ids, 4, code=-1)
 
 
 def refused(fn, *a, code, **kw):
