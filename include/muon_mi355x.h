@@ -484,7 +484,8 @@ int muon_rope_backward(const muon_qk_problem* p, void* stream);
  * Rows have unit column stride; strides are in elements; only alignment to the
  * element size is required.  Outputs overlap no input. */
 typedef struct muon_embedding_problem {
-  int64_t tokens, rows, dim;   /* at most 2^28, 2^28 and 65536 */
+  int64_t tokens, rows, dim;   /* at most 2^26, 2^26 and 65536; backward: fewer
+                                * than 2^24 of tokens / 64 * dim / 256 + rows / 16 */
   const void* ids;             /* [tokens] */
   int64_t first;
   int64_t padding;             /* backward */

@@ -105,11 +105,12 @@ __device__ __forceinline__ void lds_dma16_asm(const SettledRsrc& rsrc, uint32_t 
 }
 
 // Launch a kernel taking one parameter block by value, `threads` (256 unless
-// given) threads per workgroup; returns the launch's own status.
+// given) threads and `lds` bytes of dynamic LDS per workgroup; returns the
+// launch's own status.
 template <typename P>
-inline hipError_t launch_kernel(void (*kernel)(const P), dim3 grid, const P& p, hipStream_t s, int threads = 256) {
+inline hipError_t launch_kernel(void (*kernel)(const P), dim3 grid, const P& p, hipStream_t s, int threads = 256, int lds = 0) {
   void* args[] = {const_cast<P*>(&p)};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, (size_t)lds, s);
 }
 
 }  // namespace muon

@@ -8,7 +8,7 @@
 // units and fp32 would not be faster, since the loads bound it.  The order of
 // the additions depends on the sizes alone: lanes, waves and workgroups take
 // fixed items, and the partials are added in order.
-#include "linear_epilogue.h"
+#include "chunks.h"
 #include "pass_internal.h"
 
 namespace muon {
@@ -60,10 +60,18 @@ struct Acc {
   }
 };
 
-template <bool MAX, bool BF>
+// NT_LOAD: the gradients are not read again soon (nontemporal loads leave the
+// caches to what is).
+template <bool NT_LOAD>
+__device__ __forceinline__ u32x4 load_words(const void* p) {
+  if constexpr (NT_LOAD) return __builtin_nontemporal_load((const u32x4_any*)p);
+  else return *(const u32x4_any*)p;
+}
+
+template <bool MAX, bool BF, bool NT_LOAD>
 __device__ __forceinline__ void add_item(const void* base, int64_t first, int64_t n, int lane, Acc<MAX>& acc) {
-  constexpr int W = BF ? 8 : 4;            // elements of a 16-byte load
-  constexpr int U = 8;                     // loads in flight
+  constexpr int W = BF ? 8 : 4;                      // elements of a 16-byte load
+  constexpr int U = kListItem / (64 * W) < 8 ? kListItem / (64 * W) : 8;  // loads in flight
   const char* const p = (const char*)base + first * (BF ? 2 : 4);
   auto use = [&](u32x4 a) {
 #pragma unroll
@@ -81,18 +89,18 @@ __device__ __forceinline__ void add_item(const void* base, int64_t first, int64_
     for (int r = 0; r < kListItem / (64 * W * U); ++r) {
       u32x4 a[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) a[u] = load16(p + (int64_t)((r * U + u) * 64 + lane) * 16);
+      for (int u = 0; u < U; ++u) a[u] = load_words<NT_LOAD>(p + ((r * U + u) * 64 + lane) * 16);
 #pragma unroll
       for (int u = 0; u < U; ++u) use(a[u]);
     }
     return;
   }
   const int whole = (int)n / W;
-  for (int v = lane; v < whole; v += 64) use(load16(p + (int64_t)v * 16));
+  for (int v = lane; v < whole; v += 64) use(load_words<NT_LOAD>(p + v * 16));
   for (int e = whole * W + lane; e < n; e += 64) acc.add(load_elem(p, e, BF), 0);
 }
 
-template <bool MAX>
+template <bool MAX, bool NT_LOAD>
 __global__ __launch_bounds__(NT) void norm_partial_kernel(const NormPartial p) {
   __shared__ uint64_t red[NT / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -101,8 +109,8 @@ __global__ __launch_bounds__(NT) void norm_partial_kernel(const NormPartial p) {
     int64_t first;
     const int t = find_item(p.list, item, first);
     const int64_t left = p.list.numel[t] - first;
-    if (bit(p.list.x_bf16, t)) add_item<MAX, true>(p.list.x[t], first, left, lane, acc);
-    else add_item<MAX, false>(p.list.x[t], first, left, lane, acc);
+    if (bit(p.list.x_bf16, t)) add_item<MAX, true, NT_LOAD>(p.list.x[t], first, left, lane, acc);
+    else add_item<MAX, false, NT_LOAD>(p.list.x[t], first, left, lane, acc);
   }
   uint64_t v;
   if constexpr (MAX) v = wave_max(acc.top);
@@ -170,31 +178,34 @@ __global__ __launch_bounds__(NT) void norm_total_kernel(const NormTotal p) {
   }
 }
 
-template <bool XBF, bool YBF>
+// X, Y: uint16_t for bf16.
+template <typename X, typename Y>
 __device__ __forceinline__ void scale_item(const void* x, void* y, int64_t first, int64_t n, int lane, float f) {
-  constexpr int U = 4;
+  constexpr int V = chunk_values<X, Y>(), U = 4;
+  const X* const from = (const X*)x + first;
+  Y* const to = (Y*)y + first;
+  auto store = [&](auto chunk, int at, int valid) {
+    float v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = chunk.value(e) * f;
+    round_store<Y, V, decltype(chunk)::kEdge, kStream>(to, at, valid, v);
+  };
   if (n >= kListItem) {
 #pragma unroll
-    for (int r = 0; r < kListItem / (64 * 8 * U); ++r) {
-      float v[U][8];
+    for (int r = 0; r < kListItem / (64 * V * U); ++r) {
+      Chunk<X, V, false> c[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) get8(x, first + ((r * U + u) * 64 + lane) * 8, XBF, 8, v[u]);
+      for (int u = 0; u < U; ++u) c[u].load(from, ((r * U + u) * 64 + lane) * V, V);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[u][e] *= f;
-        put8(y, first + ((r * U + u) * 64 + lane) * 8, YBF, 8, v[u]);
-      }
+      for (int u = 0; u < U; ++u) store(c[u], ((r * U + u) * 64 + lane) * V, V);
     }
     return;
   }
-  for (int at = lane * 8; at < n; at += 64 * 8) {
-    const int valid = n - at < 8 ? (int)(n - at) : 8;
-    float v[8];
-    get8(x, first + at, XBF, valid, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= f;
-    put8(y, first + at, YBF, valid, v);
+  for (int at = lane * V; at < n; at += 64 * V) {
+    const int valid = n - at < V ? (int)(n - at) : V;
+    Chunk<X, V, true> c;
+    c.load(from, at, valid);
+    store(c, at, valid);
   }
 }
 
@@ -213,18 +224,19 @@ __global__ __launch_bounds__(NT) void clip_kernel(const ClipParams p) {
     const bool xb = bit(p.list.x_bf16, t), yb = bit(p.list.y_bf16, t);
     const void* const x = p.list.x[t];
     void* const y = p.list.y[t];
-    if (xb && yb) scale_item<true, true>(x, y, first, left, lane, f);
-    else if (xb) scale_item<true, false>(x, y, first, left, lane, f);
-    else if (yb) scale_item<false, true>(x, y, first, left, lane, f);
-    else scale_item<false, false>(x, y, first, left, lane, f);
+    if (xb && yb) scale_item<uint16_t, uint16_t>(x, y, first, left, lane, f);
+    else if (xb) scale_item<uint16_t, float>(x, y, first, left, lane, f);
+    else if (yb) scale_item<float, uint16_t>(x, y, first, left, lane, f);
+    else scale_item<float, float>(x, y, first, left, lane, f);
   }
 }
 
 }  // namespace
 
 hipError_t launch_norm_partial(const NormPartial& p, int blocks, hipStream_t s) {
-  return p.max_norm_kind ? launch_kernel(norm_partial_kernel<true>, dim3(blocks), p, s, NT)
-                         : launch_kernel(norm_partial_kernel<false>, dim3(blocks), p, s, NT);
+  void (*const kernel)(const NormPartial) = p.max_norm_kind ? (p.once ? norm_partial_kernel<true, true> : norm_partial_kernel<true, false>)
+                                                            : (p.once ? norm_partial_kernel<false, true> : norm_partial_kernel<false, false>);
+  return launch_kernel(kernel, dim3(blocks), p, s, NT);
 }
 hipError_t launch_norm_total(const NormTotal& p, hipStream_t s) { return launch_kernel(norm_total_kernel, dim3(1), p, s, NT); }
 hipError_t launch_clip(const ClipParams& p, int blocks, hipStream_t s) { return launch_kernel(clip_kernel, dim3(blocks), p, s, NT); }

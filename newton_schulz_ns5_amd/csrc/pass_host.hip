@@ -16,13 +16,13 @@ namespace {
 
 // ---- gradient norm and clipping -------------------------------------------------------
 constexpr int64_t kMaxTensors = (int64_t)1 << 20;
-constexpr int kNormBlocks = 2048;  // workgroups of a launch: eight per CU
+constexpr int kNormBlocks = 1024, kClipBlocks = 16384;  // workgroups of a launch
 
 // Tensors [begin, end) of a list, one launch's: at most kListMax that are not
 // empty, and 2^30 items.
 struct ListPart { int64_t begin, end, items; };
 
-int blocks_of(int64_t items) { return (int)std::min<int64_t>(cdiv(items, 4), kNormBlocks); }
+int blocks_of(int64_t items, int most) { return (int)std::min<int64_t>(cdiv(items, 4), most); }
 
 // Calls f(part) for every launch of a list.
 template <class F>
@@ -54,7 +54,7 @@ ListPlan plan_list(int64_t n, const int64_t* numel) {
   ListPlan P;
   each_part(n, numel, [&](const ListPart& part) {
     ++P.parts;
-    P.partials += blocks_of(part.items);
+    P.partials += blocks_of(part.items, kNormBlocks);
     return MUON_OK;
   });
   return P;
@@ -137,14 +137,22 @@ int check_kind(int32_t kind) {
   return MUON_OK;
 }
 
+constexpr int64_t kInfinityCache = (int64_t)256 << 20;
+int64_t list_size(int64_t n, const int32_t* xt, const int64_t* numel) {
+  int64_t bytes = 0;
+  for (int64_t i = 0; i < n; ++i) bytes += numel[i] * esize(xt[i]);
+  return bytes;
+}
+
 // The partials of a list into the workspace.
-int run_partials(int64_t n, const void* const* x, const int32_t* xt, const int64_t* numel, int32_t kind, uint64_t* partial, hipStream_t s) {
+int run_partials(int64_t n, const void* const* x, const int32_t* xt, const int64_t* numel, int32_t kind, bool once, uint64_t* partial, hipStream_t s) {
   return each_part(n, numel, [&](const ListPart& part) {
     NormPartial p;
     fill_list(p.list, part, x, xt, nullptr, nullptr, numel);
-    const int blocks = blocks_of(part.items);
+    const int blocks = blocks_of(part.items, kNormBlocks);
     p.partial = partial;
     p.max_norm_kind = kind == MUON_NORM_MAX;
+    p.once = once;
     partial += blocks;
     const hipError_t e = launch_norm_partial(p, blocks, s);
     return e == hipSuccess ? MUON_OK : hip_fail(e, "gradient norm");
@@ -171,7 +179,7 @@ int clip(int64_t n, const void* const* x, const int32_t* xt, const int64_t* nume
   if (!total && P.parts) {
     if ((rc = check_workspace(workspace, workspace_bytes, list_bytes(P)))) return rc;
     uint64_t* const partial = (uint64_t*)workspace;
-    if ((rc = run_partials(n, x, xt, numel, kind, partial, s))) return rc;
+    if ((rc = run_partials(n, x, xt, numel, kind, list_size(n, xt, numel) > kInfinityCache, partial, s))) return rc;
     t.partial = partial; t.count = P.partials;
     // The partials of one launch are added by every workgroup of the next one
     // (one launch less); those of several once, in between.
@@ -191,7 +199,7 @@ int clip(int64_t n, const void* const* x, const int32_t* xt, const int64_t* nume
     p.max_norm = max_norm; p.eps = eps;
     p.in_place = 1;
     for (int i = 0; i < p.list.n; ++i) p.in_place &= p.list.x[i] == p.list.y[i];
-    const hipError_t e = launch_clip(p, blocks_of(part.items), s);
+    const hipError_t e = launch_clip(p, blocks_of(part.items, kClipBlocks), s);
     return e == hipSuccess ? MUON_OK : hip_fail(e, "clipping");
   });
 }
@@ -222,7 +230,7 @@ int muon_grad_norm(int64_t n, const void* const* x, const int32_t* x_dtype, cons
       return fail(MUON_ERR_INVALID_ARG, "norm or square overlaps gradient %lld", (long long)i);
   const ListPlan P = plan_list(n, numel);
   if (P.parts && (rc = check_workspace(workspace, workspace_bytes, list_bytes(P)))) return rc;
-  if ((rc = run_partials(n, x, x_dtype, numel, kind, (uint64_t*)workspace, (hipStream_t)stream))) return rc;
+  if ((rc = run_partials(n, x, x_dtype, numel, kind, true, (uint64_t*)workspace, (hipStream_t)stream))) return rc;
   NormTotal t{};
   t.partial = (const uint64_t*)workspace; t.count = P.partials;
   t.max_norm_kind = kind == MUON_NORM_MAX;
@@ -345,6 +353,13 @@ int check_norms(const muon_residual_norm_problem* q, bool backward) {
   return MUON_OK;
 }
 
+// Workgroups of the gradients' kernels that a CU holds: four waves per SIMD,
+// and a workgroup's waves are dealt out to the four SIMDs in turn.
+int norm_resident(int threads) {
+  const int waves = threads / 64;
+  return waves < 4 ? 16 / waves : 4 / (int)cdiv(waves, 4);
+}
+
 // Launch geometry of the gradients; it depends on the sizes only.
 struct NormPlan {
   int blocks = 0;
@@ -357,13 +372,13 @@ struct NormPlan {
 NormPlan plan_norm_grad(const muon_residual_norm_problem* q) {
   NormPlan P;
   const NormShape shape = norm_shape(q->cols);
-  const int threads = norm_threads(shape), rpw = threads / shape.group;
-  const int target = 256 * (1024 / threads);
+  const int threads = norm_threads(shape), rpw = norm_rows(shape);
+  const int target = 256 * norm_resident(threads);
   const int64_t each = gate_each(q);
   const bool gate_sum = q->gate && (each > 1 || q->rows == 1);
   P.gates = gate_sum ? q->rows / each : 1;
   P.span = q->rows / P.gates;
-  const int64_t chunks = std::min<int64_t>(cdiv(P.span, rpw), P.gates < target ? cdiv(target, P.gates) : 1);
+  const int64_t chunks = std::min<int64_t>(cdiv(P.span, rpw), std::max<int64_t>(1, target / P.gates));
   P.unit_rows = cdiv(cdiv(P.span, chunks), rpw) * rpw;
   P.chunks = (int)cdiv(P.span, P.unit_rows);
   P.units = P.gates * P.chunks;
@@ -391,6 +406,12 @@ ResidualNorm norm_params(const muon_residual_norm_problem* q) {
   p.gate = q->gate; p.ldg = q->gate_row_stride; p.gate_bf16 = q->gate_dtype == MUON_BF16;
   p.gate_each = gate_each(q);
   p.scale = q->scale; p.residual_scale = q->residual_scale; p.eps = q->eps; p.offset = q->weight_offset;
+  // The vectors of every row in LDS where those of the workgroups that a CU
+  // holds fit (160 KiB, less what a workgroup has besides).
+  const NormShape shape = norm_shape(q->cols);
+  const int64_t width = (int64_t)shape.group * shape.columns;
+  const int64_t held = 4 * width * ((q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && p.gate_each >= q->rows));
+  p.held = (held + 12288) * norm_resident(norm_threads(shape)) <= 163840 ? (int32_t)held : 0;
   return p;
 }
 
@@ -403,7 +424,7 @@ int muon_residual_norm(const muon_residual_norm_problem* q, void* stream) {
   if (rc) return rc;
   if (!q->rows || !q->cols) return ok();
   const NormShape shape = norm_shape(q->cols);
-  const int threads = norm_threads(shape), rpw = threads / shape.group;
+  const int threads = norm_threads(shape), rpw = norm_rows(shape);
   const int blocks = (int)std::min<int64_t>(cdiv(q->rows, rpw), 256 * (2048 / threads));
   const hipError_t e = launch_residual_norm(norm_params(q), q->dtype == MUON_BF16, q->stream_dtype == MUON_BF16, blocks, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "norms around a block");
@@ -453,12 +474,13 @@ int muon_residual_norm_backward(const muon_residual_norm_problem* q, void* works
 namespace {
 
 // ---- embedding ----------------------------------------------------------------------------
-constexpr int64_t kMaxTokens = (int64_t)1 << 28, kMaxVocab = (int64_t)1 << 28, kMaxWidth = 65536;
+constexpr int64_t kMaxTokens = (int64_t)1 << 26, kMaxVocab = (int64_t)1 << 26, kMaxWidth = 65536;
+constexpr int64_t kMaxGrid = (int64_t)1 << 24;  // workgroups of 256 threads: fewer than 2^32 in all
 
 int check_embedding(const muon_embedding_problem* q, bool backward) {
   if (!q) return fail(MUON_ERR_INVALID_ARG, "problem is NULL");
   if (q->tokens < 0 || q->rows < 0 || q->dim < 0) return fail(MUON_ERR_INVALID_ARG, "negative tokens, rows or dim");
-  if (q->tokens > kMaxTokens || q->rows > kMaxVocab) return fail(MUON_ERR_INVALID_ARG, "tokens and rows must be at most 2^28");
+  if (q->tokens > kMaxTokens || q->rows > kMaxVocab) return fail(MUON_ERR_INVALID_ARG, "tokens and rows must be at most 2^26");
   if (q->dim > kMaxWidth) return fail(MUON_ERR_INVALID_ARG, "dim must be at most %lld", (long long)kMaxWidth);
   if (!dtype_ok(q->y_dtype) || !dtype_ok(q->w_dtype)) return fail(MUON_ERR_UNSUPPORTED, "w_dtype and y_dtype must be MUON_F32 or MUON_BF16");
   if (!std::isfinite(q->scale)) return fail(MUON_ERR_INVALID_ARG, "scale must be finite");
@@ -471,6 +493,8 @@ int check_embedding(const muon_embedding_problem* q, bool backward) {
     if ((uintptr_t)q->ids % (q->ids_i64 ? 8 : 4)) return fail(MUON_ERR_INVALID_ARG, "ids is not aligned to its element size");
     if ((rc = check_rows(backward ? "dy" : "y", q->y, q->y_dtype, q->tokens, q->dim, q->y_row_stride))) return rc;
   }
+  if (backward && cdiv(q->tokens, kPieceMost) * cdiv(q->dim, kJoinCols) + cdiv(q->rows, kClearRows) >= kMaxGrid)
+    return fail(MUON_ERR_INVALID_ARG, "tokens, rows and dim are too many together");
   const bool table = q->rows && q->dim && (backward || q->tokens);
   if (table && (rc = check_rows(backward ? "dw" : "w", q->w, q->w_dtype, q->rows, q->dim, q->w_row_stride))) return rc;
   if (!q->dim || !q->tokens) return MUON_OK;
@@ -489,7 +513,8 @@ EmbedIds ids_of(const muon_embedding_problem* q) {
 
 // How the gradient's tokens are sorted and summed; it depends on the sizes only.
 struct EmbedPlan {
-  int passes = 0, bits = 0, rounds = 0, tiles = 0, scanned = 0;
+  bool ranked = false;
+  int passes = 0, bits = 0, tiles = 0, scanned = 0;
   int piece = 0, sum_blocks = 0, col_blocks = 0;
   int64_t pieces = 0;
   size_t key[2] = {0, 0}, tok[2] = {0, 0}, hist = 0, totals = 0, slots = 0, bytes = 0;
@@ -499,17 +524,18 @@ EmbedPlan plan_embed(const muon_embedding_problem* q) {
   EmbedPlan P;
   const int64_t n = q->tokens;
   if (!n || !q->rows || !q->dim) return P;
+  P.ranked = n <= kRankMost;
   int width = 1;  // bits of the largest key, which is `rows`
   while ((q->rows >> width) != 0) ++width;
   P.passes = (width + kSortBits - 1) / kSortBits;
   P.bits = (width + P.passes - 1) / P.passes;
-  P.rounds = n <= 131072 ? 8 : 32;
-  P.tiles = (int)cdiv(n, 256 * P.rounds);
+  P.tiles = (int)cdiv(n, kSortTile);
   P.scanned = P.tiles > 64;
-  const int group = embed_group(q->dim), per = 256 / group;
-  P.col_blocks = (int)cdiv(q->dim, 8 * group);
-  P.piece = 16;
-  while (cdiv(cdiv(n, P.piece), per) * P.col_blocks > 4096) P.piece *= 2;
+  const int chunk = embed_chunk(q->y_dtype == MUON_BF16, q->w_dtype == MUON_BF16);
+  const int group = embed_group(q->dim, chunk), per = 256 / group;
+  P.col_blocks = (int)cdiv(q->dim, chunk * group);
+  P.piece = kPieceLeast;
+  while (P.piece < kPieceMost && cdiv(cdiv(n, P.piece), per) * P.col_blocks > 4096) P.piece *= 2;
   P.pieces = cdiv(n, P.piece);
   P.sum_blocks = (int)(cdiv(P.pieces, per) * P.col_blocks);
   auto take = [&](size_t bytes) {
@@ -517,12 +543,14 @@ EmbedPlan plan_embed(const muon_embedding_problem* q) {
     P.bytes += align256(bytes);
     return at;
   };
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < (P.ranked ? 1 : 2); ++i) {
     P.key[i] = take((size_t)n * 4);
     P.tok[i] = take((size_t)n * 4);
   }
-  P.hist = take((size_t)P.tiles * kSortBins * 4);
-  P.totals = take((size_t)kSortBins * 4);
+  if (!P.ranked) {
+    P.hist = take((size_t)P.tiles * kSortBins * 4);
+    P.totals = take((size_t)kSortBins * 4);
+  }
   P.slots = take((size_t)P.pieces * 2 * q->dim * 4);
   return P;
 }
@@ -558,13 +586,22 @@ int muon_embedding_backward(const muon_embedding_problem* q, void* workspace, si
   char* const ws = (char*)workspace;
   hipError_t e;
   int from = 1;
-  for (int pass = 0; pass < P.passes; ++pass) {
+  if (P.ranked) {
+    EmbedSort p{};
+    p.ids = ids_of(q);
+    p.key_out = (uint32_t*)(ws + P.key[0]); p.tok_out = (uint32_t*)(ws + P.tok[0]);
+    p.first_pass = 1;
+    p.n = q->tokens;
+    if ((e = launch_sort_rank(p, s)) != hipSuccess) return hip_fail(e, "token sort");
+    from = 0;
+  }
+  for (int pass = 0; !P.ranked && pass < P.passes; ++pass) {
     EmbedSort p{};
     p.ids = ids_of(q);
     p.key_in = (const uint32_t*)(ws + P.key[from]); p.tok_in = (const uint32_t*)(ws + P.tok[from]);
     p.key_out = (uint32_t*)(ws + P.key[from ^ 1]); p.tok_out = (uint32_t*)(ws + P.tok[from ^ 1]);
     p.hist = (uint32_t*)(ws + P.hist); p.totals = (uint32_t*)(ws + P.totals);
-    p.first_pass = pass == 0; p.shift = pass * P.bits; p.bits = P.bits; p.rounds = P.rounds; p.scanned = P.scanned;
+    p.first_pass = pass == 0; p.shift = pass * P.bits; p.bits = P.bits; p.scanned = P.scanned;
     p.n = q->tokens;
     if ((e = launch_sort_hist(p, P.tiles, s)) != hipSuccess) return hip_fail(e, "token counts");
     if (P.scanned && (e = launch_sort_scan(p, P.tiles, s)) != hipSuccess) return hip_fail(e, "token counts");
@@ -579,7 +616,7 @@ int muon_embedding_backward(const muon_embedding_problem* q, void* workspace, si
   g.scale = q->scale; g.accumulate = q->accumulate;
   g.slots = (float*)(ws + P.slots);
   g.sum_blocks = P.sum_blocks; g.col_blocks = P.col_blocks;
-  const int clear = q->accumulate ? 0 : (int)cdiv(q->rows, 64);
+  const int clear = q->accumulate ? 0 : (int)cdiv(q->rows, kClearRows);
   e = launch_embed_grad(g, q->y_dtype == MUON_BF16, q->w_dtype == MUON_BF16, P.sum_blocks + clear, s);
   if (e != hipSuccess) return hip_fail(e, "embedding gradient");
   if (P.pieces > 1 && (e = launch_embed_join(g, q->w_dtype == MUON_BF16, s)) != hipSuccess) return hip_fail(e, "embedding gradient");

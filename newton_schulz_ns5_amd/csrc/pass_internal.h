@@ -14,7 +14,7 @@ namespace muon {
 // of one tensor (or what is left of it); end[i] is the items up to and with
 // tensor i.
 constexpr int kListMax = 128;
-constexpr int kListItem = 4096;
+constexpr int kListItem = 2048;
 struct TensorList {
   const void* x[kListMax];
   void* y[kListMax];                       // clipping only
@@ -29,6 +29,7 @@ struct NormPartial {
   TensorList list;
   uint64_t* partial;                       // of this launch's workgroups
   int32_t max_norm_kind;                   // 1: largest magnitude
+  int32_t once;                            // the tensors are not read again while caches hold them
 };
 // The norm from `count` partials (or `total`), and what becomes of it.
 struct NormTotal {
@@ -49,8 +50,7 @@ hipError_t launch_norm_total(const NormTotal& p, hipStream_t s);
 hipError_t launch_clip(const ClipParams& p, int blocks, hipStream_t s);
 
 // ---- norms around a block -----------------------------------------------------------
-// A row is held by kGroup threads, 8 consecutive columns per chunk, K chunks per
-// thread (columns 8 (j + k kGroup) of thread j).
+// A row is held by a group of threads, 8 or 16 columns each.
 constexpr int kNormMaxCols = 16384;
 struct ResidualNorm {
   int64_t rows;
@@ -75,11 +75,14 @@ struct ResidualNorm {
   // unit_rows each but the last.
   int64_t units, unit_rows, span;          // span: rows that gate_chunks units cover
   int32_t gate_chunks;
+  int32_t held;                            // bytes of LDS that hold the vectors of every row; 0: not held
 };
-// threads that hold a row, and chunks of 8 columns each
-struct NormShape { int group, chunks; };
+// Threads that hold a row (8 or 32, or the whole waves of a workgroup), and
+// columns of each.
+struct NormShape { int group, columns; };
 NormShape norm_shape(int64_t cols);
-int norm_threads(const NormShape& s);      // of a workgroup
+inline int norm_threads(const NormShape& s) { return s.group < 64 ? 256 : s.group; }  // of a workgroup
+inline int norm_rows(const NormShape& s) { return s.group < 64 ? 256 / s.group : 1; }
 hipError_t launch_residual_norm(const ResidualNorm& p, bool bf16, bool stream_bf16, int blocks, hipStream_t s);
 hipError_t launch_residual_norm_grad(const ResidualNorm& p, bool bf16, bool stream_bf16, int blocks, hipStream_t s);
 // out[o][j] = the sum over count[o] rows of part[o], for each of groups[o]
@@ -91,9 +94,10 @@ struct NormSums {
 hipError_t launch_norm_sums(const NormSums& p, hipStream_t s);
 
 // ---- embedding -------------------------------------------------------------------------
-// A group of threads holds a row, 8 columns each; kEmbedCols columns per
-// workgroup at most.
-constexpr int kEmbedCols = 2048;
+// A group of threads holds a row, or as much of it as a workgroup's, one chunk
+// of embed_chunk() columns each.
+int embed_chunk(bool a_bf16, bool b_bf16);
+int embed_group(int64_t dim, int chunk);   // threads of a group
 struct EmbedIds {
   const void* ids; int32_t i64;
   int64_t first, rows, padding;            // padding: an id without a gradient (has_padding)
@@ -110,18 +114,22 @@ struct Embed {
 hipError_t launch_embed(const Embed& p, bool w_bf16, bool y_bf16, hipStream_t s);
 
 // Sorting token numbers by their row, stable: digits of `bits` bits from the
-// lowest on, by tiles of 256 * rounds tokens.  A token without a row has the
+// lowest on, by tiles of kSortTile tokens.  A token without a row has the
 // key `rows`.
-constexpr int kSortBits = 9, kSortBins = 1 << kSortBits;
+constexpr int kSortBits = 9, kSortBins = 1 << kSortBits, kSortThreads = 512;
+constexpr int kSortBatch = 4, kSortTile = kSortThreads * kSortBatch;  // tokens of a thread, of a workgroup
 struct EmbedSort {
   EmbedIds ids;                            // first pass: where keys come from
   const uint32_t *key_in, *tok_in;         // later passes
   uint32_t *key_out, *tok_out;
   uint32_t* hist;                          // [tiles][kSortBins]
   uint32_t* totals;                        // [kSortBins], where hist holds sums over the tiles before
-  int32_t first_pass, shift, bits, rounds, scanned;
+  int32_t first_pass, shift, bits, scanned;
   int64_t n;
 };
+// One launch for up to kRankMost tokens; n^2 comparisons.
+constexpr int kRankMost = 8192, kRankTokens = 32;
+hipError_t launch_sort_rank(const EmbedSort& p, hipStream_t s);
 hipError_t launch_sort_hist(const EmbedSort& p, int tiles, hipStream_t s);
 hipError_t launch_sort_scan(const EmbedSort& p, int tiles, hipStream_t s);
 hipError_t launch_sort_scatter(const EmbedSort& p, int tiles, hipStream_t s);
@@ -138,7 +146,9 @@ struct EmbedGrad {
   float* slots;                            // [pieces][2][dim]: sums that go on in the next or come from the last piece
   int32_t sum_blocks, col_blocks;          // workgroups of the sums; those behind them clear rows without tokens
 };
-int embed_group(int64_t dim);              // threads of a group
+constexpr int kPieceLeast = 16, kPieceMost = 64;  // multiples of 8
+constexpr int kClearRows = 16;             // rows that a workgroup clears
+constexpr int kJoinCols = 256;             // columns that a workgroup joins
 hipError_t launch_embed_grad(const EmbedGrad& p, bool dy_bf16, bool dw_bf16, int blocks, hipStream_t s);
 hipError_t launch_embed_join(const EmbedGrad& p, bool dw_bf16, hipStream_t s);
 

@@ -2,141 +2,150 @@
 // row in the registers of a group of threads.
 #pragma once
 
+#include "chunks.h"
 #include "pass_internal.h"
-#include "row8.h"
 
 namespace muon {
 
-// Row r of a tensor of `bf16` (or fp32) values.  Where a wave holds one row its
-// address is made scalar: the lanes add 32-bit offsets to it.
+// A row is held by GS threads of a wave (8 or 32), or by a whole workgroup
+// (GS 0), which has as many waves as the row needs.
+template <int GS>
+struct Group {
+  static constexpr int kRows = GS ? 256 / GS : 1;  // rows of a workgroup
+  static constexpr int kMaxThreads = GS ? 256 : 1024;
+  static __device__ __forceinline__ int size() { return GS ? GS : (int)blockDim.x; }
+  static __device__ __forceinline__ int lane() { return GS ? (int)threadIdx.x % (GS ? GS : 1) : (int)threadIdx.x; }
+  static __device__ __forceinline__ int row() { return GS ? (int)threadIdx.x / (GS ? GS : 1) : 0; }
+};
+
+// Row r of a tensor.  Where a wave holds one row its address is made scalar:
+// the lanes add 32-bit offsets to it.
 template <int GS>
 __device__ __forceinline__ void* row_of(const void* base, int64_t r, int64_t ld, int bytes) {
   uint64_t a = (uint64_t)base + (uint64_t)(r * ld * bytes);
-  if constexpr (GS >= 64) {
+  if constexpr (GS == 0) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
     a = ((uint64_t)hi << 32) | lo;
   }
   return (void*)a;
 }
 
-// Threads of a workgroup that holds rows with groups of GS, and the rows it
-// holds at once.
-template <int GS>
-struct Rows8 {
-  static constexpr int NT = GS < 256 && GS <= 64 ? 256 : GS;
-  static constexpr int RPW = NT / GS;
-};
-
 // Sums of N values over the group that holds a row, the same bits in all its
-// threads.  Above a wave's 64 threads through LDS, two buffers in turn: one
-// barrier per sum, since a buffer is written again only after the other one's
-// barrier.
+// threads.  Over a workgroup through LDS, two buffers in turn: one barrier per
+// sum, since a buffer is written again only after the other one's barrier.
 template <int GS, int N>
 struct GroupSum {
-  float (*red)[2][N][GS > 64 ? GS / 64 : 1];
+  struct Buffer { __attribute__((aligned(16))) float v[2][N][GS ? 4 : 16]; };
+  Buffer* red;
   int turn = 0;
+  __device__ __forceinline__ explicit GroupSum(Buffer* b) : red(b) {
+    if constexpr (GS == 0) {
+      for (int i = threadIdx.x; i < 2 * N * 16; i += blockDim.x) (&red->v[0][0][0])[i] = 0.f;  // of waves that are not there
+      __syncthreads();
+    }
+  }
   template <int M>
   __device__ __forceinline__ void operator()(float (&v)[M]) {
     static_assert(M <= N, "more sums than the buffer holds");
-    constexpr int L = GS < 64 ? GS : 64;
 #pragma unroll
-    for (int off = L / 2; off >= 1; off >>= 1) {
+    for (int i = 0; i < M; ++i) v[i] = GS ? lanes_sum<GS ? GS : 64>(v[i]) : lanes_sum_last(v[i]);
+    if constexpr (GS == 0) {
+      if ((threadIdx.x & 63) == 63) {
 #pragma unroll
-      for (int i = 0; i < M; ++i) v[i] += __shfl_xor(v[i], off, 64);
-    }
-    if constexpr (GS > 64) {
-      const int wave = threadIdx.x >> 6;
-      if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-        for (int i = 0; i < M; ++i) (*red)[turn][i][wave] = v[i];
+        for (int i = 0; i < M; ++i) red->v[turn][i][threadIdx.x >> 6] = v[i];
       }
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        float t = (*red)[turn][i][0];
+      for (int i = 0; i < M; ++i) v[i] = 0.f;
+      for (int w = 0; w < (int)blockDim.x; w += 256) {
 #pragma unroll
-        for (int w = 1; w < GS / 64; ++w) t += (*red)[turn][i][w];
-        v[i] = t;
+        for (int i = 0; i < M; ++i) {
+          const f32x4 t = *(const f32x4*)&red->v[turn][i][w >> 6];
+          v[i] += (t[0] + t[1]) + (t[2] + t[3]);
+        }
       }
       turn ^= 1;
     }
   }
 };
 
-// The vectors of every row (weights, a gate for all rows) in fp32: in LDS where
-// a thread has one chunk, read again for every row where it has two.
-template <int GS, int K, int N, bool EDGE>
+// The vectors of every row (weights, a gate for all rows): held in LDS in fp32,
+// 16 bytes of a thread beside those of the others, or read from memory again
+// for every row.
+template <int GS, int K, int V, int N, bool EDGE>
 struct Vectors {
-  static constexpr bool kLds = K == 1;
-  static constexpr int kFloats = kLds ? N * 8 * GS : 4;
+  static constexpr int Q = K * V / 4;  // quarters of a thread
   const void* p[N];
-  bool bf16[N];
+  int bf16[N];
   float offset[N];  // added
-  float* lds;
-  __device__ __forceinline__ void set(int i, const void* ptr, int bf, float off) {
+  f32x4* lds[N];    // null: not held
+  __device__ __forceinline__ void set(int i, const void* ptr, int bf, float off, f32x4*& at, int held) {
     p[i] = ptr;
-    bf16[i] = bf != 0;
+    bf16[i] = bf;
     offset[i] = off;
+    lds[i] = held && ptr ? at : nullptr;
+    if (lds[i]) at += Q * Group<GS>::size();
   }
-  // Fills the LDS copies (threads of the first group); a barrier follows.
-  __device__ __forceinline__ void fill(int cols) {
-    if constexpr (kLds) {
-      if ((int)threadIdx.x < GS) {
-        const int col = 8 * threadIdx.x, valid = cols - col < 0 ? 0 : (cols - col < 8 ? cols - col : 8);
+  __device__ __forceinline__ void read(int i, int col, int valid, float (&v)[V]) const {
+    load_values<V, EDGE>(p[i], col, bf16[i] != 0, valid, v);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          float v[8] = {};
-          if (valid > 0) read(i, col, valid, v);
+    for (int e = 0; e < V; ++e) v[e] += offset[i];
+  }
+  // Threads of the workgroup's first row; a barrier follows.
+  __device__ __forceinline__ void fill(const int (&col)[K], const int (&valid)[K]) {
+    if (Group<GS>::row() == 0) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            ((f32x4*)lds)[(2 * i + h) * GS + threadIdx.x] = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+      for (int i = 0; i < N; ++i) {
+        if (!lds[i]) continue;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          if (valid[k] <= 0) continue;
+          float v[V];
+          read(i, col[k], valid[k], v);
+#pragma unroll
+          for (int h = 0; h < V / 4; ++h)
+            lds[i][(k * (V / 4) + h) * Group<GS>::size() + Group<GS>::lane()] = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
         }
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
-  __device__ __forceinline__ void read(int i, int col, int valid, float (&v)[8]) const {
-    if (p[i]) {
-      load_values<EDGE>(p[i], col, bf16[i], valid, v);
+  // Chunk k of this thread: ones without a vector.
+  __device__ __forceinline__ void get(int i, int k, int col, int valid, float (&v)[V]) const {
+    if (lds[i]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += offset[i];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 1.f;
-    }
-  }
-  // Columns col .. col + 7, chunk j of the group.
-  __device__ __forceinline__ void get(int i, int j, int col, int valid, float (&v)[8]) const {
-    if constexpr (kLds) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4 t = ((const f32x4*)lds)[(2 * i + h) * GS + j];
+      for (int h = 0; h < V / 4; ++h) {
+        const f32x4 t = lds[i][(k * (V / 4) + h) * Group<GS>::size() + Group<GS>::lane()];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[4 * h + e] = t[e];
       }
-    } else {
+    } else if (p[i]) {
       read(i, col, valid, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = 1.f;
     }
   }
 };
 
-// f called with the group size and chunk count of a row of `cols` columns.
-template <class F>
-hipError_t with_norm_shape(const NormShape& s, bool edge, F&& f) {
-#define MUON_SHAPE(G, K)                                                                                                \
-  if (s.group == G && s.chunks == K)                                                                                    \
-    return edge ? f(std::integral_constant<int, G>{}, std::integral_constant<int, K>{}, std::integral_constant<bool, true>{}) \
-                : f(std::integral_constant<int, G>{}, std::integral_constant<int, K>{}, std::integral_constant<bool, false>{})
-  MUON_SHAPE(8, 1);
-  MUON_SHAPE(16, 1);
-  MUON_SHAPE(32, 1);
-  MUON_SHAPE(64, 1);
-  MUON_SHAPE(128, 1);
-  MUON_SHAPE(256, 1);
-  MUON_SHAPE(512, 1);
-  MUON_SHAPE(1024, 1);
-  MUON_SHAPE(1024, 2);
-#undef MUON_SHAPE
+// f called with what a kernel is compiled for: the threads that hold a row and
+// the columns of each, a norm after the block, a gate, rows that end in part of
+// a chunk.
+template <int GS, int C, typename F>
+hipError_t with_norm_flags(const ResidualNorm& p, F&& f) {
+  using std::bool_constant;
+  const std::integral_constant<int, GS> g;
+  const std::integral_constant<int, C> c;
+  auto edge = [&](auto post, auto gate) { return p.cols % 8 ? f(g, c, post, gate, bool_constant<true>{}) : f(g, c, post, gate, bool_constant<false>{}); };
+  if (p.post) return p.gate ? edge(bool_constant<true>{}, bool_constant<true>{}) : edge(bool_constant<true>{}, bool_constant<false>{});
+  return p.gate ? edge(bool_constant<false>{}, bool_constant<true>{}) : edge(bool_constant<false>{}, bool_constant<false>{});
+}
+template <typename F>
+hipError_t with_norm_form(const NormShape& s, const ResidualNorm& p, F&& f) {
+  if (s.group == 8 && s.columns == 8) return with_norm_flags<8, 8>(p, f);
+  if (s.group == 32 && s.columns == 8) return with_norm_flags<32, 8>(p, f);
+  if (s.group >= 64 && s.columns == 8) return with_norm_flags<0, 8>(p, f);
+  if (s.group >= 64 && s.columns == 16) return with_norm_flags<0, 16>(p, f);
   return hipErrorInvalidValue;
 }
 

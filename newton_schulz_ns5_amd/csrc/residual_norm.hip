@@ -12,31 +12,31 @@
 namespace muon {
 namespace {
 
-template <typename T, typename R, int GS, int K, bool EDGE>
-__global__ __launch_bounds__(Rows8<GS>::NT) void residual_norm_kernel(const ResidualNorm p) {
-  constexpr int RPW = Rows8<GS>::RPW;
-  constexpr bool AHEAD = K == 1;     // the next row's loads in flight
+template <typename T, typename R, int GS, int C, bool POST, bool GATE, bool EDGE>
+__global__ __launch_bounds__(Group<GS>::kMaxThreads) void residual_norm_kernel(const ResidualNorm p) {
+  constexpr int V = chunk_values<T, R>(), K = C / V;
+  constexpr bool AHEAD = C == 8;     // the next row's loads in flight
+  constexpr StorePolicy TO_STREAM = kPlain, TO_Y = kPlain;
   enum { W, PW, G };
-  __shared__ float red[2][1][GS > 64 ? GS / 64 : 1];
-  __shared__ __attribute__((aligned(16))) float held[Vectors<GS, K, 3, EDGE>::kFloats];
-  GroupSum<GS, 1> sum{&red};
-  const int j = threadIdx.x % GS, grp = threadIdx.x / GS;
+  extern __shared__ __attribute__((aligned(16))) f32x4 held[];
+  __shared__ typename GroupSum<GS, 1>::Buffer red;
+  GroupSum<GS, 1> sum(&red);
   int col[K], valid[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    col[k] = 8 * (j + k * GS);
-    valid[k] = p.cols - col[k] < 0 ? 0 : (p.cols - col[k] < 8 ? p.cols - col[k] : 8);
+    col[k] = V * (Group<GS>::lane() + k * Group<GS>::size());
+    valid[k] = p.cols - col[k] < 0 ? 0 : (p.cols - col[k] < V ? p.cols - col[k] : V);
   }
-  const bool gate_all = p.gate && p.gate_each >= p.rows;  // one row of the gate
-  Vectors<GS, K, 3, EDGE> vec;
-  vec.lds = held;
-  vec.set(W, p.weight, p.weight_bf16, p.offset);
-  vec.set(PW, p.post_weight, p.weight_bf16, p.offset);
-  vec.set(G, gate_all ? p.gate : nullptr, p.gate_bf16, 0.f);
-  vec.fill(p.cols);
+  const bool gate_all = GATE && p.gate_each >= p.rows;  // one row of the gate
+  Vectors<GS, K, V, 3, EDGE> vec;
+  f32x4* at = held;
+  vec.set(W, p.norm ? p.weight : nullptr, p.weight_bf16, p.offset, at, p.held);
+  vec.set(PW, POST ? p.post_weight : nullptr, p.weight_bf16, p.offset, at, p.held);
+  vec.set(G, gate_all ? p.gate : nullptr, p.gate_bf16, 0.f, at, p.held);
+  vec.fill(col, valid);
   const float inv = 1.f / (float)p.cols;
-  Raw8<T, EDGE> bn[K];
-  Raw8<R, EDGE> xn[K];
+  Chunk<T, V, EDGE> bn[K];
+  Chunk<R, V, EDGE> xn[K];
   auto load_row = [&](int64_t r) {
     const void* const b = row_of<GS>(p.block, r, p.ldb, sizeof(T));
     const void* const x = row_of<GS>(p.residual, r, p.ldr, sizeof(R));
@@ -47,59 +47,59 @@ __global__ __launch_bounds__(Rows8<GS>::NT) void residual_norm_kernel(const Resi
       if (p.residual) xn[k].load(x, col[k], valid[k]);
     }
   };
-  const int64_t step = (int64_t)gridDim.x * RPW;
-  int64_t r = (int64_t)blockIdx.x * RPW + grp;
+  const int64_t step = (int64_t)gridDim.x * Group<GS>::kRows;
+  int64_t r = (int64_t)blockIdx.x * Group<GS>::kRows + Group<GS>::row();
   if (AHEAD && r < p.rows) load_row(r);
   for (; r < p.rows; r += step) {
     if constexpr (!AHEAD) load_row(r);
-    float v[K][8];
-    Raw8<R, EDGE> x[K];
+    float v[K][V];
+    Chunk<R, V, EDGE> x[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = valid[k] > 0 ? bn[k].value(e) : 0.f;
+      for (int e = 0; e < V; ++e) v[k][e] = valid[k] > 0 ? bn[k].value(e) : 0.f;
       x[k] = xn[k];
     }
     if (AHEAD && r + step < p.rows) load_row(r + step);
-    if (p.post) {
+    if (POST) {
       float ss[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] += v[k][e] * v[k][e];
+        for (int e = 0; e < V; ++e) ss[0] += v[k][e] * v[k][e];
       }
       sum(ss);
       const float rs = __frsqrt_rn(ss[0] * inv + p.eps);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (valid[k] <= 0) continue;
-        float t[8];
-        vec.get(PW, j, col[k], valid[k], t);
+        float t[V];
+        vec.get(PW, k, col[k], valid[k], t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= rs * t[e];
+        for (int e = 0; e < V; ++e) v[k][e] *= rs * t[e];
       }
     }
-    const int64_t gr = !p.gate || gate_all ? 0 : (int64_t)((uint32_t)r / (uint32_t)p.gate_each);
+    const int64_t gr = !GATE || gate_all ? 0 : (int64_t)((uint32_t)r / (uint32_t)p.gate_each);
     const void* const gate = row_of<GS>(p.gate, gr, p.ldg, p.gate_bf16 ? 2 : 4);
     void* const stream = row_of<GS>(p.stream, r, p.lds, sizeof(R));
     float ss[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (valid[k] <= 0) continue;
-      if (p.gate) {
-        float t[8];
-        if (gate_all) vec.get(G, j, col[k], valid[k], t);
-        else load_values<EDGE>(gate, col[k], p.gate_bf16 != 0, valid[k], t);
+      if (GATE) {
+        float t[V];
+        if (gate_all) vec.get(G, k, col[k], valid[k], t);
+        else load_values<V, EDGE>(gate, col[k], p.gate_bf16 != 0, valid[k], t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= t[e];
+        for (int e = 0; e < V; ++e) v[k][e] *= t[e];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < V; ++e) {
         v[k][e] *= p.scale;
         if (p.residual) v[k][e] = fmaf(p.residual_scale, x[k].value(e), v[k][e]);
         ss[0] += v[k][e] * v[k][e];
       }
-      if (p.stream) round_store<R, EDGE>(stream, col[k], valid[k], v[k]);
+      if (p.stream) round_store<R, V, EDGE, TO_STREAM>(stream, col[k], valid[k], v[k]);
     }
     if (p.norm) {
       sum(ss);
@@ -108,11 +108,11 @@ __global__ __launch_bounds__(Rows8<GS>::NT) void residual_norm_kernel(const Resi
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (valid[k] <= 0) continue;
-        float t[8];
-        vec.get(W, j, col[k], valid[k], t);
+        float t[V];
+        vec.get(W, k, col[k], valid[k], t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= rs * t[e];
-        round_store<T, EDGE>(y, col[k], valid[k], v[k]);
+        for (int e = 0; e < V; ++e) v[k][e] *= rs * t[e];
+        round_store<T, V, EDGE, TO_Y>(y, col[k], valid[k], v[k]);
       }
     }
   }
@@ -120,9 +120,11 @@ __global__ __launch_bounds__(Rows8<GS>::NT) void residual_norm_kernel(const Resi
 
 template <typename T, typename R>
 hipError_t launch_types(const ResidualNorm& p, int blocks, hipStream_t s) {
-  return with_norm_shape(norm_shape(p.cols), p.cols % 8 != 0, [&](auto g, auto k, auto e) {
-    constexpr int GS = decltype(g)::value, K = decltype(k)::value;
-    return launch_kernel(residual_norm_kernel<T, R, GS, K, decltype(e)::value>, dim3((unsigned)blocks), p, s, Rows8<GS>::NT);
+  const NormShape shape = norm_shape(p.cols);
+  return with_norm_form(shape, p, [&](auto g, auto c, auto post, auto gate, auto e) {
+    return launch_kernel(residual_norm_kernel<T, R, decltype(g)::value, decltype(c)::value, decltype(post)::value, decltype(gate)::value,
+                                              decltype(e)::value>,
+                         dim3((unsigned)blocks), p, s, norm_threads(shape), p.held);
   });
 }
 
@@ -130,13 +132,10 @@ hipError_t launch_types(const ResidualNorm& p, int blocks, hipStream_t s) {
 
 NormShape norm_shape(int64_t cols) {
   const int64_t chunks = (cols + 7) / 8;
-  int g = 8;
-  while (g < 1024 && g < chunks) g *= 2;
-  int k = 1;
-  while ((int64_t)k * g < chunks) k *= 2;
-  return {g, k};
+  if (chunks <= 32) return {chunks <= 8 ? 8 : 32, 8};
+  if (chunks <= 1024) return {(int)((chunks + 63) / 64 * 64), 8};
+  return {(int)((chunks + 127) / 128 * 64), 16};
 }
-int norm_threads(const NormShape& s) { return s.group <= 64 ? 256 : s.group; }
 
 hipError_t launch_residual_norm(const ResidualNorm& p, bool bf16, bool stream_bf16, int blocks, hipStream_t s) {
   if (bf16) return stream_bf16 ? launch_types<uint16_t, uint16_t>(p, blocks, s) : launch_types<uint16_t, float>(p, blocks, s);

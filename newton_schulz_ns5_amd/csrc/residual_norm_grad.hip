@@ -16,64 +16,66 @@
 namespace muon {
 namespace {
 
-template <typename T, typename R, int GS, int K, bool EDGE>
-__global__ __launch_bounds__(Rows8<GS>::NT, 4) void residual_norm_grad_kernel(const ResidualNorm p) {
-  constexpr int RPW = Rows8<GS>::RPW, NT = Rows8<GS>::NT;
-  constexpr bool AHEAD = K == 1;     // the next row's loads in flight
+template <typename T, typename R, int GS, int C, bool POST, bool GATE, bool EDGE>
+__global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_kernel(const ResidualNorm p) {
+  constexpr int V = chunk_values<T, R>(), K = C / V;
+  constexpr int ROWS = Group<GS>::kRows;
+  constexpr bool AHEAD = C == 8;  // the next row's loads in flight, where the registers allow it
+  constexpr bool NEED_B = POST || GATE;
   enum { W, PW, G };
-  __shared__ float red[2][3][GS > 64 ? GS / 64 : 1];
-  __shared__ float rows[RPW > 1 ? NT / 64 : 1][RPW > 1 ? 8 * GS : 1];
-  __shared__ __attribute__((aligned(16))) float held[Vectors<GS, K, 3, EDGE>::kFloats];
-  GroupSum<GS, 3> sum{&red};
-  const int j = threadIdx.x % GS, grp = threadIdx.x / GS;
+  extern __shared__ __attribute__((aligned(16))) f32x4 held[];
+  __shared__ typename GroupSum<GS, 3>::Buffer red;
+  __shared__ float rows[ROWS > 1 ? 4 : 1][ROWS > 1 ? V * GS : 1];
+  GroupSum<GS, 3> sum(&red);
+  const int lane = Group<GS>::lane(), grp = Group<GS>::row();
   int col[K], valid[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    col[k] = 8 * (j + k * GS);
-    valid[k] = p.cols - col[k] < 0 ? 0 : (p.cols - col[k] < 8 ? p.cols - col[k] : 8);
+    col[k] = V * (lane + k * Group<GS>::size());
+    valid[k] = p.cols - col[k] < 0 ? 0 : (p.cols - col[k] < V ? p.cols - col[k] : V);
   }
-  const bool gate_all = p.gate && p.gate_each >= p.rows;
-  const bool gate_row = p.gate && p.gate_each == 1 && !gate_all;  // a gate for every row: its gradient is not a sum
-  Vectors<GS, K, 3, EDGE> vec;
-  vec.lds = held;
-  vec.set(W, p.weight, p.weight_bf16, p.offset);
-  vec.set(PW, p.post_weight, p.weight_bf16, p.offset);
-  vec.set(G, gate_all ? p.gate : nullptr, p.gate_bf16, 0.f);
-  vec.fill(p.cols);
-  float aw[K][8], ap[K][8], ag[K][8];
+  const bool gate_all = GATE && p.gate_each >= p.rows;
+  const bool gate_row = GATE && p.gate_each == 1 && !gate_all;  // a gate for every row: its gradient is not a sum
+  const int gate_bytes = p.gate_bf16 ? 2 : 4;
+  Vectors<GS, K, V, 3, EDGE> vec;
+  f32x4* at = held;
+  vec.set(W, p.norm ? p.weight : nullptr, p.weight_bf16, p.offset, at, p.held);
+  vec.set(PW, POST ? p.post_weight : nullptr, p.weight_bf16, p.offset, at, p.held);
+  vec.set(G, gate_all ? p.gate : nullptr, p.gate_bf16, 0.f, at, p.held);
+  vec.fill(col, valid);
+  float aw[K][V], ap[K][V], ag[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) aw[k][e] = ap[k][e] = ag[k][e] = 0.f;
+    for (int e = 0; e < V; ++e) aw[k][e] = ap[k][e] = ag[k][e] = 0.f;
   }
   // A sum over a workgroup's rows: its groups' sums in order, by the threads
   // of the first group.
-  auto total = [&](float (&a)[8]) {
-    if constexpr (RPW > 1) {
+  auto total = [&](float (&a)[V]) {
+    if constexpr (ROWS > 1) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < V; ++e) {
 #pragma unroll
-        for (int off = 32; off >= GS; off >>= 1) a[e] += __shfl_xor(a[e], off, 64);
+        for (int off = 32; off >= (GS ? GS : 64); off >>= 1) a[e] += __shfl_xor(a[e], off, 64);
       }
       __syncthreads();  // what was there has been read
       if ((threadIdx.x & 63) < GS) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) rows[threadIdx.x >> 6][8 * j + e] = a[e];
+        for (int e = 0; e < V; ++e) rows[threadIdx.x >> 6][V * lane + e] = a[e];
       }
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = rows[0][8 * j + e];
+      for (int e = 0; e < V; ++e) {
+        a[e] = rows[0][V * lane + e];
 #pragma unroll
-        for (int q = 1; q < NT / 64; ++q) a[e] += rows[q][8 * j + e];
+        for (int q = 1; q < 4; ++q) a[e] += rows[q][V * lane + e];
       }
     }
   };
   const float inv = 1.f / (float)p.cols;
-  const bool need_b = p.post || p.gate;
   struct Row {
-    Raw8<T, EDGE> dy[K], b[K];
-    Raw8<R, EDGE> s[K], ds[K];
+    Chunk<T, V, EDGE> dy[K], b[K];
+    Chunk<R, V, EDGE> s[K], ds[K];
   };
   auto load_row = [&](int64_t r, Row& w) {
     const void* const dy = row_of<GS>(p.dy, r, p.lddy, sizeof(T));
@@ -88,7 +90,7 @@ __global__ __launch_bounds__(Rows8<GS>::NT, 4) void residual_norm_grad_kernel(co
         w.s[k].load(st, col[k], valid[k]);
       }
       if (p.dstream) w.ds[k].load(ds, col[k], valid[k]);
-      if (need_b) w.b[k].load(b, col[k], valid[k]);
+      if (NEED_B) w.b[k].load(b, col[k], valid[k]);
     }
   };
   for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
@@ -96,126 +98,137 @@ __global__ __launch_bounds__(Rows8<GS>::NT, 4) void residual_norm_grad_kernel(co
     const int64_t r0 = g * p.span + (u - g * p.gate_chunks) * p.unit_rows;
     const int64_t end = (g + 1) * p.span < p.rows ? (g + 1) * p.span : p.rows;
     const int64_t r1 = r0 + p.unit_rows < end ? r0 + p.unit_rows : end;
+    const void* gate = GATE && !gate_all && !gate_row ? row_of<GS>(p.gate, g, p.ldg, gate_bytes) : nullptr;
     int64_t r = r0 + grp;
     Row row, next;
     if (AHEAD && r < r1) load_row(r, next);
-    for (; r < r1; r += RPW) {
+    for (; r < r1; r += ROWS) {
       if constexpr (AHEAD) {
         row = next;
-        if (r + RPW < r1) load_row(r + RPW, next);
+        if (r + ROWS < r1) load_row(r + ROWS, next);
       } else {
         load_row(r, row);
       }
+      if (gate_row) gate = row_of<GS>(p.gate, r, p.ldg, gate_bytes);
+      // sum s^2, sum dy w s, sum b^2
       float q[3] = {0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (valid[k] <= 0) continue;
         if (p.norm) {
-          float w[8];
-          vec.get(W, j, col[k], valid[k], w);
+          float w[V];
+          vec.get(W, k, col[k], valid[k], w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < V; ++e) {
             q[0] += row.s[k].value(e) * row.s[k].value(e);
             q[1] += row.dy[k].value(e) * w[e] * row.s[k].value(e);
           }
         }
-        if (p.post) {
+        if (POST) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q[2] += row.b[k].value(e) * row.b[k].value(e);
+          for (int e = 0; e < V; ++e) q[2] += row.b[k].value(e) * row.b[k].value(e);
         }
       }
-      if (p.norm || p.post) sum(q);
-      const float rs = p.norm ? __frsqrt_rn(q[0] * inv + p.eps) : 0.f, mean = q[1] * rs * inv;
-      const float rb = p.post ? __frsqrt_rn(q[2] * inv + p.eps) : 1.f;
-      const int64_t gr = !p.gate || gate_all ? 0 : (int64_t)((uint32_t)r / (uint32_t)p.gate_each);
+      if constexpr (POST) {
+        sum(q);
+      } else if (p.norm) {
+        float two[2] = {q[0], q[1]};
+        sum(two);
+        q[0] = two[0];
+        q[1] = two[1];
+      }
+      // D = ds + rs dy w - c s, c = rs^3 mean(dy w s)
+      const float rs = p.norm ? __frsqrt_rn(q[0] * inv + p.eps) : 0.f, c = q[1] * inv * rs * rs * rs;
+      const float rb = POST ? __frsqrt_rn(q[2] * inv + p.eps) : 1.f;
       void* const dres = row_of<GS>(p.dresidual, r, p.lddr, sizeof(R));
-      const void* const gate = row_of<GS>(p.gate, gr, p.ldg, p.gate_bf16 ? 2 : 4);
-      float d[K][8];
+      float d[K][V];
       float dot[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (valid[k] <= 0) continue;
+        if (p.dstream) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[k][e] = p.dstream ? row.ds[k].value(e) : 0.f;
+          for (int e = 0; e < V; ++e) d[k][e] = row.ds[k].value(e);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) d[k][e] = 0.f;
+        }
         if (p.norm) {
-          float w[8];
-          vec.get(W, j, col[k], valid[k], w);
+          float w[V];
+          vec.get(W, k, col[k], valid[k], w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float n = row.s[k].value(e) * rs, dy = row.dy[k].value(e);
-            aw[k][e] += dy * n;
-            d[k][e] += rs * (dy * w[e] - n * mean);
+          for (int e = 0; e < V; ++e) {
+            const float dy = row.dy[k].value(e), s = row.s[k].value(e);
+            aw[k][e] += dy * (s * rs);
+            d[k][e] = fmaf(-c, s, fmaf(rs, dy * w[e], d[k][e]));
           }
         }
         if (p.dresidual) {
-          float t[8];
+          float t[V];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) t[e] = p.residual_scale * d[k][e];
-          round_store<R, EDGE>(dres, col[k], valid[k], t);
+          for (int e = 0; e < V; ++e) t[e] = p.residual_scale * d[k][e];
+          round_store<R, V, EDGE, kPlain>(dres, col[k], valid[k], t);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[k][e] *= p.scale;       // t
-        float pw[8];
-        if (p.post) {
-          vec.get(PW, j, col[k], valid[k], pw);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pw[e] = 1.f;
+        for (int e = 0; e < V; ++e) d[k][e] *= p.scale;        // t
+        float gt[V], pw[V];
+        if (GATE) {
+          if (gate_all) vec.get(G, k, col[k], valid[k], gt);
+          else load_values<V, EDGE>(gate, col[k], p.gate_bf16 != 0, valid[k], gt);
         }
-        if (p.gate) {
-          float gt[8], dg[8];
-          if (gate_all) vec.get(G, j, col[k], valid[k], gt);
-          else load_values<EDGE>(gate, col[k], p.gate_bf16 != 0, valid[k], gt);
+        if (POST) vec.get(PW, k, col[k], valid[k], pw);
+        float dg[V];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            dg[e] = d[k][e] * (row.b[k].value(e) * rb) * pw[e];
+        for (int e = 0; e < V; ++e) {
+          const float m = POST ? row.b[k].value(e) * rb : NEED_B ? row.b[k].value(e) : 0.f;
+          const float tm = d[k][e] * m;
+          if (GATE) {
+            dg[e] = POST ? tm * pw[e] : tm;
             d[k][e] *= gt[e];
           }
-          if (gate_row) {
-            if (p.dgate) store_values<EDGE>(row_of<GS>(p.dgate, r, p.lddg, p.gate_bf16 ? 2 : 4), col[k], p.gate_bf16 != 0, valid[k], dg);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ag[k][e] += dg[e];
-          }
-        }
-        if (p.post) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float m = row.b[k].value(e) * rb;
-            ap[k][e] += d[k][e] * m;
+          if (POST) {
+            ap[k][e] += GATE ? tm * gt[e] : tm;
             d[k][e] *= pw[e];                                  // k
             dot[0] += d[k][e] * m;
           }
         }
+        if (GATE) {
+          if (gate_row) {
+            if (p.dgate) store_values<V, EDGE>(row_of<GS>(p.dgate, r, p.lddg, gate_bytes), col[k], p.gate_bf16 != 0, valid[k], dg);
+          } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) ag[k][e] += dg[e];
+          }
+        }
       }
-      if (p.post) {
+      if (POST) {
         sum(dot);
-        const float mk = dot[0] * inv;
+        const float cb = dot[0] * inv * rb * rb;               // of b, which is m / rb
 #pragma unroll
         for (int k = 0; k < K; ++k) {
           if (valid[k] <= 0) continue;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[k][e] = rb * (d[k][e] - row.b[k].value(e) * rb * mk);
+          for (int e = 0; e < V; ++e) d[k][e] = fmaf(-cb, row.b[k].value(e), rb * d[k][e]);
         }
       }
       if (p.dblock) {
         void* const db = row_of<GS>(p.dblock, r, p.lddb, sizeof(T));
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (valid[k] > 0) round_store<T, EDGE>(db, col[k], valid[k], d[k]);
+          if (valid[k] > 0) round_store<T, V, EDGE, kPlain>(db, col[k], valid[k], d[k]);
         }
       }
     }
-    if (p.gate && !gate_row && (p.dgate || p.part[2])) {
+    if (GATE && !gate_row && (p.dgate || p.part[2])) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         total(ag[k]);
         if (grp == 0 && valid[k] > 0) {
-          if (p.part[2]) round_store<float, EDGE>(p.part[2] + u * p.cols, col[k], valid[k], ag[k]);
-          else store_values<EDGE>((char*)p.dgate + g * p.lddg * (p.gate_bf16 ? 2 : 4), col[k], p.gate_bf16 != 0, valid[k], ag[k]);
+          if (p.part[2]) round_store<float, V, EDGE, kPlain>(p.part[2] + u * p.cols, col[k], valid[k], ag[k]);
+          else store_values<V, EDGE>((char*)p.dgate + g * p.lddg * gate_bytes, col[k], p.gate_bf16 != 0, valid[k], ag[k]);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ag[k][e] = 0.f;
+        for (int e = 0; e < V; ++e) ag[k][e] = 0.f;
       }
     }
   }
@@ -223,11 +236,11 @@ __global__ __launch_bounds__(Rows8<GS>::NT, 4) void residual_norm_grad_kernel(co
   for (int k = 0; k < K; ++k) {
     if (p.part[0]) {
       total(aw[k]);
-      if (grp == 0 && valid[k] > 0) round_store<float, EDGE>(p.part[0] + (int64_t)blockIdx.x * p.cols, col[k], valid[k], aw[k]);
+      if (grp == 0 && valid[k] > 0) round_store<float, V, EDGE, kPlain>(p.part[0] + (int64_t)blockIdx.x * p.cols, col[k], valid[k], aw[k]);
     }
-    if (p.part[1]) {
+    if (POST && p.part[1]) {
       total(ap[k]);
-      if (grp == 0 && valid[k] > 0) round_store<float, EDGE>(p.part[1] + (int64_t)blockIdx.x * p.cols, col[k], valid[k], ap[k]);
+      if (grp == 0 && valid[k] > 0) round_store<float, V, EDGE, kPlain>(p.part[1] + (int64_t)blockIdx.x * p.cols, col[k], valid[k], ap[k]);
     }
   }
 }
@@ -258,9 +271,11 @@ __global__ __launch_bounds__(SC * SP) void norm_sums_kernel(const NormSums p) {
 
 template <typename T, typename R>
 hipError_t launch_types(const ResidualNorm& p, int blocks, hipStream_t s) {
-  return with_norm_shape(norm_shape(p.cols), p.cols % 8 != 0, [&](auto g, auto k, auto e) {
-    constexpr int GS = decltype(g)::value, K = decltype(k)::value;
-    return launch_kernel(residual_norm_grad_kernel<T, R, GS, K, decltype(e)::value>, dim3((unsigned)blocks), p, s, Rows8<GS>::NT);
+  const NormShape shape = norm_shape(p.cols);
+  return with_norm_form(shape, p, [&](auto g, auto c, auto post, auto gate, auto e) {
+    return launch_kernel(residual_norm_grad_kernel<T, R, decltype(g)::value, decltype(c)::value, decltype(post)::value,
+                                                   decltype(gate)::value, decltype(e)::value>,
+                         dim3((unsigned)blocks), p, s, norm_threads(shape), p.held);
   });
 }
 

@@ -9,6 +9,7 @@ place with their autograd version counters moved, tracers and forward-mode
 inputs refused.
 """
 import ctypes
+import functools
 import math
 import operator
 import struct
@@ -79,8 +80,10 @@ def _embedding(ids, weight, scale, first, padding_idx, dtype, out=None):
     weight, wp, ldw = _input_rows(weight, "weight", weight.shape)
     shape = ids.shape + (dim,)
     if out is None:
-        out = torch.empty(shape, dtype=dtype or weight.dtype, device=weight.device)
-    y = _output_rows(out, "out", shape, dtype or out.dtype)
+        out = weight.new_empty(shape) if dtype is None else torch.empty(shape, dtype=dtype, device=weight.device)
+        y = out.data_ptr(), dim
+    else:
+        y = _output_rows(out, "out", shape, dtype or out.dtype)
     prob = _embed_pack(ids.numel(), rows, dim, ids, first, padding_idx, (wp, ldw), y, wcode, _dt(out), False, scale)
     _call(dev, _lib.lib().muon_embedding, prob, None)
     if given:
@@ -147,6 +150,8 @@ def _input_rows(t, name, shape):
     elements."""
     if t.shape != shape:
         _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if t.is_contiguous():
+        return t, t.data_ptr(), shape[-1]
     if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel():
         _bad(f"{name} needs unit column stride")
     try:
@@ -165,6 +170,8 @@ def _output_rows(t, name, shape, dtype):
         _bad(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype != dtype:
         _unsupported(f"{name} is {t.dtype}, not {dtype}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[-1]
     p, _, _, ld = _rows(t, name)
     return p, ld
 
@@ -250,33 +257,37 @@ def _residual_norm(block, residual, weight, post_weight, gate, norm, post_norm, 
     if not shape:
         _bad("block needs at least one dimension")
     cols = shape[-1]
-    same = _is_block(residual, gate, post, scale, stream)
-    wcode, wp, pwp = _norm_vectors(weight, post_weight, cols)
     source = block
     block, bp, ldb = _input_rows(block, "block", shape)
-    rp = ldr = gp = grows = ldg = gcode = 0
+    rp = ldr = gp = grows = ldg = gcode = wcode = wp = pwp = sp = lds = yp = ldy = 0
+    if weight is not None or post_weight is not None:
+        wcode, wp, pwp = _norm_vectors(weight, post_weight, cols)
     kept = residual
     if residual is not None:
         kept, rp, ldr = _input_rows(residual, "residual", shape)
     if gate is not None:
         gate, gp, grows, ldg = _gate_rows(gate, shape)
         gcode = _dt(gate)
-    st = residual.dtype if residual is not None else stream.dtype if stream is not None else block.dtype
-    sp = lds = yp = ldy = 0
+    same = residual is None and _is_block(residual, gate, post, scale, stream)
     if same:
-        stream = source
+        stream, scode = source, code
     else:
         if stream is None:
-            stream = torch.empty(shape, dtype=st, device=block.device)
-        sp, lds = _output_rows(stream, "stream", shape, st)
+            stream = (kept if residual is not None else block).new_empty(shape)
+            sp, lds = stream.data_ptr(), cols
+        else:
+            sp, lds = _output_rows(stream, "stream", shape, residual.dtype if residual is not None else stream.dtype)
+        scode = _dt(stream)
     if norm:
         if out is None:
-            out = torch.empty(shape, dtype=block.dtype, device=block.device)
-        yp, ldy = _output_rows(out, "out", shape, block.dtype)
+            out = block.new_empty(shape)
+            yp, ldy = out.data_ptr(), cols
+        else:
+            yp, ldy = _output_rows(out, "out", shape, block.dtype)
     elif out is not None:
         _bad("out goes with norm")
     if norm or not same:
-        prob = _pack_norm(shape[:-1].numel(), cols, code, _dt(stream), wcode, gcode, post, norm, bp, ldb, rp, ldr, sp, lds,
+        prob = _pack_norm(shape[:-1].numel(), cols, code, scode, wcode, gcode, post, norm, bp, ldb, rp, ldr, sp, lds,
                           yp, ldy, wp, pwp, gp, grows, ldg, scale, residual_scale, eps, weight_offset,
                           0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
         _call(dev, _lib.lib().muon_residual_norm, prob, None)
@@ -412,8 +423,14 @@ def _norm_kind(norm_type):
     _unsupported(f"norm_type {norm_type!r} is not 2 or inf")
 
 
+_is_none = functools.partial(operator.is_, None)
+
+
 def _tensors(grads):
-    return [grads] if isinstance(grads, torch.Tensor) else [t for t in grads if t is not None]
+    if isinstance(grads, torch.Tensor):
+        return [grads]
+    ts = list(grads)
+    return [t for t in ts if t is not None] if any(map(_is_none, ts)) else ts
 
 
 def _dense(t):
@@ -428,24 +445,42 @@ def _dense(t):
     return True
 
 
-def _codes(ts):
-    codes = [_CODE.get(t.dtype) for t in ts]
+# What is asked of every tensor of a list, without an attribute lookup for each.
+_data_ptr, _numel, _get_device, _is_contiguous = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device,
+                                                  torch.Tensor.is_contiguous)
+_dtype, _shape, _needs_grad = (operator.attrgetter(n) for n in ("dtype", "shape", "requires_grad"))
+
+
+def _list_device(*lists):
+    """The index of the one GPU that holds every tensor of the lists (the first is not empty)."""
+    first = lists[0][0]
+    dev = _same_device(first)
+    for ts in lists:
+        if set(map(_get_device, ts)) - {dev}:
+            _same_device(first, *ts)
+    return dev
+
+
+def _table(ts, sizes=True):
+    """(count, pointers, types, sizes) of a list as the library takes them."""
+    n = len(ts)
+    codes = list(map(_CODE.get, map(_dtype, ts)))
     if None in codes:
         _unsupported(f"dtype {ts[codes.index(None)].dtype} is not float32 or bfloat16")
-    return codes
+    return (n, struct.pack(f"{n}Q", *map(_data_ptr, ts)), struct.pack(f"{n}i", *codes),
+            struct.pack(f"{n}q", *map(_numel, ts)) if sizes else None)
 
 
-def _table(ts):
-    """(count, pointers, types, sizes) as the library takes them, and the packed sizes' own count."""
-    n = len(ts)
-    return (n, struct.pack(f"{n}Q", *[t.data_ptr() for t in ts]), struct.pack(f"{n}i", *_codes(ts)),
-            struct.pack(f"{n}q", *[t.numel() for t in ts]))
+# Bytes that the partials of a list of one launch fit (up to 128 tensors).
+_ONE_LAUNCH, _ONE_LAUNCH_BYTES = 128, 8448
 
 
 def _norm_workspace(n, sizes, device):
+    if n <= _ONE_LAUNCH:
+        return torch.empty(_ONE_LAUNCH_BYTES, dtype=torch.uint8, device=device)
     need = ctypes.c_size_t(0)
     _lib.check(_lib.lib().muon_grad_norm_workspace_bytes(n, sizes, ctypes.byref(need)))
-    return torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None
+    return torch.empty(max(need.value, 1), dtype=torch.uint8, device=device)
 
 
 def _no_gradients(dtype=torch.float32):
@@ -467,20 +502,20 @@ def grad_norm(grads, *, norm_type=2, squared=False):
     ts = _tensors(grads)
     if not ts:
         return _no_gradients(torch.float64 if squared else torch.float32)
-    dev = _same_device(*ts)
+    dev = _list_device(ts)
     if _dual["_current_level"] >= 0:
         _refuse_tangents(*ts)
-    if torch.is_grad_enabled() and any(t.requires_grad for t in ts):
+    if torch.is_grad_enabled() and any(map(_needs_grad, ts)):
         _unsupported("the norm carries no gradient: detach the tensors")
-    ts = [t if _dense(t) else t.contiguous() for t in ts]
+    if not all(map(_is_contiguous, ts)):
+        ts = [t if _dense(t) else t.contiguous() for t in ts]
     n, ptrs, codes, sizes = _table(ts)
     out = torch.empty((), dtype=torch.float64 if squared else torch.float32, device=ts[0].device)
     at = (None, out.data_ptr()) if squared else (out.data_ptr(), None)
 
     def call():
         ws = _norm_workspace(n, sizes, out.device)
-        _lib.check(_lib.lib().muon_grad_norm(n, ptrs, codes, sizes, kind, *at, ws.data_ptr() if ws is not None else _NO_WORKSPACE,
-                                             ws.numel() if ws is not None else 0, _raw_stream(dev)))
+        _lib.check(_lib.lib().muon_grad_norm(n, ptrs, codes, sizes, kind, *at, ws.data_ptr(), ws.numel(), _raw_stream(dev)))
     _on(dev, call)
     return out
 
@@ -499,9 +534,7 @@ def clip_grad_norm(grads, max_norm, *, norm_type=2, eps=1e-6, total=None, out=No
     if out is not None:
         grads, out = _pair(grads, out)
     ts = _tensors(grads)
-    outs = ts if out is None else [o for o in out if o is not None]
-    if len(outs) != len(ts):
-        _bad(f"{len(outs)} outputs for {len(ts)} gradients")
+    outs = ts if out is None else out
     if total is not None:
         if total.numel() != 1 or total.dtype not in (torch.float32, torch.float64):
             _bad("total must be one fp32 or fp64 value")
@@ -513,23 +546,26 @@ def clip_grad_norm(grads, max_norm, *, norm_type=2, eps=1e-6, total=None, out=No
         _bad(f"max_norm and eps must be numbers, not {max_norm!r} and {eps!r}")
     if not ts:
         return _no_gradients() if total is None else (total.sqrt().float() if total.dtype is torch.float64 else total.clone()).reshape(())
-    dev = _same_device(*ts, *(outs if out is not None else ()), total)
+    dev = _list_device(ts, outs) if total is None else _list_device(ts, outs, [total])
     if _dual["_current_level"] >= 0:
         _refuse_tangents(*ts, *outs, total)
-    _given(*outs)
-    for t in ts:
-        if not _dense(t):
-            _bad("a gradient's elements do not lie side by side: it cannot be scaled as a whole")
+    if torch.is_grad_enabled() and any(map(_needs_grad, ts)):
+        if out is None:
+            _bad("a gradient to be written requires a gradient itself: detach it")
+        _unsupported("clipped gradients carry no gradient: detach the tensors")
+    whole = all(map(_is_contiguous, ts))
+    if not whole and not all(map(_dense, ts)):
+        _bad("a gradient's elements do not lie side by side: it cannot be scaled as a whole")
     if out is not None:
-        if torch.is_grad_enabled() and any(t.requires_grad for t in ts):
-            _unsupported("clipped gradients carry no gradient: detach the tensors")
-        for t, o in zip(ts, outs):
-            if o.shape != t.shape:
-                _bad(f"an output is {tuple(o.shape)}, not {tuple(t.shape)}")
-            if not (t.is_contiguous() and o.is_contiguous()) and t.stride() != o.stride():
-                _bad("an output's memory order is not its gradient's")
+        _given(*outs)
+        if list(map(_shape, ts)) != list(map(_shape, outs)):
+            _bad("an output has not its gradient's shape")
+        if not (whole and all(map(_is_contiguous, outs))):
+            for t, o in zip(ts, outs):
+                if not (t.is_contiguous() and o.is_contiguous()) and t.stride() != o.stride():
+                    _bad("an output's memory order is not its gradient's")
     n, ptrs, codes, sizes = _table(ts)
-    optrs, ocodes = (ptrs, codes) if out is None else _table(outs)[1:3]
+    optrs, ocodes = (ptrs, codes) if out is None else _table(outs, False)[1:3]
     norm = torch.empty((), dtype=torch.float32, device=ts[0].device)
 
     def call():
@@ -547,7 +583,8 @@ def _pair(grads, out):
     grads, out = ([t] if isinstance(t, torch.Tensor) else list(t) for t in (grads, out))
     if len(grads) != len(out):
         _bad(f"{len(out)} outputs for {len(grads)} gradients")
-    keep = [(g, o) for g, o in zip(grads, out) if g is not None]
-    if any(o is None for _, o in keep):
+    if any(map(_is_none, grads)):
+        out = [o for g, o in zip(grads, out) if g is not None]
+    if any(map(_is_none, out)):
         _bad("a gradient has no output")
-    return [g for g, _ in keep], [o for _, o in keep]
+    return grads, out

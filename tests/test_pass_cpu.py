@@ -74,7 +74,11 @@ def test_norm_workspace():
     assert L.muon_grad_norm_workspace_bytes(0, None, ctypes.byref(need)) == 0 and need.value == 0
     assert L.muon_grad_norm_workspace_bytes(2, struct.pack("2q", 0, 0), ctypes.byref(need)) == 0 and need.value == 0
     assert L.muon_grad_norm_workspace_bytes(1, struct.pack("q", 1 << 36), ctypes.byref(need)) == 0
-    assert 2048 * 8 < need.value <= 2049 * 8 + 256  # one launch's workgroups and their sum
+    assert 1024 * 8 < need.value <= 1025 * 8 + 256  # one launch's workgroups and their sum
+    from newton_schulz_ns5_amd import pass_ops
+    sizes = struct.pack("128q", *[1 << 23] * 128)
+    assert L.muon_grad_norm_workspace_bytes(pass_ops._ONE_LAUNCH, sizes, ctypes.byref(need)) == 0
+    assert need.value <= pass_ops._ONE_LAUNCH_BYTES
     assert L.muon_grad_norm_workspace_bytes(1, None, ctypes.byref(need)) == -1
     assert L.muon_grad_norm_workspace_bytes(-1, None, ctypes.byref(need)) == -1
     assert L.muon_grad_norm_workspace_bytes(1, struct.pack("q", 1), None) == -1
@@ -205,7 +209,7 @@ def embed_problem(**over):
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(tokens=-1), -1), (dict(rows=-1), -1), (dict(dim=-1), -1), (dict(tokens=(1 << 28) + 1), -1), (dict(rows=(1 << 28) + 1), -1),
+    (dict(tokens=-1), -1), (dict(rows=-1), -1), (dict(dim=-1), -1), (dict(tokens=(1 << 26) + 1), -1), (dict(rows=(1 << 26) + 1), -1),
     (dict(dim=65537), -1), (dict(w_dtype=2), -2), (dict(y_dtype=-1), -2), (dict(scale=math.nan), -1), (dict(ids_i64=2), -1),
     (dict(has_padding=-1), -1), (dict(accumulate=2), -1), (dict(reserved=1), -1), (dict(ids=None), -1), (dict(ids=FAKE + 4), -1),
     (dict(ids_i64=0, ids=FAKE + 2), -1), (dict(w=None), -1), (dict(y=None), -1), (dict(w=FAKE + MIB + 1), -1), (dict(y=FAKE + 1), -1),
@@ -216,6 +220,12 @@ def test_embedding_refusals(over, code):
     assert L.muon_embedding(ctypes.byref(embed_problem(**over)), None) == code
     assert L.muon_last_error()
     assert L.muon_embedding_backward(ctypes.byref(embed_problem(**over)), FAKE + 20 * MIB, 1 << 40, None) == code
+
+
+def test_embedding_gradients_of_too_many_workgroups_refused():
+    p = embed_problem(tokens=1 << 26, dim=4096, w_row_stride=4096, y_row_stride=4096, w=1 << 50, rows=4)
+    assert _lib.lib().muon_embedding_backward(ctypes.byref(p), FAKE + 20 * MIB, 1 << 60, None) == -1
+    assert b"together" in _lib.lib().muon_last_error()
 
 
 def test_embedding_outputs_over_the_ids():
