@@ -400,29 +400,30 @@ __global__ __launch_bounds__(NT) void embed_grad_kernel(const EmbedGrad p) {
 }
 
 // Joins the runs that reach over pieces.  A workgroup looks at one piece and
-// kJoinCols columns: where a run begins in the piece and goes on, it adds the
-// slots of the pieces it reaches, four parts of them at once, then the parts.
-constexpr int kJoinParts = NT / 64;
-template <typename O, bool EDGE>
+// 4 G columns: where a run begins in the piece and goes on, it adds the slots
+// of the pieces it reaches, NT / G parts of them at once, then the parts.  Narrow
+// rows take few lanes, so that a frequent token's many slots go by in parts.
+template <typename O, int G, bool EDGE>
 __global__ __launch_bounds__(NT) void embed_join_kernel(const EmbedGrad p) {
-  constexpr int V = kJoinCols / 64;
-  __shared__ float red[kJoinParts][64][V + 1];
+  constexpr int V = 4, PARTS = NT / G;
+  __shared__ float red[PARTS][G][V + 1];
   const int64_t piece = blockIdx.x;
   const int64_t i0 = piece * p.piece, i1 = i0 + p.piece;
   if (i1 >= p.n) return;
   const uint32_t run = p.key[i1 - 1], next = p.key[i1], first = p.key[i0], before = p.key[i0 ? i0 - 1 : 0];
   if (run == (uint32_t)p.rows || next != run || (first == run && i0 && before == run)) return;
-  const int j = threadIdx.x & 63, part = threadIdx.x >> 6;
   // The last piece that begins with the run, 64 pieces looked at together.
   const int64_t pieces = (p.n + p.piece - 1) / p.piece;
+  const int look = threadIdx.x & 63;
   int64_t last = piece + 1;
   for (int64_t q = piece + 1;; q += 64) {
-    const uint64_t same = __ballot(q + j < pieces && p.key[q + j < pieces ? (q + j) * p.piece : 0] == run);
+    const uint64_t same = __ballot(q + look < pieces && p.key[q + look < pieces ? (q + look) * p.piece : 0] == run);
     const int count = same == ~(uint64_t)0 ? 64 : __ffsll((unsigned long long)~same) - 1;
     if (count) last = q + count - 1;
     if (count < 64) break;
   }
-  const int col = V * (int)(blockIdx.y * 64 + j);
+  const int j = threadIdx.x % G, part = threadIdx.x / G;
+  const int col = V * (int)(blockIdx.y * G + j);
   const int valid = p.dim - col < 0 ? 0 : (p.dim - col < V ? p.dim - col : V);
   float acc[V] = {};
   if (valid > 0) {
@@ -433,18 +434,22 @@ __global__ __launch_bounds__(NT) void embed_join_kernel(const EmbedGrad p) {
       for (int e = 0; e < V; ++e) acc[e] += x.value(e);
     };
     if (part == 0) add(2 * piece + 1);
-#pragma unroll 4
-    for (int64_t q = piece + 1 + part; q <= last; q += kJoinParts) add(2 * q);
+#pragma unroll 8
+    for (int64_t q = piece + 1 + part; q <= last; q += PARTS) add(2 * q);
   }
 #pragma unroll
   for (int e = 0; e < V; ++e) red[part][j][e] = acc[e];
-  __syncthreads();
+#pragma unroll
+  for (int half = PARTS / 2; half >= 1; half >>= 1) {
+    __syncthreads();
+    if (part < half) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) red[part][j][e] += red[part + half][j][e];
+    }
+  }
   if (part || valid <= 0) return;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-#pragma unroll
-    for (int q = 1; q < kJoinParts; ++q) acc[e] += red[q][j][e];
-  }
+  for (int e = 0; e < V; ++e) acc[e] = red[0][j][e];
   write_row<O, V, EDGE>(p, run, col, valid, acc);
 }
 
@@ -521,12 +526,21 @@ hipError_t launch_embed_grad(const EmbedGrad& p, bool dy_bf16, bool dw_bf16, int
   return dw_bf16 ? launch_grad_types<float, uint16_t>(p, blocks, s) : launch_grad_types<float, float>(p, blocks, s);
 }
 
-hipError_t launch_embed_join(const EmbedGrad& p, bool dw_bf16, hipStream_t s) {
+template <typename O>
+hipError_t launch_join_type(const EmbedGrad& p, hipStream_t s) {
   const int64_t pieces = (p.n + p.piece - 1) / p.piece;
-  const dim3 grid((unsigned)pieces, (unsigned)((p.dim + kJoinCols - 1) / kJoinCols));
-  if (p.dim % 8)
-    return dw_bf16 ? launch_kernel(embed_join_kernel<uint16_t, true>, grid, p, s, NT) : launch_kernel(embed_join_kernel<float, true>, grid, p, s, NT);
-  return dw_bf16 ? launch_kernel(embed_join_kernel<uint16_t, false>, grid, p, s, NT) : launch_kernel(embed_join_kernel<float, false>, grid, p, s, NT);
+  auto launch = [&](auto g, auto edge) {
+    constexpr int G = decltype(g)::value;
+    return launch_kernel(embed_join_kernel<O, G, decltype(edge)::value>, dim3((unsigned)pieces, (unsigned)((p.dim + 4 * G - 1) / (4 * G))), p, s, NT);
+  };
+  using std::integral_constant;
+  const bool edge = p.dim % 8 != 0;
+  if (p.dim <= 32) return edge ? launch(integral_constant<int, 8>{}, std::true_type{}) : launch(integral_constant<int, 8>{}, std::false_type{});
+  if (p.dim <= 256) return edge ? launch(integral_constant<int, 16>{}, std::true_type{}) : launch(integral_constant<int, 16>{}, std::false_type{});
+  return edge ? launch(integral_constant<int, 64>{}, std::true_type{}) : launch(integral_constant<int, 64>{}, std::false_type{});
+}
+hipError_t launch_embed_join(const EmbedGrad& p, bool dw_bf16, hipStream_t s) {
+  return dw_bf16 ? launch_join_type<uint16_t>(p, s) : launch_join_type<float>(p, s);
 }
 
 }  // namespace muon

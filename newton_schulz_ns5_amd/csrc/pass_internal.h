@@ -148,7 +148,7 @@ struct EmbedGrad {
 };
 constexpr int kPieceLeast = 16, kPieceMost = 64;  // multiples of 8
 constexpr int kClearRows = 16;             // rows that a workgroup clears
-constexpr int kJoinCols = 256;             // columns that a workgroup joins
+constexpr int kJoinCols = 256;             // columns that a workgroup joins (fewer of narrow rows)
 hipError_t launch_embed_grad(const EmbedGrad& p, bool dy_bf16, bool dw_bf16, int blocks, hipStream_t s);
 hipError_t launch_embed_join(const EmbedGrad& p, bool dw_bf16, hipStream_t s);
 
