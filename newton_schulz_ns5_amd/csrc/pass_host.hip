@@ -407,11 +407,11 @@ ResidualNorm norm_params(const muon_residual_norm_problem* q) {
   p.gate_each = gate_each(q);
   p.scale = q->scale; p.residual_scale = q->residual_scale; p.eps = q->eps; p.offset = q->weight_offset;
   // The vectors of every row in LDS where those of the workgroups that a CU
-  // holds fit (160 KiB, less what a workgroup has besides).
+  // holds fit its 160 KiB, beside what a workgroup has for its sums.
   const NormShape shape = norm_shape(q->cols);
   const int64_t width = (int64_t)shape.group * shape.columns;
   const int64_t held = 4 * width * ((q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && p.gate_each >= q->rows));
-  p.held = (held + 12288) * norm_resident(norm_threads(shape)) <= 163840 ? (int32_t)held : 0;
+  p.held = (held + (shape.group < 64 ? 8192 : 1024)) * norm_resident(norm_threads(shape)) <= 163840 ? (int32_t)held : 0;
   return p;
 }
 

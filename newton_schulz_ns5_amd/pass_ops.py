@@ -8,6 +8,7 @@ workspaces from torch's allocator for the one call, given outputs written in
 place with their autograd version counters moved, tracers and forward-mode
 inputs refused.
 """
+import array
 import ctypes
 import functools
 import math
@@ -435,6 +436,8 @@ def _tensors(grads):
 
 def _dense(t):
     """Whether t's elements lie side by side in memory, in whatever order of its dimensions."""
+    if t.layout is not torch.strided:
+        _unsupported(f"a tensor is {t.layout}, not strided")
     if t.is_contiguous():
         return True
     n = 1
@@ -467,8 +470,11 @@ def _table(ts, sizes=True):
     codes = list(map(_CODE.get, map(_dtype, ts)))
     if None in codes:
         _unsupported(f"dtype {ts[codes.index(None)].dtype} is not float32 or bfloat16")
-    return (n, struct.pack(f"{n}Q", *map(_data_ptr, ts)), struct.pack(f"{n}i", *codes),
-            struct.pack(f"{n}q", *map(_numel, ts)) if sizes else None)
+    try:
+        pointers = array.array("Q", map(_data_ptr, ts)).tobytes()
+    except (RuntimeError, NotImplementedError):
+        _unsupported("tensors must be strided (dense in memory)")
+    return n, pointers, array.array("i", codes).tobytes(), array.array("q", map(_numel, ts)).tobytes() if sizes else None
 
 
 # Bytes that the partials of a list of one launch fit (up to 128 tensors).

@@ -138,6 +138,27 @@ def test_infinities_and_nans(ns):
         assert torch.equal(y, k)
 
 
+def test_subnormal_values(ns):
+    for dt, tiny in ((F32, 2.0 ** -149), (BF, 2.0 ** -133)):
+        x = (torch.arange(-300, 300, device="cuda", dtype=torch.float64) * tiny).to(dt)
+        want = exact_norm([x])
+        assert want > 0
+        check_norm(ns.grad_norm([x]), want) if want > 2.0 ** -126 else None
+        outs = [torch.empty_like(x)]
+        ns.clip_grad_norm([x], 1.0, out=outs)
+        assert torch.equal(outs[0], x)  # a copy keeps them
+        ns.clip_grad_norm([x], want / 2, eps=0.0, out=outs)
+        assert bool(((outs[0].double() - x.double() / 2).abs() <= tiny / 2).all())
+
+
+def test_sparse_gradients_are_refused(ns):
+    x = torch.eye(4, device="cuda").to_sparse()
+    for call in (lambda: ns.grad_norm([x]), lambda: ns.clip_grad_norm([x], 1.0)):
+        with pytest.raises(ns.MuonError) as e:
+            call()
+        assert e.value.status == -2
+
+
 def test_zero_gradients_and_a_zero_bound(ns):
     z = torch.zeros(100, device="cuda")
     for max_norm in (0.0, 1.0):

@@ -164,3 +164,68 @@ def test_streams_of_their_own(ns):
     assert torch.equal(a, b)
     with pytest.raises(ns.MuonError):
         ns.residual_norm(a, b.cpu())
+
+
+def test_inside_torch_compile(ns):
+    """A compiled function breaks its graph at these calls: every call with new tensors gives what the plain call gives."""
+    w, n, g = rand((50, 64), 1), rand((64,), 2, 0.1, 1.0), rand((64,), 3)
+
+    def fn(t, table, x, norm):
+        e = ns.embedding(t, table, scale=2.0) * 2
+        s, y = ns.residual_norm(e, x, weight=norm, gate=g, scale=0.5)
+        return s.sum(-1) + y.sum(-1)
+
+    def clip(a, b):
+        return ns.clip_grad_norm([a, b], 1.0), a + ns.grad_norm(b)
+
+    compiled, compiled_clip = torch.compile(fn, backend="eager"), torch.compile(clip, backend="eager")
+    for i in range(3):
+        t = torch.randint(0, 50, (30 + i,), device="cuda")
+        for grad in (False, True):
+            x = rand((30 + i, 64), 10 + i)
+            a, b = [v.clone().requires_grad_(grad) for v in (w, x, n)], [v.clone().requires_grad_(grad) for v in (w, x, n)]
+            got, want = compiled(t, *a), fn(t, *b)
+            assert torch.equal(got, want)
+            if grad:
+                got.sum().backward()
+                want.sum().backward()
+                assert all(torch.equal(p.grad, q.grad) for p, q in zip(a, b))
+        a, b = [[rand((77 + i,), 20), rand((5, 3), 21)] for _ in range(2)]
+        assert all(torch.equal(p, q) for p, q in zip(compiled_clip(*a), clip(*b)))
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_tracers_are_refused(ns):
+    from torch.fx.experimental.proxy_tensor import make_fx
+    t, w = torch.arange(5, device="cuda"), rand((9, 16), 1)
+    for fn in (lambda v: ns.embedding(t, v), lambda v: ns.residual_norm(v)[1], lambda v: ns.grad_norm([v]),
+               lambda v: ns.clip_grad_norm([v], 1.0), lambda v: ns.embedding_backward(v[:5], t, 9),
+               lambda v: ns.residual_norm_backward(v, None, v, None)[0]):
+        for trace in (lambda f: torch.jit.trace(f, (w,)), lambda f: make_fx(f)(w)):
+            with pytest.raises(Exception) as e:
+                trace(fn)
+            assert "tracing" in str(e.value) or "trace" in str(e.value)
+
+
+def test_two_streams_at_once(ns):
+    """Calls of every operator in flight on two streams, each with its own workspace."""
+    t, w = torch.randint(0, 900, (5000,), device="cuda"), rand((900, 264), 1)
+    dy, n = rand((5000, 264), 2), rand((264,), 3, 0.1, 1.0)
+
+    def work():
+        e = ns.embedding(t, w)
+        dw = ns.embedding_backward(dy, t, 900)
+        s, y = ns.residual_norm(e, dy, weight=n, post_weight=n, gate=n)
+        grads = ns.residual_norm_backward(y, dy, s, e, weight=n, post_weight=n, gate=n)
+        out = [torch.empty_like(g) for g in grads]
+        return [dw, s, y, ns.clip_grad_norm(grads, 0.5, out=out), ns.grad_norm(out, squared=True)] + out
+    want = work()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(4):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(work())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for runs in got for run in runs for a, b in zip(run, want))

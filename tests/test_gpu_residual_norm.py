@@ -166,6 +166,18 @@ def test_widths(ns, cols, dtype, stream):
     check_backward(ns, dy, dst, s, None, w, None, None, what="plain")
 
 
+@pytest.mark.parametrize("cols", [40, 200, 512, 1024, 8192, 16384])
+def test_two_vectors(ns, cols):
+    """Vectors that the kernel holds where three would not fit, in fp32 and bf16."""
+    b, x, dy = rand((7, cols), BF, 8), rand((7, cols), F32, 9, 2.0), rand((7, cols), BF, 10, 0.1)
+    for dt in (F32, BF):
+        w, pw = rand((cols,), dt, 3, 0.2, 1.0), rand((cols,), dt, 4, 0.2, 1.0)
+        s, _ = check_forward(ns, b, x, w, pw, None, post=True, what=cols)
+        check_backward(ns, dy, x, s, b, w, pw, None, post=True, what=cols)
+        s, _ = check_forward(ns, b, x, w, None, pw, what=cols)
+        check_backward(ns, dy, x, s, b, w, None, pw, what=cols)
+
+
 @pytest.mark.parametrize("gate", ["none", "cols", "one", "batch", "rows"])
 @pytest.mark.parametrize("post,norm,weights", [(True, True, True), (True, False, True), (False, True, True), (False, False, True),
                                                (True, True, False), (False, True, False)])
@@ -372,6 +384,12 @@ def test_autograd(ns):
         ones = torch.ones(shape, device="cuda", dtype=out[use].dtype)
         q = ns.residual_norm_backward(ones if use else None, None if use else ones, out[0].detach(), b, weight=w, post_weight=pw, gate=g, **how)
         assert torch.equal(leaf.grad, q[1])
+    # the block and the residual are one tensor
+    leaf = b.clone().requires_grad_()
+    s, y = ns.residual_norm(leaf, leaf, weight=w)
+    y.backward(cy)
+    one = ns.residual_norm_backward(cy, None, s.detach(), None, weight=w)[0]
+    assert torch.equal(leaf.grad, one + one)
     # a stream of another type than the block, and only the stream used: the block's gradient has its type
     leaf = b.clone().requires_grad_()
     s, _ = ns.residual_norm(leaf, x, norm=False)
