@@ -20,7 +20,7 @@ template <typename T, typename R, int GS, int C, bool POST, bool GATE, bool EDGE
 __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_kernel(const ResidualNorm p) {
   constexpr int V = chunk_values<T, R>(), K = C / V;
   constexpr int ROWS = Group<GS>::kRows;
-  constexpr bool AHEAD = C == 8;  // the next row's loads in flight, where the registers allow it
+  constexpr bool AHEAD = C == 8 && (V == 8 || !(POST && GATE));  // the next row's loads in flight, where the registers allow it
   constexpr bool NEED_B = POST || GATE;
   enum { W, PW, G };
   extern __shared__ __attribute__((aligned(16))) f32x4 held[];
@@ -100,15 +100,28 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
     const int64_t r1 = r0 + p.unit_rows < end ? r0 + p.unit_rows : end;
     const void* gate = GATE && !gate_all && !gate_row ? row_of<GS>(p.gate, g, p.ldg, gate_bytes) : nullptr;
     int64_t r = r0 + grp;
-    Row row, next;
-    if (AHEAD && r < r1) load_row(r, next);
+    Row raw;
+    if (AHEAD && r < r1) load_row(r, raw);
     for (; r < r1; r += ROWS) {
-      if constexpr (AHEAD) {
-        row = next;
-        if (r + ROWS < r1) load_row(r + ROWS, next);
-      } else {
-        load_row(r, row);
+      if constexpr (!AHEAD) load_row(r, raw);
+      // The row's values: unpacked where the next row's loads take their place.
+      float dyv[AHEAD ? K : 1][V], sv[AHEAD ? K : 1][V], bv[AHEAD ? K : 1][V], d[K][V];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if constexpr (AHEAD) {
+            dyv[k][e] = raw.dy[k].value(e);
+            sv[k][e] = raw.s[k].value(e);
+            bv[k][e] = NEED_B ? raw.b[k].value(e) : 0.f;
+          }
+          d[k][e] = p.dstream ? raw.ds[k].value(e) : 0.f;
+        }
       }
+      auto dy = [&](int k, int e) { return AHEAD ? dyv[AHEAD ? k : 0][e] : raw.dy[k].value(e); };
+      auto s = [&](int k, int e) { return AHEAD ? sv[AHEAD ? k : 0][e] : raw.s[k].value(e); };
+      auto b = [&](int k, int e) { return AHEAD ? bv[AHEAD ? k : 0][e] : NEED_B ? raw.b[k].value(e) : 0.f; };
+      if (AHEAD && r + ROWS < r1) load_row(r + ROWS, raw);
       if (gate_row) gate = row_of<GS>(p.gate, r, p.ldg, gate_bytes);
       // sum s^2, sum dy w s, sum b^2
       float q[3] = {0.f, 0.f, 0.f};
@@ -120,13 +133,13 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
           vec.get(W, k, col[k], valid[k], w);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            q[0] += row.s[k].value(e) * row.s[k].value(e);
-            q[1] += row.dy[k].value(e) * w[e] * row.s[k].value(e);
+            q[0] += s(k, e) * s(k, e);
+            q[1] += dy(k, e) * w[e] * s(k, e);
           }
         }
         if (POST) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) q[2] += row.b[k].value(e) * row.b[k].value(e);
+          for (int e = 0; e < V; ++e) q[2] += b(k, e) * b(k, e);
         }
       }
       if constexpr (POST) {
@@ -140,27 +153,19 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
       // D = ds + rs dy w - c s, c = rs^3 mean(dy w s)
       const float rs = p.norm ? __frsqrt_rn(q[0] * inv + p.eps) : 0.f, c = q[1] * inv * rs * rs * rs;
       const float rb = POST ? __frsqrt_rn(q[2] * inv + p.eps) : 1.f;
+      auto m = [&](int k, int e) { return POST && !AHEAD ? b(k, e) * rb : b(k, e); };  // b holds m from here on where it can
       void* const dres = row_of<GS>(p.dresidual, r, p.lddr, sizeof(R));
-      float d[K][V];
       float dot[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (valid[k] <= 0) continue;
-        if (p.dstream) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) d[k][e] = row.ds[k].value(e);
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) d[k][e] = 0.f;
-        }
         if (p.norm) {
           float w[V];
           vec.get(W, k, col[k], valid[k], w);
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            const float dy = row.dy[k].value(e), s = row.s[k].value(e);
-            aw[k][e] += dy * (s * rs);
-            d[k][e] = fmaf(-c, s, fmaf(rs, dy * w[e], d[k][e]));
+            aw[k][e] += dy(k, e) * (s(k, e) * rs);
+            d[k][e] = fmaf(-c, s(k, e), fmaf(rs, dy(k, e) * w[e], d[k][e]));
           }
         }
         if (p.dresidual) {
@@ -171,17 +176,16 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) d[k][e] *= p.scale;        // t
-        float gt[V], pw[V];
+        float gt[V], pw[V], dg[V];
         if (GATE) {
           if (gate_all) vec.get(G, k, col[k], valid[k], gt);
           else load_values<V, EDGE>(gate, col[k], p.gate_bf16 != 0, valid[k], gt);
         }
         if (POST) vec.get(PW, k, col[k], valid[k], pw);
-        float dg[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float m = POST ? row.b[k].value(e) * rb : NEED_B ? row.b[k].value(e) : 0.f;
-          const float tm = d[k][e] * m;
+          if constexpr (POST && AHEAD) bv[k][e] *= rb;
+          const float tm = d[k][e] * m(k, e);
           if (GATE) {
             dg[e] = POST ? tm * pw[e] : tm;
             d[k][e] *= gt[e];
@@ -189,7 +193,7 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
           if (POST) {
             ap[k][e] += GATE ? tm * gt[e] : tm;
             d[k][e] *= pw[e];                                  // k
-            dot[0] += d[k][e] * m;
+            dot[0] += d[k][e] * m(k, e);
           }
         }
         if (GATE) {
@@ -203,12 +207,11 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
       }
       if (POST) {
         sum(dot);
-        const float cb = dot[0] * inv * rb * rb;               // of b, which is m / rb
+        const float cb = dot[0] * inv * rb;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-          if (valid[k] <= 0) continue;
 #pragma unroll
-          for (int e = 0; e < V; ++e) d[k][e] = fmaf(-cb, row.b[k].value(e), rb * d[k][e]);
+          for (int e = 0; e < V; ++e) d[k][e] = fmaf(-cb, m(k, e), rb * d[k][e]);
         }
       }
       if (p.dblock) {
