@@ -394,7 +394,7 @@ NormPlan plan_norm_grad(const muon_residual_norm_problem* q) {
   return P;
 }
 
-ResidualNorm norm_params(const muon_residual_norm_problem* q) {
+ResidualNorm norm_params(const muon_residual_norm_problem* q, bool backward) {
   ResidualNorm p{};
   p.rows = q->rows; p.cols = (int32_t)q->cols;
   p.post = q->post_norm; p.norm = q->norm;
@@ -411,7 +411,8 @@ ResidualNorm norm_params(const muon_residual_norm_problem* q) {
   const NormShape shape = norm_shape(q->cols);
   const int64_t width = (int64_t)shape.group * shape.columns;
   const int64_t held = 4 * width * ((q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && p.gate_each >= q->rows));
-  p.held = (held + (shape.group < 64 ? 8192 : 1024)) * norm_resident(norm_threads(shape)) <= 163840 ? (int32_t)held : 0;
+  if (backward && shape.columns == 16 && q->post_norm && q->gate) p.sums = (int32_t)(8 * width);
+  p.held = (held + p.sums + (shape.group < 64 ? 8192 : 1024)) * norm_resident(norm_threads(shape)) <= 163840 ? (int32_t)held : 0;
   return p;
 }
 
@@ -426,7 +427,7 @@ int muon_residual_norm(const muon_residual_norm_problem* q, void* stream) {
   const NormShape shape = norm_shape(q->cols);
   const int threads = norm_threads(shape), rpw = norm_rows(shape);
   const int blocks = (int)std::min<int64_t>(cdiv(q->rows, rpw), 256 * (2048 / threads));
-  const hipError_t e = launch_residual_norm(norm_params(q), q->dtype == MUON_BF16, q->stream_dtype == MUON_BF16, blocks, (hipStream_t)stream);
+  const hipError_t e = launch_residual_norm(norm_params(q, false), q->dtype == MUON_BF16, q->stream_dtype == MUON_BF16, blocks, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "norms around a block");
 }
 
@@ -444,7 +445,7 @@ int muon_residual_norm_backward(const muon_residual_norm_problem* q, void* works
   if (!q->rows || !q->cols) return ok();
   const NormPlan P = plan_norm_grad(q);
   if ((rc = check_workspace(workspace, workspace_bytes, P.bytes))) return rc;
-  ResidualNorm p = norm_params(q);
+  ResidualNorm p = norm_params(q, true);
   p.dy = q->dy; p.lddy = q->dy_row_stride;
   p.dstream = q->dstream; p.ldds = q->dstream_row_stride;
   p.dblock = q->dblock; p.lddb = q->dblock_row_stride;

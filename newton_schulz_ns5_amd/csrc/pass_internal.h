@@ -76,6 +76,7 @@ struct ResidualNorm {
   int64_t units, unit_rows, span;          // span: rows that gate_chunks units cover
   int32_t gate_chunks;
   int32_t held;                            // bytes of LDS that hold the vectors of every row; 0: not held
+  int32_t sums;                            // bytes of LDS behind them, of the gradients' sums where they are not in registers
 };
 // Threads that hold a row (8 or 32, or the whole waves of a workgroup), and
 // columns of each.

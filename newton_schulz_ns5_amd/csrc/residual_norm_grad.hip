@@ -20,8 +20,18 @@ template <typename T, typename R, int GS, int C, bool POST, bool GATE, bool EDGE
 __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_kernel(const ResidualNorm p) {
   constexpr int V = chunk_values<T, R>(), K = C / V;
   constexpr int ROWS = Group<GS>::kRows;
-  constexpr bool AHEAD = C == 8 && (V == 8 || !(POST && GATE));  // the next row's loads in flight, where the registers allow it
+  // The next row's loads are in flight where the registers hold them: this row
+  // is unpacked to fp32 first and they take its place (8192 x 4096 in bf16 with
+  // both the norm after the block and a gate: 96 us; with registers of their own
+  // 99).  Where V is 4 and both are there, or C is 16, they would be spilled
+  // (5105 x 2050 with an fp32 stream: 61 us so, 56 without).
+  constexpr bool AHEAD = C == 8 && (V == 8 || !(POST && GATE));
   constexpr bool NEED_B = POST || GATE;
+  // The sums of PW and G over rows stay in LDS where registers are short: both
+  // at 2048 rows of 16384 columns in bf16 take 154 us there, 252 from spilled
+  // registers; one of them alone 112 and 110 there, 109 and 107 in registers.
+  constexpr bool LDS_SUMS = C == 16 && POST && GATE;
+  constexpr int KR = LDS_SUMS ? 1 : K;
   enum { W, PW, G };
   extern __shared__ __attribute__((aligned(16))) f32x4 held[];
   __shared__ typename GroupSum<GS, 3>::Buffer red;
@@ -43,11 +53,38 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
   vec.set(PW, POST ? p.post_weight : nullptr, p.weight_bf16, p.offset, at, p.held);
   vec.set(G, gate_all ? p.gate : nullptr, p.gate_bf16, 0.f, at, p.held);
   vec.fill(col, valid);
-  float aw[K][V], ap[K][V], ag[K][V];
+  float aw[K][V], ap[KR][V], ag[KR][V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) aw[k][e] = ap[k][e] = ag[k][e] = 0.f;
+    for (int e = 0; e < V; ++e) aw[k][e] = ap[LDS_SUMS ? 0 : k][e] = ag[LDS_SUMS ? 0 : k][e] = 0.f;
+  }
+  // A thread's own places in LDS, behind the vectors: no other thread's.
+  auto slot = [&](bool post, int k, int h) -> f32x4& {
+    return at[((post ? C / 4 : 0) + k * (V / 4) + h) * Group<GS>::size() + Group<GS>::lane()];
+  };
+  auto clear = [&](bool post) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int h = 0; h < V / 4; ++h) slot(post, k, h) = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+  };
+  auto add = [&](bool post, int k, const float (&v)[V]) {
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) slot(post, k, h) += f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+  };
+  auto sums_of = [&](bool post, int k, float (&v)[V]) {
+#pragma unroll
+    for (int h = 0; h < V / 4; ++h) {
+      const f32x4 t = slot(post, k, h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * h + e] = t[e];
+    }
+  };
+  if constexpr (LDS_SUMS) {
+    clear(false);
+    clear(true);
   }
   // A sum over a workgroup's rows: its groups' sums in order, by the threads
   // of the first group.
@@ -176,7 +213,7 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) d[k][e] *= p.scale;        // t
-        float gt[V], pw[V], dg[V];
+        float gt[V], pw[V], dg[V], dp[V];
         if (GATE) {
           if (gate_all) vec.get(G, k, col[k], valid[k], gt);
           else load_values<V, EDGE>(gate, col[k], p.gate_bf16 != 0, valid[k], gt);
@@ -191,14 +228,18 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
             d[k][e] *= gt[e];
           }
           if (POST) {
-            ap[k][e] += GATE ? tm * gt[e] : tm;
+            if constexpr (LDS_SUMS) dp[e] = GATE ? tm * gt[e] : tm;
+            else ap[k][e] += GATE ? tm * gt[e] : tm;
             d[k][e] *= pw[e];                                  // k
             dot[0] += d[k][e] * m(k, e);
           }
         }
+        if constexpr (POST && LDS_SUMS) add(true, k, dp);
         if (GATE) {
           if (gate_row) {
             if (p.dgate) store_values<V, EDGE>(row_of<GS>(p.dgate, r, p.lddg, gate_bytes), col[k], p.gate_bf16 != 0, valid[k], dg);
+          } else if constexpr (LDS_SUMS) {
+            add(false, k, dg);
           } else {
 #pragma unroll
             for (int e = 0; e < V; ++e) ag[k][e] += dg[e];
@@ -225,14 +266,17 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
     if (GATE && !gate_row && (p.dgate || p.part[2])) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        total(ag[k]);
+        if constexpr (LDS_SUMS) sums_of(false, k, ag[0]);
+        float (&a)[V] = ag[LDS_SUMS ? 0 : k];
+        total(a);
         if (grp == 0 && valid[k] > 0) {
-          if (p.part[2]) round_store<float, V, EDGE, kPlain>(p.part[2] + u * p.cols, col[k], valid[k], ag[k]);
-          else store_values<V, EDGE>((char*)p.dgate + g * p.lddg * gate_bytes, col[k], p.gate_bf16 != 0, valid[k], ag[k]);
+          if (p.part[2]) round_store<float, V, EDGE, kPlain>(p.part[2] + u * p.cols, col[k], valid[k], a);
+          else store_values<V, EDGE>((char*)p.dgate + g * p.lddg * gate_bytes, col[k], p.gate_bf16 != 0, valid[k], a);
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) ag[k][e] = 0.f;
+        for (int e = 0; e < V; ++e) a[e] = 0.f;
       }
+      if constexpr (LDS_SUMS) clear(false);
     }
   }
 #pragma unroll
@@ -242,8 +286,10 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
       if (grp == 0 && valid[k] > 0) round_store<float, V, EDGE, kPlain>(p.part[0] + (int64_t)blockIdx.x * p.cols, col[k], valid[k], aw[k]);
     }
     if (POST && p.part[1]) {
-      total(ap[k]);
-      if (grp == 0 && valid[k] > 0) round_store<float, V, EDGE, kPlain>(p.part[1] + (int64_t)blockIdx.x * p.cols, col[k], valid[k], ap[k]);
+      auto& a = ap[LDS_SUMS ? 0 : k];
+      if constexpr (LDS_SUMS) sums_of(true, k, a);
+      total(a);
+      if (grp == 0 && valid[k] > 0) round_store<float, V, EDGE, kPlain>(p.part[1] + (int64_t)blockIdx.x * p.cols, col[k], valid[k], a);
     }
   }
 }
@@ -278,7 +324,7 @@ hipError_t launch_types(const ResidualNorm& p, int blocks, hipStream_t s) {
   return with_norm_form(shape, p, [&](auto g, auto c, auto post, auto gate, auto e) {
     return launch_kernel(residual_norm_grad_kernel<T, R, decltype(g)::value, decltype(c)::value, decltype(post)::value,
                                                    decltype(gate)::value, decltype(e)::value>,
-                         dim3((unsigned)blocks), p, s, norm_threads(shape), p.held);
+                         dim3((unsigned)blocks), p, s, norm_threads(shape), p.held + p.sums);
   });
 }
 
