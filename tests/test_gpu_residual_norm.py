@@ -465,3 +465,16 @@ def test_streams_bits_and_graphs(ns):
     with torch.cuda.graph(graph):
         with pytest.raises(ns.MuonError):
             ns.residual_norm(leaf, x)
+
+
+@pytest.mark.parametrize("cols", [8200, 12296, 16379, 16384])
+@pytest.mark.parametrize("shape", [(3, 100), (300, 2), (2, 1), (41, 1)])
+def test_wide_rows_of_sequences(ns, cols, shape):
+    """More than 8192 columns with both the norm after the block and a gate of each sequence: workgroups
+    that go through rows of one sequence, and through several sequences."""
+    for dtype, stream in ((BF, BF), (F32, F32)) if cols == 8200 else ((BF, F32),):
+        b, st = rand(shape + (cols,), dtype, 81), rand(shape + (cols,), stream, 82, 2.0)
+        w, pw = rand((cols,), dtype, 83, 0.2, 1.0), rand((cols,), dtype, 84, 0.2, 1.0)
+        g = rand((shape[0], 1, cols), dtype, 85, 0.5)
+        dy, dst = rand(shape + (cols,), dtype, 86, 0.1), rand(shape + (cols,), stream, 87, 0.1)
+        check_backward(ns, dy, dst, st, b, w, pw, g, post=True, what=(cols, shape))
