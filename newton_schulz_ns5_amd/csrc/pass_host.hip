@@ -16,7 +16,10 @@ namespace {
 
 // ---- gradient norm and clipping -------------------------------------------------------
 constexpr int64_t kMaxTensors = (int64_t)1 << 20;
-constexpr int kNormBlocks = 1024, kClipBlocks = 16384;  // workgroups of a launch
+// Workgroups of a launch.  The norm's partials are added by every workgroup of
+// the clipping behind it: 1024 (3 GiB of bf16 normed in 466 us, by 512 in 456;
+// clipped in 1748, and 1879 by 512 and 4096).
+constexpr int kNormBlocks = 1024, kClipBlocks = 16384;
 
 // Tensors [begin, end) of a list, one launch's: at most kListMax that are not
 // empty, and 2^30 items.
@@ -137,22 +140,14 @@ int check_kind(int32_t kind) {
   return MUON_OK;
 }
 
-constexpr int64_t kInfinityCache = (int64_t)256 << 20;
-int64_t list_size(int64_t n, const int32_t* xt, const int64_t* numel) {
-  int64_t bytes = 0;
-  for (int64_t i = 0; i < n; ++i) bytes += numel[i] * esize(xt[i]);
-  return bytes;
-}
-
 // The partials of a list into the workspace.
-int run_partials(int64_t n, const void* const* x, const int32_t* xt, const int64_t* numel, int32_t kind, bool once, uint64_t* partial, hipStream_t s) {
+int run_partials(int64_t n, const void* const* x, const int32_t* xt, const int64_t* numel, int32_t kind, uint64_t* partial, hipStream_t s) {
   return each_part(n, numel, [&](const ListPart& part) {
     NormPartial p;
     fill_list(p.list, part, x, xt, nullptr, nullptr, numel);
     const int blocks = blocks_of(part.items, kNormBlocks);
     p.partial = partial;
     p.max_norm_kind = kind == MUON_NORM_MAX;
-    p.once = once;
     partial += blocks;
     const hipError_t e = launch_norm_partial(p, blocks, s);
     return e == hipSuccess ? MUON_OK : hip_fail(e, "gradient norm");
@@ -179,7 +174,7 @@ int clip(int64_t n, const void* const* x, const int32_t* xt, const int64_t* nume
   if (!total && P.parts) {
     if ((rc = check_workspace(workspace, workspace_bytes, list_bytes(P)))) return rc;
     uint64_t* const partial = (uint64_t*)workspace;
-    if ((rc = run_partials(n, x, xt, numel, kind, list_size(n, xt, numel) > kInfinityCache, partial, s))) return rc;
+    if ((rc = run_partials(n, x, xt, numel, kind, partial, s))) return rc;
     t.partial = partial; t.count = P.partials;
     // The partials of one launch are added by every workgroup of the next one
     // (one launch less); those of several once, in between.
@@ -230,7 +225,7 @@ int muon_grad_norm(int64_t n, const void* const* x, const int32_t* x_dtype, cons
       return fail(MUON_ERR_INVALID_ARG, "norm or square overlaps gradient %lld", (long long)i);
   const ListPlan P = plan_list(n, numel);
   if (P.parts && (rc = check_workspace(workspace, workspace_bytes, list_bytes(P)))) return rc;
-  if ((rc = run_partials(n, x, x_dtype, numel, kind, true, (uint64_t*)workspace, (hipStream_t)stream))) return rc;
+  if ((rc = run_partials(n, x, x_dtype, numel, kind, (uint64_t*)workspace, (hipStream_t)stream))) return rc;
   NormTotal t{};
   t.partial = (const uint64_t*)workspace; t.count = P.partials;
   t.max_norm_kind = kind == MUON_NORM_MAX;
@@ -394,7 +389,8 @@ NormPlan plan_norm_grad(const muon_residual_norm_problem* q) {
   return P;
 }
 
-ResidualNorm norm_params(const muon_residual_norm_problem* q, bool backward) {
+// groups: of threads, over all workgroups.
+ResidualNorm norm_params(const muon_residual_norm_problem* q, bool backward, int64_t groups) {
   ResidualNorm p{};
   p.rows = q->rows; p.cols = (int32_t)q->cols;
   p.post = q->post_norm; p.norm = q->norm;
@@ -406,13 +402,18 @@ ResidualNorm norm_params(const muon_residual_norm_problem* q, bool backward) {
   p.gate = q->gate; p.ldg = q->gate_row_stride; p.gate_bf16 = q->gate_dtype == MUON_BF16;
   p.gate_each = gate_each(q);
   p.scale = q->scale; p.residual_scale = q->residual_scale; p.eps = q->eps; p.offset = q->weight_offset;
-  // The vectors of every row in LDS where those of the workgroups that a CU
-  // holds fit its 160 KiB, beside what a workgroup has for its sums.
+  // The vectors of every row in LDS where groups have several rows and those of
+  // the workgroups that a CU holds fit its 160 KiB, beside what a workgroup has
+  // for its sums.  8192 x 4096 in bf16 with three vectors: forward 43 us, read
+  // again for every row 48; backward 97 and 109.  Forward with one: 42 and 41.
+  // 1024 rows, one to a workgroup, forward with two: 8.9 us and 8.4.
   const NormShape shape = norm_shape(q->cols);
   const int64_t width = (int64_t)shape.group * shape.columns;
-  const int64_t held = 4 * width * ((q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && p.gate_each >= q->rows));
+  const int vectors = (q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && p.gate_each >= q->rows);
+  const int64_t held = 4 * width * vectors;
   if (backward && shape.columns == 16 && q->post_norm && q->gate) p.sums = (int32_t)(8 * width);
-  p.held = (held + p.sums + (shape.group < 64 ? 8192 : 1024)) * norm_resident(norm_threads(shape)) <= 163840 ? (int32_t)held : 0;
+  const bool fits = (held + p.sums + (shape.group < 64 ? 8192 : 1024)) * norm_resident(norm_threads(shape)) <= 163840;
+  p.held = fits && q->rows > groups && vectors > (backward ? 0 : 1) ? (int32_t)held : 0;
   return p;
 }
 
@@ -427,7 +428,7 @@ int muon_residual_norm(const muon_residual_norm_problem* q, void* stream) {
   const NormShape shape = norm_shape(q->cols);
   const int threads = norm_threads(shape), rpw = norm_rows(shape);
   const int blocks = (int)std::min<int64_t>(cdiv(q->rows, rpw), 256 * (2048 / threads));
-  const hipError_t e = launch_residual_norm(norm_params(q, false), q->dtype == MUON_BF16, q->stream_dtype == MUON_BF16, blocks, (hipStream_t)stream);
+  const hipError_t e = launch_residual_norm(norm_params(q, false, (int64_t)blocks * rpw), q->dtype == MUON_BF16, q->stream_dtype == MUON_BF16, blocks, (hipStream_t)stream);
   return e == hipSuccess ? ok() : hip_fail(e, "norms around a block");
 }
 
@@ -445,7 +446,7 @@ int muon_residual_norm_backward(const muon_residual_norm_problem* q, void* works
   if (!q->rows || !q->cols) return ok();
   const NormPlan P = plan_norm_grad(q);
   if ((rc = check_workspace(workspace, workspace_bytes, P.bytes))) return rc;
-  ResidualNorm p = norm_params(q, true);
+  ResidualNorm p = norm_params(q, true, (int64_t)P.blocks * norm_rows(norm_shape(q->cols)));
   p.dy = q->dy; p.lddy = q->dy_row_stride;
   p.dstream = q->dstream; p.ldds = q->dstream_row_stride;
   p.dblock = q->dblock; p.lddb = q->dblock_row_stride;

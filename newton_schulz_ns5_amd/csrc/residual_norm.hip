@@ -7,6 +7,9 @@
 // the registers of a group of threads, 8 columns each (16 bytes of bf16), from
 // its loads to its stores; the two sums of squares are the only traffic between
 // the threads.  The next row's loads are in flight during this row's sums.
+// 8192 rows of 4096 in bf16, both norms, a gate and a residual: 53 us for
+// 268 MB, 5.0 TB/s, a large copy's rate.  One row: 2.7 us, of which the loads,
+// two sums over a workgroup and the launch are all.
 #include "residual_norm.h"
 
 namespace muon {
@@ -16,6 +19,8 @@ template <typename T, typename R, int GS, int C, bool POST, bool GATE, bool EDGE
 __global__ __launch_bounds__(Group<GS>::kMaxThreads) void residual_norm_kernel(const ResidualNorm p) {
   constexpr int V = chunk_values<T, R>(), K = C / V;
   constexpr bool AHEAD = C == 8;     // the next row's loads in flight
+  // What is stored is read next: nontemporal stores gain 2 us of 100 alone and
+  // cost the product that reads y 5 (a norm and its product: 153 and 158 us).
   constexpr StorePolicy TO_STREAM = kPlain, TO_Y = kPlain;
   enum { W, PW, G };
   extern __shared__ __attribute__((aligned(16))) f32x4 held[];
@@ -130,6 +135,10 @@ hipError_t launch_types(const ResidualNorm& p, int blocks, hipStream_t s) {
 
 }  // namespace
 
+// Eight threads up to 64 columns (262144 x 64 in bf16: forward 21 us, backward
+// 32; by 32 threads 29 and 51), 32 up to 256 (65536 x 256 backward: 32 us, by a
+// wave 42; 131072 x 128: 33 and 63), then a workgroup of as many waves as the
+// row needs, 16 columns to a thread where 8 would take more than 1024 threads.
 NormShape norm_shape(int64_t cols) {
   const int64_t chunks = (cols + 7) / 8;
   if (chunks <= 32) return {chunks <= 8 ? 8 : 32, 8};
