@@ -405,15 +405,17 @@ ResidualNorm norm_params(const muon_residual_norm_problem* q, bool backward, int
   // The vectors of every row in LDS where groups have several rows and those of
   // the workgroups that a CU holds fit its 160 KiB, beside what a workgroup has
   // for its sums.  8192 x 4096 in bf16 with three vectors: forward 43 us, read
-  // again for every row 48; backward 97 and 109.  Forward with one: 42 and 41.
-  // 1024 rows, one to a workgroup, forward with two: 8.9 us and 8.4.
+  // again for every row 48; backward 97 and 109.  Forward with one: 42 and 41,
+  // but beside an fp32 stream (5105 x 2056) 22 and 24.  1024 rows, one to a
+  // workgroup, forward with two: 8.9 us and 8.4.  The backward pass holds the gate
+  // of a sequence too while it goes through its rows (5 of 1021 x 2050: 65 and 70).
   const NormShape shape = norm_shape(q->cols);
   const int64_t width = (int64_t)shape.group * shape.columns;
-  const int vectors = (q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && p.gate_each >= q->rows);
+  const int vectors = (q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && (p.gate_each >= q->rows || (backward && p.gate_each > 1)));
   const int64_t held = 4 * width * vectors;
   if (backward && shape.columns == 16 && q->post_norm && q->gate) p.sums = (int32_t)(8 * width);
   const bool fits = (held + p.sums + (shape.group < 64 ? 8192 : 1024)) * norm_resident(norm_threads(shape)) <= 163840;
-  p.held = fits && q->rows > groups && vectors > (backward ? 0 : 1) ? (int32_t)held : 0;
+  p.held = fits && q->rows > groups && vectors > (backward || q->dtype != q->stream_dtype ? 0 : 1) ? (int32_t)held : 0;
   return p;
 }
 

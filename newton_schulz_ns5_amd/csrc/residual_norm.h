@@ -69,9 +69,9 @@ struct GroupSum {
   }
 };
 
-// The vectors of every row (weights, a gate for all rows): held in LDS in fp32,
-// 16 bytes of a thread beside those of the others, or read from memory again
-// for every row.
+// The vectors of every row (weights, a gate for all rows or the gate of those
+// at hand): held in LDS in fp32, 16 bytes of a thread beside those of the others,
+// or read from memory again for every row.
 template <int GS, int K, int V, int N, bool EDGE>
 struct Vectors {
   static constexpr int Q = K * V / 4;  // quarters of a thread
@@ -91,24 +91,36 @@ struct Vectors {
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] += offset[i];
   }
+  // This thread's chunks of vector i.  Where a workgroup holds one row no other
+  // thread reads them.
+  __device__ __forceinline__ void hold(int i, const int (&col)[K], const int (&valid)[K]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (valid[k] <= 0) continue;
+      float v[V];
+      read(i, col[k], valid[k], v);
+#pragma unroll
+      for (int h = 0; h < V / 4; ++h)
+        lds[i][(k * (V / 4) + h) * Group<GS>::size() + Group<GS>::lane()] = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    }
+  }
   // Threads of the workgroup's first row; a barrier follows.
   __device__ __forceinline__ void fill(const int (&col)[K], const int (&valid)[K]) {
     if (Group<GS>::row() == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (!lds[i]) continue;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-          if (valid[k] <= 0) continue;
-          float v[V];
-          read(i, col[k], valid[k], v);
-#pragma unroll
-          for (int h = 0; h < V / 4; ++h)
-            lds[i][(k * (V / 4) + h) * Group<GS>::size() + Group<GS>::lane()] = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
-        }
+        if (lds[i]) hold(i, col, valid);
       }
     }
     __syncthreads();
+  }
+  // Another vector in the place of vector i, by all threads of the workgroup.
+  __device__ __forceinline__ void refill(int i, const void* ptr, const int (&col)[K], const int (&valid)[K]) {
+    p[i] = ptr;
+    if (!lds[i]) return;
+    if constexpr (Group<GS>::kRows > 1) __syncthreads();  // the other rows have read the one before
+    if (Group<GS>::row() == 0) hold(i, col, valid);
+    if constexpr (Group<GS>::kRows > 1) __syncthreads();
   }
   // Chunk k of this thread: ones without a vector.
   __device__ __forceinline__ void get(int i, int k, int col, int valid, float (&v)[V]) const {

@@ -31,7 +31,7 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
   constexpr bool AHEAD = C == 8 && (V == 8 || !(POST && GATE));
   constexpr bool NEED_B = POST || GATE;
   // The sums of PW and G over rows stay in LDS where registers are short: both
-  // at 2048 rows of 16384 columns in bf16 take 154 us there, 252 from spilled
+  // at 2048 rows of 16384 columns in bf16 take 158 us there, 252 from spilled
   // registers; one of them alone 112 and 110 there, 109 and 107 in registers.
   constexpr bool LDS_SUMS = C == 16 && POST && GATE;
   constexpr int KR = LDS_SUMS ? 1 : K;
@@ -47,14 +47,13 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
     col[k] = V * (lane + k * Group<GS>::size());
     valid[k] = p.cols - col[k] < 0 ? 0 : (p.cols - col[k] < V ? p.cols - col[k] : V);
   }
-  const bool gate_all = GATE && p.gate_each >= p.rows;
-  const bool gate_row = GATE && p.gate_each == 1 && !gate_all;  // a gate for every row: its gradient is not a sum
+  const bool gate_row = GATE && p.gate_each == 1 && p.rows > 1;  // a gate for every row: its gradient is not a sum
   const int gate_bytes = p.gate_bf16 ? 2 : 4;
   Vectors<GS, K, V, 3, EDGE> vec;
   f32x4* at = held;
   vec.set(W, p.norm ? p.weight : nullptr, p.weight_bf16, p.offset, at, p.held);
   vec.set(PW, POST ? p.post_weight : nullptr, p.weight_bf16, p.offset, at, p.held);
-  vec.set(G, gate_all ? p.gate : nullptr, p.gate_bf16, 0.f, at, p.held);
+  vec.set(G, GATE && !gate_row ? p.gate : nullptr, p.gate_bf16, 0.f, at, p.held);
   vec.fill(col, valid);
   float aw[K][V], ap[KR][V], ag[KR][V];
 #pragma unroll
@@ -133,12 +132,17 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
       if (NEED_B) w.b[k].load(b, col[k], valid[k]);
     }
   };
+  int64_t gate_at = 0;  // the gate that vec has: the first one, then that of the unit
   for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
     const int64_t g = u / p.gate_chunks;
     const int64_t r0 = g * p.span + (u - g * p.gate_chunks) * p.unit_rows;
     const int64_t end = (g + 1) * p.span < p.rows ? (g + 1) * p.span : p.rows;
     const int64_t r1 = r0 + p.unit_rows < end ? r0 + p.unit_rows : end;
-    const void* gate = GATE && !gate_all && !gate_row ? row_of<GS>(p.gate, g, p.ldg, gate_bytes) : nullptr;
+    if (GATE && !gate_row && g != gate_at) {
+      vec.refill(G, row_of<GS>(p.gate, g, p.ldg, gate_bytes), col, valid);
+      gate_at = g;
+    }
+    const void* gate = nullptr;
     int64_t r = r0 + grp;
     Row raw;
     if (AHEAD && r < r1) load_row(r, raw);
@@ -218,7 +222,7 @@ __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_
         for (int e = 0; e < V; ++e) d[k][e] *= p.scale;        // t
         float gt[V], pw[V], dg[V], dp[V];
         if (GATE) {
-          if (gate_all) vec.get(G, k, col[k], valid[k], gt);
+          if (!gate_row) vec.get(G, k, col[k], valid[k], gt);
           else load_values<V, EDGE>(gate, col[k], p.gate_bf16 != 0, valid[k], gt);
         }
         if (POST) vec.get(PW, k, col[k], valid[k], pw);

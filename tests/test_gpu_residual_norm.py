@@ -478,3 +478,16 @@ def test_wide_rows_of_sequences(ns, cols, shape):
         g = rand((shape[0], 1, cols), dtype, 85, 0.5)
         dy, dst = rand(shape + (cols,), dtype, 86, 0.1), rand(shape + (cols,), stream, 87, 0.1)
         check_backward(ns, dy, dst, st, b, w, pw, g, post=True, what=(cols, shape))
+
+
+@pytest.mark.parametrize("shape", [(1100, 40, 24), (1500, 10, 96), (1100, 2, 2048), (1100, 3, 2050)])
+@pytest.mark.parametrize("post", [True, False])
+def test_more_sequences_than_workgroups(ns, shape, post):
+    """Workgroups that go through one sequence with its gate and then through another one."""
+    cols = shape[-1]
+    b, st = rand(shape, BF, 91), rand(shape, F32, 92, 2.0)
+    w, pw = rand((cols,), BF, 93, 0.2, 1.0), rand((cols,), BF, 94, 0.2, 1.0) if post else None
+    dy, dst = rand(shape, BF, 96, 0.1), rand(shape, F32, 97, 0.1)
+    for dt in (BF, F32):
+        g = rand((shape[0], 1, cols), dt, 95, 0.5)
+        check_backward(ns, dy, dst, st, b, w, pw, g, post=post, what=shape)
