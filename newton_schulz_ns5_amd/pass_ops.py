@@ -230,7 +230,8 @@ def residual_norm(block, residual=None, *, weight=None, post_weight=None, gate=N
     trailing leading ones of 1 ([batch, 1, cols]: one per sequence; block's shape: one per row).  Columns are
     contiguous, rows of any stride; rows that share elements or are not evenly spaced are copied first.  Without
     a residual, a norm after the block, a gate and a scale the stream is ``block`` itself: the first norm of a
-    model.  ``stream`` and ``out`` may be given, and be the inputs themselves.
+    model.  ``stream`` and ``out`` may be given, and be the inputs themselves; where ``out`` is written over such
+    a block the stream is a copy of it.
     """
     if _wants_grad(block, residual, weight, post_weight, gate):
         if stream is not None or out is not None:
@@ -247,6 +248,21 @@ def residual_norm(block, residual=None, *, weight=None, post_weight=None, gate=N
 def _is_block(residual, gate, post, scale, stream):
     """Whether the stream is the block's output itself."""
     return residual is None and gate is None and not post and scale == 1 and stream is None
+
+
+def _extent(t):
+    """The addresses from the first to behind the last byte of t."""
+    at = t.data_ptr()
+    return at, at + (1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride()))) * t.element_size() if t.numel() else at
+
+
+def _written_over(out, source, read):
+    """Whether writing out changes source, of which the library reads `read`: source itself, beside which it
+    refuses every output that shares elements other than as a whole, or a copy, about which it knows nothing."""
+    if read is source:
+        return out.data_ptr() == source.data_ptr()
+    (a, b), (c, d) = _extent(out), _extent(source)
+    return a < d and c < b
 
 
 def _residual_norm(block, residual, weight, post_weight, gate, norm, post_norm, scale, residual_scale, eps,
@@ -270,6 +286,8 @@ def _residual_norm(block, residual, weight, post_weight, gate, norm, post_norm, 
         gate, gp, grows, ldg = _gate_rows(gate, shape)
         gcode = _dt(gate)
     same = residual is None and _is_block(residual, gate, post, scale, stream)
+    if same and out is not None and _written_over(out, source, block):
+        same = False
     if same:
         stream, scode = source, code
     else:
