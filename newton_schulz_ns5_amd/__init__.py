@@ -505,10 +505,10 @@ class MuonNS5:
 
     def clip_grad_norm(self, max_norm, *, extra=(), norm_type=2, eps=1e-6, total=None):
         """Clip the gradients of this optimizer's parameters, and the gradient tensors of ``extra`` with them
-        (those of parameters that another optimizer steps), by the norm of all of them; returns the norm.
-        ``total`` as for :func:`clip_grad_norm`, whose other rules hold too."""
-        from .pass_ops import clip_grad_norm
-        return clip_grad_norm([p.grad for p in self.params] + list(extra), max_norm, norm_type=norm_type, eps=eps,
+        (one tensor or several, of parameters that another optimizer steps), by the norm of all of them; returns
+        the norm.  ``total`` as for :func:`clip_grad_norm`, whose other rules hold too."""
+        from .pass_ops import _tensors, clip_grad_norm
+        return clip_grad_norm([p.grad for p in self.params] + _tensors(extra), max_norm, norm_type=norm_type, eps=eps,
                               total=total)
 
     def step(self):

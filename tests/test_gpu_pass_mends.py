@@ -45,3 +45,23 @@ def test_a_first_norm_written_over_its_block_returns_the_stream(ns, cols, dtype)
     block = both[:, :cols]
     s, y = ns.residual_norm(block, weight=w, out=both[:, cols:])
     assert s is block and torch.equal(s, b.view(15, cols)) and torch.equal(y, want.view(15, cols))
+
+
+def test_a_single_extra_gradient_is_clipped_as_a_whole(ns):
+    """One launch's list of tensors, and the bits of the call with a list of one tensor."""
+    ps = [torch.nn.Parameter(rand((64, 96), F32, 20))]
+    ps[0].grad = rand((64, 96), F32, 21)
+    table = rand((1000, 40), BF, 22)
+    opt = ns.MuonNS5(ps)
+    keep, one, two = ps[0].grad.clone(), table.clone(), table.clone()
+    norm = opt.clip_grad_norm(0.5, extra=[one])
+    clipped = ps[0].grad.clone()
+    ps[0].grad.copy_(keep)
+    assert torch.equal(opt.clip_grad_norm(0.5, extra=two), norm)
+    assert torch.equal(one, two) and torch.equal(ps[0].grad, clipped) and not torch.equal(one, table)
+    # a transposed one, whose elements lie side by side but not its rows'
+    flat = rand((33, 65), F32, 23)
+    ps[0].grad.copy_(keep)
+    exact = float((keep.double().square().sum() + flat.double().square().sum()).sqrt())
+    got = float(opt.clip_grad_norm(0.5, extra=flat.t()))
+    assert abs(got - exact) <= 2.0 ** -23 * exact  # one rounding of an fp64 sum, and a margin of as much
