@@ -148,3 +148,69 @@ def test_gradients_past_32_bits(ns):
     norms.close(dy[-3:], *want["dresidual"], "dresidual")
     norms.close(got[2], *norms.summed(want["dweight"], (0,)), "dweight")
     assert not bool(dy[:-3].any())
+
+
+def test_equal_gradients_of_two_leaves_are_theirs(ns):
+    """The block's and the residual's gradient are one tensor inside the backward pass; two leaves do not share it."""
+    a, b = (rand((9, 128), BF, 31 + i).requires_grad_() for i in range(2))
+    dy = rand((9, 128), BF, 33)
+    for _ in range(2):  # the second time onto gradients that are there
+        ns.residual_norm(a, b)[1].backward(dy)
+        assert torch.equal(a.grad, b.grad) and a.grad.data_ptr() != b.grad.data_ptr()
+    keep = b.grad.clone()
+    ns.clip_grad_norm([a.grad], 0.01)
+    assert torch.equal(b.grad, keep) and not torch.equal(a.grad, keep)
+
+
+@pytest.mark.parametrize("reentrant", [True, False])
+def test_under_checkpointing(ns, reentrant):
+    from torch.utils.checkpoint import checkpoint
+    ids = frequent(60, 40, 41)
+    ts = [rand((40, 72), BF, 42), rand((72,), BF, 43, 0.2, 1.0), rand((72,), BF, 44, 0.2, 1.0), rand((72,), BF, 45)]
+
+    def fn(table, w, pw, g):
+        x = ns.embedding(ids, table, scale=2.0)
+        s, y = ns.residual_norm(x, weight=w)
+        s, y = ns.residual_norm(y, s, weight=w, post_weight=pw, gate=g, scale=0.5)
+        return s + y
+    grads = []
+    for run in (fn, lambda *a: checkpoint(fn, *a, use_reentrant=reentrant)):
+        leaves = [t.clone().requires_grad_() for t in ts]
+        run(*leaves).backward(rand((60, 72), BF, 46))
+        grads.append([t.grad for t in leaves])
+    assert all(torch.equal(p, q) for p, q in zip(*grads))
+
+
+def test_lists_of_nothing_and_of_several_launches(ns):
+    none = torch.empty((0, 5), device="cuda")
+    for kind in (2, math.inf):
+        assert float(ns.grad_norm([none], norm_type=kind)) == 0
+        assert float(ns.clip_grad_norm([none, none], 1.0, norm_type=kind)) == 0
+        assert float(ns.clip_grad_norm([none], 1.0, norm_type=kind, total=torch.tensor(3.0, device="cuda"))) == 3
+    assert float(ns.clip_grad_norm([none], 1.0, total=torch.tensor(9.0, device="cuda", dtype=torch.float64))) == 3
+    # a given total, the largest magnitude and a NaN over three launches
+    xs = [rand((37,), F32, 50 + i) for i in range(300)]
+    keep = [x.clone() for x in xs]
+    assert float(ns.clip_grad_norm(xs, 1.0, eps=0.0, total=torch.tensor(4.0, device="cuda"))) == 4
+    assert all(torch.equal(x, k / 4) for x, k in zip(xs, keep))
+    top = max(float(x.abs().max()) for x in xs)
+    assert float(ns.clip_grad_norm(xs, top / 2, eps=0.0, norm_type="inf")) == top
+    assert all(torch.equal(x, k / 8) for x, k in zip(xs, keep))
+    xs[299][5] = math.nan
+    for kind in (2, math.inf):
+        outs = [torch.zeros_like(x) for x in xs]
+        assert math.isnan(float(ns.clip_grad_norm(xs, 1.0, norm_type=kind, out=outs)))
+        assert all(bool(o.isnan().all()) for o in outs)
+
+
+def test_inference_mode(ns):
+    ids, table, w = frequent(20, 30, 61), rand((30, 40), BF, 62).requires_grad_(), rand((40,), BF, 63, 0.2, 1.0).requires_grad_()
+    with torch.no_grad():
+        x = ns.embedding(ids, table)
+        want = (x.clone(),) + ns.residual_norm(x, x, weight=w)
+    with torch.inference_mode():
+        x = ns.embedding(ids, table, out=torch.empty((20, 40), dtype=BF, device="cuda"))
+        got = (x.clone(),) + ns.residual_norm(x, x, weight=w, out=torch.empty_like(x))
+        grads = [x.clone()]
+        assert float(ns.clip_grad_norm(grads, 1e9)) == float(ns.grad_norm(grads))
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
