@@ -513,7 +513,8 @@ int muon_embedding_backward(const muon_embedding_problem* p, void* workspace, si
  * may be NULL: ones, without the offset.  gate [gate_rows][cols] has one row
  * for rows / gate_rows consecutive rows each: one for all, one per sequence, or
  * one per row.  Everything is formed in fp32 and rounded once on store; y is
- * formed from s before its rounding.
+ * formed from s before its rounding.  So are the means: a row whose sum of
+ * squares passes 2^128 is normed to zeros.
  * Rows have unit column stride; row strides are in elements, only alignment to
  * the element size is required (16-byte aligned rows are fastest).
  * Forward: stream may be NULL with norm.  Backward reads stream as the forward

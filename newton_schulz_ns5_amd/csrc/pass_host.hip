@@ -355,7 +355,13 @@ int norm_resident(int threads) {
   return waves < 4 ? 16 / waves : 4 / (int)cdiv(waves, 4);
 }
 
-// Launch geometry of the gradients; it depends on the sizes only.
+// Launch geometry of the gradients; it depends on the sizes only.  A unit of rows
+// belongs to one row of the gate, so gates of many sequences share the card out
+// unevenly, and their partials are added by a workgroup for every 32 columns of
+// every sequence.  8192 x 4096 in bf16 takes 96 us with a gate for all rows, 99 as
+// 5 sequences, 166 as 256 (two partials each: 74 us of it in their sums), 127 as 300
+// (one workgroup each, 212 of 512 idle), 96 as 512, 117 as 513 (one workgroup has
+// two), 96 as 1024.
 struct NormPlan {
   int blocks = 0;
   int64_t units = 0, unit_rows = 0, span = 0, gates = 0;
@@ -404,11 +410,14 @@ ResidualNorm norm_params(const muon_residual_norm_problem* q, bool backward, int
   p.scale = q->scale; p.residual_scale = q->residual_scale; p.eps = q->eps; p.offset = q->weight_offset;
   // The vectors of every row in LDS where groups have several rows and those of
   // the workgroups that a CU holds fit its 160 KiB, beside what a workgroup has
-  // for its sums.  8192 x 4096 in bf16 with three vectors: forward 43 us, read
-  // again for every row 48; backward 97 and 109.  Forward with one: 42 and 41,
-  // but beside an fp32 stream (5105 x 2056) 22 and 24.  1024 rows, one to a
-  // workgroup, forward with two: 8.9 us and 8.4.  The backward pass holds the gate
-  // of a sequence too while it goes through its rows (5 of 1021 x 2050: 65 and 70).
+  // for its sums.  8192 x 4096 in bf16 with three vectors: forward 49 us, read
+  // again for every row 57; backward 97 and 110; with one 57 and 61.  Forward with
+  // one: 43 and 42, but beside an fp32 stream (5105 x 2056) 26 and 28.  1024 rows,
+  // one to a workgroup, forward with two: 10.3 us and 9.2.  The backward pass holds
+  // the gate of a sequence too while it goes through its rows (5 of 1021 x 2050: 63
+  // and 75).  All of calls behind each other on six sets of inputs in turn, whose
+  // outputs share memory and stay in the caches in part: the forward pass into
+  // memory of its own takes 54 us, a copy's rate.
   const NormShape shape = norm_shape(q->cols);
   const int64_t width = (int64_t)shape.group * shape.columns;
   const int vectors = (q->norm && q->weight) + (q->post_norm && q->post_weight) + (q->gate && (p.gate_each >= q->rows || (backward && p.gate_each > 1)));
@@ -542,6 +551,8 @@ EmbedPlan plan_embed(const muon_embedding_problem* q) {
   // where a row fills waves and there are many (8192 tokens of 4096: 218 us, by
   // 16: 223, by 64 of 65537: 89 for 75); rows that share a wave wait for each
   // other's stores, so theirs stay short (48435 tokens of 27: 12 us, by 32: 21).
+  // Many is more than 4096, where the two do not cross: 4096 tokens of 512 over 1000
+  // rows take 17.4 us, 4097 take 21.0.
   P.piece = group >= 64 && n > 4096 ? 2 * kPieceLeast : kPieceLeast;
   while (P.piece < kPieceMost && cdiv(cdiv(n, P.piece), per) * P.col_blocks > 4096) P.piece *= 2;
   P.pieces = cdiv(n, P.piece);

@@ -23,16 +23,22 @@ template <typename T, typename R, int GS, int C, bool POST, bool GATE, bool EDGE
 __global__ __launch_bounds__(Group<GS>::kMaxThreads, 4) void residual_norm_grad_kernel(const ResidualNorm p) {
   constexpr int V = chunk_values<T, R>(), K = C / V;
   constexpr int ROWS = Group<GS>::kRows;
-  // The next row's loads are in flight where the registers hold them: this row
-  // is unpacked to fp32 first and they take its place (8192 x 4096 in bf16 with
-  // both the norm after the block and a gate: 96 us; with registers of their own
-  // 99).  Where V is 4 and both are there, or C is 16, they would be spilled
-  // (5105 x 2050 with an fp32 stream: 61 us so, 56 without).
+  // The next row's loads are in flight but where V is 4 with both the norm after
+  // the block and a gate, or C is 16: this row is unpacked to fp32 first and they
+  // take its place (8192 x 4096 in bf16 with both: 96 us; with registers of their
+  // own 99; 5105 x 2050 with both and an fp32 stream, left out: 61 us so, 56
+  // without).  The choice was timed at these shapes only, and spilled registers
+  // stand on both sides of it.  With loads ahead: none to 9 of a workgroup per row,
+  // 19 to 30 of 8 or 32 threads with both at V = 8, up to 28 with a gate alone at
+  // V = 4.  Without: 4 to 20 of a workgroup, 20 to 35 of 8 or 32 threads, and at
+  // C = 16 up to 15 with neither, 135 with one, 49 to 143 with both.
   constexpr bool AHEAD = C == 8 && (V == 8 || !(POST && GATE));
   constexpr bool NEED_B = POST || GATE;
-  // The sums of PW and G over rows stay in LDS where registers are short: both
-  // at 2048 rows of 16384 columns in bf16 take 158 us there, 252 from spilled
-  // registers; one of them alone 112 and 110 there, 109 and 107 in registers.
+  // The sums of PW and G over rows stay in LDS where both are there.  2048 rows of
+  // 16384 columns in bf16: both take 158 us there, 252 from spilled registers; one
+  // of them alone 112 and 110 there, 109 and 107 in registers.  Beside fp32 a kernel
+  // with one of them spills 30 to 135 registers and was not timed in LDS: with a
+  // norm after the block and an fp32 stream it takes 152 us, both 242.
   constexpr bool LDS_SUMS = C == 16 && POST && GATE;
   constexpr int KR = LDS_SUMS ? 1 : K;
   enum { W, PW, G };
